@@ -12,6 +12,9 @@ and a visible GPU, and fails loudly otherwise (there is no fallback path).
     A_bar, log_decay_cumsum = discretise(dt, A, chunk_size=64)
     z = head_mix(y, W)                       # MIMO head mixer after the scan (W: (H*D, H*D))
     grad_y, grad_W = head_mix_backward(y, W, grad_z)
+
+The operators around the scan (module ops): gated_scan, rms_norm, fp8_quantise,
+fp8_matmul and the gradients of the first two.
 """
 
 from __future__ import annotations
@@ -23,6 +26,10 @@ import re
 import threading
 
 import torch
+
+from . import ops
+from .ops import (GATED_CHUNK, GatedGrads, GatedScan, RMSNorm, fp8_matmul, fp8_quantise, gated_scan,
+                  gated_scan_backward, rms_norm, rms_norm_backward)
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIBPATH = os.path.join(_PKG, "libssd.so")
@@ -96,6 +103,7 @@ def load_library(path: str | None = None):
         lib.ssd_head_mix_backward.argtypes = [vp, vp, vp, i64, i64, i64, vp, vp, vp,
                                               ctypes.c_size_t, vp]
         lib.ssd_head_mix_backward.restype = ctypes.c_int
+        ops.declare(lib)
         lib.ssd_status_string.argtypes = [ctypes.c_int]
         lib.ssd_status_string.restype = ctypes.c_char_p
         lib.ssd_version.restype = ctypes.c_int

@@ -13,6 +13,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libssd.so")
 ARCH = "gfx950"
+SOURCES = ("ssd_api.hip", "ssd_ops_api.hip")
 
 
 def hipcc_command(out: str, extra=()):
@@ -21,7 +22,7 @@ def hipcc_command(out: str, extra=()):
         # keep hipcc from forming packed fp32 instructions on its own
         "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
         "-I" + INCLUDE, "-I" + CSRC, *extra,
-        os.path.join(CSRC, "ssd_api.hip"), "-o", out,
+        *(os.path.join(CSRC, f) for f in SOURCES), "-o", out,
     ]
 
 

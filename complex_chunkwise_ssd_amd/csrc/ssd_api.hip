@@ -6,6 +6,7 @@
 #include <ssd_bwd_kernels.h>
 #include <ssd_segment_kernels.h>
 #include <ssd_mix_kernels.h>
+#include <ssd_host.h>
 
 #include <mutex>
 
@@ -17,15 +18,9 @@ static __device__ __align__(256) unsigned char scratch[SSD_NOALLOC_SCRATCH_BYTES
 
 namespace {
 
-bool aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
-
-int launch_status()
-{
-    const hipError_t e = hipGetLastError();
-    return e == hipSuccess ? SSD_OK : SSD_ERR_HIP;
-}
-
-unsigned grid_1d(int64_t n, int threads) { return (unsigned)((n + threads - 1) / threads); }
+using ssd::aligned;
+using ssd::grid_1d;
+using ssd::launch_status;
 
 int check_sizes(int64_t batch, int64_t T, int64_t H, int64_t N, int64_t D, int64_t chunk)
 {

@@ -1,0 +1,268 @@
+// ssd_fp8_kernels.h -- the product of two e4m3 matrices with a float32 scale per block of
+// 128 values:
+//     out[m, n] = sum over kb of sa[kb, m] sb[., .] * sum over k in block kb of a[m, k] b[n, k]
+// sb is one value per 128 x 128 block of b (weights) or one per row of b and block (both
+// operands activations or gradients).
+//
+// The inner sum of 128 products is exactly one 16x16x128 e4m3 MFMA, started from zero; its
+// four results per lane are then multiplied by the two scales and added to the float32
+// sums. That is four vector FMAs per MFMA (16 of its 32 cycles), which run beside the next
+// MFMAs. b's rows are the MFMA's rows and a's rows its columns, so that a lane holds one m:
+// its a-scale is one register per 16 rows of a, and b's block scale is the wave's.
+//
+// Precision. The e4m3 MFMA holds its inner sums to 2^-13 of the largest of each eight products,
+// measured 1.3e-5 of a result (rms, normally distributed operands): a 130th of what the
+// rounding to bfloat16 makes, so bfloat16 results are formed that way. It is 50 times
+// what float32 sums make, so float32 results (weight gradients, for the most part) are formed from the
+// same values widened to bfloat16, which is exact, by the 16x16x32 bfloat16 MFMA, which adds in
+// float32, at half the rate (measured 4.4e15 against 2.2e15 flop/s).
+#pragma once
+
+#include <ssd_elem.h>
+
+namespace ssd {
+
+struct Fp8Params {
+    const uint8_t *a, *b;
+    const float *sa;          // (KB, M)
+    const float *sb;          // (ceil(N / 128), KB), or (KB, N)
+    void *out;
+    float *part;              // (splits, M, N) when the sum over k is split
+    int64_t a_stride, b_stride, out_stride;
+    int M, N, K;
+    int tiles_m, tiles_n, splits, split_blocks;  // split_blocks: k blocks per split
+};
+
+// Bytes k .. k + 15 of a row, zeros from K on.
+SSD_DEVICE v4u fp8_chunk(const uint8_t *row, int k, int K)
+{
+    v4u r = {0u, 0u, 0u, 0u};
+    if (k + 16 <= K) {
+        __builtin_memcpy(&r, row + k, 16);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+            if (k + e < K)
+                r[e >> 2] |= (uint32_t)row[k + e] << (8 * (e & 3));
+    }
+    return r;
+}
+
+// The outputs n .. n + CNT - 1 of one row, rounded to OUT.
+template <int OUT, int CNT>
+SSD_DEVICE void fp8_store(void *out, int64_t at, int n, int N, const float (&v)[CNT])
+{
+#pragma unroll
+    for (int g = 0; g < CNT; g += 4) {
+        const int left = N - n - g;
+        char *p = (char *)out + (at + n + g) * ElemSize<OUT>::value;
+        if (OUT == kBF16) {
+            const v2u u = {cvt_pk_bf16(v[g], v[g + 1]), cvt_pk_bf16(v[g + 2], v[g + 3])};
+            if (left >= 4) {
+                __builtin_memcpy(p, &u, 8);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 3; ++e)
+                    if (e < left)
+                        ((uint16_t *)p)[e] = (uint16_t)(u[e >> 1] >> (16 * (e & 1)));
+            }
+        } else {
+            const v4f u = {v[g], v[g + 1], v[g + 2], v[g + 3]};
+            if (left >= 4) {
+                __builtin_memcpy(p, &u, 16);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 3; ++e)
+                    if (e < left)
+                        ((float *)p)[e] = u[e];
+            }
+        }
+    }
+}
+
+// A workgroup of WN x WM waves; a wave holds 16 NB rows of b and 16 MB rows of a. BROW: sb
+// per row of b. OUT: element type of the result; partial sums of a split k are float32.
+// One operand's 32 values of a lane, as its MFMA takes them.
+template <bool WIDE>
+struct Fp8Operand {
+    v4u w[WIDE ? 4 : 2];
+};
+template <bool WIDE>
+SSD_DEVICE Fp8Operand<WIDE> fp8_operand(v4u lo, v4u hi)
+{
+    Fp8Operand<WIDE> r;
+    if (WIDE) {
+        r.w[0] = e4m3_to_bf16(lo[0], lo[1]);
+        r.w[1] = e4m3_to_bf16(lo[2], lo[3]);
+        r.w[WIDE ? 2 : 0] = e4m3_to_bf16(hi[0], hi[1]);
+        r.w[WIDE ? 3 : 0] = e4m3_to_bf16(hi[2], hi[3]);
+    } else {
+        r.w[0] = lo;
+        r.w[1] = hi;
+    }
+    return r;
+}
+template <bool WIDE>
+SSD_DEVICE v4f fp8_block(const Fp8Operand<WIDE> &a, const Fp8Operand<WIDE> &b)
+{
+    v4f d = {0.f, 0.f, 0.f, 0.f};
+    if (WIDE) {
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+            d = mfma_bf16_16x16x32(a.w[WIDE ? t : 0], b.w[WIDE ? t : 0], d);
+        return d;
+    }
+    const v8i x = {(int)a.w[0][0], (int)a.w[0][1], (int)a.w[0][2], (int)a.w[0][3],
+                   (int)a.w[1][0], (int)a.w[1][1], (int)a.w[1][2], (int)a.w[1][3]};
+    const v8i y = {(int)b.w[0][0], (int)b.w[0][1], (int)b.w[0][2], (int)b.w[0][3],
+                   (int)b.w[1][0], (int)b.w[1][1], (int)b.w[1][2], (int)b.w[1][3]};
+    return mfma_e4m3_16x16x128(x, y, d);
+}
+
+template <int NB, int MB, int WN, int WM, bool BROW, int OUT>
+SSD_KERNEL(64 * WN * WM) void fp8_matmul_kernel(Fp8Params p)
+{
+    constexpr int TN = 16 * NB * WN, TM = 16 * MB * WM, THREADS = 64 * WN * WM;
+    constexpr bool WIDE = OUT == kF32;
+    constexpr int CHUNKS = (TN + TM) * 8 / THREADS;
+    static_assert((TN + TM) * 8 % THREADS == 0, "every thread stages the same number of chunks");
+    SSD_LDS uint8_t tile[(TN + TM) * 128];
+    const int tid = thread_id();
+    const int lane = tid & 63, wave = wave_id();
+    const int wn = wave % WN, wm = wave / WN;
+    const int i16 = lane & 15, q = lane >> 4;
+    const int64_t id = block_id();
+    const int tm = (int)(id % p.tiles_m);
+    const int64_t rest = id / p.tiles_m;
+    const int tn = (int)(rest % p.tiles_n);
+    const int split = (int)(rest / p.tiles_n);
+    const int n0 = tn * TN, m0 = tm * TM;
+    const int KB = (p.K + 127) >> 7;
+    const int kb0 = split * p.split_blocks;
+    const int kb1 = kb0 + p.split_blocks < KB ? kb0 + p.split_blocks : KB;
+
+    // Chunk c of staged row r lies at 16 (c ^ (r & 7)): a wave's 16 rows then spread over the banks.
+    v4u hold[CHUNKS];
+    auto fetch = [&](int kb) {
+#pragma unroll
+        for (int s = 0; s < CHUNKS; ++s) {
+            const int f = tid + THREADS * s;
+            const int r = f >> 3, c = f & 7;
+            const bool isb = r < TN;
+            int row = isb ? n0 + r : m0 + r - TN;
+            const int most = (isb ? p.N : p.M) - 1;
+            row = row < most ? row : most;  // rows past the end repeat the last one; not stored
+            const uint8_t *at = isb ? p.b + (int64_t)row * p.b_stride : p.a + (int64_t)row * p.a_stride;
+            hold[s] = fp8_chunk(at, kb * 128 + 16 * c, p.K);
+        }
+    };
+    auto stage = [&]() {
+#pragma unroll
+        for (int s = 0; s < CHUNKS; ++s) {
+            const int f = tid + THREADS * s;
+            const int r = f >> 3, c = f & 7;
+            *(v4u *)&tile[r * 128 + 16 * (c ^ (r & 7))] = hold[s];
+        }
+    };
+    auto operand = [&](int r) {
+        const v4u lo = *(const v4u *)&tile[r * 128 + 16 * (q ^ (r & 7))];
+        const v4u hi = *(const v4u *)&tile[r * 128 + 16 * ((q + 4) ^ (r & 7))];
+        return fp8_operand<WIDE>(lo, hi);
+    };
+
+    v4f acc[NB][MB];
+#pragma unroll
+    for (int j = 0; j < NB; ++j)
+#pragma unroll
+        for (int i = 0; i < MB; ++i)
+            acc[j][i] = v4f{0.f, 0.f, 0.f, 0.f};
+    const int nw = n0 + wn * 16 * NB;            // the wave's first row of b
+    const int mw = m0 + wm * 16 * MB;
+    fetch(kb0);
+    for (int kb = kb0; kb < kb1; ++kb) {
+        block_sync();
+        stage();
+        block_sync();
+        if (kb + 1 < kb1)
+            fetch(kb + 1);
+        Fp8Operand<WIDE> bf[NB];
+        // Row i16 of the MFMA's block j is b's row 4 NB (i16 / 4) + 4 j + i16 % 4: a lane's results
+        // of all blocks are then 4 NB neighbouring n.
+#pragma unroll
+        for (int j = 0; j < NB; ++j)
+            bf[j] = operand(wn * 16 * NB + 4 * NB * (i16 >> 2) + 4 * j + (i16 & 3));
+        float sb[BROW ? 4 * NB : 1];
+        if (BROW) {
+#pragma unroll
+            for (int e = 0; e < 4 * NB; ++e) {
+                const int n = nw + 4 * NB * q + e;
+                sb[e] = p.sb[(int64_t)kb * p.N + (n < p.N ? n : p.N - 1)];
+            }
+        } else {
+            const int nb = (nw < p.N ? nw : p.N - 1) >> 7;
+            sb[0] = ld_uniform(p.sb, (int64_t)nb * KB + kb);
+        }
+#pragma unroll
+        for (int i = 0; i < MB; ++i) {
+            const Fp8Operand<WIDE> af = operand(TN + wm * 16 * MB + 16 * i + i16);
+            const int m = mw + 16 * i + i16;
+            const float sa = p.sa[(int64_t)kb * p.M + (m < p.M ? m : p.M - 1)];
+#pragma unroll
+            for (int j = 0; j < NB; ++j) {
+                const v4f d = fp8_block<WIDE>(bf[j], af);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    acc[j][i][e] += d[e] * (sa * sb[BROW ? 4 * j + e : 0]);
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < MB; ++i) {
+        const int m = mw + 16 * i + i16;
+        if (m >= p.M)
+            continue;
+        float v[4 * NB];
+#pragma unroll
+        for (int e = 0; e < 4 * NB; ++e)
+            v[e] = acc[e >> 2][i][e & 3];
+        if (p.splits > 1)
+            fp8_store<kF32>(p.part, ((int64_t)split * p.M + m) * p.N, nw + 4 * NB * q, p.N, v);
+        else
+            fp8_store<OUT>(p.out, m * p.out_stride, nw + 4 * NB * q, p.N, v);
+    }
+}
+
+// out[m, n] = the sum of the splits' parts in their order, rounded to OUT.
+template <int OUT>
+SSD_KERNEL(256) void fp8_split_sum_kernel(Fp8Params p)
+{
+    const int64_t n = (int64_t)p.M * p.N;
+    const int64_t step = grid_blocks() * 256;
+    for (int64_t e = block_id() * 256 + thread_id(); e < n; e += step) {
+        float acc = 0.f;
+        for (int s = 0; s < p.splits; ++s)
+            acc += p.part[s * n + e];
+        const int64_t m = e / p.N, at = m * p.out_stride + (e - m * p.N);
+        if (OUT == kBF16)
+            ((uint16_t *)p.out)[at] = cvt_bf16(acc);
+        else
+            ((float *)p.out)[at] = acc;
+    }
+}
+
+// out = 0: K = 0 has no terms.
+template <int OUT>
+SSD_KERNEL(256) void fp8_zero_kernel(Fp8Params p)
+{
+    const int64_t n = (int64_t)p.M * p.N;
+    const int64_t step = grid_blocks() * 256;
+    for (int64_t e = block_id() * 256 + thread_id(); e < n; e += step) {
+        const int64_t m = e / p.N, at = m * p.out_stride + (e - m * p.N);
+        if (OUT == kBF16)
+            ((uint16_t *)p.out)[at] = 0;
+        else
+            ((float *)p.out)[at] = 0.f;
+    }
+}
+
+}  // namespace ssd

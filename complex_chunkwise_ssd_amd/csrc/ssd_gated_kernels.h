@@ -1,0 +1,601 @@
+// ssd_gated_kernels.h -- the gated linear recurrence: per sequence and channel, with i and r
+// the sigmoids of the input gate and of the decay gate,
+//     l_t = -k softplus(lam) r_t      a_t = exp(l_t)      m_t = sqrt(1 - a_t^2)
+//     h_t = a_t h_{t-1} + m_t i_t x_t
+// and its gradients, with g_t = gh_t + a_{t+1} g_{t+1} the adjoint of h_t:
+//     gx = g m i     g_input = g m x i (1 - i)     E = g h_{t-1} a l - g i x a^2 (l / m)
+//     g_decay = E (1 - r)     g_lam = sigmoid(lam) / softplus(lam) sum_t E
+// (l / m and not 1 / m: as r goes to 0 so do l and m, and their ratio with them).
+//
+// Both are bound by memory and, close behind, by the arithmetic of the gates (six
+// transcendentals a value). A composition of steps over a span is a pair (A, U):
+// h -> A h + U. A workgroup walks over the tokens of one block of channels in tiles; its
+// waves each take kGatedSteps neighbouring tokens of the tile, find their (A, U) with the
+// gates in registers, meet once in shared memory, fold the pairs of the waves before them
+// onto the state that entered the tile and put out their own tokens from there. So every
+// value is read once, a row of a tile is one full line per wave, and the next tile's
+// loads are in flight meanwhile. Where sequences and channels give too few workgroups, the
+// tokens are cut into segments, and a pass over the gates finds each segment's (A, U)
+// first; each segment then folds those before it.
+#pragma once
+
+#include <ssd_elem.h>
+
+namespace ssd {
+
+constexpr int kGatedChunk = 64;    // tokens between two stored states
+
+struct GatedParams {
+    const void *x, *gi, *gr;
+    const float *lam;
+    const float *init;        // nullable: (B, C)
+    const int *lengths;       // nullable: (B)
+    void *h;                  // (B, T, C)
+    float *final_state;       // nullable: (B, C)
+    float *states;            // nullable: (B, ceil(T / 64), C), the state entering each chunk
+    float *seg;               // (B, segments, 2, C): A then U of each segment (see below)
+    // backward
+    const void *gh;           // (B, T, C)
+    const float *gfinal;      // nullable: (B, C)
+    const float *chunk_states;
+    void *gx, *ggi, *ggr;     // (B, T, C)
+    float *part;              // (B * segments, C): shares of sum E
+    float *ginit;             // nullable: (B, C)
+    int64_t x_stride, gi_stride, gr_stride;  // elements between tokens; a sequence is T of them
+    int B, T, C;
+    int blocks;               // channel blocks
+    int segments, seg_tokens;
+    int launched, seg_first;  // segments of this launch: seg_first .. seg_first + launched - 1
+    float k;                  // decay scale
+};
+
+// Channels per lane: CH neighbouring channels, one load of CH elements.
+template <int T, int CH>
+struct GatedRaw {
+    uint32_t w[T == kF32 ? CH : 1];
+};
+
+template <int T, int CH>
+SSD_DEVICE GatedRaw<T, CH> gated_load(const void *p, int n)
+{
+    GatedRaw<T, CH> r;
+    if (T == kF32) {
+        if (n >= CH) {
+            __builtin_memcpy(&r, p, 4 * CH);
+        } else {
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
+                r.w[T == kF32 ? c : 0] = 0u;
+                if (c < n)
+                    __builtin_memcpy(&r.w[T == kF32 ? c : 0], (const char *)p + 4 * c, 4);
+            }
+        }
+    } else {
+        r.w[0] = 0u;
+        if (CH == 2 && n >= 2)
+            __builtin_memcpy(&r, p, 4);
+        else if (n > 0)
+            r.w[0] = *(const uint16_t *)p;
+    }
+    return r;
+}
+
+template <int T, int CH>
+SSD_DEVICE float gated_value(const GatedRaw<T, CH> &r, int c)
+{
+    if (T == kF32)
+        return u2f(r.w[T == kF32 ? c : 0]);
+    return u2f(c ? r.w[0] & 0xffff0000u : r.w[0] << 16);
+}
+
+template <int T, int CH>
+SSD_DEVICE void gated_store(void *p, int n, const float (&v)[CH])
+{
+    if (T == kF32) {
+#pragma unroll
+        for (int c = 0; c < CH; ++c)
+            if (c < n)
+                ((float *)p)[c] = v[c];
+    } else if (CH == 2) {
+        const uint32_t u = cvt_pk_bf16(v[0], v[CH - 1]);
+        if (n >= 2)
+            __builtin_memcpy(p, &u, 4);
+        else if (n > 0)
+            *(uint16_t *)p = (uint16_t)u;
+    } else if (n > 0) {
+        *(uint16_t *)p = cvt_bf16(v[0]);
+    }
+}
+
+constexpr float kLog2e = 1.44269504088896340736f;
+
+SSD_DEVICE float sigmoid(float v) { return hw_rcp(1.f + hw_exp2(-kLog2e * v)); }
+
+SSD_DEVICE float softplus(float v)
+{
+    return fmaxf(v, 0.f) + log1pf(expf(-fabsf(v)));
+}
+
+// 1 - exp(-z) for z >= 0: below 1/4 its series (the first term left out is z^6 / 5040 of it,
+// 5e-8), above it the difference, which loses at most two bits there. `e` is exp(-z).
+SSD_DEVICE float one_minus_exp(float z, float e)
+{
+    float s = -1.f / 720.f;
+    s = s * z + 1.f / 120.f;
+    s = s * z - 1.f / 24.f;
+    s = s * z + 1.f / 6.f;
+    s = s * z - 0.5f;
+    s = s * z + 1.f;
+    return z < 0.25f ? s * z : 1.f - e;
+}
+
+// The gates of one value. nk = -k softplus(lam).
+struct Gates {
+    float i, r, l, a, m;
+};
+SSD_DEVICE Gates gates(float gi, float gr, float nk)
+{
+    Gates g;
+    g.i = sigmoid(gi);
+    g.r = sigmoid(gr);
+    g.l = nk * g.r;
+    g.a = hw_exp2(kLog2e * g.l);
+    g.m = hw_sqrt(one_minus_exp(-2.f * g.l, g.a * g.a));
+    return g;
+}
+
+// Where a workgroup works: sequence, segment, and this lane's channels.
+template <int CH>
+struct GatedPlace {
+    int64_t b;
+    int seg, c0, n;           // first channel and how many of CH exist (maybe none)
+    int t0, t1, len;          // the segment's tokens; the sequence's length
+};
+template <int CH>
+SSD_DEVICE GatedPlace<CH> gated_place(const GatedParams &p)
+{
+    GatedPlace<CH> g;
+    const int64_t id = block_id();
+    const int64_t rest = id / p.blocks;
+    const int blk = (int)(id - rest * p.blocks);
+    g.b = rest / p.launched;
+    g.seg = (int)(rest - g.b * p.launched) + p.seg_first;
+    g.c0 = blk * 64 * CH + (thread_id() & 63) * CH;
+    g.n = p.C - g.c0;
+    g.n = g.n < 0 ? 0 : (g.n > CH ? CH : g.n);
+    if (g.n == 0)
+        g.c0 = 0;
+    g.t0 = g.seg * p.seg_tokens;
+    g.t1 = g.t0 + p.seg_tokens < p.T ? g.t0 + p.seg_tokens : p.T;
+    g.len = p.T;
+    if (p.lengths) {
+        const int len = p.lengths[g.b];
+        g.len = len < 0 ? 0 : (len < p.T ? len : p.T);
+    }
+    return g;
+}
+
+// SUMMARY: only the segment's (A, U) is wanted, for all but the last segment; the last one's
+// slot takes a copy of the entering state instead, so that final_state may be initial_state:
+// the pass that writes it then reads the copy. Otherwise the outputs.
+template <int T, int CH, int WAVES, int STEPS, bool SUMMARY>
+SSD_KERNEL(64 * WAVES) void gated_scan_kernel(GatedParams p)
+{
+    constexpr int E = ElemSize<T>::value;
+    constexpr int TILE = WAVES * STEPS;
+    SSD_LDS float pairs[2][WAVES][2][64 * CH];
+    const int lane = thread_id() & 63;
+    const int wave = wave_id();
+    const GatedPlace<CH> g = gated_place<CH>(p);
+    float nk[CH], carry[CH], decay[CH];
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+        nk[c] = c < g.n ? -p.k * softplus(p.lam[g.c0 + c]) : 0.f;
+        carry[c] = 0.f;
+        decay[c] = 1.f;
+        if (c < g.n) {
+            float *copy = p.seg + (g.b * p.segments + p.segments - 1) * 2 * (int64_t)p.C + g.c0 + c;
+            const float *from = p.init ? p.init + g.b * p.C + g.c0 + c : nullptr;
+            if (SUMMARY) {
+                if (g.seg == 0 && wave == 0)
+                    *copy = from ? *from : 0.f;
+            } else {
+                carry[c] = p.segments > 1 ? *copy : from ? *from : 0.f;
+            }
+        }
+    }
+    if (!SUMMARY) {
+        for (int s = 0; s < g.seg; ++s)
+#pragma unroll
+            for (int c = 0; c < CH; ++c)
+                if (c < g.n) {
+                    const float *q = p.seg + ((g.b * p.segments + s) * 2) * (int64_t)p.C + g.c0 + c;
+                    carry[c] = q[0] * carry[c] + q[p.C];
+                }
+    }
+    GatedRaw<T, CH> rx[STEPS], ri[STEPS], rr[STEPS];
+    auto fetch = [&](int t) {  // this wave's tokens from t on; those past the length stay unread
+#pragma unroll
+        for (int k = 0; k < STEPS; ++k) {
+            const int n = t + k < g.t1 && t + k < g.len ? g.n : 0;
+            const int64_t row = n > 0 ? g.b * p.T + t + k : 0;
+            rx[k] = gated_load<T, CH>((const char *)p.x + (row * p.x_stride + g.c0) * E, n);
+            ri[k] = gated_load<T, CH>((const char *)p.gi + (row * p.gi_stride + g.c0) * E, n);
+            rr[k] = gated_load<T, CH>((const char *)p.gr + (row * p.gr_stride + g.c0) * E, n);
+        }
+    };
+    fetch(g.t0 + wave * STEPS);
+    int parity = 0;
+    for (int tile = g.t0; tile < g.t1; tile += TILE, parity ^= 1) {
+        const int t = tile + wave * STEPS;
+        float a[STEPS][CH], u[STEPS][CH], A[CH], U[CH];
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            A[c] = 1.f;
+            U[c] = 0.f;
+        }
+#pragma unroll
+        for (int k = 0; k < STEPS; ++k) {
+            const bool in = t + k < g.t1 && t + k < g.len;
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
+                const Gates q = gates(gated_value<T, CH>(ri[k], c), gated_value<T, CH>(rr[k], c), nk[c]);
+                a[k][c] = in ? q.a : 1.f;
+                u[k][c] = in ? q.m * q.i * gated_value<T, CH>(rx[k], c) : 0.f;
+                A[c] *= a[k][c];
+                U[c] = a[k][c] * U[c] + u[k][c];
+            }
+        }
+        if (tile + TILE < g.t1)
+            fetch(t + TILE);
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            pairs[parity][wave][0][c * 64 + lane] = A[c];
+            pairs[parity][wave][1][c * 64 + lane] = U[c];
+        }
+        block_sync();
+        float mine[CH];
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w)
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
+                if (w == 0 || w == wave)
+                    mine[c] = carry[c];
+                const float wa = pairs[parity][w][0][c * 64 + lane];
+                carry[c] = wa * carry[c] + pairs[parity][w][1][c * 64 + lane];
+                if (SUMMARY)
+                    decay[c] *= wa;
+            }
+        if (!SUMMARY) {
+            if (p.states && t % kGatedChunk == 0 && t < g.t1)
+#pragma unroll
+                for (int c = 0; c < CH; ++c)
+                    if (c < g.n)
+                        p.states[(g.b * ((p.T + kGatedChunk - 1) / kGatedChunk) + t / kGatedChunk) * p.C + g.c0 + c] = mine[c];
+#pragma unroll
+            for (int k = 0; k < STEPS; ++k) {
+                float out[CH];
+#pragma unroll
+                for (int c = 0; c < CH; ++c) {
+                    mine[c] = a[k][c] * mine[c] + u[k][c];
+                    out[c] = t + k < g.len ? mine[c] : 0.f;
+                }
+                if (t + k < g.t1)
+                    gated_store<T, CH>((char *)p.h + ((g.b * p.T + t + k) * p.C + g.c0) * E, g.n, out);
+            }
+        }
+    }
+    if (wave != 0)
+        return;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+        if (c >= g.n)
+            continue;
+        if (SUMMARY) {
+            float *q = p.seg + ((g.b * p.segments + g.seg) * 2) * (int64_t)p.C + g.c0 + c;
+            q[0] = decay[c];
+            q[p.C] = carry[c];
+        } else if (p.final_state && g.seg == p.segments - 1) {
+            p.final_state[g.b * p.C + g.c0 + c] = carry[c];
+        }
+    }
+}
+
+// One token per sequence: a lane per channel, nothing to fold.
+template <int T>
+SSD_KERNEL(64) void gated_step_kernel(GatedParams p)
+{
+    constexpr int E = ElemSize<T>::value;
+    const int64_t b = block_id() / p.blocks;
+    const int c = (int)(block_id() - b * p.blocks) * 64 + thread_id();
+    if (c >= p.C)
+        return;
+    const float before = p.init ? p.init[b * p.C + c] : 0.f;
+    const bool in = !p.lengths || p.lengths[b] > 0;
+    float h = before;
+    if (in) {
+        const float x = gated_value<T, 1>(gated_load<T, 1>((const char *)p.x + (b * p.x_stride + c) * E, 1), 0);
+        const float gi = gated_value<T, 1>(gated_load<T, 1>((const char *)p.gi + (b * p.gi_stride + c) * E, 1), 0);
+        const float gr = gated_value<T, 1>(gated_load<T, 1>((const char *)p.gr + (b * p.gr_stride + c) * E, 1), 0);
+        const Gates q = gates(gi, gr, -p.k * softplus(p.lam[c]));
+        h = q.a * before + q.m * q.i * x;
+    }
+    const float out[1] = {in ? h : 0.f};
+    gated_store<T, 1>((char *)p.h + (b * p.C + c) * E, 1, out);
+    if (p.final_state)
+        p.final_state[b * p.C + c] = h;
+    if (p.states)
+        p.states[b * p.C + c] = before;
+}
+
+// The adjoint that enters a segment from its right, without the segments after it: each
+// segment's (A, V), Q -> A Q + V, where Q_t = a_t g_t is what token t hands to the one
+// before it. SUMMARY of the backward: reads the decay gate and gh only.
+template <int T, int CH, int WAVES, int STEPS>
+SSD_KERNEL(64 * WAVES) void gated_bwd_summary_kernel(GatedParams p)
+{
+    constexpr int E = ElemSize<T>::value;
+    constexpr int TILE = WAVES * STEPS;
+    SSD_LDS float pairs[2][WAVES][2][64 * CH];
+    const int lane = thread_id() & 63;
+    const int wave = wave_id();
+    const GatedPlace<CH> g = gated_place<CH>(p);
+    float nk[CH], carry[CH], decay[CH];
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+        nk[c] = c < g.n ? -p.k * softplus(p.lam[g.c0 + c]) : 0.f;
+        carry[c] = 0.f;
+        decay[c] = 1.f;
+    }
+    GatedRaw<T, CH> rr[STEPS], rh[STEPS];
+    auto fetch = [&](int t) {
+#pragma unroll
+        for (int k = 0; k < STEPS; ++k) {
+            const int n = t + k < g.t1 && t + k < g.len ? g.n : 0;
+            const int64_t row = n > 0 ? g.b * p.T + t + k : 0;
+            rr[k] = gated_load<T, CH>((const char *)p.gr + (row * p.gr_stride + g.c0) * E, n);
+            rh[k] = gated_load<T, CH>((const char *)p.gh + (row * p.C + g.c0) * E, n);
+        }
+    };
+    const int tiles = (g.t1 - g.t0 + TILE - 1) / TILE;
+    fetch(g.t0 + (tiles - 1) * TILE + wave * STEPS);
+    int parity = 0;
+    for (int i = tiles - 1; i >= 0; --i, parity ^= 1) {
+        const int t = g.t0 + i * TILE + wave * STEPS;
+        float A[CH], V[CH];
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            A[c] = 1.f;
+            V[c] = 0.f;
+        }
+#pragma unroll
+        for (int k = STEPS - 1; k >= 0; --k) {
+            const bool in = t + k < g.t1 && t + k < g.len;
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
+                const float a = in ? hw_exp2(kLog2e * (nk[c] * sigmoid(gated_value<T, CH>(rr[k], c)))) : 1.f;
+                A[c] *= a;
+                V[c] = a * (V[c] + gated_value<T, CH>(rh[k], c));
+            }
+        }
+        if (i > 0)
+            fetch(t - TILE);
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            pairs[parity][wave][0][c * 64 + lane] = A[c];
+            pairs[parity][wave][1][c * 64 + lane] = V[c];
+        }
+        block_sync();
+#pragma unroll
+        for (int w = WAVES - 1; w >= 0; --w)
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
+                const float wa = pairs[parity][w][0][c * 64 + lane];
+                carry[c] = wa * carry[c] + pairs[parity][w][1][c * 64 + lane];
+                decay[c] *= wa;
+            }
+    }
+    if (wave != 0)
+        return;
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+        if (c < g.n) {
+            float *q = p.seg + ((g.b * p.segments + g.seg) * 2) * (int64_t)p.C + g.c0 + c;
+            q[0] = decay[c];
+            q[p.C] = carry[c];
+        }
+}
+
+// The gradients, tile by tile from the last to the first. A tile is one chunk (64 tokens):
+// its entering state was stored, so the states inside it come from a fold to the right and
+// the adjoints from a fold to the left, over the same products A.
+template <int T, int CH>
+SSD_KERNEL(1024) void gated_scan_bwd_kernel(GatedParams p)
+{
+    constexpr int E = ElemSize<T>::value;
+    constexpr int WAVES = 16, STEPS = 4;
+    static_assert(WAVES * STEPS == kGatedChunk, "a tile is a chunk");
+    SSD_LDS float pairs[2][WAVES][3][64 * CH];
+    const int lane = thread_id() & 63;
+    const int wave = wave_id();
+    const GatedPlace<CH> g = gated_place<CH>(p);
+    const int64_t chunks = (p.T + kGatedChunk - 1) / kGatedChunk;
+    float nk[CH], carry[CH], sum_e[CH];
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+        nk[c] = c < g.n ? -p.k * softplus(p.lam[g.c0 + c]) : 0.f;
+        carry[c] = p.gfinal && c < g.n ? p.gfinal[g.b * p.C + g.c0 + c] : 0.f;
+        sum_e[c] = 0.f;
+    }
+    for (int s = p.segments - 1; s > g.seg; --s)
+#pragma unroll
+        for (int c = 0; c < CH; ++c)
+            if (c < g.n) {
+                const float *q = p.seg + ((g.b * p.segments + s) * 2) * (int64_t)p.C + g.c0 + c;
+                carry[c] = q[0] * carry[c] + q[p.C];
+            }
+    GatedRaw<T, CH> rx[STEPS], ri[STEPS], rr[STEPS], rh[STEPS];
+    float enter[CH];
+    auto fetch = [&](int t) {
+#pragma unroll
+        for (int k = 0; k < STEPS; ++k) {
+            const int n = t + k < g.t1 && t + k < g.len ? g.n : 0;
+            const int64_t row = n > 0 ? g.b * p.T + t + k : 0;
+            rx[k] = gated_load<T, CH>((const char *)p.x + (row * p.x_stride + g.c0) * E, n);
+            ri[k] = gated_load<T, CH>((const char *)p.gi + (row * p.gi_stride + g.c0) * E, n);
+            rr[k] = gated_load<T, CH>((const char *)p.gr + (row * p.gr_stride + g.c0) * E, n);
+            rh[k] = gated_load<T, CH>((const char *)p.gh + (row * p.C + g.c0) * E, n);
+        }
+    };
+    auto fetch_state = [&](int tile) {
+#pragma unroll
+        for (int c = 0; c < CH; ++c)
+            enter[c] = c < g.n ? p.chunk_states[(g.b * chunks + tile / kGatedChunk) * p.C + g.c0 + c] : 0.f;
+    };
+    const int last = g.t0 + (g.t1 - g.t0 - 1) / kGatedChunk * kGatedChunk;
+    fetch(last + wave * STEPS);
+    fetch_state(last);
+    int parity = 0;
+    for (int tile = last; tile >= g.t0; tile -= kGatedChunk, parity ^= 1) {
+        const int t = tile + wave * STEPS;
+        Gates q[STEPS][CH];
+        float x[STEPS][CH], gh[STEPS][CH], before[CH];
+        float A[CH], U[CH], V[CH];
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            A[c] = 1.f;
+            U[c] = V[c] = 0.f;
+            before[c] = enter[c];
+        }
+#pragma unroll
+        for (int k = 0; k < STEPS; ++k) {
+            const bool in = t + k < g.t1 && t + k < g.len;
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
+                x[k][c] = gated_value<T, CH>(rx[k], c);
+                gh[k][c] = gated_value<T, CH>(rh[k], c);
+                q[k][c] = gates(gated_value<T, CH>(ri[k], c), gated_value<T, CH>(rr[k], c), nk[c]);
+                if (!in) {
+                    q[k][c].a = 1.f;
+                    q[k][c].m = 0.f;
+                    q[k][c].l = 0.f;
+                }
+                A[c] *= q[k][c].a;
+                U[c] = q[k][c].a * U[c] + q[k][c].m * q[k][c].i * x[k][c];
+            }
+        }
+#pragma unroll
+        for (int k = STEPS - 1; k >= 0; --k)
+#pragma unroll
+            for (int c = 0; c < CH; ++c)
+                V[c] = q[k][c].a * (V[c] + gh[k][c]);
+        if (tile - kGatedChunk >= g.t0) {
+            fetch(t - kGatedChunk);
+            fetch_state(tile - kGatedChunk);
+        }
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            pairs[parity][wave][0][c * 64 + lane] = A[c];
+            pairs[parity][wave][1][c * 64 + lane] = U[c];
+            pairs[parity][wave][2][c * 64 + lane] = V[c];
+        }
+        block_sync();
+        for (int w = 0; w < wave; ++w)
+#pragma unroll
+            for (int c = 0; c < CH; ++c)
+                before[c] = pairs[parity][w][0][c * 64 + lane] * before[c] + pairs[parity][w][1][c * 64 + lane];
+        float right[CH];  // a g of the token after this wave's last
+#pragma unroll
+        for (int w = WAVES - 1; w >= 0; --w)
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
+                if (w == WAVES - 1 || w == wave)
+                    right[c] = carry[c];
+                carry[c] = pairs[parity][w][0][c * 64 + lane] * carry[c] + pairs[parity][w][2][c * 64 + lane];
+            }
+        float hb[STEPS][CH];
+#pragma unroll
+        for (int k = 0; k < STEPS; ++k)
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
+                hb[k][c] = before[c];
+                before[c] = q[k][c].a * before[c] + q[k][c].m * q[k][c].i * x[k][c];
+            }
+#pragma unroll
+        for (int k = STEPS - 1; k >= 0; --k) {
+            const bool in = t + k < g.t1 && t + k < g.len;
+            float gx[CH], ggi[CH], ggr[CH];
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
+                const Gates &v = q[k][c];
+                const float gt = gh[k][c] + right[c];
+                right[c] = v.a * gt;
+                const float ratio = v.m > 0.f ? v.l * hw_rcp(v.m) : 0.f;
+                const float gi = gt * v.i;
+                const float e = v.a * (gt * hb[k][c] * v.l - gi * x[k][c] * v.a * ratio);
+                gx[c] = in ? gi * v.m : 0.f;
+                ggi[c] = gx[c] * x[k][c] * (1.f - v.i);
+                ggr[c] = in ? e * (1.f - v.r) : 0.f;
+                sum_e[c] += in ? e : 0.f;
+            }
+            if (t + k < g.t1) {
+                const int64_t at = ((g.b * p.T + t + k) * p.C + g.c0) * E;
+                gated_store<T, CH>((char *)p.gx + at, g.n, gx);
+                gated_store<T, CH>((char *)p.ggi + at, g.n, ggi);
+                gated_store<T, CH>((char *)p.ggr + at, g.n, ggr);
+            }
+        }
+    }
+    // sum over the waves, in wave order (the slot that the last tile did not use)
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+        pairs[parity][wave][0][c * 64 + lane] = sum_e[c];
+    block_sync();
+    if (wave != 0)
+        return;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+        if (c >= g.n)
+            continue;
+        float e = 0.f;
+        for (int w = 0; w < WAVES; ++w)
+            e += pairs[parity][w][0][c * 64 + lane];
+        p.part[(g.b * p.segments + g.seg) * p.C + g.c0 + c] = e;
+        if (p.ginit && g.seg == 0)
+            p.ginit[g.b * p.C + g.c0 + c] = carry[c];
+    }
+}
+
+// g_lam = sigmoid(lam) / softplus(lam) * sum of the shares, in their order (the ratio goes to
+// 1 where lam is so low that both underflow). 64 channels per workgroup, 16 waves.
+SSD_KERNEL(64 * 16) void gated_lam_kernel(const float *part, int rows, int C, const float *lam, float *out)
+{
+    SSD_LDS float sums[16][64];
+    const int lane = thread_id() & 63;
+    const int wave = wave_id();
+    const int c = (int)block_id() * 64 + lane;
+    float acc = 0.f;
+    if (c < C)
+        for (int r = wave; r < rows; r += 16)
+            acc += part[(int64_t)r * C + c];
+    sums[wave][lane] = acc;
+    block_sync();
+    if (wave == 0 && c < C) {
+        float t = 0.f;
+        for (int i = 0; i < 16; ++i)
+            t += sums[i][lane];
+        const float v = lam[c];
+        const float sp = softplus(v);
+        out[c] = t * (sp > 0.f ? 1.f / (1.f + expf(-v)) / sp : 1.f);
+    }
+}
+
+// final = init (or zeros): T = 0.
+SSD_KERNEL(256) void gated_copy_kernel(const float *init, float *out, int64_t n)
+{
+    const int64_t step = grid_blocks() * 256;
+    for (int64_t e = block_id() * 256 + thread_id(); e < n; e += step)
+        out[e] = init ? init[e] : 0.f;
+}
+
+}  // namespace ssd

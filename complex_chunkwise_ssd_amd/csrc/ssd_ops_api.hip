@@ -1,0 +1,706 @@
+// ssd_ops_api.hip -- C ABI of the operators around the scan (declared in include/ssd.h): the
+// gated recurrence, the RMS norm, 8-bit quantisation and products. Argument checks, work planning and
+// kernel launches on the caller's stream; nothing is allocated.
+#include "ssd.h"
+
+#include <ssd_fp8_kernels.h>
+#include <ssd_gated_kernels.h>
+#include <ssd_norm_kernels.h>
+#include <ssd_quant_kernels.h>
+#include <ssd_host.h>
+
+namespace {
+
+using ssd::aligned;
+using ssd::grid_1d;
+using ssd::launch_status;
+using ssd::overlap_bytes;
+
+constexpr int64_t kMaxGrid = (1LL << 31) - 1;
+constexpr int64_t kMaxElems = 1LL << 40;  // of one operand: products of sizes and strides stay in 64 bits
+
+size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
+
+bool dtype_ok(int dtype) { return dtype == SSD_F32 || dtype == SSD_BF16; }
+int elem_size(int dtype) { return dtype == SSD_BF16 ? 2 : 4; }
+
+// Bytes from a strided matrix's first element to past its last.
+int64_t span(int64_t rows, int64_t cols, int64_t stride, int elem)
+{
+    return rows > 0 && cols > 0 ? ((rows - 1) * stride + cols) * elem : 0;
+}
+
+// ------------------------------------------------------------------ RMS norm
+
+int check_norm(int dtype, int64_t rows, int64_t F)
+{
+    if (!dtype_ok(dtype) || rows < 0 || F < 1)
+        return SSD_ERR_SHAPE;
+    if (F > ssd::kNormMaxF || rows > (1LL << 31) - 1)
+        return SSD_ERR_UNSUPPORTED;
+    return SSD_OK;
+}
+
+// Workgroups that the norm kernels are launched with: they walk over the rows, so about as
+// many as the GPU holds at once (256 compute units, several each).
+int64_t norm_groups(int64_t rows, int rows_per_group, int64_t most)
+{
+    const int64_t need = (rows + rows_per_group - 1) / rows_per_group;
+    return need < most ? need : most;
+}
+constexpr int64_t kNormGroups = 2048;
+constexpr int64_t kNormBwdGroups = 1024;
+
+// Rows a workgroup holds at once for this F (see launch_norm).
+int norm_rows(int64_t F) { return F <= 2048 ? 4 : 1; }
+
+template <int T, int WAVES, int STEPS>
+int launch_norm_as(const ssd::NormParams &p, hipStream_t s)
+{
+    using Shape = ssd::NormShape<WAVES>;
+    const int64_t groups = norm_groups(p.rows, Shape::rows, kNormGroups);
+    hipLaunchKernelGGL((ssd::rms_norm_kernel<T, WAVES, STEPS>), dim3((unsigned)groups),
+                       dim3(Shape::threads), 0, s, p);
+    return launch_status();
+}
+
+template <int T>
+int launch_norm(const ssd::NormParams &p, hipStream_t s)
+{
+    if (p.F <= 512)
+        return launch_norm_as<T, 1, 1>(p, s);
+    if (p.F <= 1024)
+        return launch_norm_as<T, 1, 2>(p, s);
+    if (p.F <= 2048)
+        return launch_norm_as<T, 1, 4>(p, s);
+    if (p.F <= 4096)
+        return launch_norm_as<T, 4, 2>(p, s);
+    if (p.F <= 8192)
+        return launch_norm_as<T, 4, 4>(p, s);
+    return launch_norm_as<T, 8, 4>(p, s);
+}
+
+template <int T, int WAVES, int STEPS>
+int launch_norm_bwd_as(const ssd::NormBwdParams &p, int64_t groups, hipStream_t s)
+{
+    hipLaunchKernelGGL((ssd::rms_norm_bwd_kernel<T, WAVES, STEPS>), dim3((unsigned)groups),
+                       dim3(ssd::NormShape<WAVES>::threads), 0, s, p);
+    return launch_status();
+}
+
+template <int T>
+int launch_norm_bwd(const ssd::NormBwdParams &p, int64_t groups, hipStream_t s)
+{
+    if (p.F <= 512)
+        return launch_norm_bwd_as<T, 1, 1>(p, groups, s);
+    if (p.F <= 1024)
+        return launch_norm_bwd_as<T, 1, 2>(p, groups, s);
+    if (p.F <= 2048)
+        return launch_norm_bwd_as<T, 1, 4>(p, groups, s);
+    if (p.F <= 4096)
+        return launch_norm_bwd_as<T, 4, 2>(p, groups, s);
+    if (p.F <= 8192)
+        return launch_norm_bwd_as<T, 4, 4>(p, groups, s);
+    return launch_norm_bwd_as<T, 8, 4>(p, groups, s);
+}
+
+// -------------------------------------------------------------- 8-bit values
+
+template <int T>
+int launch_quantise(const ssd::QuantParams &p, bool whole, bool turn, hipStream_t s)
+{
+    if (!whole && !turn) {
+        const int64_t blocks = p.rows * ((p.cols + 127) / 128);
+        const int64_t grid = (blocks + 16 * ssd::kQuantUnroll - 1) / (16 * ssd::kQuantUnroll);
+        if (grid > kMaxGrid)
+            return SSD_ERR_UNSUPPORTED;
+        hipLaunchKernelGGL((ssd::quantise_rows_kernel<T>), dim3((unsigned)grid), dim3(256), 0, s, p);
+        return launch_status();
+    }
+    const int64_t tiles = ((p.rows + 127) / 128) * ((p.cols + 127) / 128);
+    if (tiles > kMaxGrid)
+        return SSD_ERR_UNSUPPORTED;
+    const dim3 grid((unsigned)tiles), block(256);
+    if (whole && turn)
+        hipLaunchKernelGGL((ssd::quantise_tile_kernel<T, true, true>), grid, block, 0, s, p);
+    else if (whole)
+        hipLaunchKernelGGL((ssd::quantise_tile_kernel<T, true, false>), grid, block, 0, s, p);
+    else
+        hipLaunchKernelGGL((ssd::quantise_tile_kernel<T, false, true>), grid, block, 0, s, p);
+    return launch_status();
+}
+
+struct Fp8Plan {
+    int tiles_m, tiles_n, splits, split_blocks;
+    size_t bytes;
+};
+
+constexpr int kFp8TileN = 128, kFp8TileM = 128;
+
+int check_fp8(int64_t M, int64_t N, int64_t K, int64_t b_block_rows, int out_dtype)
+{
+    if (M < 0 || N < 1 || K < 0 || (b_block_rows != 1 && b_block_rows != 128) || !dtype_ok(out_dtype))
+        return SSD_ERR_SHAPE;
+    if (M > (1LL << 30) || N > (1LL << 30) || K > (1LL << 30))
+        return SSD_ERR_UNSUPPORTED;
+    const int64_t tiles = ((M + kFp8TileM - 1) / kFp8TileM) * ((N + kFp8TileN - 1) / kFp8TileN);
+    return tiles > kMaxGrid / 64 ? SSD_ERR_UNSUPPORTED : SSD_OK;
+}
+
+Fp8Plan fp8_plan(int64_t M, int64_t N, int64_t K)
+{
+    Fp8Plan p{};
+    p.tiles_m = (int)((M + kFp8TileM - 1) / kFp8TileM);
+    p.tiles_n = (int)((N + kFp8TileN - 1) / kFp8TileN);
+    const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n, kb = (K + 127) / 128;
+    int64_t splits = tiles > 0 ? 512 / tiles : 1;
+    splits = splits > kb / 4 ? kb / 4 : splits;
+    splits = splits > 32 ? 32 : splits;
+    splits = splits < 1 ? 1 : splits;
+    p.split_blocks = (int)((kb + splits - 1) / splits);
+    p.splits = kb > 0 ? (int)((kb + p.split_blocks - 1) / p.split_blocks) : 1;
+    p.bytes = p.splits > 1 ? align256((size_t)p.splits * M * N * 4) : 0;
+    return p;
+}
+
+template <bool BROW, int OUT>
+int launch_fp8(const ssd::Fp8Params &p, hipStream_t s)
+{
+    const int64_t n = (int64_t)p.M * p.N;
+    const unsigned flat = (unsigned)((n + 255) / 256 < 8192 ? (n + 255) / 256 : 8192);
+    if (p.K == 0) {
+        hipLaunchKernelGGL((ssd::fp8_zero_kernel<OUT>), dim3(flat), dim3(256), 0, s, p);
+        return launch_status();
+    }
+    hipLaunchKernelGGL((ssd::fp8_matmul_kernel<4, 4, 2, 2, BROW, OUT>),
+                       dim3((unsigned)((int64_t)p.tiles_m * p.tiles_n * p.splits)), dim3(256), 0, s, p);
+    if (int st = launch_status())
+        return st;
+    if (p.splits > 1) {
+        hipLaunchKernelGGL((ssd::fp8_split_sum_kernel<OUT>), dim3(flat), dim3(256), 0, s, p);
+        return launch_status();
+    }
+    return SSD_OK;
+}
+
+// ------------------------------------------------------------ gated recurrence
+
+constexpr int kGatedWaves = 16, kGatedSteps = 8;
+
+struct GatedPlan {
+    int ch;                   // channels per lane
+    int blocks;               // channel blocks
+    int segments, seg_tokens;
+    size_t seg_bytes;
+};
+
+int check_gated(int dtype, int64_t batch, int64_t T, int64_t C, int64_t s0, int64_t s1, int64_t s2)
+{
+    if (!dtype_ok(dtype) || batch < 0 || T < 0 || C < 1 || s0 < C || s1 < C || s2 < C)
+        return SSD_ERR_SHAPE;
+    if (T > (1LL << 30) || C > (1LL << 24) || batch > (1LL << 24))
+        return SSD_ERR_UNSUPPORTED;
+    const int64_t stride = s0 > s1 ? (s0 > s2 ? s0 : s2) : (s1 > s2 ? s1 : s2);
+    const int64_t tokens = batch * T;
+    if (tokens > 0 && stride > kMaxElems / tokens)
+        return SSD_ERR_UNSUPPORTED;
+    return SSD_OK;
+}
+
+// Segments: as many as give about 256 workgroups (one per compute unit), of whole chunks and
+// at least 256 tokens.
+GatedPlan gated_plan(int64_t batch, int64_t T, int64_t C, int dtype)
+{
+    GatedPlan p{};
+    p.ch = dtype == SSD_BF16 ? 2 : 1;
+    p.blocks = (int)((C + 64 * p.ch - 1) / (64 * p.ch));
+    const int64_t groups = batch * p.blocks;
+    int64_t seg = groups > 0 ? 256 / groups : 1;
+    const int64_t most = T / 256;
+    seg = seg > most ? most : seg;
+    seg = seg < 1 ? 1 : seg;
+    int64_t tokens = (T + seg - 1) / seg;
+    tokens = (tokens + ssd::kGatedChunk - 1) / ssd::kGatedChunk * ssd::kGatedChunk;
+    p.segments = T > 0 ? (int)((T + tokens - 1) / tokens) : 1;
+    p.seg_tokens = (int)tokens;
+    p.seg_bytes = p.segments > 1 ? align256((size_t)batch * p.segments * 2 * C * 4) : 0;
+    return p;
+}
+
+bool gated_grid_ok(const GatedPlan &p, int64_t batch)
+{
+    return batch * p.blocks <= kMaxGrid / p.segments;
+}
+
+template <int T, int CH>
+int launch_gated(ssd::GatedParams p, hipStream_t s)
+{
+    const dim3 block(64 * kGatedWaves);
+    if (p.segments > 1) {
+        ssd::GatedParams q = p;
+        q.launched = p.segments - 1;
+        hipLaunchKernelGGL((ssd::gated_scan_kernel<T, CH, kGatedWaves, kGatedSteps, true>),
+                           dim3((unsigned)((int64_t)p.B * p.blocks * q.launched)), block, 0, s, q);
+        if (int st = launch_status())
+            return st;
+    }
+    hipLaunchKernelGGL((ssd::gated_scan_kernel<T, CH, kGatedWaves, kGatedSteps, false>),
+                       dim3((unsigned)((int64_t)p.B * p.blocks * p.segments)), block, 0, s, p);
+    return launch_status();
+}
+
+template <int T, int CH>
+int launch_gated_bwd(ssd::GatedParams p, float *grad_lam, hipStream_t s)
+{
+    if (p.segments > 1) {
+        ssd::GatedParams q = p;
+        q.launched = p.segments - 1;
+        q.seg_first = 1;
+        hipLaunchKernelGGL((ssd::gated_bwd_summary_kernel<T, CH, kGatedWaves, kGatedSteps>),
+                           dim3((unsigned)((int64_t)p.B * p.blocks * q.launched)),
+                           dim3(64 * kGatedWaves), 0, s, q);
+        if (int st = launch_status())
+            return st;
+    }
+    hipLaunchKernelGGL((ssd::gated_scan_bwd_kernel<T, CH>),
+                       dim3((unsigned)((int64_t)p.B * p.blocks * p.segments)), dim3(1024), 0, s, p);
+    if (int st = launch_status())
+        return st;
+    hipLaunchKernelGGL(ssd::gated_lam_kernel, dim3(grid_1d(p.C, 64)), dim3(1024), 0, s,
+                       (const float *)p.part, p.B * p.segments, p.C, p.lam, grad_lam);
+    return launch_status();
+}
+
+int launch_copy(const float *from, float *to, int64_t n, hipStream_t s)
+{
+    const int64_t blocks = (n + 255) / 256 < 4096 ? (n + 255) / 256 : 4096;
+    hipLaunchKernelGGL(ssd::gated_copy_kernel, dim3((unsigned)blocks), dim3(256), 0, s, from, to, n);
+    return launch_status();
+}
+
+}  // namespace
+
+extern "C" {
+
+int ssd_rms_norm(const void *x, int64_t x_stride, const void *residual, int64_t residual_stride,
+                 const float *weight, int dtype, int64_t rows, int64_t F, float eps, void *y,
+                 void *residual_out, uint8_t *q, float *scale, float *rstd, ssd_stream_t stream)
+{
+    if (int st = check_norm(dtype, rows, F))
+        return st;
+    if (x_stride < F || (residual && residual_stride < F) || !(eps >= 0.f))
+        return SSD_ERR_SHAPE;
+    if (rows == 0)
+        return SSD_OK;
+    if (x_stride > kMaxElems / rows || (residual && residual_stride > kMaxElems / rows))
+        return SSD_ERR_UNSUPPORTED;
+    if (!x || !weight || (!y && !q) || (q && !scale) || (residual_out && !residual))
+        return SSD_ERR_NULL;
+    const int e = elem_size(dtype);
+    if (!aligned(x, e) || !aligned(residual, e) || !aligned(weight, 4) || !aligned(y, e) ||
+        !aligned(residual_out, e) || !aligned(scale, 4) || !aligned(rstd, 4))
+        return SSD_ERR_ALIGN;
+    const int64_t n = rows * F;
+    const struct { const void *p; int64_t bytes; } out[5] = {
+        {y, n * e}, {residual_out, n * e}, {q, n}, {q ? scale : nullptr, (F + 127) / 128 * rows * 4},
+        {rstd, rows * 4}};
+    const int64_t xs = span(rows, F, x_stride, e), rs = span(rows, F, residual_stride, e);
+    for (int i = 0; i < 5; ++i) {
+        const bool in_place = i == 1 && residual_out == residual && residual_stride == F;
+        if (overlap_bytes(out[i].p, out[i].bytes, x, xs) ||
+            (!in_place && overlap_bytes(out[i].p, out[i].bytes, residual, rs)) ||
+            overlap_bytes(out[i].p, out[i].bytes, weight, F * 4))
+            return SSD_ERR_ALIAS;
+        for (int j = 0; j < i; ++j)
+            if (overlap_bytes(out[i].p, out[i].bytes, out[j].p, out[j].bytes))
+                return SSD_ERR_ALIAS;
+    }
+    ssd::NormParams p{};
+    p.x = x;
+    p.res = residual;
+    p.w = weight;
+    p.y = y;
+    p.res_out = residual_out;
+    p.q = q;
+    p.scale = scale;
+    p.rstd = rstd;
+    p.rows = rows;
+    p.x_stride = x_stride;
+    p.res_stride = residual_stride;
+    p.F = (int)F;
+    p.eps = eps;
+    const hipStream_t s = (hipStream_t)stream;
+    return dtype == SSD_BF16 ? launch_norm<ssd::kBF16>(p, s) : launch_norm<ssd::kF32>(p, s);
+}
+
+size_t ssd_rms_norm_backward_workspace_bytes(int64_t rows, int64_t F)
+{
+    if (check_norm(SSD_F32, rows, F) || rows == 0)
+        return 0;
+    return align256((size_t)(norm_groups(rows, norm_rows(F), kNormBwdGroups) * F) * 4);
+}
+
+int ssd_rms_norm_backward(const void *s, int64_t s_stride, const float *weight, const float *rstd,
+                          const void *grad_y, int64_t grad_y_stride, const void *grad_residual,
+                          int64_t grad_residual_stride, int dtype, int64_t rows, int64_t F,
+                          void *grad_x, float *grad_weight, void *workspace,
+                          size_t workspace_bytes, ssd_stream_t stream)
+{
+    if (int st = check_norm(dtype, rows, F))
+        return st;
+    if (s_stride < F || grad_y_stride < F || (grad_residual && grad_residual_stride < F))
+        return SSD_ERR_SHAPE;
+    const hipStream_t st_ = (hipStream_t)stream;
+    if (!grad_weight)
+        return SSD_ERR_NULL;
+    if (!aligned(grad_weight, 4))
+        return SSD_ERR_ALIGN;
+    if (rows == 0)
+        return launch_copy(nullptr, grad_weight, F, st_);
+    if (s_stride > kMaxElems / rows || grad_y_stride > kMaxElems / rows ||
+        (grad_residual && grad_residual_stride > kMaxElems / rows))
+        return SSD_ERR_UNSUPPORTED;
+    if (!s || !weight || !rstd || !grad_y || !grad_x)
+        return SSD_ERR_NULL;
+    const int e = elem_size(dtype);
+    if (!aligned(s, e) || !aligned(weight, 4) || !aligned(rstd, 4) || !aligned(grad_y, e) ||
+        !aligned(grad_residual, e) || !aligned(grad_x, e))
+        return SSD_ERR_ALIGN;
+    const size_t need = ssd_rms_norm_backward_workspace_bytes(rows, F);
+    if (!workspace || workspace_bytes < need)
+        return SSD_ERR_WORKSPACE;
+    if (!aligned(workspace, 256))
+        return SSD_ERR_ALIGN;
+    const struct { const void *p; int64_t bytes; } in[5] = {
+        {s, span(rows, F, s_stride, e)}, {weight, F * 4}, {rstd, rows * 4},
+        {grad_y, span(rows, F, grad_y_stride, e)},
+        {grad_residual, span(rows, F, grad_residual_stride, e)}};
+    const struct { const void *p; int64_t bytes; } out[3] = {
+        {grad_x, rows * F * e}, {grad_weight, F * 4}, {workspace, (int64_t)need}};
+    for (int i = 0; i < 3; ++i) {
+        for (int j = 0; j < 5; ++j)
+            if (overlap_bytes(out[i].p, out[i].bytes, in[j].p, in[j].bytes))
+                return SSD_ERR_ALIAS;
+        for (int j = 0; j < i; ++j)
+            if (overlap_bytes(out[i].p, out[i].bytes, out[j].p, out[j].bytes))
+                return SSD_ERR_ALIAS;
+    }
+    ssd::NormBwdParams p{};
+    p.s = s;
+    p.w = weight;
+    p.rstd = rstd;
+    p.gy = grad_y;
+    p.gs = grad_residual;
+    p.gx = grad_x;
+    p.part = (float *)workspace;
+    p.rows = rows;
+    p.s_stride = s_stride;
+    p.gy_stride = grad_y_stride;
+    p.gs_stride = grad_residual_stride;
+    p.F = (int)F;
+    const int64_t groups = norm_groups(rows, norm_rows(F), kNormBwdGroups);
+    if (int st = dtype == SSD_BF16 ? launch_norm_bwd<ssd::kBF16>(p, groups, st_)
+                                   : launch_norm_bwd<ssd::kF32>(p, groups, st_))
+        return st;
+    hipLaunchKernelGGL(ssd::column_sum_kernel, dim3(grid_1d(F, 64)),
+                       dim3(64 * ssd::kColumnSumWaves), 0, st_, (const float *)workspace,
+                       (int)groups, F, grad_weight);
+    return launch_status();
+}
+
+int ssd_fp8_quantise(const void *x, int64_t x_stride, int dtype, int64_t rows, int64_t cols,
+                     int64_t block_rows, int transpose, uint8_t *q, int64_t q_stride, float *scale,
+                     ssd_stream_t stream)
+{
+    if (!dtype_ok(dtype) || rows < 0 || cols < 1 || (block_rows != 1 && block_rows != 128) ||
+        x_stride < cols || q_stride < (transpose ? rows : cols))
+        return SSD_ERR_SHAPE;
+    if (rows == 0)
+        return SSD_OK;
+    if (cols > (1LL << 31) || rows > (1LL << 31) || x_stride > kMaxElems / rows ||
+        q_stride > kMaxElems / (transpose ? cols : rows))
+        return SSD_ERR_UNSUPPORTED;
+    if (!x || !q || !scale)
+        return SSD_ERR_NULL;
+    const int e = elem_size(dtype);
+    if (!aligned(x, e) || !aligned(scale, 4))
+        return SSD_ERR_ALIGN;
+    const int64_t qr = transpose ? cols : rows, qc = transpose ? rows : cols;
+    const int64_t scales = (qc + 127) / 128 * (block_rows == 1 ? qr : (qr + 127) / 128) * 4;
+    const int64_t xs = span(rows, cols, x_stride, e), qs = span(qr, qc, q_stride, 1);
+    if (overlap_bytes(q, qs, x, xs) || overlap_bytes(scale, scales, x, xs) ||
+        overlap_bytes(q, qs, scale, scales))
+        return SSD_ERR_ALIAS;
+    ssd::QuantParams p{};
+    p.x = x;
+    p.q = q;
+    p.scale = scale;
+    p.rows = rows;
+    p.cols = cols;
+    p.x_stride = x_stride;
+    p.q_stride = q_stride;
+    const hipStream_t s = (hipStream_t)stream;
+    const bool whole = block_rows == 128, turn = transpose != 0;
+    return dtype == SSD_BF16 ? launch_quantise<ssd::kBF16>(p, whole, turn, s)
+                             : launch_quantise<ssd::kF32>(p, whole, turn, s);
+}
+
+size_t ssd_fp8_matmul_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t b_block_rows,
+                                      int out_dtype)
+{
+    if (check_fp8(M, N, K, b_block_rows, out_dtype))
+        return 0;
+    return fp8_plan(M, N, K).bytes;
+}
+
+int ssd_fp8_matmul(const uint8_t *a, int64_t a_stride, const float *a_scale, const uint8_t *b,
+                   int64_t b_stride, const float *b_scale, int64_t M, int64_t N, int64_t K,
+                   int64_t b_block_rows, int out_dtype, void *out, int64_t out_stride,
+                   void *workspace, size_t workspace_bytes, ssd_stream_t stream)
+{
+    if (int st = check_fp8(M, N, K, b_block_rows, out_dtype))
+        return st;
+    if (a_stride < K || b_stride < K || out_stride < N)
+        return SSD_ERR_SHAPE;
+    if (M == 0)
+        return SSD_OK;
+    if (a_stride > kMaxElems / M || b_stride > kMaxElems / N || out_stride > kMaxElems / M)
+        return SSD_ERR_UNSUPPORTED;
+    if (!out || (K > 0 && (!a || !b || !a_scale || !b_scale)))
+        return SSD_ERR_NULL;
+    const int e = elem_size(out_dtype);
+    if (!aligned(a_scale, 4) || !aligned(b_scale, 4) || !aligned(out, e))
+        return SSD_ERR_ALIGN;
+    const Fp8Plan plan = fp8_plan(M, N, K);
+    if (plan.bytes > 0 && (!workspace || workspace_bytes < plan.bytes))
+        return SSD_ERR_WORKSPACE;
+    if (plan.bytes > 0 && !aligned(workspace, 256))
+        return SSD_ERR_ALIGN;
+    const int64_t kb = (K + 127) / 128;
+    const struct { const void *p; int64_t bytes; } in[4] = {
+        {a, span(M, K, a_stride, 1)}, {b, span(N, K, b_stride, 1)}, {a_scale, kb * M * 4},
+        {b_scale, kb * (b_block_rows == 1 ? N : (N + 127) / 128) * 4}};
+    const int64_t os = span(M, N, out_stride, e);
+    for (int j = 0; j < 4; ++j)
+        if (overlap_bytes(out, os, in[j].p, in[j].bytes) ||
+            (plan.bytes && overlap_bytes(workspace, (int64_t)plan.bytes, in[j].p, in[j].bytes)))
+            return SSD_ERR_ALIAS;
+    if (plan.bytes && overlap_bytes(workspace, (int64_t)plan.bytes, out, os))
+        return SSD_ERR_ALIAS;
+    ssd::Fp8Params p{};
+    p.a = a;
+    p.b = b;
+    p.sa = a_scale;
+    p.sb = b_scale;
+    p.out = out;
+    p.part = (float *)workspace;
+    p.a_stride = a_stride;
+    p.b_stride = b_stride;
+    p.out_stride = out_stride;
+    p.M = (int)M;
+    p.N = (int)N;
+    p.K = (int)K;
+    p.tiles_m = plan.tiles_m;
+    p.tiles_n = plan.tiles_n;
+    p.splits = plan.splits;
+    p.split_blocks = plan.split_blocks;
+    const hipStream_t s = (hipStream_t)stream;
+    if (b_block_rows == 1)
+        return out_dtype == SSD_BF16 ? launch_fp8<true, ssd::kBF16>(p, s) : launch_fp8<true, ssd::kF32>(p, s);
+    return out_dtype == SSD_BF16 ? launch_fp8<false, ssd::kBF16>(p, s) : launch_fp8<false, ssd::kF32>(p, s);
+}
+
+size_t ssd_gated_scan_workspace_bytes(int64_t batch, int64_t T, int64_t C, int dtype)
+{
+    if (check_gated(dtype, batch, T, C, C, C, C) || batch == 0 || T == 0)
+        return 0;
+    return gated_plan(batch, T, C, dtype).seg_bytes;
+}
+
+int ssd_gated_scan(const void *x, int64_t x_stride, const void *input_gate,
+                   int64_t input_gate_stride, const void *decay_gate, int64_t decay_gate_stride,
+                   const float *lam, float decay_scale, int dtype, int64_t batch, int64_t T,
+                   int64_t C, const float *initial_state, const int32_t *lengths, void *h,
+                   float *final_state, float *chunk_states, void *workspace,
+                   size_t workspace_bytes, ssd_stream_t stream)
+{
+    if (int st = check_gated(dtype, batch, T, C, x_stride, input_gate_stride, decay_gate_stride))
+        return st;
+    if (!(decay_scale >= 0.f) || decay_scale > 1e30f)
+        return SSD_ERR_SHAPE;
+    if (batch == 0)
+        return SSD_OK;
+    const hipStream_t s = (hipStream_t)stream;
+    const int e = elem_size(dtype);
+    if (!aligned(initial_state, 4) || !aligned(final_state, 4) || !aligned(chunk_states, 4) ||
+        !aligned(x, e) || !aligned(input_gate, e) || !aligned(decay_gate, e) || !aligned(lam, 4) ||
+        !aligned(lengths, 4) || !aligned(h, e))
+        return SSD_ERR_ALIGN;
+    const int64_t bc = batch * C * 4;
+    if (T == 0) {
+        if (!final_state || final_state == initial_state)
+            return SSD_OK;
+        if (overlap_bytes(final_state, bc, initial_state, bc))
+            return SSD_ERR_ALIAS;
+        return launch_copy(initial_state, final_state, batch * C, s);
+    }
+    if (!x || !input_gate || !decay_gate || !lam || !h)
+        return SSD_ERR_NULL;
+    const GatedPlan plan = gated_plan(batch, T, C, dtype);
+    if (!gated_grid_ok(plan, batch))
+        return SSD_ERR_UNSUPPORTED;
+    if (plan.seg_bytes > 0 && (!workspace || workspace_bytes < plan.seg_bytes))
+        return SSD_ERR_WORKSPACE;
+    if (plan.seg_bytes > 0 && !aligned(workspace, 256))
+        return SSD_ERR_ALIGN;
+    const int64_t tokens = batch * T;
+    const struct { const void *p; int64_t bytes; } in[6] = {
+        {x, span(tokens, C, x_stride, e)}, {input_gate, span(tokens, C, input_gate_stride, e)},
+        {decay_gate, span(tokens, C, decay_gate_stride, e)}, {lam, C * 4}, {initial_state, bc},
+        {lengths, batch * 4}};
+    const struct { const void *p; int64_t bytes; } out[4] = {
+        {h, tokens * C * e}, {final_state, bc},
+        {chunk_states, batch * ((T + SSD_GATED_CHUNK - 1) / SSD_GATED_CHUNK) * C * 4},
+        {plan.seg_bytes ? workspace : nullptr, (int64_t)plan.seg_bytes}};
+    for (int i = 0; i < 4; ++i) {
+        for (int j = 0; j < 6; ++j)
+            if (!(i == 1 && j == 4 && final_state == initial_state) &&
+                overlap_bytes(out[i].p, out[i].bytes, in[j].p, in[j].bytes))
+                return SSD_ERR_ALIAS;
+        for (int j = 0; j < i; ++j)
+            if (overlap_bytes(out[i].p, out[i].bytes, out[j].p, out[j].bytes))
+                return SSD_ERR_ALIAS;
+    }
+    ssd::GatedParams p{};
+    p.x = x;
+    p.gi = input_gate;
+    p.gr = decay_gate;
+    p.lam = lam;
+    p.init = initial_state;
+    p.lengths = lengths;
+    p.h = h;
+    p.final_state = final_state;
+    p.states = chunk_states;
+    p.seg = (float *)workspace;
+    p.x_stride = x_stride;
+    p.gi_stride = input_gate_stride;
+    p.gr_stride = decay_gate_stride;
+    p.B = (int)batch;
+    p.T = (int)T;
+    p.C = (int)C;
+    p.blocks = plan.blocks;
+    p.segments = plan.segments;
+    p.seg_tokens = plan.seg_tokens;
+    p.launched = plan.segments;
+    p.k = decay_scale;
+    if (T == 1) {
+        p.blocks = (int)((C + 63) / 64);
+        if (batch > kMaxGrid / p.blocks)
+            return SSD_ERR_UNSUPPORTED;
+        const dim3 grid((unsigned)(batch * p.blocks));
+        if (dtype == SSD_BF16)
+            hipLaunchKernelGGL((ssd::gated_step_kernel<ssd::kBF16>), grid, dim3(64), 0, s, p);
+        else
+            hipLaunchKernelGGL((ssd::gated_step_kernel<ssd::kF32>), grid, dim3(64), 0, s, p);
+        return launch_status();
+    }
+    return dtype == SSD_BF16 ? launch_gated<ssd::kBF16, 2>(p, s) : launch_gated<ssd::kF32, 1>(p, s);
+}
+
+size_t ssd_gated_scan_backward_workspace_bytes(int64_t batch, int64_t T, int64_t C, int dtype)
+{
+    if (check_gated(dtype, batch, T, C, C, C, C) || batch == 0 || T == 0)
+        return 0;
+    const GatedPlan plan = gated_plan(batch, T, C, dtype);
+    return plan.seg_bytes + align256((size_t)batch * plan.segments * C * 4);
+}
+
+int ssd_gated_scan_backward(const void *x, int64_t x_stride, const void *input_gate,
+                            int64_t input_gate_stride, const void *decay_gate,
+                            int64_t decay_gate_stride, const float *lam, float decay_scale,
+                            int dtype, int64_t batch, int64_t T, int64_t C,
+                            const float *chunk_states, const int32_t *lengths, const void *grad_h,
+                            const float *grad_final_state, void *grad_x, void *grad_input_gate,
+                            void *grad_decay_gate, float *grad_lam, float *grad_initial_state,
+                            void *workspace, size_t workspace_bytes, ssd_stream_t stream)
+{
+    if (int st = check_gated(dtype, batch, T, C, x_stride, input_gate_stride, decay_gate_stride))
+        return st;
+    if (!(decay_scale >= 0.f) || decay_scale > 1e30f)
+        return SSD_ERR_SHAPE;
+    const hipStream_t s = (hipStream_t)stream;
+    const int e = elem_size(dtype);
+    if (!grad_lam)
+        return SSD_ERR_NULL;
+    if (!aligned(chunk_states, 4) || !aligned(grad_final_state, 4) || !aligned(grad_lam, 4) ||
+        !aligned(grad_initial_state, 4) || !aligned(x, e) || !aligned(input_gate, e) ||
+        !aligned(decay_gate, e) || !aligned(lam, 4) || !aligned(lengths, 4) || !aligned(grad_h, e) ||
+        !aligned(grad_x, e) || !aligned(grad_input_gate, e) || !aligned(grad_decay_gate, e))
+        return SSD_ERR_ALIGN;
+    const int64_t bc = batch * C * 4, tokens = batch * T;
+    if (tokens > 0 && (!x || !input_gate || !decay_gate || !lam || !chunk_states || !grad_h ||
+                       !grad_x || !grad_input_gate || !grad_decay_gate))
+        return SSD_ERR_NULL;
+    const GatedPlan plan = gated_plan(batch, T, C, dtype);
+    if (tokens > 0 && !gated_grid_ok(plan, batch))
+        return SSD_ERR_UNSUPPORTED;
+    const size_t need = ssd_gated_scan_backward_workspace_bytes(batch, T, C, dtype);
+    if (need > 0 && (!workspace || workspace_bytes < need))
+        return SSD_ERR_WORKSPACE;
+    if (need > 0 && !aligned(workspace, 256))
+        return SSD_ERR_ALIGN;
+    const struct { const void *p; int64_t bytes; } in[8] = {
+        {x, span(tokens, C, x_stride, e)}, {input_gate, span(tokens, C, input_gate_stride, e)},
+        {decay_gate, span(tokens, C, decay_gate_stride, e)}, {lam, C * 4},
+        {chunk_states, batch * ((T + SSD_GATED_CHUNK - 1) / SSD_GATED_CHUNK) * C * 4},
+        {lengths, batch * 4}, {grad_h, tokens * C * e}, {grad_final_state, bc}};
+    const struct { const void *p; int64_t bytes; } out[6] = {
+        {grad_x, tokens * C * e}, {grad_input_gate, tokens * C * e},
+        {grad_decay_gate, tokens * C * e}, {grad_lam, C * 4}, {grad_initial_state, bc},
+        {need ? workspace : nullptr, (int64_t)need}};
+    for (int i = 0; i < 6; ++i) {
+        for (int j = 0; j < 8; ++j)
+            if (overlap_bytes(out[i].p, out[i].bytes, in[j].p, in[j].bytes))
+                return SSD_ERR_ALIAS;
+        for (int j = 0; j < i; ++j)
+            if (overlap_bytes(out[i].p, out[i].bytes, out[j].p, out[j].bytes))
+                return SSD_ERR_ALIAS;
+    }
+    if (tokens == 0) {
+        if (int st = launch_copy(nullptr, grad_lam, C, s))
+            return st;
+        if (grad_initial_state && batch > 0)
+            return launch_copy(grad_final_state, grad_initial_state, batch * C, s);
+        return SSD_OK;
+    }
+    ssd::GatedParams p{};
+    p.x = x;
+    p.gi = input_gate;
+    p.gr = decay_gate;
+    p.lam = lam;
+    p.lengths = lengths;
+    p.seg = (float *)workspace;
+    p.gh = grad_h;
+    p.gfinal = grad_final_state;
+    p.chunk_states = chunk_states;
+    p.gx = grad_x;
+    p.ggi = grad_input_gate;
+    p.ggr = grad_decay_gate;
+    p.part = (float *)((char *)workspace + plan.seg_bytes);
+    p.ginit = grad_initial_state;
+    p.x_stride = x_stride;
+    p.gi_stride = input_gate_stride;
+    p.gr_stride = decay_gate_stride;
+    p.B = (int)batch;
+    p.T = (int)T;
+    p.C = (int)C;
+    p.blocks = plan.blocks;
+    p.segments = plan.segments;
+    p.seg_tokens = plan.seg_tokens;
+    p.launched = plan.segments;
+    p.k = decay_scale;
+    return dtype == SSD_BF16 ? launch_gated_bwd<ssd::kBF16, 2>(p, grad_lam, s)
+                             : launch_gated_bwd<ssd::kF32, 1>(p, grad_lam, s);
+}
+
+}  // extern "C"

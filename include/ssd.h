@@ -357,6 +357,185 @@ int ssd_head_mix_backward(const float *y, const float *W, const float *grad_z, i
                           int64_t H, int64_t D, float *grad_y, float *grad_W, void *workspace,
                           size_t workspace_bytes, ssd_stream_t stream);
 
+/* Element types of the operators below (any other value: SSD_ERR_SHAPE). */
+enum {
+    SSD_F32 = 0,
+    SSD_BF16 = 1 /* bfloat16 values as their 16-bit patterns */
+};
+
+/* Tokens between two stored states of the gated scan. */
+#define SSD_GATED_CHUNK 64
+
+/*
+ * ssd_gated_scan -- the gated linear recurrence: a real, per-channel recurrence
+ * whose decay and input are gated by the tokens. For every batch row b and
+ * channel c, with i = sigmoid(input_gate) and r = sigmoid(decay_gate),
+ *
+ *   l_t = -decay_scale * softplus(lam_c) * r_t       a_t = exp(l_t)
+ *   h_t = a_t * h_{t-1} + sqrt(1 - a_t^2) * i_t * x_t
+ *
+ *   x, input_gate, decay_gate
+ *                (batch, T, C) of `dtype`; a channel's neighbours lie side by
+ *                side, consecutive tokens *_stride elements apart (>= C) and
+ *                consecutive batch rows T * *_stride apart, so the three may be
+ *                column ranges of one matrix of projected rows. Read only.
+ *   lam          (C) float32. decay_scale: >= 0, at most 1e30.
+ *   initial_state nullable: (batch, C) float32, h_{-1}; NULL means zero.
+ *   lengths      nullable: (batch) int32 in device memory: the tokens of each
+ *                row, clamped to 0 .. T. Tokens from there on are padding: they
+ *                are not read, their h is 0, and the state stays as it is.
+ *   h            out: (batch, T, C) of `dtype`, dense.
+ *   final_state  out, nullable: (batch, C) float32, the state after the row's last
+ *                token. It may be initial_state itself (updated in place).
+ *   chunk_states out, nullable: (batch, ceil(T / SSD_GATED_CHUNK), C) float32, the
+ *                state before each chunk's first token, for the backward.
+ *   workspace    ssd_gated_scan_workspace_bytes(...) bytes, 256-byte aligned (NULL
+ *                allowed when that is 0); needed when batch and C alone give too
+ *                few workgroups, the tokens are then cut into segments.
+ * Gates, products and the state are float32; h is rounded once to `dtype`.
+ * T = 1 is the form for generation: one step on the state.
+ * No output may overlap an input or another output (SSD_ERR_ALIAS), but for the
+ * state in place. Alignment: the element size. batch equal to 0 is a no-op; T
+ * equal to 0 copies the initial state (or zeros) into final_state.
+ */
+size_t ssd_gated_scan_workspace_bytes(int64_t batch, int64_t T, int64_t C, int dtype);
+
+int ssd_gated_scan(const void *x, int64_t x_stride, const void *input_gate,
+                   int64_t input_gate_stride, const void *decay_gate, int64_t decay_gate_stride,
+                   const float *lam, float decay_scale, int dtype, int64_t batch, int64_t T,
+                   int64_t C, const float *initial_state, const int32_t *lengths, void *h,
+                   float *final_state, float *chunk_states, void *workspace,
+                   size_t workspace_bytes, ssd_stream_t stream);
+
+/*
+ * ssd_gated_scan_backward -- gradients of l = sum grad_h * h + sum
+ * grad_final_state * final_state for ssd_gated_scan.
+ *   x .. C, lengths as for the forward; chunk_states as it wrote them.
+ *   grad_h       (batch, T, C) of `dtype`, dense; not read in the padding.
+ *   grad_final_state nullable: (batch, C) float32.
+ *   grad_x, grad_input_gate, grad_decay_gate
+ *                out: (batch, T, C) of `dtype`, dense; 0 in the padding.
+ *   grad_lam     out: (C) float32, summed over batch rows and tokens in a fixed
+ *                order.
+ *   grad_initial_state out, nullable: (batch, C) float32.
+ *   workspace    ssd_gated_scan_backward_workspace_bytes(...) bytes.
+ * The states between the stored ones are computed again in float32. No output
+ * may overlap an input, another output or the workspace (SSD_ERR_ALIAS). batch or
+ * T equal to 0 sets grad_lam to zero and copies grad_final_state (or zeros).
+ */
+size_t ssd_gated_scan_backward_workspace_bytes(int64_t batch, int64_t T, int64_t C, int dtype);
+
+int ssd_gated_scan_backward(const void *x, int64_t x_stride, const void *input_gate,
+                            int64_t input_gate_stride, const void *decay_gate,
+                            int64_t decay_gate_stride, const float *lam, float decay_scale,
+                            int dtype, int64_t batch, int64_t T, int64_t C,
+                            const float *chunk_states, const int32_t *lengths, const void *grad_h,
+                            const float *grad_final_state, void *grad_x, void *grad_input_gate,
+                            void *grad_decay_gate, float *grad_lam, float *grad_initial_state,
+                            void *workspace, size_t workspace_bytes, ssd_stream_t stream);
+
+/*
+ * ssd_rms_norm -- the root-mean-square norm with the residual's addition, its
+ * result in `dtype`, in 8 bits, or both. Per row of F values:
+ *
+ *   s = x + residual        rstd = 1 / sqrt(sum s^2 / F + eps)
+ *   y = s * rstd * weight   q = e4m3(y / scale), one scale per 128 neighbours
+ *
+ *   x            (rows, F) of `dtype`, rows x_stride elements apart (>= F).
+ *   residual     nullable (s = x): as x, with its own stride.
+ *   weight       (F) float32.
+ *   y            out, nullable: (rows, F) of `dtype`, dense.
+ *   residual_out out, nullable (only with residual): s, rounded to `dtype`, dense.
+ *                It may be residual itself if that is dense.
+ *   q, scale     out, nullable together: (rows, F) e4m3 bytes and
+ *                (ceil(F / 128), rows) float32, as ssd_fp8_quantise makes them of y
+ *                and as ssd_fp8_matmul reads them; q is taken of the float32 y.
+ *                One of y and q has to be given.
+ *   rstd         out, nullable: (rows) float32, for the backward.
+ * Sums are float32 and taken of the unrounded s. F at most 16384
+ * (SSD_ERR_UNSUPPORTED). eps >= 0. rows equal to 0 is a no-op. No other overlap of
+ * outputs (SSD_ERR_ALIAS). Alignment: the element size.
+ */
+int ssd_rms_norm(const void *x, int64_t x_stride, const void *residual, int64_t residual_stride,
+                 const float *weight, int dtype, int64_t rows, int64_t F, float eps, void *y,
+                 void *residual_out, uint8_t *q, float *scale, float *rstd, ssd_stream_t stream);
+
+/*
+ * ssd_rms_norm_backward -- gradients of l = sum grad_y * y + sum grad_residual * s:
+ *
+ *   grad_x = grad_residual + rstd (w grad_y - s rstd^2 (sum w grad_y s) / F)
+ *   grad_weight = sum over rows grad_y * s * rstd
+ *
+ *   s            (rows, F) of `dtype`: the forward's residual_out (its x, without a
+ *                residual). rstd: as the forward wrote it.
+ *   grad_y       (rows, F) of `dtype`; grad_residual nullable, the same: the gradient
+ *                that reaches s through the residual stream.
+ *   grad_x       out: (rows, F) of `dtype`, dense: the gradient of x and of residual.
+ *   grad_weight  out: (F) float32, summed in a fixed order.
+ *   workspace    ssd_rms_norm_backward_workspace_bytes(rows, F) bytes, 256-byte aligned.
+ * rows equal to 0 sets grad_weight to zero. No output may overlap an input
+ * (SSD_ERR_ALIAS).
+ */
+size_t ssd_rms_norm_backward_workspace_bytes(int64_t rows, int64_t F);
+
+int ssd_rms_norm_backward(const void *s, int64_t s_stride, const float *weight, const float *rstd,
+                          const void *grad_y, int64_t grad_y_stride, const void *grad_residual,
+                          int64_t grad_residual_stride, int dtype, int64_t rows, int64_t F,
+                          void *grad_x, float *grad_weight, void *workspace,
+                          size_t workspace_bytes, ssd_stream_t stream);
+
+/*
+ * ssd_fp8_quantise -- 8-bit values (e4m3: 4 exponent and 3 mantissa bits, largest
+ * 448) with a float32 scale per block of 128: scale = max(max |v| / 448, 2^-126)
+ * over the block, q = v / scale rounded to nearest, ties to even. Let v be x
+ * (rows, cols), or, with `transpose`, x turned (cols, rows); R and K its sizes.
+ *
+ *   x            (rows, cols) of `dtype`, rows x_stride elements apart.
+ *   block_rows   1: blocks of 1 x 128 along v's rows; scale is (ceil(K / 128), R).
+ *                128: blocks of 128 x 128; scale is (ceil(R / 128), ceil(K / 128)).
+ *   q            out: (R, K) bytes, rows q_stride bytes apart (>= K); bytes between
+ *                the rows are not written.
+ * A block with an infinity or a NaN comes back as NaN (its scale is infinite or
+ * NaN); other blocks are untouched by it. rows equal to 0 is a no-op.
+ * Alignment: the element size; 4 bytes for scale.
+ */
+int ssd_fp8_quantise(const void *x, int64_t x_stride, int dtype, int64_t rows, int64_t cols,
+                     int64_t block_rows, int transpose, uint8_t *q, int64_t q_stride, float *scale,
+                     ssd_stream_t stream);
+
+/*
+ * ssd_fp8_matmul -- the product of two such operands, in_proj's and out_proj's form:
+ *
+ *   out[m, n] = sum over blocks kb of 128 k of
+ *                   a_scale[kb, m] * s_b * sum over k in kb of a[m, k] * b[n, k]
+ *   with s_b = b_scale[n / 128, kb] (b_block_rows 128) or b_scale[kb, n] (1).
+ *
+ *   a            (M, K) e4m3 bytes, rows a_stride bytes apart (>= K); a_scale
+ *                (ceil(K / 128), M): 1 x 128 blocks, as ssd_fp8_quantise and
+ *                ssd_rms_norm make them.
+ *   b            (N, K) e4m3 bytes, rows b_stride bytes apart; b_scale as
+ *                ssd_fp8_quantise makes it with block_rows b_block_rows.
+ *   out          (M, N) of out_dtype, rows out_stride elements apart (>= N); elements
+ *                between the rows are not written.
+ *   workspace    ssd_fp8_matmul_workspace_bytes(...) bytes, 256-byte aligned (NULL
+ *                allowed when that is 0): partial sums where few outputs and a long K
+ *                have the sum over k split; they are added in a fixed order.
+ * With y = x W^T: forward a = x, b = W (blocks of 128 x 128); grad_x takes a = grad_y and
+ * b = W quantised with transpose; grad_W takes a = grad_y and b = x, both quantised with
+ * transpose in blocks of 1 x 128.
+ * Products and sums are float32, rounded once to out_dtype. M equal to 0 is a no-op; K
+ * equal to 0 writes zeros. No output may overlap an input (SSD_ERR_ALIAS).
+ * Alignment: 4 bytes for the scales, the element size for out; rows of a and b that start
+ * on 16 bytes are read fastest.
+ */
+size_t ssd_fp8_matmul_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t b_block_rows,
+                                      int out_dtype);
+
+int ssd_fp8_matmul(const uint8_t *a, int64_t a_stride, const float *a_scale, const uint8_t *b,
+                   int64_t b_stride, const float *b_scale, int64_t M, int64_t N, int64_t K,
+                   int64_t b_block_rows, int out_dtype, void *out, int64_t out_stride,
+                   void *workspace, size_t workspace_bytes, ssd_stream_t stream);
+
 /* Static text for a status code (never NULL). */
 const char *ssd_status_string(int status);
 

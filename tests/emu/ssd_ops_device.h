@@ -1,0 +1,142 @@
+// ssd_ops_device.h (host emulation) -- TEST INFRASTRUCTURE. The further primitives of the
+// gfx950 header of the same name, on top of the emulator's wave collectives.
+#pragma once
+
+#include <ssd_device.h>
+
+typedef uint32_t v2u __attribute__((ext_vector_type(2)));
+typedef uint32_t v4u __attribute__((ext_vector_type(4)));
+typedef int v8i __attribute__((ext_vector_type(8)));
+
+SSD_DEVICE uint32_t f2u(float v) { return __builtin_bit_cast(uint32_t, v); }
+SSD_DEVICE float u2f(uint32_t v) { return __builtin_bit_cast(float, v); }
+
+SSD_DEVICE float hw_rcp(float x) { return 1.f / x; }
+SSD_DEVICE float hw_sqrt(float x) { return sqrtf(x); }
+SSD_DEVICE float hw_rsq(float x) { return 1.f / sqrtf(x); }
+
+// e4m3: nearest, ties to even; NaN stays NaN; past the border to overflow NaN as well.
+SSD_DEVICE uint32_t emu_e4m3(float v)
+{
+    const uint32_t sign = f2u(v) >> 31 << 7;
+    const double x = fabs((double)v);
+    if (!(x < 464.0))
+        return sign | 0x7f;
+    if (x == 0.0)
+        return sign;
+    int e;
+    (void)frexp(x, &e);
+    e = e - 1 < -6 ? -6 : e - 1;
+    const double m = nearbyint(ldexp(x, 3 - e));  // in steps of 2^(e - 3)
+    if (m < 8)
+        return sign | (uint32_t)m;                // subnormal: e is -6
+    return sign | (m >= 16 ? (uint32_t)(e + 8) << 3 : (uint32_t)(e + 7) << 3 | ((uint32_t)m - 8));
+}
+SSD_DEVICE float emu_e4m3_value(uint32_t b)
+{
+    const int e = b >> 3 & 15, m = b & 7;
+    if (e == 15 && m == 7)
+        return NAN;
+    const float v = e ? ldexpf((float)(8 + m), e - 10) : ldexpf((float)m, -9);
+    return b & 0x80 ? -v : v;
+}
+template <bool HI>
+SSD_DEVICE uint32_t cvt_pk_e4m3(float a, float b, uint32_t old)
+{
+    const uint32_t w = emu_e4m3(a) | emu_e4m3(b) << 8;
+    return HI ? (old & 0xffffu) | w << 16 : (old & 0xffff0000u) | w;
+}
+
+SSD_DEVICE uint16_t cvt_bf16(float a)
+{
+    const uint32_t u = f2u(a);
+    if (a != a)
+        return (uint16_t)(u >> 16 | 0x40);
+    return (uint16_t)((u + 0x7fffu + (u >> 16 & 1)) >> 16);
+}
+SSD_DEVICE uint32_t cvt_pk_bf16(float a, float b) { return cvt_bf16(a) | (uint32_t)cvt_bf16(b) << 16; }
+
+template <int x>
+SSD_DEVICE uint32_t row_xor(uint32_t v)
+{
+    return f2u(lane_fetch(u2f(v), (thread_id() & 63) ^ x));
+}
+
+SSD_DEVICE v4f mfma_e4m3_16x16x128(v8i a, v8i b, v4f c)
+{
+    struct Operands {
+        uint8_t a[64][32], b[64][32];
+    };
+    static Operands waves[16];
+    Operands &o = waves[thread_id() >> 6];
+    const int lane = thread_id() & 63;
+    memcpy(o.a[lane], &a, 32);
+    memcpy(o.b[lane], &b, 32);
+    wave_lds_sync();
+    v4f d = c;
+    for (int r = 0; r < 4; ++r) {
+        double acc = c[r];
+        for (int q = 0; q < 4; ++q)
+            for (int k = 0; k < 32; ++k)
+                acc += (double)emu_e4m3_value(o.a[16 * q + 4 * (lane >> 4) + r][k]) *
+                       emu_e4m3_value(o.b[16 * q + (lane & 15)][k]);
+        d[r] = (float)acc;
+    }
+    wave_lds_sync();
+    return d;
+}
+
+SSD_DEVICE v4u e4m3_to_bf16(uint32_t lo, uint32_t hi)
+{
+    v4u r;
+    for (int e = 0; e < 4; ++e) {
+        const uint32_t w = e < 2 ? lo : hi;
+        const uint32_t b = w >> (16 * (e & 1));
+        r[e] = f2u(emu_e4m3_value(b & 0xff)) >> 16 | (f2u(emu_e4m3_value(b >> 8 & 0xff)) & 0xffff0000u);
+    }
+    return r;
+}
+
+SSD_DEVICE v4f mfma_bf16_16x16x32(v4u a, v4u b, v4f c)
+{
+    struct Operands {
+        v4u a[64], b[64];
+    };
+    static Operands waves[16];
+    Operands &o = waves[thread_id() >> 6];
+    const int lane = thread_id() & 63;
+    o.a[lane] = a;
+    o.b[lane] = b;
+    wave_lds_sync();
+    v4f d = c;
+    for (int r = 0; r < 4; ++r) {
+        double acc = c[r];
+        for (int q = 0; q < 4; ++q)
+            for (int k = 0; k < 8; ++k) {
+                const uint32_t x = o.a[16 * q + 4 * (lane >> 4) + r][k >> 1];
+                const uint32_t y = o.b[16 * q + (lane & 15)][k >> 1];
+                acc += (double)u2f(k & 1 ? x & 0xffff0000u : x << 16) * u2f(k & 1 ? y & 0xffff0000u : y << 16);
+            }
+        d[r] = (float)acc;
+    }
+    wave_lds_sync();
+    return d;
+}
+
+SSD_DEVICE void async_load16(buf_t r, uint32_t off, void *lds)
+{
+    const v4f v = buf_load4(r, off);
+    memcpy((char *)lds + 16 * (thread_id() & 63), &v, 16);
+}
+SSD_DEVICE void async_load4(buf_t r, uint32_t off, void *lds)
+{
+    const uint32_t v = buf_load_u32(r, off);
+    memcpy((char *)lds + 4 * (thread_id() & 63), &v, 4);
+}
+template <int n>
+SSD_DEVICE void async_wait()
+{
+}
+SSD_DEVICE void bare_barrier() { block_sync(); }
+
+SSD_DEVICE float ld_uniform(const float *p, int64_t i) { return p[i]; }

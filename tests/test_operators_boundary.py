@@ -1,0 +1,197 @@
+"""The operators' C ABI on the CPU: what is rejected before anything is launched."""
+
+import ctypes
+import os
+
+import pytest
+import torch
+
+import complex_chunkwise_ssd_amd as ssd
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(ssd.LIBPATH):
+        from complex_chunkwise_ssd_amd import build
+        build.build()
+    return ssd.load_library()
+
+
+def _at(k, off=0):
+    """Made-up device addresses, 4 GiB apart."""
+    return ctypes.c_void_p((k + 1 << 32) + off)
+
+
+def _gated(lib, **kw):
+    a = dict(x=_at(0), xs=8, gi=_at(1), gis=8, gr=_at(2), grs=8, lam=_at(3), k=8.0, dt=0, B=2, T=10, C=8, init=None,
+             n=None, h=_at(4), fin=_at(5), cs=None, ws=None, wn=0)
+    a.update(kw)
+    return lib.ssd_gated_scan(*a.values(), None)
+
+
+def test_gated_scan_refusals(lib):
+    for bad in (dict(B=-1), dict(T=-1), dict(C=0), dict(xs=7), dict(gis=7), dict(grs=7), dict(dt=2), dict(k=-1.0),
+                dict(k=float("nan")), dict(k=float("inf"))):
+        assert _gated(lib, **bad) == ssd.SSD_ERR_SHAPE, bad
+    for bad in (dict(T=(1 << 30) + 1), dict(xs=1 << 40), dict(B=1 << 25), dict(C=1 << 25, xs=1 << 25, gis=1 << 25, grs=1 << 25)):
+        assert _gated(lib, **bad) == ssd.SSD_ERR_UNSUPPORTED, bad
+    for name in ("x", "gi", "gr", "lam", "h"):
+        assert _gated(lib, **{name: None}) == ssd.SSD_ERR_NULL, name
+    for name in ("x", "gi", "gr", "lam", "h", "fin", "init", "n", "cs"):
+        assert _gated(lib, **{name: _at(9, 2)}) == ssd.SSD_ERR_ALIGN, name
+    for name in ("gi", "lam", "init", "n"):
+        assert _gated(lib, h=_at(9), **{name: _at(9)}) == ssd.SSD_ERR_ALIAS, name
+    assert _gated(lib, fin=_at(4)) == ssd.SSD_ERR_ALIAS
+    assert _gated(lib, init=_at(5, 4)) == ssd.SSD_ERR_ALIAS     # in place only as a whole
+    assert _gated(lib, cs=_at(5)) == ssd.SSD_ERR_ALIAS
+    assert _gated(lib, B=0, x=None, h=None) == ssd.SSD_OK
+    assert _gated(lib, T=0, x=None, h=None, fin=None) == ssd.SSD_OK
+    need = lib.ssd_gated_scan_workspace_bytes(1, 9000, 64, 0)
+    assert need > 0 and lib.ssd_gated_scan_workspace_bytes(1, 9000, 64, 3) == 0
+    long = dict(B=1, T=9000, C=64, xs=64, gis=64, grs=64)
+    assert _gated(lib, **long) == ssd.SSD_ERR_WORKSPACE
+    assert _gated(lib, ws=_at(9), wn=need - 1, **long) == ssd.SSD_ERR_WORKSPACE
+    assert _gated(lib, ws=_at(9, 16), wn=need, **long) == ssd.SSD_ERR_ALIGN
+    assert _gated(lib, ws=_at(4), wn=need, **long) == ssd.SSD_ERR_ALIAS
+
+
+def _gated_bwd(lib, **kw):
+    a = dict(x=_at(0), xs=8, gi=_at(1), gis=8, gr=_at(2), grs=8, lam=_at(3), k=8.0, dt=0, B=2, T=10, C=8, cs=_at(4),
+             n=None, gh=_at(5), gf=None, gx=_at(6), ggi=_at(7), ggr=_at(8), gl=_at(9), g0=_at(10), ws=_at(11), wn=1 << 20)
+    a.update(kw)
+    return lib.ssd_gated_scan_backward(*a.values(), None)
+
+
+def test_gated_scan_backward_refusals(lib):
+    for bad in (dict(B=-1), dict(C=0), dict(xs=7), dict(dt=-1), dict(k=-1.0)):
+        assert _gated_bwd(lib, **bad) == ssd.SSD_ERR_SHAPE, bad
+    for name in ("x", "gi", "gr", "lam", "cs", "gh", "gx", "ggi", "ggr", "gl"):
+        assert _gated_bwd(lib, **{name: None}) == ssd.SSD_ERR_NULL, name
+    for name in ("x", "gh", "gx", "gl", "cs", "gf", "g0", "n"):
+        assert _gated_bwd(lib, **{name: _at(20, 2)}) == ssd.SSD_ERR_ALIGN, name
+    for a, b in (("gx", 0), ("ggi", 1), ("ggr", 5), ("gl", 3), ("g0", 4), ("gx", 7), ("ws", 6)):
+        assert _gated_bwd(lib, **{a: _at(b)}) == ssd.SSD_ERR_ALIAS, (a, b)
+    assert _gated_bwd(lib, ws=None) == ssd.SSD_ERR_WORKSPACE
+    assert _gated_bwd(lib, wn=8) == ssd.SSD_ERR_WORKSPACE
+    assert _gated_bwd(lib, ws=_at(11, 8)) == ssd.SSD_ERR_ALIGN
+
+
+def _norm(lib, **kw):
+    a = dict(x=_at(0), xs=8, r=_at(1), rs=8, w=_at(2), dt=1, rows=4, F=8, eps=1e-6, y=_at(3), s=_at(4), q=_at(5),
+             sc=_at(6), rstd=None)
+    a.update(kw)
+    return lib.ssd_rms_norm(*a.values(), None)
+
+
+def test_rms_norm_refusals(lib):
+    for bad in (dict(rows=-1), dict(F=0), dict(xs=7), dict(rs=7), dict(dt=5), dict(eps=-1.0), dict(eps=float("nan"))):
+        assert _norm(lib, **bad) == ssd.SSD_ERR_SHAPE, bad
+    assert _norm(lib, F=16385, xs=16385, rs=16385) == ssd.SSD_ERR_UNSUPPORTED
+    assert _norm(lib, xs=1 << 60) == ssd.SSD_ERR_UNSUPPORTED
+    for bad in (dict(x=None), dict(w=None), dict(y=None, q=None), dict(sc=None), dict(r=None)):
+        assert _norm(lib, **bad) == ssd.SSD_ERR_NULL, bad
+    for name, off in (("x", 1), ("r", 1), ("w", 2), ("y", 1), ("s", 1), ("sc", 2), ("rstd", 2)):
+        assert _norm(lib, **{name: _at(20, off)}) == ssd.SSD_ERR_ALIGN, name
+    for a, b in (("y", 0), ("y", 1), ("q", 2), ("s", 0), ("s", 3), ("sc", 5), ("rstd", 6)):
+        assert _norm(lib, **{a: _at(b)}) == ssd.SSD_ERR_ALIAS, (a, b)
+    assert _norm(lib, s=_at(1), rs=9) == ssd.SSD_ERR_ALIAS      # in place only where the rows are dense
+    assert _norm(lib, rows=0, x=None) == ssd.SSD_OK
+
+
+def _norm_bwd(lib, **kw):
+    a = dict(s=_at(0), ss=8, w=_at(1), rstd=_at(2), gy=_at(3), gys=8, gs=None, gss=0, dt=0, rows=4, F=8, gx=_at(4),
+             gw=_at(5), ws=_at(6), wn=1 << 20)
+    a.update(kw)
+    return lib.ssd_rms_norm_backward(*a.values(), None)
+
+
+def test_rms_norm_backward_refusals(lib):
+    for bad in (dict(rows=-1), dict(F=0), dict(ss=7), dict(gys=7), dict(gs=_at(8), gss=7), dict(dt=5)):
+        assert _norm_bwd(lib, **bad) == ssd.SSD_ERR_SHAPE, bad
+    for name in ("s", "w", "rstd", "gy", "gx", "gw"):
+        assert _norm_bwd(lib, **{name: None}) == ssd.SSD_ERR_NULL, name
+    for a, b in (("gx", 0), ("gx", 3), ("gw", 1), ("gw", 4), ("ws", 2)):
+        assert _norm_bwd(lib, **{a: _at(b)}) == ssd.SSD_ERR_ALIAS, (a, b)
+    assert _norm_bwd(lib, ws=None) == ssd.SSD_ERR_WORKSPACE
+    assert _norm_bwd(lib, wn=16) == ssd.SSD_ERR_WORKSPACE
+    assert _norm_bwd(lib, ws=_at(6, 4)) == ssd.SSD_ERR_ALIGN
+
+
+def _quant(lib, **kw):
+    a = dict(x=_at(0), xs=8, dt=0, rows=4, cols=8, br=1, t=0, q=_at(1), qs=8, sc=_at(2))
+    a.update(kw)
+    return lib.ssd_fp8_quantise(*a.values(), None)
+
+
+def test_fp8_quantise_refusals(lib):
+    for bad in (dict(rows=-1), dict(cols=0), dict(xs=7), dict(qs=7), dict(t=1, qs=3), dict(br=64), dict(dt=2)):
+        assert _quant(lib, **bad) == ssd.SSD_ERR_SHAPE, bad
+    for name in ("x", "q", "sc"):
+        assert _quant(lib, **{name: None}) == ssd.SSD_ERR_NULL, name
+    assert _quant(lib, x=_at(0, 2)) == ssd.SSD_ERR_ALIGN and _quant(lib, sc=_at(2, 2)) == ssd.SSD_ERR_ALIGN
+    assert _quant(lib, q=_at(0)) == ssd.SSD_ERR_ALIAS and _quant(lib, sc=_at(1)) == ssd.SSD_ERR_ALIAS
+    assert _quant(lib, xs=1 << 60) == ssd.SSD_ERR_UNSUPPORTED
+    assert _quant(lib, rows=0, x=None) == ssd.SSD_OK
+
+
+def _mm(lib, **kw):
+    a = dict(a=_at(0), as_=256, sa=_at(1), b=_at(2), bs=256, sb=_at(3), M=4, N=8, K=256, br=128, dt=1, out=_at(4), os=8,
+             ws=None, wn=0)
+    a.update(kw)
+    return lib.ssd_fp8_matmul(*a.values(), None)
+
+
+def test_fp8_matmul_refusals(lib):
+    for bad in (dict(M=-1), dict(N=0), dict(K=-1), dict(as_=255), dict(bs=255), dict(os=7), dict(br=2), dict(dt=2)):
+        assert _mm(lib, **bad) == ssd.SSD_ERR_SHAPE, bad
+    for name in ("a", "sa", "b", "sb", "out"):
+        assert _mm(lib, **{name: None}) == ssd.SSD_ERR_NULL, name
+    for name, off in (("sa", 2), ("sb", 2), ("out", 1)):
+        assert _mm(lib, **{name: _at(9, off)}) == ssd.SSD_ERR_ALIGN, name
+    for b in range(4):
+        assert _mm(lib, out=_at(b)) == ssd.SSD_ERR_ALIAS, b
+    assert _mm(lib, as_=1 << 60) == ssd.SSD_ERR_UNSUPPORTED
+    assert _mm(lib, M=0, a=None, out=None) == ssd.SSD_OK
+    need = lib.ssd_fp8_matmul_workspace_bytes(512, 512, 1 << 16, 1, 0)
+    assert need > 0 and lib.ssd_fp8_matmul_workspace_bytes(512, 512, 1 << 16, 3, 0) == 0
+    long = dict(M=512, N=512, K=1 << 16, as_=1 << 16, bs=1 << 16, os=512, br=1, dt=0)
+    assert _mm(lib, **long) == ssd.SSD_ERR_WORKSPACE
+    assert _mm(lib, ws=_at(9), wn=need - 1, **long) == ssd.SSD_ERR_WORKSPACE
+    assert _mm(lib, ws=_at(9, 8), wn=need, **long) == ssd.SSD_ERR_ALIGN
+    assert _mm(lib, ws=_at(0), wn=need, **long) == ssd.SSD_ERR_ALIAS
+
+
+def test_python_layer_rejects_bad_tensors():
+    x = torch.zeros(2, 4, 8)
+    with pytest.raises(ValueError):
+        ssd.gated_scan(x, x, x, torch.zeros(8))         # CPU tensors
+    with pytest.raises(ValueError):
+        ssd.rms_norm(x, torch.zeros(8))
+    with pytest.raises(ValueError):
+        ssd.fp8_quantise(x)
+    with pytest.raises(ValueError):
+        ssd.fp8_matmul(x, x, x, x)
+    with pytest.raises(ValueError):
+        ssd.rms_norm_backward(x, x, x, x)
+    with pytest.raises(ValueError):
+        ssd.gated_scan_backward(x, x, x, x, x, x)
+
+
+def test_row_strides():
+    from complex_chunkwise_ssd_amd.ops import _row_stride
+    cpu = torch.device("cpu")
+
+    def stride(t):
+        return _row_stride(t, "t", t.dtype, t.shape, cpu)
+    whole = torch.zeros(3, 5, 24)
+    assert stride(whole) == 24 and stride(whole[..., 8:16]) == 24
+    assert stride(whole[:, :1, 8:16]) == 120 and stride(whole[:1, :, 8:16]) == 24
+    assert stride(whole[:1, :1, 8:16]) == 8 and stride(whole[0, :, 3:4]) == 24
+    for bad in (whole[:, :4, 8:16], whole.transpose(1, 2), torch.zeros(1, 8).expand(4, 8), whole[..., ::2]):
+        with pytest.raises(ValueError):
+            stride(bad)
+
+
+def test_gated_chunk_matches_the_header():
+    text = open(ssd.HEADER).read()
+    assert "#define SSD_GATED_CHUNK %d" % ssd.GATED_CHUNK in text
