@@ -48,36 +48,12 @@ SSD_DEVICE v4u fp8_chunk(const uint8_t *row, int k, int K)
     return r;
 }
 
-// The outputs n .. n + CNT - 1 of one row, rounded to OUT.
-template <int OUT, int CNT>
-SSD_DEVICE void fp8_store(void *out, int64_t at, int n, int N, const float (&v)[CNT])
+// The outputs n .. n + 7 of one row, rounded to OUT.
+template <int OUT>
+SSD_DEVICE void fp8_store(void *out, int64_t at, int n, int N, const float (&v)[8])
 {
-#pragma unroll
-    for (int g = 0; g < CNT; g += 4) {
-        const int left = N - n - g;
-        char *p = (char *)out + (at + n + g) * ElemSize<OUT>::value;
-        if (OUT == kBF16) {
-            const v2u u = {cvt_pk_bf16(v[g], v[g + 1]), cvt_pk_bf16(v[g + 2], v[g + 3])};
-            if (left >= 4) {
-                __builtin_memcpy(p, &u, 8);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 3; ++e)
-                    if (e < left)
-                        ((uint16_t *)p)[e] = (uint16_t)(u[e >> 1] >> (16 * (e & 1)));
-            }
-        } else {
-            const v4f u = {v[g], v[g + 1], v[g + 2], v[g + 3]};
-            if (left >= 4) {
-                __builtin_memcpy(p, &u, 16);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 3; ++e)
-                    if (e < left)
-                        ((float *)p)[e] = u[e];
-            }
-        }
-    }
+    if (n < N)
+        store8<OUT>((char *)out + (at + n) * ElemSize<OUT>::value, N - n, v);
 }
 
 // A workgroup of WN x WM waves; a wave holds 16 NB rows of b and 16 MB rows of a. BROW: sb
@@ -221,14 +197,195 @@ SSD_KERNEL(64 * WN * WM) void fp8_matmul_kernel(Fp8Params p)
         const int m = mw + 16 * i + i16;
         if (m >= p.M)
             continue;
-        float v[4 * NB];
 #pragma unroll
-        for (int e = 0; e < 4 * NB; ++e)
-            v[e] = acc[e >> 2][i][e & 3];
-        if (p.splits > 1)
-            fp8_store<kF32>(p.part, ((int64_t)split * p.M + m) * p.N, nw + 4 * NB * q, p.N, v);
-        else
-            fp8_store<OUT>(p.out, m * p.out_stride, nw + 4 * NB * q, p.N, v);
+        for (int g = 0; g < NB / 2; ++g) {
+            float v[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                v[e] = acc[2 * g + (e >> 2)][i][e & 3];
+            if (p.splits > 1)
+                fp8_store<kF32>(p.part, ((int64_t)split * p.M + m) * p.N, nw + 4 * NB * q + 8 * g, p.N, v);
+            else
+                fp8_store<OUT>(p.out, m * p.out_stride, nw + 4 * NB * q + 8 * g, p.N, v);
+        }
+    }
+}
+
+// The large form: 256 x 256 results per workgroup of 8 waves, each 64 rows of b by 128 rows of a.
+constexpr int kBigT = 256;
+constexpr int kBigStage = 2 * kBigT * 128;        // bytes of one k block of both operands
+constexpr uint32_t kBigOut = 0xfffffff0u;         // a byte offset past every buffer
+
+// Where chunk c of staged row r lies in its row of eight: neighbouring lanes of a wave's read
+// (rows r, r + 1, .. of a; rows 0-3, 8-11, 16-19, 24-27 of b) then meet different banks.
+SSD_DEVICE int big_key_a(int r) { return r & 7; }
+SSD_DEVICE int big_key_b(int r) { return (r & 3) | (r >> 1 & 4); }
+
+// Which tile a workgroup takes. Workgroup i runs on XCD i % 8, each with an L2 of its own, so
+// each XCD gets a contiguous part of an order in which four row tiles of a go over all
+// column tiles: the 32 workgroups that it runs at a time share 4 tiles of a and 8 of b.
+SSD_DEVICE void fp8_place(const Fp8Params &p, int64_t id, int &tm, int &tn)
+{
+    const int64_t all = (int64_t)p.tiles_m * p.tiles_n;
+    const int64_t each = all >> 3, more = all & 7, x = id & 7;
+    const int64_t at = x * each + (x < more ? x : more) + (id >> 3);
+    const int64_t group = at / (4 * p.tiles_n);
+    const int rest = (int)(at - group * (4 * p.tiles_n));
+    const int in = p.tiles_m - 4 * group < 4 ? (int)(p.tiles_m - 4 * group) : 4;
+    tn = rest / in;
+    tm = (int)(4 * group) + rest - tn * in;
+}
+
+template <bool BROW, int OUT>
+SSD_KERNEL_WAVES(512, 2) void fp8_matmul_big_kernel(Fp8Params p)
+{
+    constexpr bool WIDE = false;
+    constexpr int NB = 4, MB = 8;
+    // Two stages, each an array of its own: the compiler then knows that reading one need not wait
+    // for the loads into the other. Scales: a's, then b's (BROW).
+    SSD_LDS uint8_t tile0[kBigStage];
+    SSD_LDS uint8_t tile1[kBigStage];
+    SSD_LDS float scales0[2 * kBigT];
+    SSD_LDS float scales1[2 * kBigT];
+    const int tid = thread_id();
+    const int lane = tid & 63, wave = wave_id();
+    const int wn = wave & 3, wm = wave >> 2;
+    const int i16 = lane & 15, q = lane >> 4;
+    const int KB = (p.K + 127) >> 7;
+    const int64_t all = (int64_t)p.tiles_m * p.tiles_n;
+    const int split = (int)(block_id() / all);
+    int tm, tn;
+    fp8_place(p, block_id() - split * all, tm, tn);
+    const int n0 = tn * kBigT, m0 = tm * kBigT;
+    const int kb0 = split * p.split_blocks;
+    const int kb1 = kb0 + p.split_blocks < KB ? kb0 + p.split_blocks : KB;
+    const int rows_n = p.N - n0 < kBigT ? p.N - n0 : kBigT;
+    const int rows_m = p.M - m0 < kBigT ? p.M - m0 : kBigT;
+    // Staging: this lane's place in the 8 rows that its wave loads at once (64 rows further on for
+    // each of the four loads of an operand; the keys do not depend on which).
+    const int r8 = lane >> 3, c8 = lane & 7;
+    const int ka = 16 * (c8 ^ big_key_a(r8)), kb_ = 16 * (c8 ^ big_key_b(wave * 8 + r8));
+    const uint32_t off_a = (uint32_t)(wave * 8 + r8) * (uint32_t)p.a_stride + (uint32_t)ka;
+    const uint32_t off_b = (uint32_t)(wave * 8 + r8) * (uint32_t)p.b_stride + (uint32_t)kb_;
+    // No branches in here: past the last block (and for scales that there are not) the buffers are empty.
+    auto fetch = [&](int kb, uint8_t *tile, float *scales) {
+        const int k = kb * 128;
+        const bool any = kb < kb1;
+        // 16 bytes from K on lie past the buffer's end, as rows past the matrix's do: zeros
+        const uint32_t oa = k + ka < p.K ? off_a : kBigOut, ob = k + kb_ < p.K ? off_b : kBigOut;
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            const int nb_rows = rows_n - s * 64, na_rows = rows_m - s * 64;
+            async_load16(make_buf(p.b + (n0 + s * 64) * p.b_stride + k,
+                                  any && nb_rows > 0 ? (uint32_t)(nb_rows - 1) * (uint32_t)p.b_stride + (uint32_t)(p.K - k) : 0u),
+                         ob, &tile[(s * 64 + wave * 8) * 128]);
+            async_load16(make_buf(p.a + (m0 + s * 64) * p.a_stride + k,
+                                  any && na_rows > 0 ? (uint32_t)(na_rows - 1) * (uint32_t)p.a_stride + (uint32_t)(p.K - k) : 0u),
+                         oa, &tile[kBigT * 128 + (s * 64 + wave * 8) * 128]);
+        }
+        const bool isa = wave < 4;
+        const float *from = isa || !BROW ? p.sa + (int64_t)kb * p.M + m0 : p.sb + (int64_t)kb * p.N + n0;
+        const int many = !any ? 0 : isa ? rows_m : BROW ? rows_n : 0;
+        async_load4(make_buf(from, (uint32_t)many * 4u), (uint32_t)(tid & (kBigT - 1)) * 4u, &scales[wave * 64]);
+    };
+    // Operands: row 8 (i16 / 4) + i16 % 4 + 4 (j % 2) + 32 (j / 2) of b's 64, row 16 i + i16 of a's
+    // 128; the keys do not depend on i and j, so that these are constant distances. A lane's
+    // results of blocks 2 g and 2 g + 1 are then the eight n from 32 g + 8 q on, one 16-byte
+    // store of bfloat16, and four lanes' stores are 64 neighbouring bytes.
+    const int rb = wn * 64 + 8 * (i16 >> 2) + (i16 & 3), ra = wm * 128 + i16;
+    const int b_lo = rb * 128 + 16 * (q ^ big_key_b(rb)), b_hi = rb * 128 + 16 * ((q + 4) ^ big_key_b(rb));
+    const int a_lo = kBigT * 128 + ra * 128 + 16 * (q ^ big_key_a(ra));
+    const int a_hi = kBigT * 128 + ra * 128 + 16 * ((q + 4) ^ big_key_a(ra));
+
+    v4f acc[NB][MB];
+#pragma unroll
+    for (int j = 0; j < NB; ++j)
+#pragma unroll
+        for (int i = 0; i < MB; ++i)
+            acc[j][i] = v4f{0.f, 0.f, 0.f, 0.f};
+    const int nw = n0 + wn * 64, mw = m0 + wm * 128;
+    const int nb128 = (nw < p.N ? nw : p.N - 1) >> 7;
+    auto step = [&](int kb, uint8_t *tile, float *scales, uint8_t *next_tile, float *next_scales) {
+        async_wait<0>();
+        bare_barrier();
+        fetch(kb + 1, next_tile, next_scales);
+        Fp8Operand<WIDE> bf[NB];
+#pragma unroll
+        for (int j = 0; j < NB; ++j)
+            bf[j] = fp8_operand<WIDE>(*(const v4u *)&tile[b_lo + 512 * (j & 1) + 4096 * (j >> 1)], *(const v4u *)&tile[b_hi + 512 * (j & 1) + 4096 * (j >> 1)]);
+        v4f sb4[BROW ? NB : 1];
+        float sb = 1.f;
+        if (BROW) {
+#pragma unroll
+            for (int j = 0; j < NB; ++j)
+                sb4[BROW ? j : 0] = *(const v4f *)&scales[kBigT + wn * 64 + 8 * q + 4 * (j & 1) + 32 * (j >> 1)];
+        } else {
+            sb = ld_uniform(p.sb, (int64_t)nb128 * KB + kb);
+        }
+        // Two MFMAs behind, results are scaled and added while the next two run; the next rows of a
+        // are on their way from shared memory.
+        v4f d[2][2];
+        float sa = 0.f, sa_before = 0.f;
+        v4u lo = *(const v4u *)&tile[a_lo], hi = *(const v4u *)&tile[a_hi];
+        Fp8Operand<WIDE> af = fp8_operand<WIDE>(lo, hi);
+#pragma unroll
+        for (int u = 0; u <= 2 * MB; ++u) {
+            const int i = u >> 1, j = 2 * (u & 1);
+            sched_fence();
+            if (u < 2 * MB) {
+                if (j == 0) {
+                    af = fp8_operand<WIDE>(lo, hi);
+                    sa_before = sa;
+                    sa = scales[ra + 16 * i] * sb;
+                    if (i + 1 < MB) {
+                        lo = *(const v4u *)&tile[a_lo + 2048 * (i + 1)];
+                        hi = *(const v4u *)&tile[a_hi + 2048 * (i + 1)];
+                    }
+                } else {
+                    sa_before = sa;
+                }
+                d[u & 1][0] = fp8_block<WIDE>(bf[j], af);
+                d[u & 1][1] = fp8_block<WIDE>(bf[j + 1], af);
+            } else {
+                sa_before = sa;
+            }
+            if (u > 0) {
+                const int pi = (u - 1) >> 1, pj = 2 * ((u - 1) & 1);
+#pragma unroll
+                for (int g = 0; g < 2; ++g)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float f = BROW ? sa_before * sb4[BROW ? pj + g : 0][e] : sa_before;
+                        acc[pj + g][pi][e] += d[(u - 1) & 1][g][e] * f;
+                    }
+            }
+        }
+    };
+    fetch(kb0, tile0, scales0);
+    int kb = kb0;
+    for (; kb + 1 < kb1; kb += 2) {
+        step(kb, tile0, scales0, tile1, scales1);
+        step(kb + 1, tile1, scales1, tile0, scales0);
+    }
+    if (kb < kb1)
+        step(kb, tile0, scales0, tile1, scales1);
+    async_wait<0>();  // the loads past the last block, before the shared memory is given back
+#pragma unroll
+    for (int i = 0; i < MB; ++i) {
+        const int m = mw + 16 * i + i16;
+        if (m >= p.M)
+            continue;
+#pragma unroll
+        for (int g = 0; g < NB / 2; ++g) {
+            float v[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                v[e] = acc[2 * g + (e >> 2)][i][e & 3];
+            if (p.splits > 1)
+                fp8_store<kF32>(p.part, ((int64_t)split * p.M + m) * p.N, nw + 32 * g + 8 * q, p.N, v);
+            else
+                fp8_store<OUT>(p.out, m * p.out_stride, nw + 32 * g + 8 * q, p.N, v);
+        }
     }
 }
 

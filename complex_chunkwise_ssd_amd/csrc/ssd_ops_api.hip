@@ -172,6 +172,15 @@ int launch_fp8(const ssd::Fp8Params &p, hipStream_t s)
         hipLaunchKernelGGL((ssd::fp8_zero_kernel<OUT>), dim3(flat), dim3(256), 0, s, p);
         return launch_status();
     }
+    const bool vec = p.K % 16 == 0 && aligned(p.a, 16) && aligned(p.b, 16) && p.a_stride % 16 == 0 &&
+                     p.b_stride % 16 == 0 && p.a_stride < (1 << 24) && p.b_stride < (1 << 24);
+    if (OUT == ssd::kBF16 && vec && p.M > 128 && p.splits == 1) {
+        ssd::Fp8Params b = p;
+        b.tiles_m = (p.M + 255) / 256;
+        b.tiles_n = (p.N + 255) / 256;
+        hipLaunchKernelGGL((ssd::fp8_matmul_big_kernel<BROW, OUT>), dim3((unsigned)(b.tiles_m * b.tiles_n)), dim3(512), 0, s, b);
+        return launch_status();
+    }
     hipLaunchKernelGGL((ssd::fp8_matmul_kernel<4, 4, 2, 2, BROW, OUT>),
                        dim3((unsigned)((int64_t)p.tiles_m * p.tiles_n * p.splits)), dim3(256), 0, s, p);
     if (int st = launch_status())

@@ -87,13 +87,14 @@ SSD_DEVICE void async_load4(buf_t r, uint32_t off, void *lds)
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void *)lds, 4,
                                              (int)off, 0, 0, 0);
 }
-// Waits until at most `n` of this wave's vector memory operations are outstanding.
+// Waits until at most `n` of this wave's vector memory operations are outstanding, and none
+// of its shared-memory operations.
 template <int n>
 SSD_DEVICE void async_wait()
 {
     static_assert(n >= 0 && n < 64, "the wait counter has six bits");
-    // vmcnt in bits 3:0 and 15:14, expcnt (7) in 6:4, lgkmcnt (15) in 11:8: only vmcnt waits
-    __builtin_amdgcn_s_waitcnt((n & 15) | ((n >> 4) << 14) | (7 << 4) | (15 << 8));
+    // vmcnt in bits 3:0 and 15:14, expcnt (7: no wait) in 6:4, lgkmcnt (0) in 11:8
+    __builtin_amdgcn_s_waitcnt((n & 15) | ((n >> 4) << 14) | (7 << 4));
 }
 // A workgroup barrier that waits for nothing but the other waves.
 SSD_DEVICE void bare_barrier()
