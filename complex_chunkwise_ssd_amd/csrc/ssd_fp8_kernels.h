@@ -95,6 +95,24 @@ SSD_DEVICE v4f fp8_block(const Fp8Operand<WIDE> &a, const Fp8Operand<WIDE> &b)
     return mfma_e4m3_16x16x128(x, y, d);
 }
 
+// Two at a time, their steps in turn.
+template <bool WIDE>
+SSD_DEVICE void fp8_blocks(const Fp8Operand<WIDE> &a0, const Fp8Operand<WIDE> &a1,
+                           const Fp8Operand<WIDE> &b, v4f &d0, v4f &d1)
+{
+    if (!WIDE) {
+        d0 = fp8_block<WIDE>(a0, b);
+        d1 = fp8_block<WIDE>(a1, b);
+        return;
+    }
+    d0 = d1 = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+        d0 = mfma_bf16_16x16x32(a0.w[WIDE ? t : 0], b.w[WIDE ? t : 0], d0);
+        d1 = mfma_bf16_16x16x32(a1.w[WIDE ? t : 0], b.w[WIDE ? t : 0], d1);
+    }
+}
+
 template <int NB, int MB, int WN, int WM, bool BROW, int OUT>
 SSD_KERNEL(64 * WN * WM) void fp8_matmul_kernel(Fp8Params p)
 {
@@ -211,9 +229,9 @@ SSD_KERNEL(64 * WN * WM) void fp8_matmul_kernel(Fp8Params p)
     }
 }
 
-// The large form: 256 x 256 results per workgroup of 8 waves, each 64 rows of b by 128 rows of a.
-constexpr int kBigT = 256;
-constexpr int kBigStage = 2 * kBigT * 128;        // bytes of one k block of both operands
+// The large form: a workgroup of 8 waves, 4 along b's rows and 2 along a's, each 64 rows of b by
+// 16 MB rows of a: 256 x 32 MB results.
+constexpr int kBigN = 256;
 constexpr uint32_t kBigOut = 0xfffffff0u;         // a byte offset past every buffer
 
 // Where chunk c of staged row r lies in its row of eight: neighbouring lanes of a wave's read
@@ -236,17 +254,18 @@ SSD_DEVICE void fp8_place(const Fp8Params &p, int64_t id, int &tm, int &tn)
     tm = (int)(4 * group) + rest - tn * in;
 }
 
-template <bool BROW, int OUT>
+template <int MB, bool BROW, int OUT>
 SSD_KERNEL_WAVES(512, 2) void fp8_matmul_big_kernel(Fp8Params p)
 {
-    constexpr bool WIDE = false;
-    constexpr int NB = 4, MB = 8;
+    constexpr bool WIDE = OUT == kF32;
+    constexpr int NB = 4, TM = 32 * MB, STAGE = (kBigN + TM) * 128;
+    static_assert(MB % 2 == 0 && MB <= 8, "whole loads of 64 rows, and at most 256 of them");
     // Two stages, each an array of its own: the compiler then knows that reading one need not wait
     // for the loads into the other. Scales: a's, then b's (BROW).
-    SSD_LDS uint8_t tile0[kBigStage];
-    SSD_LDS uint8_t tile1[kBigStage];
-    SSD_LDS float scales0[2 * kBigT];
-    SSD_LDS float scales1[2 * kBigT];
+    SSD_LDS uint8_t tile0[STAGE];
+    SSD_LDS uint8_t tile1[STAGE];
+    SSD_LDS float scales0[512];
+    SSD_LDS float scales1[512];
     const int tid = thread_id();
     const int lane = tid & 63, wave = wave_id();
     const int wn = wave & 3, wm = wave >> 2;
@@ -256,11 +275,11 @@ SSD_KERNEL_WAVES(512, 2) void fp8_matmul_big_kernel(Fp8Params p)
     const int split = (int)(block_id() / all);
     int tm, tn;
     fp8_place(p, block_id() - split * all, tm, tn);
-    const int n0 = tn * kBigT, m0 = tm * kBigT;
+    const int n0 = tn * kBigN, m0 = tm * TM;
     const int kb0 = split * p.split_blocks;
     const int kb1 = kb0 + p.split_blocks < KB ? kb0 + p.split_blocks : KB;
-    const int rows_n = p.N - n0 < kBigT ? p.N - n0 : kBigT;
-    const int rows_m = p.M - m0 < kBigT ? p.M - m0 : kBigT;
+    const int rows_n = p.N - n0 < kBigN ? p.N - n0 : kBigN;
+    const int rows_m = p.M - m0 < TM ? p.M - m0 : TM;
     // Staging: this lane's place in the 8 rows that its wave loads at once (64 rows further on for
     // each of the four loads of an operand; the keys do not depend on which).
     const int r8 = lane >> 3, c8 = lane & 7;
@@ -279,23 +298,25 @@ SSD_KERNEL_WAVES(512, 2) void fp8_matmul_big_kernel(Fp8Params p)
             async_load16(make_buf(p.b + (n0 + s * 64) * p.b_stride + k,
                                   any && nb_rows > 0 ? (uint32_t)(nb_rows - 1) * (uint32_t)p.b_stride + (uint32_t)(p.K - k) : 0u),
                          ob, &tile[(s * 64 + wave * 8) * 128]);
+            if (s >= TM / 64)
+                continue;
             async_load16(make_buf(p.a + (m0 + s * 64) * p.a_stride + k,
                                   any && na_rows > 0 ? (uint32_t)(na_rows - 1) * (uint32_t)p.a_stride + (uint32_t)(p.K - k) : 0u),
-                         oa, &tile[kBigT * 128 + (s * 64 + wave * 8) * 128]);
+                         oa, &tile[kBigN * 128 + (s * 64 + wave * 8) * 128]);
         }
         const bool isa = wave < 4;
         const float *from = isa || !BROW ? p.sa + (int64_t)kb * p.M + m0 : p.sb + (int64_t)kb * p.N + n0;
         const int many = !any ? 0 : isa ? rows_m : BROW ? rows_n : 0;
-        async_load4(make_buf(from, (uint32_t)many * 4u), (uint32_t)(tid & (kBigT - 1)) * 4u, &scales[wave * 64]);
+        async_load4(make_buf(from, (uint32_t)many * 4u), (uint32_t)(tid & 255) * 4u, &scales[wave * 64]);
     };
     // Operands: row 8 (i16 / 4) + i16 % 4 + 4 (j % 2) + 32 (j / 2) of b's 64, row 16 i + i16 of a's
-    // 128; the keys do not depend on i and j, so that these are constant distances. A lane's
+    // 16 MB; the keys do not depend on i and j, so that these are constant distances. A lane's
     // results of blocks 2 g and 2 g + 1 are then the eight n from 32 g + 8 q on, one 16-byte
     // store of bfloat16, and four lanes' stores are 64 neighbouring bytes.
-    const int rb = wn * 64 + 8 * (i16 >> 2) + (i16 & 3), ra = wm * 128 + i16;
+    const int rb = wn * 64 + 8 * (i16 >> 2) + (i16 & 3), ra = wm * 16 * MB + i16;
     const int b_lo = rb * 128 + 16 * (q ^ big_key_b(rb)), b_hi = rb * 128 + 16 * ((q + 4) ^ big_key_b(rb));
-    const int a_lo = kBigT * 128 + ra * 128 + 16 * (q ^ big_key_a(ra));
-    const int a_hi = kBigT * 128 + ra * 128 + 16 * ((q + 4) ^ big_key_a(ra));
+    const int a_lo = kBigN * 128 + ra * 128 + 16 * (q ^ big_key_a(ra));
+    const int a_hi = kBigN * 128 + ra * 128 + 16 * ((q + 4) ^ big_key_a(ra));
 
     v4f acc[NB][MB];
 #pragma unroll
@@ -303,7 +324,7 @@ SSD_KERNEL_WAVES(512, 2) void fp8_matmul_big_kernel(Fp8Params p)
 #pragma unroll
         for (int i = 0; i < MB; ++i)
             acc[j][i] = v4f{0.f, 0.f, 0.f, 0.f};
-    const int nw = n0 + wn * 64, mw = m0 + wm * 128;
+    const int nw = n0 + wn * 64, mw = m0 + wm * 16 * MB;
     const int nb128 = (nw < p.N ? nw : p.N - 1) >> 7;
     auto step = [&](int kb, uint8_t *tile, float *scales, uint8_t *next_tile, float *next_scales) {
         async_wait<0>();
@@ -318,7 +339,7 @@ SSD_KERNEL_WAVES(512, 2) void fp8_matmul_big_kernel(Fp8Params p)
         if (BROW) {
 #pragma unroll
             for (int j = 0; j < NB; ++j)
-                sb4[BROW ? j : 0] = *(const v4f *)&scales[kBigT + wn * 64 + 8 * q + 4 * (j & 1) + 32 * (j >> 1)];
+                sb4[BROW ? j : 0] = *(const v4f *)&scales[256 + wn * 64 + 8 * q + 4 * (j & 1) + 32 * (j >> 1)];
         } else {
             sb = ld_uniform(p.sb, (int64_t)nb128 * KB + kb);
         }
@@ -344,8 +365,7 @@ SSD_KERNEL_WAVES(512, 2) void fp8_matmul_big_kernel(Fp8Params p)
                 } else {
                     sa_before = sa;
                 }
-                d[u & 1][0] = fp8_block<WIDE>(bf[j], af);
-                d[u & 1][1] = fp8_block<WIDE>(bf[j + 1], af);
+                fp8_blocks<WIDE>(bf[j], bf[j + 1], af, d[u & 1][0], d[u & 1][1]);
             } else {
                 sa_before = sa;
             }
@@ -385,6 +405,136 @@ SSD_KERNEL_WAVES(512, 2) void fp8_matmul_big_kernel(Fp8Params p)
                 fp8_store<kF32>(p.part, ((int64_t)split * p.M + m) * p.N, nw + 32 * g + 8 * q, p.N, v);
             else
                 fp8_store<OUT>(p.out, m * p.out_stride, nw + 32 * g + 8 * q, p.N, v);
+        }
+    }
+}
+
+// Few rows of a (16 MB at most): bound by reading b once. A wave takes 16 rows of b and every
+// WK-th k block, straight from memory into the MFMA's registers (four lanes cover a row's 128
+// bytes), AHEAD blocks in flight; the workgroup's WK waves add up through shared memory in
+// wave order. a comes from the caches.
+template <int MB, int WK, bool BROW, int OUT>
+SSD_KERNEL(64 * WK) void fp8_matmul_few_kernel(Fp8Params p)
+{
+    constexpr bool WIDE = OUT == kF32;
+    constexpr int AHEAD = MB == 1 ? (WK == 4 ? 4 : 3) : MB == 2 ? 2 : (WK == 4 ? 2 : 1);  // what the registers hold
+    SSD_LDS float sums[WK - 1][MB * 4][64];
+    const int lane = thread_id() & 63, wave = wave_id();
+    const int i16 = lane & 15, q = lane >> 4;
+    const int n0 = (int)block_id() * 16;
+    const int full = p.K >> 7, KB = (p.K + 127) >> 7;
+    const int brow = n0 + i16 < p.N ? n0 + i16 : p.N - 1;   // rows past the end repeat the last; not stored
+    const uint8_t *b = p.b + (int64_t)brow * p.b_stride + 32 * q;
+    const uint8_t *a[MB];
+    int arow[MB];
+#pragma unroll
+    for (int i = 0; i < MB; ++i) {
+        arow[i] = 16 * i + i16 < p.M ? 16 * i + i16 : p.M - 1;
+        a[i] = p.a + (int64_t)arow[i] * p.a_stride + 32 * q;
+    }
+    v4f acc[MB];
+#pragma unroll
+    for (int i = 0; i < MB; ++i)
+        acc[i] = v4f{0.f, 0.f, 0.f, 0.f};
+    struct Block {
+        v4u b[2], a[MB][2];
+        float sa[MB], sb[BROW ? 4 : 1];
+    };
+    auto scales = [&](Block &h, int kb) {
+#pragma unroll
+        for (int i = 0; i < MB; ++i)
+            h.sa[i] = p.sa[(int64_t)kb * p.M + arow[i]];
+        if (BROW) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int n = n0 + 4 * q + e;
+                h.sb[BROW ? e : 0] = p.sb[(int64_t)kb * p.N + (n < p.N ? n : p.N - 1)];
+            }
+        } else {
+            h.sb[0] = ld_uniform(p.sb, (int64_t)(n0 >> 7) * KB + kb);
+        }
+    };
+    auto add = [&](const Block &h) {
+        const Fp8Operand<WIDE> bf = fp8_operand<WIDE>(h.b[0], h.b[1]);
+#pragma unroll
+        for (int i = 0; i < MB; ++i) {
+            const v4f d = fp8_block<WIDE>(bf, fp8_operand<WIDE>(h.a[i][0], h.a[i][1]));
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                acc[i][e] += d[e] * (h.sa[i] * h.sb[BROW ? e : 0]);
+        }
+    };
+    for (int first = wave; first < full; first += WK * AHEAD) {
+        Block h[AHEAD];
+#pragma unroll
+        for (int g = 0; g < AHEAD; ++g) {
+            const int kb = first + WK * g;
+            if (kb >= full)
+                break;
+            __builtin_memcpy(h[g].b, b + kb * 128, 32);
+#pragma unroll
+            for (int i = 0; i < MB; ++i)
+                __builtin_memcpy(h[g].a[i], a[i] + kb * 128, 32);
+            scales(h[g], kb);
+        }
+#pragma unroll
+        for (int g = 0; g < AHEAD; ++g) {
+            if (first + WK * g >= full)
+                break;
+            add(h[g]);
+        }
+    }
+    if (full < KB && full % WK == wave) {  // the block that K cuts
+        Block h;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            const int k = full * 128 + 16 * t;
+            h.b[t] = fp8_chunk(b, k, p.K - 32 * q);
+#pragma unroll
+            for (int i = 0; i < MB; ++i)
+                h.a[i][t] = fp8_chunk(a[i], k, p.K - 32 * q);
+        }
+        scales(h, full);
+        add(h);
+    }
+    if (wave > 0) {
+#pragma unroll
+        for (int i = 0; i < MB; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                sums[wave - 1][4 * i + e][lane] = acc[i][e];
+    }
+    block_sync();
+    if (wave > 0)
+        return;
+#pragma unroll
+    for (int i = 0; i < MB; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            for (int w = 0; w < WK - 1; ++w)
+                acc[i][e] += sums[w][4 * i + e][lane];
+    const int left = p.N - n0 - 4 * q;
+#pragma unroll
+    for (int i = 0; i < MB; ++i) {
+        const int m = 16 * i + i16;
+        if (m >= p.M || left <= 0)
+            continue;
+        char *out = (char *)p.out + (m * p.out_stride + n0 + 4 * q) * ElemSize<OUT>::value;
+        const v2u u = {cvt_pk_bf16(acc[i][0], acc[i][1]), cvt_pk_bf16(acc[i][2], acc[i][3])};
+        if (left >= 4) {
+            if (OUT == kBF16)
+                __builtin_memcpy(out, &u, 8);
+            else
+                __builtin_memcpy(out, &acc[i], 16);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 3; ++e)
+                if (e < left) {
+                    if (OUT == kBF16)
+                        ((uint16_t *)out)[e] = (uint16_t)(u[e >> 1] >> (16 * (e & 1)));
+                    else
+                        ((float *)out)[e] = acc[i][e];
+                }
         }
     }
 }

@@ -130,12 +130,14 @@ int launch_quantise(const ssd::QuantParams &p, bool whole, bool turn, hipStream_
     return launch_status();
 }
 
+// Which kernel a product takes, and how the sum over k is split.
+enum { kFp8Few, kFp8Big, kFp8General };
 struct Fp8Plan {
+    int form;
+    int mb;                   // 16 mb rows of a per wave (few, big)
     int tiles_m, tiles_n, splits, split_blocks;
     size_t bytes;
 };
-
-constexpr int kFp8TileN = 128, kFp8TileM = 128;
 
 int check_fp8(int64_t M, int64_t N, int64_t K, int64_t b_block_rows, int out_dtype)
 {
@@ -143,28 +145,83 @@ int check_fp8(int64_t M, int64_t N, int64_t K, int64_t b_block_rows, int out_dty
         return SSD_ERR_SHAPE;
     if (M > (1LL << 30) || N > (1LL << 30) || K > (1LL << 30))
         return SSD_ERR_UNSUPPORTED;
-    const int64_t tiles = ((M + kFp8TileM - 1) / kFp8TileM) * ((N + kFp8TileN - 1) / kFp8TileN);
+    const int64_t tiles = ((M + 127) / 128) * ((N + 127) / 128);
     return tiles > kMaxGrid / 64 ? SSD_ERR_UNSUPPORTED : SSD_OK;
 }
 
-Fp8Plan fp8_plan(int64_t M, int64_t N, int64_t K)
+// Time of a product in us by a tile form: every compute unit takes tiles * splits / 256 of them,
+// each its k blocks (per_block us) and a start and end (per_tile us); the parts of a split sum are
+// written and read once more.
+double fp8_cost(int64_t M, int64_t N, int64_t tiles, int64_t kb, int splits, double per_block,
+                double per_tile)
+{
+    const double rounds = (double)((tiles * splits + 255) / 256);
+    const double parts = splits > 1 ? 4 + 8e-6 / 4.5 * splits * (double)M * (double)N : 0.;
+    return rounds * (per_block * (double)((kb + splits - 1) / splits) + per_tile) + parts;
+}
+
+// `vec`: rows of both operands start on 16 bytes and K is a multiple of 16.
+Fp8Plan fp8_plan(int64_t M, int64_t N, int64_t K, int out_dtype, bool vec)
 {
     Fp8Plan p{};
-    p.tiles_m = (int)((M + kFp8TileM - 1) / kFp8TileM);
-    p.tiles_n = (int)((N + kFp8TileN - 1) / kFp8TileN);
-    const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n, kb = (K + 127) / 128;
-    int64_t splits = tiles > 0 ? 512 / tiles : 1;
-    splits = splits > kb / 4 ? kb / 4 : splits;
-    splits = splits > 32 ? 32 : splits;
-    splits = splits < 1 ? 1 : splits;
-    p.split_blocks = (int)((kb + splits - 1) / splits);
+    const int64_t kb = (K + 127) / 128;
+    p.splits = 1;
+    p.split_blocks = (int)kb;
+    if (M <= 64) {
+        p.form = kFp8Few;
+        p.mb = M <= 16 ? 1 : M <= 32 ? 2 : 4;
+        return p;
+    }
+    double best = 0.;
+    const bool wide = out_dtype == SSD_F32;
+    for (int form = 0; form < 2; ++form) {
+        const int mb = vec ? (form == 0 ? 4 : 8) : 0;
+        if (form == 1 && (!vec || wide))
+            break;
+        const int64_t tm = vec ? (M + 32 * mb - 1) / (32 * mb) : (M + 127) / 128;
+        const int64_t tn = vec ? (N + 255) / 256 : (N + 127) / 128;
+        const double per_block = !vec ? (wide ? 3. : 1.5) : mb == 8 ? 1.9 : wide ? 1.9 : 1.1;
+        for (int s = 1; s <= 32 && (s == 1 || s * 2 <= kb); ++s) {
+            const double cost = fp8_cost(M, N, tm * tn, kb, s, per_block, mb == 8 ? 6. : 3.);
+            if ((form == 0 && s == 1) || cost < best) {
+                best = cost;
+                p.form = vec ? kFp8Big : kFp8General;
+                p.mb = mb;
+                p.tiles_m = (int)tm;
+                p.tiles_n = (int)tn;
+                p.split_blocks = (int)((kb + s - 1) / s);
+            }
+        }
+    }
     p.splits = kb > 0 ? (int)((kb + p.split_blocks - 1) / p.split_blocks) : 1;
     p.bytes = p.splits > 1 ? align256((size_t)p.splits * M * N * 4) : 0;
     return p;
 }
 
+// The workspace covers either alignment of the operands.
+size_t fp8_bytes(int64_t M, int64_t N, int64_t K, int out_dtype)
+{
+    const size_t a = fp8_plan(M, N, K, out_dtype, false).bytes;
+    const size_t b = K % 16 == 0 ? fp8_plan(M, N, K, out_dtype, true).bytes : 0;
+    return a > b ? a : b;
+}
+
+template <int MB, bool BROW, int OUT>
+int launch_fp8_few(const ssd::Fp8Params &p, hipStream_t s)
+{
+    const unsigned groups = (unsigned)((p.N + 15) / 16);
+    const int kb = (p.K + 127) / 128;
+    // a workgroup per 16 rows of b: with fewer of those than fill the chip, more waves share its sum
+    constexpr int MANY = MB == 1 ? 16 : 8;
+    if (groups < 512 && kb > 8)
+        hipLaunchKernelGGL((ssd::fp8_matmul_few_kernel<MB, MANY, BROW, OUT>), dim3(groups), dim3(64 * MANY), 0, s, p);
+    else
+        hipLaunchKernelGGL((ssd::fp8_matmul_few_kernel<MB, 4, BROW, OUT>), dim3(groups), dim3(256), 0, s, p);
+    return launch_status();
+}
+
 template <bool BROW, int OUT>
-int launch_fp8(const ssd::Fp8Params &p, hipStream_t s)
+int launch_fp8(const ssd::Fp8Params &p, const Fp8Plan &plan, hipStream_t s)
 {
     const int64_t n = (int64_t)p.M * p.N;
     const unsigned flat = (unsigned)((n + 255) / 256 < 8192 ? (n + 255) / 256 : 8192);
@@ -172,17 +229,17 @@ int launch_fp8(const ssd::Fp8Params &p, hipStream_t s)
         hipLaunchKernelGGL((ssd::fp8_zero_kernel<OUT>), dim3(flat), dim3(256), 0, s, p);
         return launch_status();
     }
-    const bool vec = p.K % 16 == 0 && aligned(p.a, 16) && aligned(p.b, 16) && p.a_stride % 16 == 0 &&
-                     p.b_stride % 16 == 0 && p.a_stride < (1 << 24) && p.b_stride < (1 << 24);
-    if (OUT == ssd::kBF16 && vec && p.M > 128 && p.splits == 1) {
-        ssd::Fp8Params b = p;
-        b.tiles_m = (p.M + 255) / 256;
-        b.tiles_n = (p.N + 255) / 256;
-        hipLaunchKernelGGL((ssd::fp8_matmul_big_kernel<BROW, OUT>), dim3((unsigned)(b.tiles_m * b.tiles_n)), dim3(512), 0, s, b);
-        return launch_status();
-    }
-    hipLaunchKernelGGL((ssd::fp8_matmul_kernel<4, 4, 2, 2, BROW, OUT>),
-                       dim3((unsigned)((int64_t)p.tiles_m * p.tiles_n * p.splits)), dim3(256), 0, s, p);
+    if (plan.form == kFp8Few)
+        return plan.mb == 1   ? launch_fp8_few<1, BROW, OUT>(p, s)
+               : plan.mb == 2 ? launch_fp8_few<2, BROW, OUT>(p, s)
+                              : launch_fp8_few<4, BROW, OUT>(p, s);
+    const dim3 grid((unsigned)((int64_t)p.tiles_m * p.tiles_n * p.splits));
+    if (plan.form == kFp8General)
+        hipLaunchKernelGGL((ssd::fp8_matmul_kernel<4, 4, 2, 2, BROW, OUT>), grid, dim3(256), 0, s, p);
+    else if (OUT == ssd::kBF16 && plan.mb == 8)
+        hipLaunchKernelGGL((ssd::fp8_matmul_big_kernel<8, BROW, ssd::kBF16>), grid, dim3(512), 0, s, p);
+    else
+        hipLaunchKernelGGL((ssd::fp8_matmul_big_kernel<4, BROW, OUT>), grid, dim3(512), 0, s, p);
     if (int st = launch_status())
         return st;
     if (p.splits > 1) {
@@ -459,7 +516,7 @@ size_t ssd_fp8_matmul_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t b
 {
     if (check_fp8(M, N, K, b_block_rows, out_dtype))
         return 0;
-    return fp8_plan(M, N, K).bytes;
+    return fp8_bytes(M, N, K, out_dtype);
 }
 
 int ssd_fp8_matmul(const uint8_t *a, int64_t a_stride, const float *a_scale, const uint8_t *b,
@@ -480,10 +537,13 @@ int ssd_fp8_matmul(const uint8_t *a, int64_t a_stride, const float *a_scale, con
     const int e = elem_size(out_dtype);
     if (!aligned(a_scale, 4) || !aligned(b_scale, 4) || !aligned(out, e))
         return SSD_ERR_ALIGN;
-    const Fp8Plan plan = fp8_plan(M, N, K);
-    if (plan.bytes > 0 && (!workspace || workspace_bytes < plan.bytes))
+    const bool vec = K % 16 == 0 && aligned(a, 16) && aligned(b, 16) && a_stride % 16 == 0 &&
+                     b_stride % 16 == 0 && a_stride < (1 << 24) && b_stride < (1 << 24);
+    const Fp8Plan plan = fp8_plan(M, N, K, out_dtype, vec);
+    const size_t need = fp8_bytes(M, N, K, out_dtype);
+    if (need > 0 && (!workspace || workspace_bytes < need))
         return SSD_ERR_WORKSPACE;
-    if (plan.bytes > 0 && !aligned(workspace, 256))
+    if (need > 0 && !aligned(workspace, 256))
         return SSD_ERR_ALIGN;
     const int64_t kb = (K + 127) / 128;
     const struct { const void *p; int64_t bytes; } in[4] = {
@@ -515,8 +575,8 @@ int ssd_fp8_matmul(const uint8_t *a, int64_t a_stride, const float *a_scale, con
     p.split_blocks = plan.split_blocks;
     const hipStream_t s = (hipStream_t)stream;
     if (b_block_rows == 1)
-        return out_dtype == SSD_BF16 ? launch_fp8<true, ssd::kBF16>(p, s) : launch_fp8<true, ssd::kF32>(p, s);
-    return out_dtype == SSD_BF16 ? launch_fp8<false, ssd::kBF16>(p, s) : launch_fp8<false, ssd::kF32>(p, s);
+        return out_dtype == SSD_BF16 ? launch_fp8<true, ssd::kBF16>(p, plan, s) : launch_fp8<true, ssd::kF32>(p, plan, s);
+    return out_dtype == SSD_BF16 ? launch_fp8<false, ssd::kBF16>(p, plan, s) : launch_fp8<false, ssd::kF32>(p, plan, s);
 }
 
 size_t ssd_gated_scan_workspace_bytes(int64_t batch, int64_t T, int64_t C, int dtype)

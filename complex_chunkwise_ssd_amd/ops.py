@@ -51,9 +51,20 @@ def declare(lib):
           vp)
 
 
-def _lib():
-    from . import load_library
-    return load_library()
+_entries = {}  # name -> function of the loaded library
+
+
+def _entry(name):
+    fn = _entries.get(name)
+    if fn is None:
+        from . import load_library
+        fn = _entries[name] = getattr(load_library(), name)
+    return fn
+
+
+# The stream as an integer; the public way builds a Stream object first (1.5 us of a 10 us call).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _ptr(t):
@@ -63,29 +74,32 @@ def _ptr(t):
 def _call(name, dev, *args):
     """One entry point on the current stream of `dev`, which becomes the current device for
     the call if it is not."""
-    from . import SSDError
-    fn = getattr(_lib(), name)
-    if dev.index == torch.cuda.current_device():
-        st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    fn = _entries.get(name) or _entry(name)
+    index = dev.index
+    if index == torch.cuda.current_device():
+        st = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(dev):
-            st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+            st = fn(*args, _raw_stream(index))
     if st != 0:
+        from . import SSDError
         raise SSDError(st, name)
 
 
 def _device(t, name):
     if not isinstance(t, torch.Tensor):
         raise ValueError("%s must be a torch.Tensor" % name)
-    if t.device.type != "cuda":
-        raise ValueError("tensors must be on a GPU device, got %s" % t.device)
-    return t.device
+    dev = t.device
+    if dev.type != "cuda":
+        raise ValueError("tensors must be on a GPU device, got %s" % dev)
+    return dev
 
 
 def _dtype(t, name):
-    if t.dtype not in _DTYPES:
+    dt = _DTYPES.get(t.dtype)
+    if dt is None:
         raise ValueError("%s must be float32 or bfloat16, got %s" % (name, t.dtype))
-    return _DTYPES[t.dtype]
+    return dt
 
 
 def _check(t, name, dtype, shape, dev):
@@ -96,7 +110,7 @@ def _check(t, name, dtype, shape, dev):
         raise ValueError("%s must be %s, got %s" % (name, dtype, t.dtype))
     if t.device != dev:
         raise ValueError("%s must be on %s, got %s" % (name, dev, t.device))
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
@@ -123,29 +137,30 @@ def _row_stride(t, name, dtype, shape, dev):
     spaced (a contiguous tensor, or a column range of one)."""
     if not isinstance(t, torch.Tensor):
         raise ValueError("%s must be a torch.Tensor" % name)
-    if t.dtype != dtype or t.device != dev or tuple(t.shape) != tuple(shape):
+    if t.dtype != dtype or t.device != dev or t.shape != shape:
         raise ValueError("%s must be %s of shape %s on %s, got %s of shape %s on %s" % (
             name, dtype, tuple(shape), dev, t.dtype, tuple(t.shape), t.device))
-    F = t.shape[-1]
+    F = shape[-1]
     if t.is_contiguous():
         return F
+    strides = t.stride()
     want = step = None  # between neighbouring rows; that the next dimension out has to have
-    for d in range(t.dim() - 2, -1, -1):
-        if t.shape[d] == 1:
+    for d in range(len(shape) - 2, -1, -1):
+        if shape[d] == 1:
             continue
         if want is None:
-            want = step = t.stride(d)
-        if t.stride(d) != step:
+            want = step = strides[d]
+        if strides[d] != step:
             want = 0
             break
-        step *= t.shape[d]
-    if F > 1 and t.stride(-1) != 1:
+        step *= shape[d]
+    if F > 1 and strides[-1] != 1:
         want = 0
     if want is None:
         want = F
     if want < F:
         raise ValueError("%s must have a dense last dimension and evenly spaced rows, got strides %s"
-                         % (name, tuple(t.stride())))
+                         % (name, strides))
     return want
 
 
@@ -162,8 +177,10 @@ def _gated_inputs(x, input_gate, decay_gate, lam, lengths):
         raise ValueError("x must be a (B, T, C) tensor")
     dt = _dtype(x, "x")
     B, T, C = x.shape
-    strides = [_row_stride(t, n, x.dtype, x.shape, dev)
-               for t, n in ((x, "x"), (input_gate, "input_gate"), (decay_gate, "decay_gate"))]
+    shape, ty = x.shape, x.dtype
+    strides = (_row_stride(x, "x", ty, shape, dev),
+               _row_stride(input_gate, "input_gate", ty, shape, dev),
+               _row_stride(decay_gate, "decay_gate", ty, shape, dev))
     _check(lam, "lam", torch.float32, (C,), dev)
     if lengths is not None:
         _check(lengths, "lengths", torch.int32, (B,), dev)
@@ -191,7 +208,7 @@ def gated_scan(x, input_gate, decay_gate, lam, decay_scale: float = 8.0, initial
     final_state = _out(final_state, "final_state", torch.float32, (B, C), dev, want_final_state)
     chunk_states = _out(chunk_states, "chunk_states", torch.float32,
                         (B, -(-T // GATED_CHUNK), C), dev, want_chunk_states)
-    ws, size = _workspace(workspace, _lib().ssd_gated_scan_workspace_bytes(B, T, C, dt), dev)
+    ws, size = _workspace(workspace, _entry("ssd_gated_scan_workspace_bytes")(B, T, C, dt), dev)
     _call("ssd_gated_scan", dev, _ptr(x), st[0], _ptr(input_gate), st[1], _ptr(decay_gate), st[2],
           _ptr(lam), float(decay_scale), dt, B, T, C, _ptr(initial_state), _ptr(lengths), _ptr(h),
           _ptr(final_state), _ptr(chunk_states), _ptr(ws), size)
@@ -217,7 +234,7 @@ def gated_scan_backward(x, input_gate, decay_gate, lam, chunk_states, grad_h, gr
     glam = _out(o.lam, "grad lam", torch.float32, (C,), dev)
     ginit = _out(o.initial_state, "grad initial_state", torch.float32, (B, C), dev,
                  want_initial_state_grad)
-    ws, size = _workspace(workspace, _lib().ssd_gated_scan_backward_workspace_bytes(B, T, C, dt), dev)
+    ws, size = _workspace(workspace, _entry("ssd_gated_scan_backward_workspace_bytes")(B, T, C, dt), dev)
     _call("ssd_gated_scan_backward", dev, _ptr(x), st[0], _ptr(input_gate), st[1], _ptr(decay_gate),
           st[2], _ptr(lam), float(decay_scale), dt, B, T, C, _ptr(chunk_states), _ptr(lengths),
           _ptr(grad_h), _ptr(grad_final_state), _ptr(gx), _ptr(gi), _ptr(gr), _ptr(glam),
@@ -274,7 +291,7 @@ def rms_norm_backward(s, weight, rstd, grad_y, grad_residual=None, grad_x=None, 
     _check(rstd, "rstd", torch.float32, (rows,), dev)
     grad_x = _out(grad_x, "grad_x", s.dtype, s.shape, dev)
     grad_weight = _out(grad_weight, "grad_weight", torch.float32, (F,), dev)
-    ws, size = _workspace(workspace, _lib().ssd_rms_norm_backward_workspace_bytes(rows, F), dev)
+    ws, size = _workspace(workspace, _entry("ssd_rms_norm_backward_workspace_bytes")(rows, F), dev)
     _call("ssd_rms_norm_backward", dev, _ptr(s), ss, _ptr(weight), _ptr(rstd), _ptr(grad_y), sg,
           _ptr(grad_residual), sr, dt, rows, F, _ptr(grad_x), _ptr(grad_weight), _ptr(ws), size)
     return grad_x, grad_weight
@@ -338,7 +355,7 @@ def fp8_matmul(a, a_scale, b, b_scale, block_rows: int = 128, out_dtype=torch.bf
         out = torch.empty(shape, dtype=out_dtype, device=dev)
     so = _row_stride(out, "out", out_dtype, shape, dev)
     dt = _DTYPES[out_dtype]
-    ws, size = _workspace(workspace, _lib().ssd_fp8_matmul_workspace_bytes(M, N, K, int(block_rows), dt), dev)
+    ws, size = _workspace(workspace, _entry("ssd_fp8_matmul_workspace_bytes")(M, N, K, int(block_rows), dt), dev)
     _call("ssd_fp8_matmul", dev, _ptr(a), sa, _ptr(a_scale), _ptr(b), sb, _ptr(b_scale), M, N, K,
           int(block_rows), dt, _ptr(out), so, _ptr(ws), size)
     return out
