@@ -56,8 +56,6 @@ SSD_DEVICE void fp8_store(void *out, int64_t at, int n, int N, const float (&v)[
         store8<OUT>((char *)out + (at + n) * ElemSize<OUT>::value, N - n, v);
 }
 
-// A workgroup of WN x WM waves; a wave holds 16 NB rows of b and 16 MB rows of a. BROW: sb
-// per row of b. OUT: element type of the result; partial sums of a split k are float32.
 // One operand's 32 values of a lane, as its MFMA takes them.
 template <bool WIDE>
 struct Fp8Operand {
@@ -113,119 +111,16 @@ SSD_DEVICE void fp8_blocks(const Fp8Operand<WIDE> &a0, const Fp8Operand<WIDE> &a
     }
 }
 
-template <int NB, int MB, int WN, int WM, bool BROW, int OUT>
-SSD_KERNEL(64 * WN * WM) void fp8_matmul_kernel(Fp8Params p)
+// The rows of an operand that do not start on 16 bytes, laid out anew so that they do, with zeros
+// up to the next multiple of 16: what the large form reads. One 16-byte piece per thread.
+SSD_KERNEL(256) void fp8_pack_kernel(const uint8_t *x, int64_t stride, int64_t rows, int K, uint8_t *out)
 {
-    constexpr int TN = 16 * NB * WN, TM = 16 * MB * WM, THREADS = 64 * WN * WM;
-    constexpr bool WIDE = OUT == kF32;
-    constexpr int CHUNKS = (TN + TM) * 8 / THREADS;
-    static_assert((TN + TM) * 8 % THREADS == 0, "every thread stages the same number of chunks");
-    SSD_LDS uint8_t tile[(TN + TM) * 128];
-    const int tid = thread_id();
-    const int lane = tid & 63, wave = wave_id();
-    const int wn = wave % WN, wm = wave / WN;
-    const int i16 = lane & 15, q = lane >> 4;
-    const int64_t id = block_id();
-    const int tm = (int)(id % p.tiles_m);
-    const int64_t rest = id / p.tiles_m;
-    const int tn = (int)(rest % p.tiles_n);
-    const int split = (int)(rest / p.tiles_n);
-    const int n0 = tn * TN, m0 = tm * TM;
-    const int KB = (p.K + 127) >> 7;
-    const int kb0 = split * p.split_blocks;
-    const int kb1 = kb0 + p.split_blocks < KB ? kb0 + p.split_blocks : KB;
-
-    // Chunk c of staged row r lies at 16 (c ^ (r & 7)): a wave's 16 rows then spread over the banks.
-    v4u hold[CHUNKS];
-    auto fetch = [&](int kb) {
-#pragma unroll
-        for (int s = 0; s < CHUNKS; ++s) {
-            const int f = tid + THREADS * s;
-            const int r = f >> 3, c = f & 7;
-            const bool isb = r < TN;
-            int row = isb ? n0 + r : m0 + r - TN;
-            const int most = (isb ? p.N : p.M) - 1;
-            row = row < most ? row : most;  // rows past the end repeat the last one; not stored
-            const uint8_t *at = isb ? p.b + (int64_t)row * p.b_stride : p.a + (int64_t)row * p.a_stride;
-            hold[s] = fp8_chunk(at, kb * 128 + 16 * c, p.K);
-        }
-    };
-    auto stage = [&]() {
-#pragma unroll
-        for (int s = 0; s < CHUNKS; ++s) {
-            const int f = tid + THREADS * s;
-            const int r = f >> 3, c = f & 7;
-            *(v4u *)&tile[r * 128 + 16 * (c ^ (r & 7))] = hold[s];
-        }
-    };
-    auto operand = [&](int r) {
-        const v4u lo = *(const v4u *)&tile[r * 128 + 16 * (q ^ (r & 7))];
-        const v4u hi = *(const v4u *)&tile[r * 128 + 16 * ((q + 4) ^ (r & 7))];
-        return fp8_operand<WIDE>(lo, hi);
-    };
-
-    v4f acc[NB][MB];
-#pragma unroll
-    for (int j = 0; j < NB; ++j)
-#pragma unroll
-        for (int i = 0; i < MB; ++i)
-            acc[j][i] = v4f{0.f, 0.f, 0.f, 0.f};
-    const int nw = n0 + wn * 16 * NB;            // the wave's first row of b
-    const int mw = m0 + wm * 16 * MB;
-    fetch(kb0);
-    for (int kb = kb0; kb < kb1; ++kb) {
-        block_sync();
-        stage();
-        block_sync();
-        if (kb + 1 < kb1)
-            fetch(kb + 1);
-        Fp8Operand<WIDE> bf[NB];
-        // Row i16 of the MFMA's block j is b's row 4 NB (i16 / 4) + 4 j + i16 % 4: a lane's results
-        // of all blocks are then 4 NB neighbouring n.
-#pragma unroll
-        for (int j = 0; j < NB; ++j)
-            bf[j] = operand(wn * 16 * NB + 4 * NB * (i16 >> 2) + 4 * j + (i16 & 3));
-        float sb[BROW ? 4 * NB : 1];
-        if (BROW) {
-#pragma unroll
-            for (int e = 0; e < 4 * NB; ++e) {
-                const int n = nw + 4 * NB * q + e;
-                sb[e] = p.sb[(int64_t)kb * p.N + (n < p.N ? n : p.N - 1)];
-            }
-        } else {
-            const int nb = (nw < p.N ? nw : p.N - 1) >> 7;
-            sb[0] = ld_uniform(p.sb, (int64_t)nb * KB + kb);
-        }
-#pragma unroll
-        for (int i = 0; i < MB; ++i) {
-            const Fp8Operand<WIDE> af = operand(TN + wm * 16 * MB + 16 * i + i16);
-            const int m = mw + 16 * i + i16;
-            const float sa = p.sa[(int64_t)kb * p.M + (m < p.M ? m : p.M - 1)];
-#pragma unroll
-            for (int j = 0; j < NB; ++j) {
-                const v4f d = fp8_block<WIDE>(bf[j], af);
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    acc[j][i][e] += d[e] * (sa * sb[BROW ? 4 * j + e : 0]);
-            }
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < MB; ++i) {
-        const int m = mw + 16 * i + i16;
-        if (m >= p.M)
-            continue;
-#pragma unroll
-        for (int g = 0; g < NB / 2; ++g) {
-            float v[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                v[e] = acc[2 * g + (e >> 2)][i][e & 3];
-            if (p.splits > 1)
-                fp8_store<kF32>(p.part, ((int64_t)split * p.M + m) * p.N, nw + 4 * NB * q + 8 * g, p.N, v);
-            else
-                fp8_store<OUT>(p.out, m * p.out_stride, nw + 4 * NB * q + 8 * g, p.N, v);
-        }
+    const int pieces = (K + 15) >> 4;
+    const int64_t n = rows * pieces, step = grid_blocks() * 256;
+    for (int64_t e = block_id() * 256 + thread_id(); e < n; e += step) {
+        const int64_t r = e / pieces;
+        const int k = (int)(e - r * pieces) * 16;
+        *(v4u *)(out + (r * pieces) * 16 + k) = fp8_chunk(x + r * stride, k, K);
     }
 }
 
@@ -284,30 +179,35 @@ SSD_KERNEL_WAVES(512, 2) void fp8_matmul_big_kernel(Fp8Params p)
     // each of the four loads of an operand; the keys do not depend on which).
     const int r8 = lane >> 3, c8 = lane & 7;
     const int ka = 16 * (c8 ^ big_key_a(r8)), kb_ = 16 * (c8 ^ big_key_b(wave * 8 + r8));
-    const uint32_t off_a = (uint32_t)(wave * 8 + r8) * (uint32_t)p.a_stride + (uint32_t)ka;
-    const uint32_t off_b = (uint32_t)(wave * 8 + r8) * (uint32_t)p.b_stride + (uint32_t)kb_;
-    // No branches in here: past the last block (and for scales that there are not) the buffers are empty.
-    auto fetch = [&](int kb, uint8_t *tile, float *scales) {
+    uint32_t off_a[TM / 64], off_b[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        off_b[r] = (uint32_t)(64 * r + wave * 8 + r8) * (uint32_t)p.b_stride + (uint32_t)kb_;
+        if (r < TM / 64)
+            off_a[r % (TM / 64)] = (uint32_t)(64 * r + wave * 8 + r8) * (uint32_t)p.a_stride + (uint32_t)ka;
+    }
+    const uint8_t *first_a = p.a + m0 * p.a_stride, *first_b = p.b + n0 * p.b_stride;
+    const uint32_t end_a = (uint32_t)(rows_m - 1) * (uint32_t)p.a_stride + (uint32_t)p.K;
+    const uint32_t end_b = (uint32_t)(rows_n - 1) * (uint32_t)p.b_stride + (uint32_t)p.K;
+    // One of the five parts of a block's loads. No branches in here: past the last block (and for
+    // scales that there are not) the buffers are empty.
+    auto fetch = [&](int part, int kb, uint8_t *tile, float *scales) {
         const int k = kb * 128;
         const bool any = kb < kb1;
-        // 16 bytes from K on lie past the buffer's end, as rows past the matrix's do: zeros
-        const uint32_t oa = k + ka < p.K ? off_a : kBigOut, ob = k + kb_ < p.K ? off_b : kBigOut;
-#pragma unroll
-        for (int s = 0; s < 4; ++s) {
-            const int nb_rows = rows_n - s * 64, na_rows = rows_m - s * 64;
-            async_load16(make_buf(p.b + (n0 + s * 64) * p.b_stride + k,
-                                  any && nb_rows > 0 ? (uint32_t)(nb_rows - 1) * (uint32_t)p.b_stride + (uint32_t)(p.K - k) : 0u),
-                         ob, &tile[(s * 64 + wave * 8) * 128]);
-            if (s >= TM / 64)
-                continue;
-            async_load16(make_buf(p.a + (m0 + s * 64) * p.a_stride + k,
-                                  any && na_rows > 0 ? (uint32_t)(na_rows - 1) * (uint32_t)p.a_stride + (uint32_t)(p.K - k) : 0u),
-                         oa, &tile[kBigN * 128 + (s * 64 + wave * 8) * 128]);
+        if (part < 4) {
+            // 16 bytes from K on lie past the buffer's end, as rows past the matrix's do: zeros
+            async_load16(make_buf(first_b + k, any ? end_b - (uint32_t)k : 0u), k + kb_ < p.K ? off_b[part % 4] : kBigOut,
+                         &tile[(64 * part + wave * 8) * 128]);
+            if (part < TM / 64)
+                async_load16(make_buf(first_a + k, any ? end_a - (uint32_t)k : 0u),
+                             k + ka < p.K ? off_a[part % (TM / 64)] : kBigOut,
+                             &tile[kBigN * 128 + (64 * part + wave * 8) * 128]);
+        } else {
+            const bool isa = wave < 4;
+            const float *from = isa || !BROW ? p.sa + (int64_t)kb * p.M + m0 : p.sb + (int64_t)kb * p.N + n0;
+            const int many = !any ? 0 : isa ? rows_m : BROW ? rows_n : 0;
+            async_load4(make_buf(from, (uint32_t)many * 4u), (uint32_t)(tid & 255) * 4u, &scales[wave * 64]);
         }
-        const bool isa = wave < 4;
-        const float *from = isa || !BROW ? p.sa + (int64_t)kb * p.M + m0 : p.sb + (int64_t)kb * p.N + n0;
-        const int many = !any ? 0 : isa ? rows_m : BROW ? rows_n : 0;
-        async_load4(make_buf(from, (uint32_t)many * 4u), (uint32_t)(tid & 255) * 4u, &scales[wave * 64]);
     };
     // Operands: row 8 (i16 / 4) + i16 % 4 + 4 (j % 2) + 32 (j / 2) of b's 64, row 16 i + i16 of a's
     // 16 MB; the keys do not depend on i and j, so that these are constant distances. A lane's
@@ -329,7 +229,6 @@ SSD_KERNEL_WAVES(512, 2) void fp8_matmul_big_kernel(Fp8Params p)
     auto step = [&](int kb, uint8_t *tile, float *scales, uint8_t *next_tile, float *next_scales) {
         async_wait<0>();
         bare_barrier();
-        fetch(kb + 1, next_tile, next_scales);
         Fp8Operand<WIDE> bf[NB];
 #pragma unroll
         for (int j = 0; j < NB; ++j)
@@ -348,17 +247,21 @@ SSD_KERNEL_WAVES(512, 2) void fp8_matmul_big_kernel(Fp8Params p)
         v4f d[2][2];
         float sa = 0.f, sa_before = 0.f;
         v4u lo = *(const v4u *)&tile[a_lo], hi = *(const v4u *)&tile[a_hi];
+        float sa_next = scales[ra];
         Fp8Operand<WIDE> af = fp8_operand<WIDE>(lo, hi);
 #pragma unroll
         for (int u = 0; u <= 2 * MB; ++u) {
             const int i = u >> 1, j = 2 * (u & 1);
             sched_fence();
+            if (u < 5)
+                fetch(u, kb + 1, next_tile, next_scales);
             if (u < 2 * MB) {
                 if (j == 0) {
                     af = fp8_operand<WIDE>(lo, hi);
                     sa_before = sa;
-                    sa = scales[ra + 16 * i] * sb;
+                    sa = sa_next * sb;
                     if (i + 1 < MB) {
+                        sa_next = scales[ra + 16 * (i + 1)];
                         lo = *(const v4u *)&tile[a_lo + 2048 * (i + 1)];
                         hi = *(const v4u *)&tile[a_hi + 2048 * (i + 1)];
                     }
@@ -369,6 +272,7 @@ SSD_KERNEL_WAVES(512, 2) void fp8_matmul_big_kernel(Fp8Params p)
             } else {
                 sa_before = sa;
             }
+            sched_fence();
             if (u > 0) {
                 const int pi = (u - 1) >> 1, pj = 2 * ((u - 1) & 1);
 #pragma unroll
@@ -381,7 +285,9 @@ SSD_KERNEL_WAVES(512, 2) void fp8_matmul_big_kernel(Fp8Params p)
             }
         }
     };
-    fetch(kb0, tile0, scales0);
+#pragma unroll
+    for (int part = 0; part < 5; ++part)
+        fetch(part, kb0, tile0, scales0);
     int kb = kb0;
     for (; kb + 1 < kb1; kb += 2) {
         step(kb, tile0, scales0, tile1, scales1);

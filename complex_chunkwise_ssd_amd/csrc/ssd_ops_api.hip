@@ -131,27 +131,28 @@ int launch_quantise(const ssd::QuantParams &p, bool whole, bool turn, hipStream_
 }
 
 // Which kernel a product takes, and how the sum over k is split.
-enum { kFp8Few, kFp8Big, kFp8General };
 struct Fp8Plan {
-    int form;
-    int mb;                   // 16 mb rows of a per wave (few, big)
+    bool few;
+    int mb;                   // 16 mb rows of a per wave
     int tiles_m, tiles_n, splits, split_blocks;
-    size_t bytes;
+    size_t part_bytes;        // partial sums
+    size_t a_bytes, b_bytes;  // operands laid out anew (rows that do not start on 16 bytes)
+    size_t bytes() const { return part_bytes + a_bytes + b_bytes; }
 };
 
 int check_fp8(int64_t M, int64_t N, int64_t K, int64_t b_block_rows, int out_dtype)
 {
     if (M < 0 || N < 1 || K < 0 || (b_block_rows != 1 && b_block_rows != 128) || !dtype_ok(out_dtype))
         return SSD_ERR_SHAPE;
-    if (M > (1LL << 30) || N > (1LL << 30) || K > (1LL << 30))
+    if (M > (1LL << 30) || N > (1LL << 30) || K > (1LL << 24) - 16)
         return SSD_ERR_UNSUPPORTED;
     const int64_t tiles = ((M + 127) / 128) * ((N + 127) / 128);
     return tiles > kMaxGrid / 64 ? SSD_ERR_UNSUPPORTED : SSD_OK;
 }
 
-// Time of a product in us by a tile form: every compute unit takes tiles * splits / 256 of them,
-// each its k blocks (per_block us) and a start and end (per_tile us); the parts of a split sum are
-// written and read once more.
+// Time of a product in us by the large form: every compute unit takes tiles * splits / 256 of
+// them, each its k blocks (per_block us) and a start and end (per_tile us); the parts of a split
+// sum are written and read once more.
 double fp8_cost(int64_t M, int64_t N, int64_t tiles, int64_t kb, int splits, double per_block,
                 double per_tile)
 {
@@ -160,32 +161,21 @@ double fp8_cost(int64_t M, int64_t N, int64_t tiles, int64_t kb, int splits, dou
     return rounds * (per_block * (double)((kb + splits - 1) / splits) + per_tile) + parts;
 }
 
-// `vec`: rows of both operands start on 16 bytes and K is a multiple of 16.
-Fp8Plan fp8_plan(int64_t M, int64_t N, int64_t K, int out_dtype, bool vec)
+// `aligned_rows`: rows of both operands start on 16 bytes and K is a multiple of 16.
+Fp8Plan fp8_plan(int64_t M, int64_t N, int64_t K, int out_dtype, bool aligned_rows)
 {
     Fp8Plan p{};
-    const int64_t kb = (K + 127) / 128;
-    p.splits = 1;
-    p.split_blocks = (int)kb;
-    if (M <= 64) {
-        p.form = kFp8Few;
-        p.mb = M <= 16 ? 1 : M <= 32 ? 2 : 4;
-        return p;
-    }
-    double best = 0.;
     const bool wide = out_dtype == SSD_F32;
-    for (int form = 0; form < 2; ++form) {
-        const int mb = vec ? (form == 0 ? 4 : 8) : 0;
-        if (form == 1 && (!vec || wide))
-            break;
-        const int64_t tm = vec ? (M + 32 * mb - 1) / (32 * mb) : (M + 127) / 128;
-        const int64_t tn = vec ? (N + 255) / 256 : (N + 127) / 128;
-        const double per_block = !vec ? (wide ? 3. : 1.5) : mb == 8 ? 1.9 : wide ? 1.9 : 1.1;
+    const int64_t kb = (K + 127) / 128;
+    double best = -1.;
+    for (int mb = 4; mb <= (wide ? 4 : 8); mb += 4) {
+        const int64_t tm = (M + 32 * mb - 1) / (32 * mb), tn = (N + 255) / 256;
+        // measured: 256 x 256 tiles of bfloat16 results, 256 x 128 of float32 and of bfloat16
+        const double per_block = mb == 8 || wide ? 1.85 : 1.1;
         for (int s = 1; s <= 32 && (s == 1 || s * 2 <= kb); ++s) {
             const double cost = fp8_cost(M, N, tm * tn, kb, s, per_block, mb == 8 ? 6. : 3.);
-            if ((form == 0 && s == 1) || cost < best) {
+            if (best < 0. || cost < best) {
                 best = cost;
-                p.form = vec ? kFp8Big : kFp8General;
                 p.mb = mb;
                 p.tiles_m = (int)tm;
                 p.tiles_n = (int)tn;
@@ -194,16 +184,28 @@ Fp8Plan fp8_plan(int64_t M, int64_t N, int64_t K, int out_dtype, bool vec)
         }
     }
     p.splits = kb > 0 ? (int)((kb + p.split_blocks - 1) / p.split_blocks) : 1;
-    p.bytes = p.splits > 1 ? align256((size_t)p.splits * M * N * 4) : 0;
+    if (M <= 64) {
+        // The form for few rows: a wave's time per k block grows with the rows of a it holds, and
+        // 16 rows of b are a workgroup's. With N small and K long the large form's splits win
+        // (64 x 512 x 16384: 38 us against 18.5).
+        const int mb = M <= 16 ? 1 : M <= 32 ? 2 : 4;
+        const int64_t groups = (N + 15) / 16;
+        const int waves = groups < 512 && kb > 8 ? (mb == 1 ? 16 : 8) : 4;
+        const double few = 3 + (double)((groups + 511) / 512) * (double)((kb + waves - 1) / waves) *
+                                   (mb == 1 ? 1.2 : mb == 2 ? 1.4 : 2.2);
+        if (few < best + (aligned_rows ? 6. : 10.)) {
+            p.few = true;
+            p.mb = mb;
+            p.splits = 1;
+            return p;
+        }
+    }
+    p.part_bytes = p.splits > 1 ? align256((size_t)p.splits * M * N * 4) : 0;
+    if (!aligned_rows) {
+        p.a_bytes = align256((size_t)M * ((K + 15) / 16) * 16);
+        p.b_bytes = align256((size_t)N * ((K + 15) / 16) * 16);
+    }
     return p;
-}
-
-// The workspace covers either alignment of the operands.
-size_t fp8_bytes(int64_t M, int64_t N, int64_t K, int out_dtype)
-{
-    const size_t a = fp8_plan(M, N, K, out_dtype, false).bytes;
-    const size_t b = K % 16 == 0 ? fp8_plan(M, N, K, out_dtype, true).bytes : 0;
-    return a > b ? a : b;
 }
 
 template <int MB, bool BROW, int OUT>
@@ -220,8 +222,16 @@ int launch_fp8_few(const ssd::Fp8Params &p, hipStream_t s)
     return launch_status();
 }
 
+int launch_pack(const uint8_t *x, int64_t stride, int64_t rows, int K, uint8_t *out, hipStream_t s)
+{
+    const int64_t n = rows * ((K + 15) / 16);
+    const int64_t blocks = (n + 255) / 256 < 16384 ? (n + 255) / 256 : 16384;
+    hipLaunchKernelGGL(ssd::fp8_pack_kernel, dim3((unsigned)blocks), dim3(256), 0, s, x, stride, rows, K, out);
+    return launch_status();
+}
+
 template <bool BROW, int OUT>
-int launch_fp8(const ssd::Fp8Params &p, const Fp8Plan &plan, hipStream_t s)
+int launch_fp8(ssd::Fp8Params p, const Fp8Plan &plan, bool aligned_rows, char *workspace, hipStream_t s)
 {
     const int64_t n = (int64_t)p.M * p.N;
     const unsigned flat = (unsigned)((n + 255) / 256 < 8192 ? (n + 255) / 256 : 8192);
@@ -229,14 +239,23 @@ int launch_fp8(const ssd::Fp8Params &p, const Fp8Plan &plan, hipStream_t s)
         hipLaunchKernelGGL((ssd::fp8_zero_kernel<OUT>), dim3(flat), dim3(256), 0, s, p);
         return launch_status();
     }
-    if (plan.form == kFp8Few)
+    if (plan.few)
         return plan.mb == 1   ? launch_fp8_few<1, BROW, OUT>(p, s)
                : plan.mb == 2 ? launch_fp8_few<2, BROW, OUT>(p, s)
                               : launch_fp8_few<4, BROW, OUT>(p, s);
+    if (!aligned_rows) {
+        uint8_t *a = (uint8_t *)workspace + plan.part_bytes, *b = a + plan.a_bytes;
+        if (int st = launch_pack(p.a, p.a_stride, p.M, p.K, a, s))
+            return st;
+        if (int st = launch_pack(p.b, p.b_stride, p.N, p.K, b, s))
+            return st;
+        p.a = a;
+        p.b = b;
+        p.K = (p.K + 15) / 16 * 16;  // the same k blocks
+        p.a_stride = p.b_stride = p.K;
+    }
     const dim3 grid((unsigned)((int64_t)p.tiles_m * p.tiles_n * p.splits));
-    if (plan.form == kFp8General)
-        hipLaunchKernelGGL((ssd::fp8_matmul_kernel<4, 4, 2, 2, BROW, OUT>), grid, dim3(256), 0, s, p);
-    else if (OUT == ssd::kBF16 && plan.mb == 8)
+    if (OUT == ssd::kBF16 && plan.mb == 8)
         hipLaunchKernelGGL((ssd::fp8_matmul_big_kernel<8, BROW, ssd::kBF16>), grid, dim3(512), 0, s, p);
     else
         hipLaunchKernelGGL((ssd::fp8_matmul_big_kernel<4, BROW, OUT>), grid, dim3(512), 0, s, p);
@@ -512,11 +531,11 @@ int ssd_fp8_quantise(const void *x, int64_t x_stride, int dtype, int64_t rows, i
 }
 
 size_t ssd_fp8_matmul_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t b_block_rows,
-                                      int out_dtype)
+                                      int out_dtype, int rows_on_16)
 {
-    if (check_fp8(M, N, K, b_block_rows, out_dtype))
+    if (check_fp8(M, N, K, b_block_rows, out_dtype) || M == 0 || K == 0)
         return 0;
-    return fp8_bytes(M, N, K, out_dtype);
+    return fp8_plan(M, N, K, out_dtype, rows_on_16 && K % 16 == 0).bytes();
 }
 
 int ssd_fp8_matmul(const uint8_t *a, int64_t a_stride, const float *a_scale, const uint8_t *b,
@@ -537,10 +556,10 @@ int ssd_fp8_matmul(const uint8_t *a, int64_t a_stride, const float *a_scale, con
     const int e = elem_size(out_dtype);
     if (!aligned(a_scale, 4) || !aligned(b_scale, 4) || !aligned(out, e))
         return SSD_ERR_ALIGN;
-    const bool vec = K % 16 == 0 && aligned(a, 16) && aligned(b, 16) && a_stride % 16 == 0 &&
-                     b_stride % 16 == 0 && a_stride < (1 << 24) && b_stride < (1 << 24);
-    const Fp8Plan plan = fp8_plan(M, N, K, out_dtype, vec);
-    const size_t need = fp8_bytes(M, N, K, out_dtype);
+    const bool rows16 = K % 16 == 0 && aligned(a, 16) && aligned(b, 16) && a_stride % 16 == 0 &&
+                        b_stride % 16 == 0 && a_stride < (1 << 24) && b_stride < (1 << 24);
+    const Fp8Plan plan = fp8_plan(M, N, K, out_dtype, rows16);
+    const size_t need = K > 0 ? plan.bytes() : 0;
     if (need > 0 && (!workspace || workspace_bytes < need))
         return SSD_ERR_WORKSPACE;
     if (need > 0 && !aligned(workspace, 256))
@@ -552,9 +571,9 @@ int ssd_fp8_matmul(const uint8_t *a, int64_t a_stride, const float *a_scale, con
     const int64_t os = span(M, N, out_stride, e);
     for (int j = 0; j < 4; ++j)
         if (overlap_bytes(out, os, in[j].p, in[j].bytes) ||
-            (plan.bytes && overlap_bytes(workspace, (int64_t)plan.bytes, in[j].p, in[j].bytes)))
+            (need && overlap_bytes(workspace, (int64_t)need, in[j].p, in[j].bytes)))
             return SSD_ERR_ALIAS;
-    if (plan.bytes && overlap_bytes(workspace, (int64_t)plan.bytes, out, os))
+    if (need && overlap_bytes(workspace, (int64_t)need, out, os))
         return SSD_ERR_ALIAS;
     ssd::Fp8Params p{};
     p.a = a;
@@ -574,9 +593,10 @@ int ssd_fp8_matmul(const uint8_t *a, int64_t a_stride, const float *a_scale, con
     p.splits = plan.splits;
     p.split_blocks = plan.split_blocks;
     const hipStream_t s = (hipStream_t)stream;
+    char *ws = (char *)workspace;
     if (b_block_rows == 1)
-        return out_dtype == SSD_BF16 ? launch_fp8<true, ssd::kBF16>(p, plan, s) : launch_fp8<true, ssd::kF32>(p, plan, s);
-    return out_dtype == SSD_BF16 ? launch_fp8<false, ssd::kBF16>(p, plan, s) : launch_fp8<false, ssd::kF32>(p, plan, s);
+        return out_dtype == SSD_BF16 ? launch_fp8<true, ssd::kBF16>(p, plan, rows16, ws, s) : launch_fp8<true, ssd::kF32>(p, plan, rows16, ws, s);
+    return out_dtype == SSD_BF16 ? launch_fp8<false, ssd::kBF16>(p, plan, rows16, ws, s) : launch_fp8<false, ssd::kF32>(p, plan, rows16, ws, s);
 }
 
 size_t ssd_gated_scan_workspace_bytes(int64_t batch, int64_t T, int64_t C, int dtype)

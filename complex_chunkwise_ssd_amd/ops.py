@@ -46,7 +46,7 @@ def declare(lib):
     entry("ssd_rms_norm_backward", i32, vp, i64, vp, vp, vp, i64, vp, i64, i32, i64, i64, vp, vp, vp,
           size, vp)
     entry("ssd_fp8_quantise", i32, vp, i64, i32, i64, i64, i64, i32, vp, i64, vp, vp)
-    entry("ssd_fp8_matmul_workspace_bytes", size, i64, i64, i64, i64, i32)
+    entry("ssd_fp8_matmul_workspace_bytes", size, i64, i64, i64, i64, i32, i32)
     entry("ssd_fp8_matmul", i32, vp, i64, vp, vp, i64, vp, i64, i64, i64, i64, i32, vp, i64, vp, size,
           vp)
 
@@ -330,6 +330,19 @@ def fp8_quantise(x, block_rows: int = 1, transpose: bool = False, q=None, scale=
     return q, scale
 
 
+def fp8_matmul_workspace_bytes(M, N, K, block_rows=128, out_dtype=torch.bfloat16, rows_on_16=True) -> int:
+    return int(_entry("ssd_fp8_matmul_workspace_bytes")(M, N, K, int(block_rows), _DTYPES[out_dtype], int(rows_on_16)))
+
+
+def gated_scan_workspace_bytes(B, T, C, dtype, backward=False) -> int:
+    name = "ssd_gated_scan_backward_workspace_bytes" if backward else "ssd_gated_scan_workspace_bytes"
+    return int(_entry(name)(B, T, C, _DTYPES[dtype]))
+
+
+def rms_norm_backward_workspace_bytes(rows, F) -> int:
+    return int(_entry("ssd_rms_norm_backward_workspace_bytes")(rows, F))
+
+
 def fp8_matmul(a, a_scale, b, b_scale, block_rows: int = 128, out_dtype=torch.bfloat16, out=None,
                workspace=None):
     """out[..., n] = sum over k of (a a_scale)[..., k] (b b_scale)[n, k], both operands 8-bit with a
@@ -355,7 +368,9 @@ def fp8_matmul(a, a_scale, b, b_scale, block_rows: int = 128, out_dtype=torch.bf
         out = torch.empty(shape, dtype=out_dtype, device=dev)
     so = _row_stride(out, "out", out_dtype, shape, dev)
     dt = _DTYPES[out_dtype]
-    ws, size = _workspace(workspace, _entry("ssd_fp8_matmul_workspace_bytes")(M, N, K, int(block_rows), dt), dev)
-    _call("ssd_fp8_matmul", dev, _ptr(a), sa, _ptr(a_scale), _ptr(b), sb, _ptr(b_scale), M, N, K,
+    pa, pb = a.data_ptr(), b.data_ptr()
+    on16 = int((pa | pb | sa | sb) % 16 == 0 and sa < 1 << 24 and sb < 1 << 24)
+    ws, size = _workspace(workspace, fp8_matmul_workspace_bytes(M, N, K, block_rows, out_dtype, on16), dev)
+    _call("ssd_fp8_matmul", dev, pa, sa, _ptr(a_scale), pb, sb, _ptr(b_scale), M, N, K,
           int(block_rows), dt, _ptr(out), so, _ptr(ws), size)
     return out

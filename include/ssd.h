@@ -519,17 +519,22 @@ int ssd_fp8_quantise(const void *x, int64_t x_stride, int dtype, int64_t rows, i
  *                between the rows are not written.
  *   workspace    ssd_fp8_matmul_workspace_bytes(...) bytes, 256-byte aligned (NULL
  *                allowed when that is 0): partial sums where few outputs and a long K
- *                have the sum over k split; they are added in a fixed order.
+ *                have the sum over k split (they are added in a fixed order), and the
+ *                operands laid out anew where their rows do not start on 16 bytes.
+ *                rows_on_16: whether they do, that is a, b, a_stride and b_stride are
+ *                multiples of 16 and the strides below 2^24.
  * With y = x W^T: forward a = x, b = W (blocks of 128 x 128); grad_x takes a = grad_y and
  * b = W quantised with transpose; grad_W takes a = grad_y and b = x, both quantised with
  * transpose in blocks of 1 x 128.
- * Products and sums are float32, rounded once to out_dtype. M equal to 0 is a no-op; K
- * equal to 0 writes zeros. No output may overlap an input (SSD_ERR_ALIAS).
+ * Sums are float32, rounded once to out_dtype; for a bfloat16 result the sum inside a block
+ * is the 8-bit matrix instruction's, which holds each eight neighbouring products to 2^-13
+ * of the largest of them. M equal to 0 is a no-op; K equal to 0 writes zeros. K below 2^24
+ * (SSD_ERR_UNSUPPORTED). No output may overlap an input (SSD_ERR_ALIAS).
  * Alignment: 4 bytes for the scales, the element size for out; rows of a and b that start
  * on 16 bytes are read fastest.
  */
 size_t ssd_fp8_matmul_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t b_block_rows,
-                                      int out_dtype);
+                                      int out_dtype, int rows_on_16);
 
 int ssd_fp8_matmul(const uint8_t *a, int64_t a_stride, const float *a_scale, const uint8_t *b,
                    int64_t b_stride, const float *b_scale, int64_t M, int64_t N, int64_t K,

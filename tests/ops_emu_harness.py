@@ -210,7 +210,8 @@ def matmul(lib, a, sa, b, sb, block_rows, out, a_pad=0, b_pad=0, out_pad=0, alig
     SA, SB = put(sa, "f32"), put(sb, "f32")
     e = SIZE[out]
     O = Guarded(((M - 1) * (N + out_pad) + N) * e, e)
-    n = lib.ssd_fp8_matmul_workspace_bytes(M, N, K, block_rows, KIND[out])
+    on16 = int((A.at | B.at | (K + a_pad) | (K + b_pad)) % 16 == 0)
+    n = lib.ssd_fp8_matmul_workspace_bytes(M, N, K, block_rows, KIND[out], on16)
     ws = space(n)
     rc = lib.ssd_fp8_matmul(p(A), K + a_pad, p(SA), p(B), K + b_pad, p(SB), M, N, K, block_rows, KIND[out],
                             p(O), N + out_pad, p(ws), n, None)

@@ -152,13 +152,19 @@ def test_fp8_matmul_refusals(lib):
         assert _mm(lib, out=_at(b)) == ssd.SSD_ERR_ALIAS, b
     assert _mm(lib, as_=1 << 60) == ssd.SSD_ERR_UNSUPPORTED
     assert _mm(lib, M=0, a=None, out=None) == ssd.SSD_OK
-    need = lib.ssd_fp8_matmul_workspace_bytes(512, 512, 1 << 16, 1, 0)
-    assert need > 0 and lib.ssd_fp8_matmul_workspace_bytes(512, 512, 1 << 16, 3, 0) == 0
+    need = lib.ssd_fp8_matmul_workspace_bytes(512, 512, 1 << 16, 1, 0, 1)
+    assert need > 0 and lib.ssd_fp8_matmul_workspace_bytes(512, 512, 1 << 16, 3, 0, 1) == 0
     long = dict(M=512, N=512, K=1 << 16, as_=1 << 16, bs=1 << 16, os=512, br=1, dt=0)
     assert _mm(lib, **long) == ssd.SSD_ERR_WORKSPACE
     assert _mm(lib, ws=_at(9), wn=need - 1, **long) == ssd.SSD_ERR_WORKSPACE
     assert _mm(lib, ws=_at(9, 8), wn=need, **long) == ssd.SSD_ERR_ALIGN
     assert _mm(lib, ws=_at(0), wn=need, **long) == ssd.SSD_ERR_ALIAS
+    # rows that do not start on 16 bytes are laid out anew: more workspace
+    more = lib.ssd_fp8_matmul_workspace_bytes(512, 512, 1 << 16, 1, 0, 0)
+    assert more >= need + 2 * 512 * (1 << 16)
+    assert _mm(lib, ws=_at(9), wn=need, **{**long, "as_": (1 << 16) + 1}) == ssd.SSD_ERR_WORKSPACE
+    assert _mm(lib, ws=_at(9), wn=need, a=_at(0, 1), **long) == ssd.SSD_ERR_WORKSPACE
+    assert _mm(lib, K=1 << 24, as_=1 << 24, bs=1 << 24) == ssd.SSD_ERR_UNSUPPORTED
 
 
 def test_python_layer_rejects_bad_tensors():
