@@ -149,7 +149,8 @@ template <int CH>
 struct GatedPlace {
     int64_t b;
     int seg, c0, n;           // first channel and how many of CH exist (maybe none)
-    int t0, t1, len;          // the segment's tokens; the sequence's length
+    int t0, t1, lim;          // the segment's tokens; the first of them that is padding (or t1)
+    bool full;                // every lane of the block has all CH channels
 };
 template <int CH>
 SSD_DEVICE GatedPlace<CH> gated_place(const GatedParams &p)
@@ -167,12 +168,45 @@ SSD_DEVICE GatedPlace<CH> gated_place(const GatedParams &p)
         g.c0 = 0;
     g.t0 = g.seg * p.seg_tokens;
     g.t1 = g.t0 + p.seg_tokens < p.T ? g.t0 + p.seg_tokens : p.T;
-    g.len = p.T;
+    g.lim = g.t1;
     if (p.lengths) {
-        const int len = p.lengths[g.b];
-        g.len = len < 0 ? 0 : (len < p.T ? len : p.T);
+        const int len = uniform_i(p.lengths[g.b]);
+        g.lim = len < g.t1 ? len : g.t1;
     }
+    g.full = (blk + 1) * 64 * CH <= p.C;
     return g;
+}
+
+// One token's channels of this lane. A token that is padding or past the segment reads the last
+// one that is not (the segment's first, if none is): its values are replaced afterwards.
+template <int T, int CH>
+SSD_DEVICE GatedRaw<T, CH> gated_read(const void *p, int64_t stride, const GatedParams &q,
+                                      const GatedPlace<CH> &g, int t)
+{
+    t = t < g.lim ? t : g.lim - 1;
+    t = t > g.t0 ? t : g.t0;
+    const char *row = (const char *)p + (g.b * q.T + t) * stride * ElemSize<T>::value;
+    const uint32_t off = (uint32_t)g.c0 * ElemSize<T>::value;
+    if (g.full) {
+        GatedRaw<T, CH> r;
+        if (T == kBF16 && CH == 1)
+            r.w[0] = *(const uint16_t *)(row + off);
+        else
+            __builtin_memcpy(&r, row + off, sizeof(r));
+        return r;
+    }
+    return gated_load<T, CH>(row + off, g.n);
+}
+template <int T, int CH>
+SSD_DEVICE void gated_write(void *p, const GatedParams &q, const GatedPlace<CH> &g, int t,
+                            const float (&v)[CH])
+{
+    char *row = (char *)p + (g.b * q.T + t) * q.C * ElemSize<T>::value;
+    const uint32_t off = (uint32_t)g.c0 * ElemSize<T>::value;
+    if (g.full)
+        gated_store<T, CH>(row + off, CH, v);
+    else
+        gated_store<T, CH>(row + off, g.n, v);
 }
 
 // SUMMARY: only the segment's (A, U) is wanted, for all but the last segment; the last one's
@@ -181,7 +215,6 @@ SSD_DEVICE GatedPlace<CH> gated_place(const GatedParams &p)
 template <int T, int CH, int WAVES, int STEPS, bool SUMMARY>
 SSD_KERNEL(64 * WAVES) void gated_scan_kernel(GatedParams p)
 {
-    constexpr int E = ElemSize<T>::value;
     constexpr int TILE = WAVES * STEPS;
     SSD_LDS float pairs[2][WAVES][2][64 * CH];
     const int lane = thread_id() & 63;
@@ -214,34 +247,44 @@ SSD_KERNEL(64 * WAVES) void gated_scan_kernel(GatedParams p)
                 }
     }
     GatedRaw<T, CH> rx[STEPS], ri[STEPS], rr[STEPS];
-    auto fetch = [&](int t) {  // this wave's tokens from t on; those past the length stay unread
+    auto fetch = [&](int t) {  // this wave's tokens from t on
 #pragma unroll
         for (int k = 0; k < STEPS; ++k) {
-            const int n = t + k < g.t1 && t + k < g.len ? g.n : 0;
-            const int64_t row = n > 0 ? g.b * p.T + t + k : 0;
-            rx[k] = gated_load<T, CH>((const char *)p.x + (row * p.x_stride + g.c0) * E, n);
-            ri[k] = gated_load<T, CH>((const char *)p.gi + (row * p.gi_stride + g.c0) * E, n);
-            rr[k] = gated_load<T, CH>((const char *)p.gr + (row * p.gr_stride + g.c0) * E, n);
+            rx[k] = gated_read<T, CH>(p.x, p.x_stride, p, g, t + k);
+            ri[k] = gated_read<T, CH>(p.gi, p.gi_stride, p, g, t + k);
+            rr[k] = gated_read<T, CH>(p.gr, p.gr_stride, p, g, t + k);
         }
     };
     fetch(g.t0 + wave * STEPS);
     int parity = 0;
     for (int tile = g.t0; tile < g.t1; tile += TILE, parity ^= 1) {
         const int t = tile + wave * STEPS;
+        const bool whole = t + STEPS <= g.lim;
         float a[STEPS][CH], u[STEPS][CH], A[CH], U[CH];
 #pragma unroll
-        for (int c = 0; c < CH; ++c) {
-            A[c] = 1.f;
-            U[c] = 0.f;
-        }
-#pragma unroll
-        for (int k = 0; k < STEPS; ++k) {
-            const bool in = t + k < g.t1 && t + k < g.len;
+        for (int k = 0; k < STEPS; ++k)
 #pragma unroll
             for (int c = 0; c < CH; ++c) {
                 const Gates q = gates(gated_value<T, CH>(ri[k], c), gated_value<T, CH>(rr[k], c), nk[c]);
-                a[k][c] = in ? q.a : 1.f;
-                u[k][c] = in ? q.m * q.i * gated_value<T, CH>(rx[k], c) : 0.f;
+                a[k][c] = q.a;
+                u[k][c] = q.m * q.i * gated_value<T, CH>(rx[k], c);
+            }
+        if (!whole) {  // padding and what lies past the segment: a step that changes nothing
+#pragma unroll
+            for (int k = 0; k < STEPS; ++k)
+                if (t + k >= g.lim)
+#pragma unroll
+                    for (int c = 0; c < CH; ++c) {
+                        a[k][c] = 1.f;
+                        u[k][c] = 0.f;
+                    }
+        }
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            A[c] = a[0][c];
+            U[c] = u[0][c];
+#pragma unroll
+            for (int k = 1; k < STEPS; ++k) {
                 A[c] *= a[k][c];
                 U[c] = a[k][c] * U[c] + u[k][c];
             }
@@ -278,10 +321,10 @@ SSD_KERNEL(64 * WAVES) void gated_scan_kernel(GatedParams p)
 #pragma unroll
                 for (int c = 0; c < CH; ++c) {
                     mine[c] = a[k][c] * mine[c] + u[k][c];
-                    out[c] = t + k < g.len ? mine[c] : 0.f;
+                    out[c] = whole || t + k < g.lim ? mine[c] : 0.f;
                 }
-                if (t + k < g.t1)
-                    gated_store<T, CH>((char *)p.h + ((g.b * p.T + t + k) * p.C + g.c0) * E, g.n, out);
+                if (whole || t + k < g.t1)
+                    gated_write<T, CH>(p.h, p, g, t + k, out);
             }
         }
     }
@@ -334,7 +377,6 @@ SSD_KERNEL(64) void gated_step_kernel(GatedParams p)
 template <int T, int CH, int WAVES, int STEPS>
 SSD_KERNEL(64 * WAVES) void gated_bwd_summary_kernel(GatedParams p)
 {
-    constexpr int E = ElemSize<T>::value;
     constexpr int TILE = WAVES * STEPS;
     SSD_LDS float pairs[2][WAVES][2][64 * CH];
     const int lane = thread_id() & 63;
@@ -351,10 +393,8 @@ SSD_KERNEL(64 * WAVES) void gated_bwd_summary_kernel(GatedParams p)
     auto fetch = [&](int t) {
 #pragma unroll
         for (int k = 0; k < STEPS; ++k) {
-            const int n = t + k < g.t1 && t + k < g.len ? g.n : 0;
-            const int64_t row = n > 0 ? g.b * p.T + t + k : 0;
-            rr[k] = gated_load<T, CH>((const char *)p.gr + (row * p.gr_stride + g.c0) * E, n);
-            rh[k] = gated_load<T, CH>((const char *)p.gh + (row * p.C + g.c0) * E, n);
+            rr[k] = gated_read<T, CH>(p.gr, p.gr_stride, p, g, t + k);
+            rh[k] = gated_read<T, CH>(p.gh, p.C, p, g, t + k);
         }
     };
     const int tiles = (g.t1 - g.t0 + TILE - 1) / TILE;
@@ -370,12 +410,12 @@ SSD_KERNEL(64 * WAVES) void gated_bwd_summary_kernel(GatedParams p)
         }
 #pragma unroll
         for (int k = STEPS - 1; k >= 0; --k) {
-            const bool in = t + k < g.t1 && t + k < g.len;
+            const bool in = t + k < g.lim;
 #pragma unroll
             for (int c = 0; c < CH; ++c) {
                 const float a = in ? hw_exp2(kLog2e * (nk[c] * sigmoid(gated_value<T, CH>(rr[k], c)))) : 1.f;
                 A[c] *= a;
-                V[c] = a * (V[c] + gated_value<T, CH>(rh[k], c));
+                V[c] = a * (V[c] + (in ? gated_value<T, CH>(rh[k], c) : 0.f));
             }
         }
         if (i > 0)
@@ -412,7 +452,6 @@ SSD_KERNEL(64 * WAVES) void gated_bwd_summary_kernel(GatedParams p)
 template <int T, int CH>
 SSD_KERNEL(1024) void gated_scan_bwd_kernel(GatedParams p)
 {
-    constexpr int E = ElemSize<T>::value;
     constexpr int WAVES = 16, STEPS = 4;
     static_assert(WAVES * STEPS == kGatedChunk, "a tile is a chunk");
     SSD_LDS float pairs[2][WAVES][3][64 * CH];
@@ -439,12 +478,10 @@ SSD_KERNEL(1024) void gated_scan_bwd_kernel(GatedParams p)
     auto fetch = [&](int t) {
 #pragma unroll
         for (int k = 0; k < STEPS; ++k) {
-            const int n = t + k < g.t1 && t + k < g.len ? g.n : 0;
-            const int64_t row = n > 0 ? g.b * p.T + t + k : 0;
-            rx[k] = gated_load<T, CH>((const char *)p.x + (row * p.x_stride + g.c0) * E, n);
-            ri[k] = gated_load<T, CH>((const char *)p.gi + (row * p.gi_stride + g.c0) * E, n);
-            rr[k] = gated_load<T, CH>((const char *)p.gr + (row * p.gr_stride + g.c0) * E, n);
-            rh[k] = gated_load<T, CH>((const char *)p.gh + (row * p.C + g.c0) * E, n);
+            rx[k] = gated_read<T, CH>(p.x, p.x_stride, p, g, t + k);
+            ri[k] = gated_read<T, CH>(p.gi, p.gi_stride, p, g, t + k);
+            rr[k] = gated_read<T, CH>(p.gr, p.gr_stride, p, g, t + k);
+            rh[k] = gated_read<T, CH>(p.gh, p.C, p, g, t + k);
         }
     };
     auto fetch_state = [&](int tile) {
@@ -458,37 +495,52 @@ SSD_KERNEL(1024) void gated_scan_bwd_kernel(GatedParams p)
     int parity = 0;
     for (int tile = last; tile >= g.t0; tile -= kGatedChunk, parity ^= 1) {
         const int t = tile + wave * STEPS;
-        Gates q[STEPS][CH];
-        float x[STEPS][CH], gh[STEPS][CH], before[CH];
-        float A[CH], U[CH], V[CH];
-#pragma unroll
-        for (int c = 0; c < CH; ++c) {
-            A[c] = 1.f;
-            U[c] = V[c] = 0.f;
-            before[c] = enter[c];
-        }
+        // i, r, a, m of each value; x and gh stay as they were loaded, l is nk r again
+        float vi[STEPS][CH], vr[STEPS][CH], va[STEPS][CH], vm[STEPS][CH];
+        GatedRaw<T, CH> x[STEPS], gh[STEPS];
+        float before[CH], A[CH], U[CH], V[CH];
+        const bool whole = t + STEPS <= g.lim;
 #pragma unroll
         for (int k = 0; k < STEPS; ++k) {
-            const bool in = t + k < g.t1 && t + k < g.len;
+            x[k] = rx[k];
+            gh[k] = rh[k];
 #pragma unroll
             for (int c = 0; c < CH; ++c) {
-                x[k][c] = gated_value<T, CH>(rx[k], c);
-                gh[k][c] = gated_value<T, CH>(rh[k], c);
-                q[k][c] = gates(gated_value<T, CH>(ri[k], c), gated_value<T, CH>(rr[k], c), nk[c]);
-                if (!in) {
-                    q[k][c].a = 1.f;
-                    q[k][c].m = 0.f;
-                    q[k][c].l = 0.f;
-                }
-                A[c] *= q[k][c].a;
-                U[c] = q[k][c].a * U[c] + q[k][c].m * q[k][c].i * x[k][c];
+                const Gates q = gates(gated_value<T, CH>(ri[k], c), gated_value<T, CH>(rr[k], c), nk[c]);
+                vi[k][c] = q.i;
+                vr[k][c] = q.r;
+                va[k][c] = q.a;
+                vm[k][c] = q.m;
             }
         }
+        if (!whole) {  // padding and what lies past the segment: nothing goes in, a = 1, l = m = 0
 #pragma unroll
-        for (int k = STEPS - 1; k >= 0; --k)
+            for (int k = 0; k < STEPS; ++k)
+                if (t + k >= g.lim) {
+                    x[k] = GatedRaw<T, CH>{};
+                    gh[k] = GatedRaw<T, CH>{};
 #pragma unroll
-            for (int c = 0; c < CH; ++c)
-                V[c] = q[k][c].a * (V[c] + gh[k][c]);
+                    for (int c = 0; c < CH; ++c) {
+                        vi[k][c] = vr[k][c] = vm[k][c] = 0.f;
+                        va[k][c] = 1.f;
+                    }
+                }
+        }
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            before[c] = enter[c];
+            A[c] = va[0][c];
+            U[c] = vm[0][c] * vi[0][c] * gated_value<T, CH>(x[0], c);
+            V[c] = 0.f;
+#pragma unroll
+            for (int k = 1; k < STEPS; ++k) {
+                A[c] *= va[k][c];
+                U[c] = va[k][c] * U[c] + vm[k][c] * vi[k][c] * gated_value<T, CH>(x[k], c);
+            }
+#pragma unroll
+            for (int k = STEPS - 1; k >= 0; --k)
+                V[c] = va[k][c] * (V[c] + gated_value<T, CH>(gh[k], c));
+        }
         if (tile - kGatedChunk >= g.t0) {
             fetch(t - kGatedChunk);
             fetch_state(tile - kGatedChunk);
@@ -519,31 +571,36 @@ SSD_KERNEL(1024) void gated_scan_bwd_kernel(GatedParams p)
 #pragma unroll
             for (int c = 0; c < CH; ++c) {
                 hb[k][c] = before[c];
-                before[c] = q[k][c].a * before[c] + q[k][c].m * q[k][c].i * x[k][c];
+                before[c] = va[k][c] * before[c] + vm[k][c] * vi[k][c] * gated_value<T, CH>(x[k], c);
             }
 #pragma unroll
         for (int k = STEPS - 1; k >= 0; --k) {
-            const bool in = t + k < g.t1 && t + k < g.len;
             float gx[CH], ggi[CH], ggr[CH];
 #pragma unroll
             for (int c = 0; c < CH; ++c) {
-                const Gates &v = q[k][c];
-                const float gt = gh[k][c] + right[c];
-                right[c] = v.a * gt;
-                const float ratio = v.m > 0.f ? v.l * hw_rcp(v.m) : 0.f;
-                const float gi = gt * v.i;
-                const float e = v.a * (gt * hb[k][c] * v.l - gi * x[k][c] * v.a * ratio);
-                gx[c] = in ? gi * v.m : 0.f;
-                ggi[c] = gx[c] * x[k][c] * (1.f - v.i);
-                ggr[c] = in ? e * (1.f - v.r) : 0.f;
-                sum_e[c] += in ? e : 0.f;
+                const float a = va[k][c], m = vm[k][c], i = vi[k][c], r = vr[k][c];
+                const float l = nk[c] * r, xv = gated_value<T, CH>(x[k], c);
+                const float gt = gated_value<T, CH>(gh[k], c) + right[c];
+                right[c] = a * gt;
+                const float ratio = m > 0.f ? l * hw_rcp(m) : 0.f;
+                const float gi = gt * i;
+                const float e = right[c] * (hb[k][c] * l) - gi * xv * (a * a * ratio);
+                gx[c] = gi * m;
+                ggi[c] = gx[c] * xv * (1.f - i);
+                ggr[c] = e * (1.f - r);
+                sum_e[c] += e;
             }
-            if (t + k < g.t1) {
-                const int64_t at = ((g.b * p.T + t + k) * p.C + g.c0) * E;
-                gated_store<T, CH>((char *)p.gx + at, g.n, gx);
-                gated_store<T, CH>((char *)p.ggi + at, g.n, ggi);
-                gated_store<T, CH>((char *)p.ggr + at, g.n, ggr);
+            if (!whole) {
+                if (t + k >= g.t1)
+                    continue;
+                if (t + k >= g.lim)  // padding, whatever adjoint passes over it
+#pragma unroll
+                    for (int c = 0; c < CH; ++c)
+                        gx[c] = ggi[c] = ggr[c] = 0.f;
             }
+            gated_write<T, CH>(p.gx, p, g, t + k, gx);
+            gated_write<T, CH>(p.ggi, p, g, t + k, ggi);
+            gated_write<T, CH>(p.ggr, p, g, t + k, ggr);
         }
     }
     // sum over the waves, in wave order (the slot that the last tile did not use)
