@@ -1,4 +1,5 @@
-"""Compiles the gfx950 scan library (libssd.so) in place with hipcc.
+"""Compiles the gfx950 library (libssd.so, hipcc) and the compiled part of the Python
+binding (_binding.so, the C++ compiler against torch's headers) in place.
 
     python -m complex_chunkwise_ssd_amd.build
 """
@@ -12,6 +13,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libssd.so")
+BINDING = os.path.join(PKG, "_binding.so")
 ARCH = "gfx950"
 SOURCES = ("ssd_api.hip", "ssd_ops_api.hip")
 
@@ -21,21 +23,43 @@ def hipcc_command(out: str, extra=()):
         "hipcc", "--offload-arch=" + ARCH, "-O3", "-std=c++17", "-fPIC", "-shared",
         # keep hipcc from forming packed fp32 instructions on its own
         "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
-        "-I" + INCLUDE, "-I" + CSRC, *extra,
+        "-Wl,-soname,libssd.so", "-I" + INCLUDE, "-I" + CSRC, *extra,
         *(os.path.join(CSRC, f) for f in SOURCES), "-o", out,
     ]
 
 
-def build(verbose: bool = False, extra=()) -> str:
-    tmp = LIB + ".tmp%d" % os.getpid()
-    cmd = hipcc_command(tmp, extra)
+def binding_command(out: str):
+    import sysconfig
+
+    import torch
+    torch_dir = os.path.dirname(torch.__file__)
+    include = os.path.join(torch_dir, "include")
+    return [
+        "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-D__HIP_PLATFORM_AMD__=1",
+        "-DTORCH_API_INCLUDE_EXTENSION_H", "-DTORCH_EXTENSION_NAME=_binding", "-w",
+        "-I" + INCLUDE, "-I" + include, "-I" + os.path.join(include, "torch", "csrc", "api", "include"),
+        "-I/opt/rocm/include", "-I" + sysconfig.get_paths()["include"],
+        os.path.join(CSRC, "ssd_ops_binding.cpp"), "-o", out,
+        LIB, "-L" + os.path.join(torch_dir, "lib"), "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch",
+        "-ltorch_python", "-Wl,-rpath,$ORIGIN",
+    ]
+
+
+def _compile(cmd, out: str, tmp: str, verbose: bool):
     if verbose:
         print(" ".join(cmd), flush=True)
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         sys.stderr.write(res.stdout + res.stderr)
-        raise RuntimeError("hipcc failed for libssd.so")
-    os.replace(tmp, LIB)
+        raise RuntimeError("%s failed for %s" % (cmd[0], os.path.basename(out)))
+    os.replace(tmp, out)
+
+
+def build(verbose: bool = False, extra=()) -> str:
+    tmp = LIB + ".tmp%d" % os.getpid()
+    _compile(hipcc_command(tmp, extra), LIB, tmp, verbose)
+    tmp = BINDING + ".tmp%d" % os.getpid()
+    _compile(binding_command(tmp), BINDING, tmp, verbose)
     return LIB
 
 

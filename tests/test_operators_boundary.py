@@ -184,11 +184,7 @@ def test_python_layer_rejects_bad_tensors():
 
 
 def test_row_strides():
-    from complex_chunkwise_ssd_amd.ops import _row_stride
-    cpu = torch.device("cpu")
-
-    def stride(t):
-        return _row_stride(t, "t", t.dtype, t.shape, cpu)
+    stride = ssd.ops._binding().row_stride
     whole = torch.zeros(3, 5, 24)
     assert stride(whole) == 24 and stride(whole[..., 8:16]) == 24
     assert stride(whole[:, :1, 8:16]) == 120 and stride(whole[:1, :, 8:16]) == 24
