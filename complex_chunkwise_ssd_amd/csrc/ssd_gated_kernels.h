@@ -56,27 +56,13 @@ struct GatedRaw {
 };
 
 template <int T, int CH>
-SSD_DEVICE GatedRaw<T, CH> gated_load(const void *p, int n)
+SSD_DEVICE GatedRaw<T, CH> gated_load(const void *p)
 {
     GatedRaw<T, CH> r;
-    if (T == kF32) {
-        if (n >= CH) {
-            __builtin_memcpy(&r, p, 4 * CH);
-        } else {
-#pragma unroll
-            for (int c = 0; c < CH; ++c) {
-                r.w[T == kF32 ? c : 0] = 0u;
-                if (c < n)
-                    __builtin_memcpy(&r.w[T == kF32 ? c : 0], (const char *)p + 4 * c, 4);
-            }
-        }
-    } else {
-        r.w[0] = 0u;
-        if (CH == 2 && n >= 2)
-            __builtin_memcpy(&r, p, 4);
-        else if (n > 0)
-            r.w[0] = *(const uint16_t *)p;
-    }
+    if (T == kBF16 && CH == 1)
+        r.w[0] = *(const uint16_t *)p;
+    else
+        __builtin_memcpy(&r, p, sizeof(r));
     return r;
 }
 
@@ -89,20 +75,14 @@ SSD_DEVICE float gated_value(const GatedRaw<T, CH> &r, int c)
 }
 
 template <int T, int CH>
-SSD_DEVICE void gated_store(void *p, int n, const float (&v)[CH])
+SSD_DEVICE void gated_store(void *p, const float (&v)[CH])
 {
     if (T == kF32) {
-#pragma unroll
-        for (int c = 0; c < CH; ++c)
-            if (c < n)
-                ((float *)p)[c] = v[c];
+        __builtin_memcpy(p, v, 4 * CH);
     } else if (CH == 2) {
         const uint32_t u = cvt_pk_bf16(v[0], v[CH - 1]);
-        if (n >= 2)
-            __builtin_memcpy(p, &u, 4);
-        else if (n > 0)
-            *(uint16_t *)p = (uint16_t)u;
-    } else if (n > 0) {
+        __builtin_memcpy(p, &u, 4);
+    } else {
         *(uint16_t *)p = cvt_bf16(v[0]);
     }
 }
@@ -116,20 +96,11 @@ SSD_DEVICE float softplus(float v)
     return fmaxf(v, 0.f) + log1pf(expf(-fabsf(v)));
 }
 
-// 1 - exp(-z) for z >= 0: below 1/4 its series (the first term left out is z^6 / 5040 of it,
-// 5e-8), above it the difference, which loses at most two bits there. `e` is exp(-z).
-SSD_DEVICE float one_minus_exp(float z, float e)
-{
-    float s = -1.f / 720.f;
-    s = s * z + 1.f / 120.f;
-    s = s * z - 1.f / 24.f;
-    s = s * z + 1.f / 6.f;
-    s = s * z - 0.5f;
-    s = s * z + 1.f;
-    return z < 0.25f ? s * z : 1.f - e;
-}
-
-// The gates of one value. nk = -k softplus(lam).
+// The gates of one value. nk = -k softplus(lam). Near a = 1 the recurrence remembers 1 / (1 - a)
+// steps, and an error of the exponential would add up over them: with w = -l below 1/4,
+// 1 - exp(-w) comes from its series (the first term left out is w^6 / 5040 of it, 5e-8) and a is
+// one minus that, right to half a unit; above, 1 - a loses at most three bits. 1 - a^2 is (1 - a)
+// (1 + a) in either case.
 struct Gates {
     float i, r, l, a, m;
 };
@@ -139,8 +110,19 @@ SSD_DEVICE Gates gates(float gi, float gr, float nk)
     g.i = sigmoid(gi);
     g.r = sigmoid(gr);
     g.l = nk * g.r;
-    g.a = hw_exp2(kLog2e * g.l);
-    g.m = hw_sqrt(one_minus_exp(-2.f * g.l, g.a * g.a));
+    const float w = -g.l;
+    float s = -1.f / 720.f;
+    s = s * w + 1.f / 120.f;
+    s = s * w - 1.f / 24.f;
+    s = s * w + 1.f / 6.f;
+    s = s * w - 0.5f;
+    s = s * w + 1.f;
+    s = s * w;
+    const float e = hw_exp2(kLog2e * g.l);
+    const bool near = w < 0.25f;
+    const float rest = near ? s : 1.f - e;
+    g.a = near ? 1.f - s : e;
+    g.m = hw_sqrt(rest * (1.f + g.a));
     return g;
 }
 
@@ -148,9 +130,9 @@ SSD_DEVICE Gates gates(float gi, float gr, float nk)
 template <int CH>
 struct GatedPlace {
     int64_t b;
-    int seg, c0, n;           // first channel and how many of CH exist (maybe none)
+    int seg, c0;              // first channel; a lane past the last channel reads channel 0
+    bool live;                // whether the lane has channels: all CH of them (C is a multiple of CH)
     int t0, t1, lim;          // the segment's tokens; the first of them that is padding (or t1)
-    bool full;                // every lane of the block has all CH channels
 };
 template <int CH>
 SSD_DEVICE GatedPlace<CH> gated_place(const GatedParams &p)
@@ -162,10 +144,8 @@ SSD_DEVICE GatedPlace<CH> gated_place(const GatedParams &p)
     g.b = rest / p.launched;
     g.seg = (int)(rest - g.b * p.launched) + p.seg_first;
     g.c0 = blk * 64 * CH + (thread_id() & 63) * CH;
-    g.n = p.C - g.c0;
-    g.n = g.n < 0 ? 0 : (g.n > CH ? CH : g.n);
-    if (g.n == 0)
-        g.c0 = 0;
+    g.live = g.c0 < p.C;
+    g.c0 = g.live ? g.c0 : 0;
     g.t0 = g.seg * p.seg_tokens;
     g.t1 = g.t0 + p.seg_tokens < p.T ? g.t0 + p.seg_tokens : p.T;
     g.lim = g.t1;
@@ -173,7 +153,6 @@ SSD_DEVICE GatedPlace<CH> gated_place(const GatedParams &p)
         const int len = uniform_i(p.lengths[g.b]);
         g.lim = len < g.t1 ? len : g.t1;
     }
-    g.full = (blk + 1) * 64 * CH <= p.C;
     return g;
 }
 
@@ -186,27 +165,15 @@ SSD_DEVICE GatedRaw<T, CH> gated_read(const void *p, int64_t stride, const Gated
     t = t < g.lim ? t : g.lim - 1;
     t = t > g.t0 ? t : g.t0;
     const char *row = (const char *)p + (g.b * q.T + t) * stride * ElemSize<T>::value;
-    const uint32_t off = (uint32_t)g.c0 * ElemSize<T>::value;
-    if (g.full) {
-        GatedRaw<T, CH> r;
-        if (T == kBF16 && CH == 1)
-            r.w[0] = *(const uint16_t *)(row + off);
-        else
-            __builtin_memcpy(&r, row + off, sizeof(r));
-        return r;
-    }
-    return gated_load<T, CH>(row + off, g.n);
+    return gated_load<T, CH>(row + (uint32_t)g.c0 * ElemSize<T>::value);
 }
 template <int T, int CH>
 SSD_DEVICE void gated_write(void *p, const GatedParams &q, const GatedPlace<CH> &g, int t,
                             const float (&v)[CH])
 {
     char *row = (char *)p + (g.b * q.T + t) * q.C * ElemSize<T>::value;
-    const uint32_t off = (uint32_t)g.c0 * ElemSize<T>::value;
-    if (g.full)
-        gated_store<T, CH>(row + off, CH, v);
-    else
-        gated_store<T, CH>(row + off, g.n, v);
+    if (g.live)
+        gated_store<T, CH>(row + (uint32_t)g.c0 * ElemSize<T>::value, v);
 }
 
 // SUMMARY: only the segment's (A, U) is wanted, for all but the last segment; the last one's
@@ -223,10 +190,10 @@ SSD_KERNEL(64 * WAVES) void gated_scan_kernel(GatedParams p)
     float nk[CH], carry[CH], decay[CH];
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-        nk[c] = c < g.n ? -p.k * softplus(p.lam[g.c0 + c]) : 0.f;
+        nk[c] = g.live ? -p.k * softplus(p.lam[g.c0 + c]) : 0.f;
         carry[c] = 0.f;
         decay[c] = 1.f;
-        if (c < g.n) {
+        if (g.live) {
             float *copy = p.seg + (g.b * p.segments + p.segments - 1) * 2 * (int64_t)p.C + g.c0 + c;
             const float *from = p.init ? p.init + g.b * p.C + g.c0 + c : nullptr;
             if (SUMMARY) {
@@ -241,7 +208,7 @@ SSD_KERNEL(64 * WAVES) void gated_scan_kernel(GatedParams p)
         for (int s = 0; s < g.seg; ++s)
 #pragma unroll
             for (int c = 0; c < CH; ++c)
-                if (c < g.n) {
+                if (g.live) {
                     const float *q = p.seg + ((g.b * p.segments + s) * 2) * (int64_t)p.C + g.c0 + c;
                     carry[c] = q[0] * carry[c] + q[p.C];
                 }
@@ -313,7 +280,7 @@ SSD_KERNEL(64 * WAVES) void gated_scan_kernel(GatedParams p)
             if (p.states && t % kGatedChunk == 0 && t < g.t1)
 #pragma unroll
                 for (int c = 0; c < CH; ++c)
-                    if (c < g.n)
+                    if (g.live)
                         p.states[(g.b * ((p.T + kGatedChunk - 1) / kGatedChunk) + t / kGatedChunk) * p.C + g.c0 + c] = mine[c];
 #pragma unroll
             for (int k = 0; k < STEPS; ++k) {
@@ -332,7 +299,7 @@ SSD_KERNEL(64 * WAVES) void gated_scan_kernel(GatedParams p)
         return;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-        if (c >= g.n)
+        if (!g.live)
             continue;
         if (SUMMARY) {
             float *q = p.seg + ((g.b * p.segments + g.seg) * 2) * (int64_t)p.C + g.c0 + c;
@@ -344,31 +311,31 @@ SSD_KERNEL(64 * WAVES) void gated_scan_kernel(GatedParams p)
     }
 }
 
-// One token per sequence: a lane per channel, nothing to fold.
+// A few tokens per sequence: a lane per channel walks over them, nothing to fold.
+constexpr int kGatedFew = 8;
+
 template <int T>
 SSD_KERNEL(64) void gated_step_kernel(GatedParams p)
 {
-    constexpr int E = ElemSize<T>::value;
-    const int64_t b = block_id() / p.blocks;
-    const int c = (int)(block_id() - b * p.blocks) * 64 + thread_id();
-    if (c >= p.C)
+    const GatedPlace<1> g = gated_place<1>(p);
+    if (!g.live)
         return;
-    const float before = p.init ? p.init[b * p.C + c] : 0.f;
-    const bool in = !p.lengths || p.lengths[b] > 0;
-    float h = before;
-    if (in) {
-        const float x = gated_value<T, 1>(gated_load<T, 1>((const char *)p.x + (b * p.x_stride + c) * E, 1), 0);
-        const float gi = gated_value<T, 1>(gated_load<T, 1>((const char *)p.gi + (b * p.gi_stride + c) * E, 1), 0);
-        const float gr = gated_value<T, 1>(gated_load<T, 1>((const char *)p.gr + (b * p.gr_stride + c) * E, 1), 0);
-        const Gates q = gates(gi, gr, -p.k * softplus(p.lam[c]));
-        h = q.a * before + q.m * q.i * x;
-    }
-    const float out[1] = {in ? h : 0.f};
-    gated_store<T, 1>((char *)p.h + (b * p.C + c) * E, 1, out);
-    if (p.final_state)
-        p.final_state[b * p.C + c] = h;
+    const float nk = -p.k * softplus(p.lam[g.c0]);
+    float h = p.init ? p.init[g.b * p.C + g.c0] : 0.f;
     if (p.states)
-        p.states[b * p.C + c] = before;
+        p.states[g.b * p.C + g.c0] = h;
+    for (int t = 0; t < p.T; ++t) {
+        const bool in = t < g.lim;
+        if (in) {
+            const Gates q = gates(gated_value<T, 1>(gated_read<T, 1>(p.gi, p.gi_stride, p, g, t), 0),
+                                  gated_value<T, 1>(gated_read<T, 1>(p.gr, p.gr_stride, p, g, t), 0), nk);
+            h = q.a * h + q.m * q.i * gated_value<T, 1>(gated_read<T, 1>(p.x, p.x_stride, p, g, t), 0);
+        }
+        const float out[1] = {in ? h : 0.f};
+        gated_write<T, 1>(p.h, p, g, t, out);
+    }
+    if (p.final_state)
+        p.final_state[g.b * p.C + g.c0] = h;
 }
 
 // The adjoint that enters a segment from its right, without the segments after it: each
@@ -385,7 +352,7 @@ SSD_KERNEL(64 * WAVES) void gated_bwd_summary_kernel(GatedParams p)
     float nk[CH], carry[CH], decay[CH];
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-        nk[c] = c < g.n ? -p.k * softplus(p.lam[g.c0 + c]) : 0.f;
+        nk[c] = g.live ? -p.k * softplus(p.lam[g.c0 + c]) : 0.f;
         carry[c] = 0.f;
         decay[c] = 1.f;
     }
@@ -439,7 +406,7 @@ SSD_KERNEL(64 * WAVES) void gated_bwd_summary_kernel(GatedParams p)
         return;
 #pragma unroll
     for (int c = 0; c < CH; ++c)
-        if (c < g.n) {
+        if (g.live) {
             float *q = p.seg + ((g.b * p.segments + g.seg) * 2) * (int64_t)p.C + g.c0 + c;
             q[0] = decay[c];
             q[p.C] = carry[c];
@@ -449,11 +416,10 @@ SSD_KERNEL(64 * WAVES) void gated_bwd_summary_kernel(GatedParams p)
 // The gradients, tile by tile from the last to the first. A tile is one chunk (64 tokens):
 // its entering state was stored, so the states inside it come from a fold to the right and
 // the adjoints from a fold to the left, over the same products A.
-template <int T, int CH>
-SSD_KERNEL(1024) void gated_scan_bwd_kernel(GatedParams p)
+template <int T, int CH, int WAVES>
+SSD_KERNEL(64 * WAVES) void gated_scan_bwd_kernel(GatedParams p)
 {
-    constexpr int WAVES = 16, STEPS = 4;
-    static_assert(WAVES * STEPS == kGatedChunk, "a tile is a chunk");
+    constexpr int STEPS = kGatedChunk / WAVES;  // a tile is a chunk
     SSD_LDS float pairs[2][WAVES][3][64 * CH];
     const int lane = thread_id() & 63;
     const int wave = wave_id();
@@ -462,14 +428,14 @@ SSD_KERNEL(1024) void gated_scan_bwd_kernel(GatedParams p)
     float nk[CH], carry[CH], sum_e[CH];
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-        nk[c] = c < g.n ? -p.k * softplus(p.lam[g.c0 + c]) : 0.f;
-        carry[c] = p.gfinal && c < g.n ? p.gfinal[g.b * p.C + g.c0 + c] : 0.f;
+        nk[c] = g.live ? -p.k * softplus(p.lam[g.c0 + c]) : 0.f;
+        carry[c] = p.gfinal && g.live ? p.gfinal[g.b * p.C + g.c0 + c] : 0.f;
         sum_e[c] = 0.f;
     }
     for (int s = p.segments - 1; s > g.seg; --s)
 #pragma unroll
         for (int c = 0; c < CH; ++c)
-            if (c < g.n) {
+            if (g.live) {
                 const float *q = p.seg + ((g.b * p.segments + s) * 2) * (int64_t)p.C + g.c0 + c;
                 carry[c] = q[0] * carry[c] + q[p.C];
             }
@@ -487,7 +453,7 @@ SSD_KERNEL(1024) void gated_scan_bwd_kernel(GatedParams p)
     auto fetch_state = [&](int tile) {
 #pragma unroll
         for (int c = 0; c < CH; ++c)
-            enter[c] = c < g.n ? p.chunk_states[(g.b * chunks + tile / kGatedChunk) * p.C + g.c0 + c] : 0.f;
+            enter[c] = g.live ? p.chunk_states[(g.b * chunks + tile / kGatedChunk) * p.C + g.c0 + c] : 0.f;
     };
     const int last = g.t0 + (g.t1 - g.t0 - 1) / kGatedChunk * kGatedChunk;
     fetch(last + wave * STEPS);
@@ -612,7 +578,7 @@ SSD_KERNEL(1024) void gated_scan_bwd_kernel(GatedParams p)
         return;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-        if (c >= g.n)
+        if (!g.live)
             continue;
         float e = 0.f;
         for (int w = 0; w < WAVES; ++w)

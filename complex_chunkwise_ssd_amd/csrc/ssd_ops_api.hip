@@ -270,7 +270,7 @@ int launch_fp8(ssd::Fp8Params p, const Fp8Plan &plan, bool aligned_rows, char *w
 
 // ------------------------------------------------------------ gated recurrence
 
-constexpr int kGatedWaves = 16, kGatedSteps = 8;
+constexpr int kGatedWaves = 16, kGatedSteps = 8, kGatedBwdWaves = 16;
 
 struct GatedPlan {
     int ch;                   // channels per lane
@@ -297,7 +297,7 @@ int check_gated(int dtype, int64_t batch, int64_t T, int64_t C, int64_t s0, int6
 GatedPlan gated_plan(int64_t batch, int64_t T, int64_t C, int dtype)
 {
     GatedPlan p{};
-    p.ch = dtype == SSD_BF16 ? 2 : 1;
+    p.ch = dtype == SSD_BF16 && C % 2 == 0 && batch * ((C + 127) / 128) >= 256 ? 2 : 1;
     p.blocks = (int)((C + 64 * p.ch - 1) / (64 * p.ch));
     const int64_t groups = batch * p.blocks;
     int64_t seg = groups > 0 ? 256 / groups : 1;
@@ -347,8 +347,8 @@ int launch_gated_bwd(ssd::GatedParams p, float *grad_lam, hipStream_t s)
         if (int st = launch_status())
             return st;
     }
-    hipLaunchKernelGGL((ssd::gated_scan_bwd_kernel<T, CH>),
-                       dim3((unsigned)((int64_t)p.B * p.blocks * p.segments)), dim3(1024), 0, s, p);
+    hipLaunchKernelGGL((ssd::gated_scan_bwd_kernel<T, CH, kGatedBwdWaves>),
+                       dim3((unsigned)((int64_t)p.B * p.blocks * p.segments)), dim3(64 * kGatedBwdWaves), 0, s, p);
     if (int st = launch_status())
         return st;
     hipLaunchKernelGGL(ssd::gated_lam_kernel, dim3(grid_1d(p.C, 64)), dim3(1024), 0, s,
@@ -682,8 +682,10 @@ int ssd_gated_scan(const void *x, int64_t x_stride, const void *input_gate,
     p.seg_tokens = plan.seg_tokens;
     p.launched = plan.segments;
     p.k = decay_scale;
-    if (T == 1) {
+    if (T <= ssd::kGatedFew) {
         p.blocks = (int)((C + 63) / 64);
+        p.segments = p.launched = 1;
+        p.seg_tokens = (int)T;
         if (batch > kMaxGrid / p.blocks)
             return SSD_ERR_UNSUPPORTED;
         const dim3 grid((unsigned)(batch * p.blocks));
@@ -693,7 +695,9 @@ int ssd_gated_scan(const void *x, int64_t x_stride, const void *input_gate,
             hipLaunchKernelGGL((ssd::gated_step_kernel<ssd::kF32>), grid, dim3(64), 0, s, p);
         return launch_status();
     }
-    return dtype == SSD_BF16 ? launch_gated<ssd::kBF16, 2>(p, s) : launch_gated<ssd::kF32, 1>(p, s);
+    return dtype == SSD_F32 ? launch_gated<ssd::kF32, 1>(p, s)
+           : plan.ch == 2   ? launch_gated<ssd::kBF16, 2>(p, s)
+                            : launch_gated<ssd::kBF16, 1>(p, s);
 }
 
 size_t ssd_gated_scan_backward_workspace_bytes(int64_t batch, int64_t T, int64_t C, int dtype)
@@ -788,8 +792,9 @@ int ssd_gated_scan_backward(const void *x, int64_t x_stride, const void *input_g
     p.seg_tokens = plan.seg_tokens;
     p.launched = plan.segments;
     p.k = decay_scale;
-    return dtype == SSD_BF16 ? launch_gated_bwd<ssd::kBF16, 2>(p, grad_lam, s)
-                             : launch_gated_bwd<ssd::kF32, 1>(p, grad_lam, s);
+    return dtype == SSD_F32 ? launch_gated_bwd<ssd::kF32, 1>(p, grad_lam, s)
+           : plan.ch == 2   ? launch_gated_bwd<ssd::kBF16, 2>(p, grad_lam, s)
+                            : launch_gated_bwd<ssd::kBF16, 1>(p, grad_lam, s);
 }
 
 }  // extern "C"
