@@ -37,7 +37,11 @@ SSD_DEVICE Raw8<T> load8(const void *p, int n)
         __builtin_memcpy(&r, p, 8 * ElemSize<T>::value);
         return r;
     }
-    uint32_t u[T == kBF16 ? 4 : 8];
+    uint32_t u[T == kBF16 ? 4 : 8] = {};
+    if (n <= 0) {  // a lane past the row's end; kept apart so that whole rows skip what follows
+        __builtin_memcpy(&r, u, sizeof(r));
+        return r;
+    }
     if (T == kBF16) {
         const uint16_t *s = (const uint16_t *)p;
 #pragma unroll
@@ -125,13 +129,17 @@ SSD_DEVICE uint32_t row16_max(uint32_t v)
     return max_u(v, row_xor<15>(v));
 }
 
-// Sum over the wave's 64 lanes (a fixed order), in every lane.
-SSD_DEVICE float wave_sum(float v)
+// Sums over a row of 16 lanes and over the wave's 64 (a fixed order), in every lane.
+SSD_DEVICE float row16_sum(float v)
 {
     v += u2f(row_xor<1>(f2u(v)));
     v += u2f(row_xor<2>(f2u(v)));
     v += u2f(row_xor<7>(f2u(v)));
-    v += u2f(row_xor<15>(f2u(v)));
+    return v + u2f(row_xor<15>(f2u(v)));
+}
+SSD_DEVICE float wave_sum(float v)
+{
+    v = row16_sum(v);
     return (lane_read(v, 0) + lane_read(v, 16)) + (lane_read(v, 32) + lane_read(v, 48));
 }
 

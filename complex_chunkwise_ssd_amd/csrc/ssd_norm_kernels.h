@@ -6,11 +6,10 @@
 //     gx = gs + rstd (w gy - s rstd^2 (sum w gy s) / F)      gw = sum over rows gy s rstd
 // A row is read once: its values stay in registers between the sum and the output.
 //
-// WAVES waves hold a row, STEPS groups of eight elements per lane (512 WAVES STEPS
-// elements at most). A row of up to 2048 values is one wave's, without any barrier;
-// a longer one is shared by four or eight waves, which meet once per row. The
-// workgroups walk over the rows, so that the weights are loaded once per wave, and
-// hold the next row's values in flight.
+// LANES lanes hold a row, STEPS groups of eight elements each (8 LANES STEPS elements at most):
+// 16 lanes a row of up to 128 values, a wave one of up to 1024, and four to sixteen waves a
+// longer one, which meet once per row. The workgroups walk over the rows, so that the weights
+// are loaded once per wave, and hold the next row's values in flight.
 #pragma once
 
 #include <ssd_elem.h>
@@ -33,45 +32,45 @@ struct NormParams {
     float eps;
 };
 
-template <int WAVES>
+template <int LANES>
 struct NormShape {
-    static constexpr int waves = WAVES < 4 ? 4 : WAVES;       // waves of a workgroup
-    static constexpr int rows = waves / WAVES;                // rows it holds at once
+    static constexpr int waves = LANES <= 256 ? 4 : LANES / 64;   // waves of a workgroup
     static constexpr int threads = 64 * waves;
+    static constexpr int rows = threads / LANES;                  // rows it holds at once
 };
 
-// Sum over the WAVES waves that hold a row, in every lane. `red` is this row's slot;
-// rows alternate between two of them, so one barrier per row is enough.
-template <int WAVES>
-SSD_DEVICE float row_sum(float v, float *red, int wave)
+// Sum over the LANES lanes that hold a row, in every one of them. `red` is this row's slot; rows
+// alternate between two of them, so one barrier per row is enough.
+template <int LANES>
+SSD_DEVICE float row_sum(float v, float *red)
 {
+    if (LANES == 16)
+        return row16_sum(v);
     v = wave_sum(v);
-    if (WAVES == 1)
+    if (LANES == 64)
         return v;
     if ((thread_id() & 63) == 0)
-        red[wave] = v;
+        red[wave_id()] = v;
     block_sync();
     float t = 0.f;
 #pragma unroll
-    for (int i = 0; i < WAVES; ++i)
+    for (int i = 0; i < LANES / 64; ++i)
         t += red[i];
     return t;
 }
 
-template <int T, int WAVES, int STEPS>
-SSD_KERNEL(NormShape<WAVES>::threads) void rms_norm_kernel(NormParams p)
+template <int T, int LANES, int STEPS>
+SSD_KERNEL(NormShape<LANES>::threads) void rms_norm_kernel(NormParams p)
 {
-    using Shape = NormShape<WAVES>;
-    SSD_LDS float red[2][WAVES];
-    const int lane = thread_id() & 63;
-    const int wave = wave_id();
-    const int sub = wave % WAVES;
+    using Shape = NormShape<LANES>;
+    SSD_LDS float red[2][LANES > 64 ? LANES / 64 : 1];
+    const int lane = thread_id() % LANES;          // of those that hold the row
     const int64_t step = grid_blocks() * Shape::rows;
     int at[STEPS], n[STEPS];
     float w[STEPS][8];
 #pragma unroll
     for (int k = 0; k < STEPS; ++k) {
-        at[k] = 8 * ((k * WAVES + sub) * 64 + lane);
+        at[k] = 8 * (k * LANES + lane);
         n[k] = p.F - at[k];
         unpack8<kF32>(load8<kF32>(p.w + (n[k] > 0 ? at[k] : 0), n[k]), w[k]);
     }
@@ -79,7 +78,7 @@ SSD_KERNEL(NormShape<WAVES>::threads) void rms_norm_kernel(NormParams p)
     const char *res = (const char *)p.res;
     constexpr int E = ElemSize<T>::value;
     Raw8<T> rx[STEPS], rr[STEPS];
-    int64_t row = block_id() * Shape::rows + wave / WAVES;
+    int64_t row = block_id() * Shape::rows + thread_id() / LANES;
     const int64_t end = (p.rows + Shape::rows - 1) / Shape::rows * Shape::rows;
     const int64_t last = p.rows - 1;
     auto fetch = [&](int64_t r) {
@@ -113,8 +112,8 @@ SSD_KERNEL(NormShape<WAVES>::threads) void rms_norm_kernel(NormParams p)
         }
         if (row + step < end)
             fetch(row + step);
-        const float rstd = hw_rsq(row_sum<WAVES>(sum, red[parity], sub) / (float)p.F + p.eps);
-        if (live && p.rstd && sub == 0 && lane == 0)
+        const float rstd = hw_rsq(row_sum<LANES>(sum, red[parity]) / (float)p.F + p.eps);
+        if (live && p.rstd && lane == 0)
             p.rstd[row] = rstd;
 #pragma unroll
         for (int k = 0; k < STEPS; ++k) {
@@ -151,31 +150,32 @@ struct NormBwdParams {
     int F;
 };
 
-template <int T, int WAVES, int STEPS>
-SSD_KERNEL(NormShape<WAVES>::threads) void rms_norm_bwd_kernel(NormBwdParams p)
+template <int T, int LANES, int STEPS>
+SSD_KERNEL(NormShape<LANES>::threads) void rms_norm_bwd_kernel(NormBwdParams p)
 {
-    using Shape = NormShape<WAVES>;
-    SSD_LDS float red[2][WAVES];
-    SSD_LDS float total[Shape::rows > 1 ? 512 * WAVES * STEPS : 1];
-    const int lane = thread_id() & 63;
-    const int wave = wave_id();
-    const int sub = wave % WAVES;
+    using Shape = NormShape<LANES>;
+    SSD_LDS float red[2][LANES > 64 ? LANES / 64 : 1];
+    SSD_LDS float total[Shape::rows > 1 ? 8 * LANES * STEPS : 1];
+    const int lane = thread_id() % LANES;          // of those that hold the row
     const int64_t step = grid_blocks() * Shape::rows;
+    // with 16 waves to a row there are 128 registers: the weights come from the caches each time
+    constexpr bool KEEP = LANES < 1024;
     int at[STEPS], n[STEPS];
-    float w[STEPS][8], gw[STEPS][8];
+    float w[KEEP ? STEPS : 1][8], gw[STEPS][8];
 #pragma unroll
     for (int k = 0; k < STEPS; ++k) {
-        at[k] = 8 * ((k * WAVES + sub) * 64 + lane);
+        at[k] = 8 * (k * LANES + lane);
         n[k] = p.F - at[k];
-        unpack8<kF32>(load8<kF32>(p.w + (n[k] > 0 ? at[k] : 0), n[k]), w[k]);
+        if (KEEP)
+            unpack8<kF32>(load8<kF32>(p.w + (n[k] > 0 ? at[k] : 0), n[k]), w[KEEP ? k : 0]);
 #pragma unroll
         for (int e = 0; e < 8; ++e)
             gw[k][e] = 0.f;
     }
     constexpr int E = ElemSize<T>::value;
-    Raw8<T> rs[STEPS], rg[STEPS], rr[STEPS];
+    Raw8<T> rs[STEPS], rg[STEPS], rr[STEPS] = {};  // rr stays zero without gs
     float next_rstd = 0.f;
-    int64_t row = block_id() * Shape::rows + wave / WAVES;
+    int64_t row = block_id() * Shape::rows + thread_id() / LANES;
     const int64_t end = (p.rows + Shape::rows - 1) / Shape::rows * Shape::rows;
     const int64_t last = p.rows - 1;
     auto fetch = [&](int64_t r) {
@@ -195,45 +195,44 @@ SSD_KERNEL(NormShape<WAVES>::threads) void rms_norm_bwd_kernel(NormBwdParams p)
     for (; row < end; row += step, parity ^= 1) {
         const bool live = row <= last;
         const float rstd = next_rstd;
-        float s[STEPS][8], g[STEPS][8], r[STEPS][8];
+        float s[STEPS][8], g[STEPS][8];
+        Raw8<T> cr[STEPS];
         float sum = 0.f;
 #pragma unroll
         for (int k = 0; k < STEPS; ++k) {
             unpack8<T>(rs[k], s[k]);
             unpack8<T>(rg[k], g[k]);
-            if (p.gs) {
-                unpack8<T>(rr[k], r[k]);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    r[k][e] = 0.f;
-            }
+            cr[k] = rr[k];
+            if (!KEEP)
+                unpack8<kF32>(load8<kF32>(p.w + (n[k] > 0 ? at[k] : 0), n[k]), w[0]);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 s[k][e] *= rstd;                       // the normalised value
                 if (live)
                     gw[k][e] += g[k][e] * s[k][e];
-                g[k][e] *= w[k][e];
+                g[k][e] *= w[KEEP ? k : 0][e];
                 sum += g[k][e] * s[k][e];
             }
         }
         if (row + step < end)
             fetch(row + step);
-        const float mean = row_sum<WAVES>(sum, red[parity], sub) / (float)p.F;
+        const float mean = row_sum<LANES>(sum, red[parity]) / (float)p.F;
 #pragma unroll
         for (int k = 0; k < STEPS; ++k) {
             float gx[8];
+            unpack8<T>(cr[k], gx);
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-                gx[e] = r[k][e] + rstd * (g[k][e] - s[k][e] * mean);
+                gx[e] += rstd * (g[k][e] - s[k][e] * mean);
             if (live && n[k] > 0)
                 store8<T>((char *)p.gx + (row * p.F + at[k]) * E, n[k], gx);
         }
     }
-    // The workgroup's share of gw: the waves that held different rows add theirs in turn.
+    // The workgroup's share of gw: the lanes that held different rows add theirs in turn.
+    const int mine = thread_id() / LANES;
     if (Shape::rows > 1) {
-        for (int i = 0; i < Shape::waves; i += WAVES) {
-            if (wave / WAVES == i / WAVES) {
+        for (int i = 0; i < Shape::rows; ++i) {
+            if (mine == i) {
 #pragma unroll
                 for (int k = 0; k < STEPS; ++k)
 #pragma unroll
@@ -246,7 +245,7 @@ SSD_KERNEL(NormShape<WAVES>::threads) void rms_norm_bwd_kernel(NormBwdParams p)
             block_sync();
         }
     }
-    if (wave / WAVES == Shape::rows - 1)
+    if (mine == Shape::rows - 1)
 #pragma unroll
         for (int k = 0; k < STEPS; ++k)
             if (n[k] > 0)

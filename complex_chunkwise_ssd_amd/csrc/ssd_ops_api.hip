@@ -49,17 +49,13 @@ int64_t norm_groups(int64_t rows, int rows_per_group, int64_t most)
     return need < most ? need : most;
 }
 constexpr int64_t kNormGroups = 2048;
-constexpr int64_t kNormBwdGroups = 1024;
 
-// Rows a workgroup holds at once for this F (see launch_norm).
-int norm_rows(int64_t F) { return F <= 2048 ? 4 : 1; }
-
-template <int T, int WAVES, int STEPS>
+template <int T, int LANES, int STEPS>
 int launch_norm_as(const ssd::NormParams &p, hipStream_t s)
 {
-    using Shape = ssd::NormShape<WAVES>;
+    using Shape = ssd::NormShape<LANES>;
     const int64_t groups = norm_groups(p.rows, Shape::rows, kNormGroups);
-    hipLaunchKernelGGL((ssd::rms_norm_kernel<T, WAVES, STEPS>), dim3((unsigned)groups),
+    hipLaunchKernelGGL((ssd::rms_norm_kernel<T, LANES, STEPS>), dim3((unsigned)groups),
                        dim3(Shape::threads), 0, s, p);
     return launch_status();
 }
@@ -67,41 +63,52 @@ int launch_norm_as(const ssd::NormParams &p, hipStream_t s)
 template <int T>
 int launch_norm(const ssd::NormParams &p, hipStream_t s)
 {
+    if (p.F <= 128)
+        return launch_norm_as<T, 16, 1>(p, s);
     if (p.F <= 512)
-        return launch_norm_as<T, 1, 1>(p, s);
+        return launch_norm_as<T, 64, 1>(p, s);
     if (p.F <= 1024)
-        return launch_norm_as<T, 1, 2>(p, s);
+        return launch_norm_as<T, 64, 2>(p, s);
     if (p.F <= 2048)
-        return launch_norm_as<T, 1, 4>(p, s);
+        return launch_norm_as<T, 256, 1>(p, s);
     if (p.F <= 4096)
-        return launch_norm_as<T, 4, 2>(p, s);
+        return launch_norm_as<T, 256, 2>(p, s);
     if (p.F <= 8192)
-        return launch_norm_as<T, 4, 4>(p, s);
-    return launch_norm_as<T, 8, 4>(p, s);
+        return launch_norm_as<T, 512, 2>(p, s);
+    return launch_norm_as<T, 1024, 2>(p, s);
 }
 
-template <int T, int WAVES, int STEPS>
+// Workgroups of the gradients' kernel: each leaves a row of shares of grad_weight.
+int64_t norm_bwd_groups(int64_t rows, int64_t F)
+{
+    const int held = F <= 128 ? 16 : F <= 1024 ? 4 : 1;
+    return norm_groups(rows, held, F <= 4096 ? 1024 : 512);
+}
+
+template <int T, int LANES, int STEPS>
 int launch_norm_bwd_as(const ssd::NormBwdParams &p, int64_t groups, hipStream_t s)
 {
-    hipLaunchKernelGGL((ssd::rms_norm_bwd_kernel<T, WAVES, STEPS>), dim3((unsigned)groups),
-                       dim3(ssd::NormShape<WAVES>::threads), 0, s, p);
+    hipLaunchKernelGGL((ssd::rms_norm_bwd_kernel<T, LANES, STEPS>), dim3((unsigned)groups),
+                       dim3(ssd::NormShape<LANES>::threads), 0, s, p);
     return launch_status();
 }
 
 template <int T>
 int launch_norm_bwd(const ssd::NormBwdParams &p, int64_t groups, hipStream_t s)
 {
+    if (p.F <= 128)
+        return launch_norm_bwd_as<T, 16, 1>(p, groups, s);
     if (p.F <= 512)
-        return launch_norm_bwd_as<T, 1, 1>(p, groups, s);
+        return launch_norm_bwd_as<T, 64, 1>(p, groups, s);
     if (p.F <= 1024)
-        return launch_norm_bwd_as<T, 1, 2>(p, groups, s);
+        return launch_norm_bwd_as<T, 64, 2>(p, groups, s);
     if (p.F <= 2048)
-        return launch_norm_bwd_as<T, 1, 4>(p, groups, s);
+        return launch_norm_bwd_as<T, 256, 1>(p, groups, s);
     if (p.F <= 4096)
-        return launch_norm_bwd_as<T, 4, 2>(p, groups, s);
+        return launch_norm_bwd_as<T, 256, 2>(p, groups, s);
     if (p.F <= 8192)
-        return launch_norm_bwd_as<T, 4, 4>(p, groups, s);
-    return launch_norm_bwd_as<T, 8, 4>(p, groups, s);
+        return launch_norm_bwd_as<T, 512, 2>(p, groups, s);
+    return launch_norm_bwd_as<T, 1024, 2>(p, groups, s);
 }
 
 // -------------------------------------------------------------- 8-bit values
@@ -422,7 +429,7 @@ size_t ssd_rms_norm_backward_workspace_bytes(int64_t rows, int64_t F)
 {
     if (check_norm(SSD_F32, rows, F) || rows == 0)
         return 0;
-    return align256((size_t)(norm_groups(rows, norm_rows(F), kNormBwdGroups) * F) * 4);
+    return align256((size_t)(norm_bwd_groups(rows, F) * F) * 4);
 }
 
 int ssd_rms_norm_backward(const void *s, int64_t s_stride, const float *weight, const float *rstd,
@@ -483,7 +490,7 @@ int ssd_rms_norm_backward(const void *s, int64_t s_stride, const float *weight, 
     p.gy_stride = grad_y_stride;
     p.gs_stride = grad_residual_stride;
     p.F = (int)F;
-    const int64_t groups = norm_groups(rows, norm_rows(F), kNormBwdGroups);
+    const int64_t groups = norm_bwd_groups(rows, F);
     if (int st = dtype == SSD_BF16 ? launch_norm_bwd<ssd::kBF16>(p, groups, st_)
                                    : launch_norm_bwd<ssd::kF32>(p, groups, st_))
         return st;
