@@ -97,9 +97,9 @@ SSD_DEVICE float softplus(float v)
 }
 
 // The gates of one value. nk = -k softplus(lam). Near a = 1 the recurrence remembers 1 / (1 - a)
-// steps, and an error of the exponential would add up over them: with w = -l below 1/4,
-// 1 - exp(-w) comes from its series (the first term left out is w^6 / 5040 of it, 5e-8) and a is
-// one minus that, right to half a unit; above, 1 - a loses at most three bits. 1 - a^2 is (1 - a)
+// steps, and an error of the exponential would add up over them: with w = -l below 1/16,
+// 1 - exp(-w) comes from its series (the first term left out is w^5 / 720 of it, 1e-9) and a is one
+// minus that, right to half a unit; above, 1 - a loses at most four bits. 1 - a^2 is (1 - a)
 // (1 + a) in either case.
 struct Gates {
     float i, r, l, a, m;
@@ -111,15 +111,14 @@ SSD_DEVICE Gates gates(float gi, float gr, float nk)
     g.r = sigmoid(gr);
     g.l = nk * g.r;
     const float w = -g.l;
-    float s = -1.f / 720.f;
-    s = s * w + 1.f / 120.f;
+    float s = 1.f / 120.f;
     s = s * w - 1.f / 24.f;
     s = s * w + 1.f / 6.f;
     s = s * w - 0.5f;
     s = s * w + 1.f;
     s = s * w;
     const float e = hw_exp2(kLog2e * g.l);
-    const bool near = w < 0.25f;
+    const bool near = w < 0.0625f;
     const float rest = near ? s : 1.f - e;
     g.a = near ? 1.f - s : e;
     g.m = hw_sqrt(rest * (1.f + g.a));

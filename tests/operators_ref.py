@@ -25,10 +25,10 @@ def softplus(v):
 # A gate's error, in U and relative: sigmoid(v) = 1 / (1 + 2^(-v log2 e)): the argument is off by
 # 3 U |v| (two roundings), the exponential by that and 2, the sum and the reciprocal by 3.
 # With |v| <= 6 in these tests: below 30. l = -k softplus(lam) r adds 6 (softplus 4, products 2):
-# 36. a = 2^(l log2 e): off by |l| 39 + 2. m^2 = 1 - a^2 = f(z), z = -2 l: below z = 1/4 the series is off by
-# 8 of it and z f'(z) / f(z) <= 1 carries 36: m by 22 + 2; above, f >= 0.22 and a^2's error is
-# 2 (39 |l| + 2) + 1 with |l| a^2 <= 0.19: (78 * 0.19 + 5) / 0.22 = 90 of f, 45 + 2 of m. u = m i x: below
-# 47 + 30 + 2 = 80.
+# 36. a = 2^(l log2 e): off by |l| 39 + 2. m^2 = (1 - a)(1 + a). Below w = -l = 1/16, 1 - a is a series: off by 8 of
+# it and, since w f'(w) / f(w) <= 1 for f = 1 - exp(-w), by 36: m by 22 + 4. Above, 1 - a is off by (39 w + 2) a /
+# (1 - a), largest at w = 1/16, where it is 4.5 * 0.94 / 0.06 = 70, and 1 + a by 4: m by 37 + 4. u = m i x: below
+# 41 + 30 + 2 = 73.
 U_ERR = 80.0
 
 
