@@ -175,7 +175,49 @@ SSD_DEVICE void gated_write(void *p, const GatedParams &q, const GatedPlace<CH> 
         gated_store<T, CH>(row + (uint32_t)g.c0 * ElemSize<T>::value, v);
 }
 
-// SUMMARY: only the segment's (A, U) is wanted, for all but the last segment; the last one's
+// Folds `count` segments' pairs (number first, first + step, ...) onto carry: every wave folds its
+// share of them, then all fold the waves' pairs from shared memory. One wait for memory and not
+// one per segment.
+template <int CH, int WAVES, int PARTS>
+SSD_DEVICE void gated_fold(const GatedParams &p, const GatedPlace<CH> &g, int first, int step, int count,
+                           float (&slots)[WAVES][PARTS][64 * CH], float (&carry)[CH])
+{
+    const int lane = thread_id() & 63;
+    const int wave = wave_id();
+    const int share = (count + WAVES - 1) / WAVES;
+    const int end = (wave + 1) * share < count ? (wave + 1) * share : count;
+    float A[CH], U[CH];
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+        A[c] = 1.f;
+        U[c] = 0.f;
+    }
+#pragma unroll 4
+    for (int i = wave * share; i < end; ++i) {
+        const float *q = p.seg + ((g.b * p.segments + first + step * i) * 2) * (int64_t)p.C + g.c0;
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            const float a = q[c];
+            A[c] *= a;
+            U[c] = a * U[c] + q[p.C + c];
+        }
+    }
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+        slots[wave][0][c * 64 + lane] = A[c];
+        slots[wave][1][c * 64 + lane] = U[c];
+    }
+    block_sync();
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w)
+#pragma unroll
+        for (int c = 0; c < CH; ++c)
+            carry[c] = slots[w][0][c * 64 + lane] * carry[c] + slots[w][1][c * 64 + lane];
+}
+
+// SUMMARY: only the segment's (A, U) is wanted, for all but the last segment. That pass walks
+// over its tiles from the last to the first: what it read last, and the caches behind the
+// compute units still hold, is what the pass after it reads first. The last segment's
 // slot takes a copy of the entering state instead, so that final_state may be initial_state:
 // the pass that writes it then reads the copy. Otherwise the outputs.
 template <int T, int CH, int WAVES, int STEPS, bool SUMMARY>
@@ -203,15 +245,8 @@ SSD_KERNEL(64 * WAVES) void gated_scan_kernel(GatedParams p)
             }
         }
     }
-    if (!SUMMARY) {
-        for (int s = 0; s < g.seg; ++s)
-#pragma unroll
-            for (int c = 0; c < CH; ++c)
-                if (g.live) {
-                    const float *q = p.seg + ((g.b * p.segments + s) * 2) * (int64_t)p.C + g.c0 + c;
-                    carry[c] = q[0] * carry[c] + q[p.C];
-                }
-    }
+    if (!SUMMARY && g.seg > 0)  // the slots are the second tile's: its writes are a barrier away
+        gated_fold<CH, WAVES>(p, g, 0, 1, g.seg, pairs[1], carry);
     GatedRaw<T, CH> rx[STEPS], ri[STEPS], rr[STEPS];
     auto fetch = [&](int t) {  // this wave's tokens from t on
 #pragma unroll
@@ -221,10 +256,12 @@ SSD_KERNEL(64 * WAVES) void gated_scan_kernel(GatedParams p)
             rr[k] = gated_read<T, CH>(p.gr, p.gr_stride, p, g, t + k);
         }
     };
-    fetch(g.t0 + wave * STEPS);
+    const int tiles = (g.t1 - g.t0 + TILE - 1) / TILE;
+    constexpr int NEXT = SUMMARY ? -TILE : TILE;
+    int t = g.t0 + (SUMMARY ? (tiles - 1) * TILE : 0) + wave * STEPS;
+    fetch(t);
     int parity = 0;
-    for (int tile = g.t0; tile < g.t1; tile += TILE, parity ^= 1) {
-        const int t = tile + wave * STEPS;
+    for (int tile = 0; tile < tiles; ++tile, t += NEXT, parity ^= 1) {
         const bool whole = t + STEPS <= g.lim;
         float a[STEPS][CH], u[STEPS][CH], A[CH], U[CH];
 #pragma unroll
@@ -255,27 +292,32 @@ SSD_KERNEL(64 * WAVES) void gated_scan_kernel(GatedParams p)
                 U[c] = a[k][c] * U[c] + u[k][c];
             }
         }
-        if (tile + TILE < g.t1)
-            fetch(t + TILE);
+        if (tile + 1 < tiles)
+            fetch(t + NEXT);
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
             pairs[parity][wave][0][c * 64 + lane] = A[c];
             pairs[parity][wave][1][c * 64 + lane] = U[c];
         }
         block_sync();
-        float mine[CH];
+        if (SUMMARY) {  // this tile comes before what is in (decay, carry)
 #pragma unroll
-        for (int w = 0; w < WAVES; ++w)
+            for (int w = WAVES - 1; w >= 0; --w)
 #pragma unroll
-            for (int c = 0; c < CH; ++c) {
-                if (w == 0 || w == wave)
-                    mine[c] = carry[c];
-                const float wa = pairs[parity][w][0][c * 64 + lane];
-                carry[c] = wa * carry[c] + pairs[parity][w][1][c * 64 + lane];
-                if (SUMMARY)
-                    decay[c] *= wa;
-            }
-        if (!SUMMARY) {
+                for (int c = 0; c < CH; ++c) {
+                    carry[c] += decay[c] * pairs[parity][w][1][c * 64 + lane];
+                    decay[c] *= pairs[parity][w][0][c * 64 + lane];
+                }
+        } else {
+            float mine[CH];
+#pragma unroll
+            for (int w = 0; w < WAVES; ++w)
+#pragma unroll
+                for (int c = 0; c < CH; ++c) {
+                    if (w == 0 || w == wave)
+                        mine[c] = carry[c];
+                    carry[c] = pairs[parity][w][0][c * 64 + lane] * carry[c] + pairs[parity][w][1][c * 64 + lane];
+                }
             if (p.states && t % kGatedChunk == 0 && t < g.t1)
 #pragma unroll
                 for (int c = 0; c < CH; ++c)
@@ -431,13 +473,8 @@ SSD_KERNEL(64 * WAVES) void gated_scan_bwd_kernel(GatedParams p)
         carry[c] = p.gfinal && g.live ? p.gfinal[g.b * p.C + g.c0 + c] : 0.f;
         sum_e[c] = 0.f;
     }
-    for (int s = p.segments - 1; s > g.seg; --s)
-#pragma unroll
-        for (int c = 0; c < CH; ++c)
-            if (g.live) {
-                const float *q = p.seg + ((g.b * p.segments + s) * 2) * (int64_t)p.C + g.c0 + c;
-                carry[c] = q[0] * carry[c] + q[p.C];
-            }
+    if (g.seg < p.segments - 1)  // the slots are the second tile's: its writes are a barrier away
+        gated_fold<CH, WAVES>(p, g, p.segments - 1, -1, p.segments - 1 - g.seg, pairs[1], carry);
     GatedRaw<T, CH> rx[STEPS], ri[STEPS], rr[STEPS], rh[STEPS];
     float enter[CH];
     auto fetch = [&](int t) {
