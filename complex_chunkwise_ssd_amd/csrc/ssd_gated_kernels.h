@@ -577,7 +577,7 @@ SSD_KERNEL(64 * WAVES) void gated_scan_bwd_kernel(GatedParams p)
             }
 #pragma unroll
         for (int k = STEPS - 1; k >= 0; --k) {
-            float gx[CH], ggi[CH], ggr[CH];
+            float gx[CH], ggi[CH], ggr[CH], e[CH];
 #pragma unroll
             for (int c = 0; c < CH; ++c) {
                 const float a = va[k][c], m = vm[k][c], i = vi[k][c], r = vr[k][c];
@@ -586,11 +586,10 @@ SSD_KERNEL(64 * WAVES) void gated_scan_bwd_kernel(GatedParams p)
                 right[c] = a * gt;
                 const float ratio = m > 0.f ? l * hw_rcp(m) : 0.f;
                 const float gi = gt * i;
-                const float e = right[c] * (hb[k][c] * l) - gi * xv * (a * a * ratio);
+                e[c] = right[c] * (hb[k][c] * l) - gi * xv * (a * a * ratio);
                 gx[c] = gi * m;
                 ggi[c] = gx[c] * xv * (1.f - i);
-                ggr[c] = e * (1.f - r);
-                sum_e[c] += e;
+                ggr[c] = e[c] * (1.f - r);
             }
             if (!whole) {
                 if (t + k >= g.t1)
@@ -598,8 +597,11 @@ SSD_KERNEL(64 * WAVES) void gated_scan_bwd_kernel(GatedParams p)
                 if (t + k >= g.lim)  // padding, whatever adjoint passes over it
 #pragma unroll
                     for (int c = 0; c < CH; ++c)
-                        gx[c] = ggi[c] = ggr[c] = 0.f;
+                        gx[c] = ggi[c] = ggr[c] = e[c] = 0.f;
             }
+#pragma unroll
+            for (int c = 0; c < CH; ++c)
+                sum_e[c] += e[c];
             gated_write<T, CH>(p.gx, p, g, t + k, gx);
             gated_write<T, CH>(p.ggi, p, g, t + k, ggi);
             gated_write<T, CH>(p.ggr, p, g, t + k, ggr);
@@ -634,9 +636,11 @@ SSD_KERNEL(64 * 16) void gated_lam_kernel(const float *part, int rows, int C, co
     const int wave = wave_id();
     const int c = (int)block_id() * 64 + lane;
     float acc = 0.f;
-    if (c < C)
+    if (c < C) {
+#pragma unroll 8
         for (int r = wave; r < rows; r += 16)
             acc += part[(int64_t)r * C + c];
+    }
     sums[wave][lane] = acc;
     block_sync();
     if (wave == 0 && c < C) {

@@ -20,6 +20,9 @@ GATED = [
     (1, 700, 65, "f32", True, [650], 1),     # several segments, the end inside the last
     (1, 1025, 131, "bf16", False, None, 0),
     (3, 600, 2, "bf16", True, [0, 300, 600], 0),
+    (2, 8, 65, "bf16", True, [8, 3], 0),     # the longest that is walked by lanes, and one more
+    (2, 9, 65, "bf16", True, [9, 3], 0),
+    (1, 4700, 3, "f32", True, [4650], 0),    # more segments than waves that fold them
 ]
 
 
@@ -54,6 +57,28 @@ def gated_backward(run, B, T, C, kind, state, lengths, pad):
         ref.close(v, w, e, k, name)
 
 
+def gated_lengths_clamped(run):
+    """Lengths below 0 and past T are taken as 0 and as T."""
+    x, gi, gr, lam, init, _ = ref.gated_case(3, 70, 6, "f32", 5, state=True)
+    a = run.gated(x, gi, gr, lam, 8.0, "f32", init=init, lengths=np.array([-3, 75, 2 ** 31 - 1], np.int32))
+    b = run.gated(x, gi, gr, lam, 8.0, "f32", init=init, lengths=np.array([0, 70, 70], np.int32))
+    assert np.array_equal(a[0], b[0]) and np.array_equal(a[1], b[1])
+
+
+def gated_empty_row_infinite(run):
+    """A row without tokens hands its final state's gradient to the initial state and leaves the
+    others' gradients alone, be it infinite."""
+    x, gi, gr, lam, init, _ = ref.gated_case(2, 70, 6, "f32", 6, state=True)
+    n = np.array([70, 0], np.int32)
+    states = ref.gated(x, gi, gr, lam, 8.0, init, n)[0][2]
+    gf = np.ones((2, 6))
+    want = run.gated_backward(x, gi, gr, lam, 8.0, "f32", states, x, gfinal=gf, lengths=n)
+    gf[1] = np.inf
+    got = run.gated_backward(x, gi, gr, lam, 8.0, "f32", states, x, gfinal=gf, lengths=n)
+    assert all(np.array_equal(a, b) for a, b in zip(got[:4], want[:4]))
+    assert np.array_equal(got[4][0], want[4][0]) and np.isposinf(got[4][1]).all()
+
+
 # rows, F, kind, residual, padding between rows
 NORM = [
     (1, 1, "f32", False, 0),
@@ -67,6 +92,8 @@ NORM = [
     (2, 4096, "f32", True, 0),
     (3, 5000, "bf16", False, 0),
     (2, 16384, "bf16", True, 0),
+    (2, 8193, "f32", True, 0),
+    (18, 65, "bf16", True, 0),
 ]
 
 
@@ -166,7 +193,21 @@ MATMUL = [
     (130, 70, 2048, 128, "f32", 0, 0, 0),
     (260, 260, 200, 128, "bf16", 8, 8, 0),
     (70, 12, 2176, 1, "bf16", 0, 0, 0),
+    (64, 48, 131, 1, "f32", 0, 0, 0),
+    (65, 48, 131, 128, "bf16", 0, 0, 0),
 ]
+
+
+def matmul_special(run, M, out):
+    """A NaN in a row of a and one in a row of b come out in that row and that column only."""
+    N, K = 40, 400
+    a, sa, b, sb = matmul_inputs(M, N, K, 1, M)
+    clean = run.matmul(a, sa, b, sb, 1, out)
+    a[M // 2, 200], b[33, 399] = 0x7f, 0xff
+    got = run.matmul(a, sa, b, sb, 1, out)
+    bad = np.zeros((M, N), bool)
+    bad[M // 2], bad[:, 33] = True, True
+    assert np.isnan(got[bad]).all() and np.array_equal(got[~bad], clean[~bad])
 
 
 def matmul_inputs(M, N, K, block_rows, seed):

@@ -144,6 +144,78 @@ def test_fp8_matmul(case, align):
     cases.matmul(_Gpu, *case, align=align)
 
 
+def test_gated_lengths_and_empty_rows():
+    cases.gated_lengths_clamped(_Gpu)
+    cases.gated_empty_row_infinite(_Gpu)
+
+
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("M", [5, 70, 300])
+def test_fp8_matmul_nan(M, out):
+    cases.matmul_special(_Gpu, M, out)
+
+
+def test_refusals_on_the_device():
+    x = torch.zeros(2, 6, 8, device=DEV)
+    lam = torch.zeros(8, device=DEV)
+    neg = torch.complex(x, x).conj().imag           # a lazily negated view
+    for bad in (x.half(), x.cpu(), x[0], neg, x[..., :4], x.transpose(0, 1), x[:1].expand(2, 6, 8)):
+        with pytest.raises(ValueError):
+            ssd.gated_scan(x, bad, x, lam)
+        with pytest.raises(ValueError):
+            ssd.rms_norm(x, lam, residual=bad)
+    for kw in (dict(lengths=torch.zeros(2, device=DEV)), dict(lengths=torch.zeros(3, dtype=torch.int32, device=DEV)),
+               dict(initial_state=torch.zeros(2, 7, device=DEV)), dict(h=torch.zeros(2, 6, 16, device=DEV)[..., ::2])):
+        with pytest.raises(ValueError):
+            ssd.gated_scan(x, x, x, lam, **kw)
+    with pytest.raises(ssd.SSDError):
+        ssd.gated_scan(x, x, x, lam, h=x)
+    with pytest.raises(ssd.SSDError):
+        ssd.rms_norm(x, lam, want_y=False)
+    with pytest.raises(ssd.SSDError):
+        ssd.rms_norm(torch.zeros(2, 16385, device=DEV), torch.zeros(16385, device=DEV))
+    q, s = ssd.fp8_quantise(x)
+    for a, sa, b, sb in ((q, s, q, s), (q, s[:, :5], q[0], s[:, :6]), (q.view(torch.uint8), s, q[0], s)):
+        with pytest.raises(ValueError):
+            ssd.fp8_matmul(a, sa, b, sb, block_rows=1)
+    with pytest.raises(ValueError):
+        ssd.fp8_matmul(q, s, q[0], s[:, :6].contiguous(), block_rows=1, out_dtype=torch.float16)
+
+
+def test_rows_past_32_bit_offsets():
+    """Column ranges of matrices of more than 2^32 elements, against the same values packed."""
+    S, C = 65536, 100
+    rows = 2 ** 32 // S + 64
+    same = lambda a, b: torch.equal(a.view(torch.uint8), b.contiguous().view(torch.uint8))  # noqa: E731
+    wide = torch.empty(rows, S, dtype=torch.bfloat16, device=DEV)[:, S - C:]
+    wide.copy_(torch.randn(rows, C, generator=torch.Generator(device=DEV).manual_seed(1), device=DEV))
+    dense = wide.contiguous()
+    w = torch.linspace(0.5, 2, C, device=DEV)
+    a, b = (ssd.rms_norm(v, w, residual=v, want_rstd=True) for v in (wide, dense))
+    assert same(a.y, b.y) and same(a.residual, b.residual)
+    a, b = (ssd.rms_norm_backward(v, w, a.rstd, v, grad_residual=v) for v in (wide, dense))
+    assert same(a[0], b[0]) and same(a[1], b[1])
+    lam = torch.linspace(-9, 0, C, device=DEV)
+    wide, dense = wide[None], dense[None]
+    a, b = (ssd.gated_scan(v, v, v, lam, want_chunk_states=True) for v in (wide, dense))
+    assert all(same(p, q) for p, q in zip(a, b))
+    a, b = (ssd.gated_scan_backward(v, v, v, lam, a.chunk_states, dense) for v in (wide, dense))
+    assert all(same(p, q) for p, q in zip(a, b))
+    wide, dense = wide[0], dense[0]
+    for turn in (False, True):
+        a, b = (ssd.fp8_quantise(v, transpose=turn) for v in (wide, dense))
+        assert same(a[0].contiguous(), b[0]) and same(a[1], b[1])
+    q, s = ssd.fp8_quantise(dense)
+    del wide
+    far = torch.empty(rows, S, dtype=torch.uint8, device=DEV)[:, S - 112:S - 12].view(FP8)
+    far.view(torch.uint8).copy_(q.view(torch.uint8))
+    assert far.data_ptr() % 16 == 0
+    qb, sb = ssd.fp8_quantise(torch.randn(64, C, device=DEV), block_rows=128)
+    out = torch.empty(rows, S, dtype=torch.bfloat16, device=DEV)[:, S - 64:]
+    ssd.fp8_matmul(far, s, qb, sb, out=out)
+    assert same(out.contiguous(), ssd.fp8_matmul(q, s, qb, sb))
+
+
 # ------------------------------------------------------------------- calls as a program makes them
 
 def _calls(seed, T=700):

@@ -45,6 +45,11 @@ def everything(lib):
     for c in cases.MATMUL:
         for align in (16, 1):
             todo.append(("matmul %s align %d" % (c, align), lambda c=c, align=align: cases.matmul(run, *c, align=align)))
+    todo.append(("gated lengths clamped", lambda: cases.gated_lengths_clamped(run)))
+    todo.append(("gated empty row, infinite gradient", lambda: cases.gated_empty_row_infinite(run)))
+    for M in (5, 70):
+        for out in ("bf16", "f32"):
+            todo.append(("matmul_special %d %s" % (M, out), lambda M=M, out=out: cases.matmul_special(run, M, out)))
     return todo
 
 
