@@ -337,7 +337,8 @@ def test_gated_scan_of_many_groups(B, T, C):
 @pytest.mark.parametrize("M,N,K,block_rows,out", [
     (1, 5136, 1024, 128, "bf16"), (33, 5136, 1024, 128, "bf16"), (64, 1024, 2048, 1, "f32"),
     (257, 1040, 1024, 128, "bf16"), (1000, 520, 1000, 128, "f32"), (2048, 1296, 640, 128, "bf16"),
-    (5136, 1024, 1280, 1, "f32"), (640, 512, 20000, 1, "f32"), (4097, 5136, 256, 128, "bf16"), (515, 300, 8192, 128, "f32")])
+    (5136, 1024, 1280, 1, "f32"), (640, 512, 20000, 1, "f32"), (4097, 5136, 256, 128, "bf16"), (515, 300, 8192, 128, "f32"),
+    (5136, 2100, 256, 1, "f32"), (5136, 2100, 256, 128, "f32"), (4400, 5000, 200, 1, "bf16"), (2000, 9000, 1, 128, "bf16")])
 def test_fp8_matmul_of_many_tiles(M, N, K, block_rows, out):
     cases.matmul(_Gpu, M, N, K, block_rows, out, -K % 16, -K % 16, 0)
 
