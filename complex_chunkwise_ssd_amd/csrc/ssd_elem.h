@@ -152,15 +152,28 @@ SSD_DEVICE float e4m3_scale(uint32_t amax)
     return s < kTinyScale ? kTinyScale : s;
 }
 
-// Eight values over their scale, rounded to e4m3. The products stay within
-// 448 (1 + 2^-22), which rounds to 448: nothing overflows.
-SSD_DEVICE v2u e4m3_pack8(const float (&v)[8], float inv)
+// v / scale with the rounding of a division, inv = 1 / scale: one correction of v * inv by its
+// remainder. (The product alone is off by up to one and a half units, which moves a value next to a
+// border of two e4m3 values across it.)
+SSD_DEVICE float e4m3_over(float v, float scale, float inv)
 {
+    const float q = v * inv;
+    return __builtin_fmaf(__builtin_fmaf(-q, scale, v), inv, q);
+}
+
+// Eight values over their scale, rounded to e4m3. The quotients stay within
+// 448 (1 + 2^-23), which rounds to 448: nothing overflows.
+SSD_DEVICE v2u e4m3_pack8(const float (&v)[8], float scale, float inv)
+{
+    float t[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        t[e] = e4m3_over(v[e], scale, inv);
     v2u r = {0u, 0u};
-    r[0] = cvt_pk_e4m3<false>(v[0] * inv, v[1] * inv, r[0]);
-    r[0] = cvt_pk_e4m3<true>(v[2] * inv, v[3] * inv, r[0]);
-    r[1] = cvt_pk_e4m3<false>(v[4] * inv, v[5] * inv, r[1]);
-    r[1] = cvt_pk_e4m3<true>(v[6] * inv, v[7] * inv, r[1]);
+    r[0] = cvt_pk_e4m3<false>(t[0], t[1], r[0]);
+    r[0] = cvt_pk_e4m3<true>(t[2], t[3], r[0]);
+    r[1] = cvt_pk_e4m3<false>(t[4], t[5], r[1]);
+    r[1] = cvt_pk_e4m3<true>(t[6], t[7], r[1]);
     return r;
 }
 

@@ -59,6 +59,17 @@ SSD_DEVICE float row_sum(float v, float *red)
     return t;
 }
 
+// 1 / sqrt(v) to little more than half a unit, once per row: a Newton step on the hardware's, its
+// residue 1 - v r^2 without rounding errors of the first order (left out where it is no number: v
+// is 0, infinite or NaN).
+SSD_DEVICE float exact_rsq(float v)
+{
+    const float r = hw_rsq(v);
+    const float h = v * r, low = __builtin_fmaf(v, r, -h);
+    const float d = __builtin_fmaf(-h, r, 1.f) - low * r;
+    return d * d < 1.f ? __builtin_fmaf(0.5f * r, d, r) : r;
+}
+
 template <int T, int LANES, int STEPS>
 SSD_KERNEL(NormShape<LANES>::threads) void rms_norm_kernel(NormParams p)
 {
@@ -112,7 +123,7 @@ SSD_KERNEL(NormShape<LANES>::threads) void rms_norm_kernel(NormParams p)
         }
         if (row + step < end)
             fetch(row + step);
-        const float rstd = hw_rsq(row_sum<LANES>(sum, red[parity]) / (float)p.F + p.eps);
+        const float rstd = exact_rsq(row_sum<LANES>(sum, red[parity]) / (float)p.F + p.eps);
         if (live && p.rstd && lane == 0)
             p.rstd[row] = rstd;
 #pragma unroll
@@ -129,7 +140,7 @@ SSD_KERNEL(NormShape<LANES>::threads) void rms_norm_kernel(NormParams p)
             if (p.q) {
                 const float scale = e4m3_scale(row16_max(amax8(y)));
                 if (in) {
-                    store_e4m3(p.q + row * p.F + at[k], n[k], e4m3_pack8(y, 1.f / scale));
+                    store_e4m3(p.q + row * p.F + at[k], n[k], e4m3_pack8(y, scale, 1.f / scale));
                     if ((lane & 15) == 0)
                         p.scale[(int64_t)(at[k] >> 7) * p.rows + row] = scale;
                 }

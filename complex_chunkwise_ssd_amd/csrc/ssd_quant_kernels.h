@@ -48,7 +48,7 @@ SSD_KERNEL(256) void quantise_rows_kernel(QuantParams p)
         unpack8<T>(raw[k], v);
         const float scale = e4m3_scale(row16_max(amax8(v)));
         if (n[k] > 0) {
-            store_e4m3(p.q + row[k] * p.q_stride + col[k], n[k], e4m3_pack8(v, 1.f / scale));
+            store_e4m3(p.q + row[k] * p.q_stride + col[k], n[k], e4m3_pack8(v, scale, 1.f / scale));
             if (lane16 == 0)
                 p.scale[(col[k] >> 7) * p.rows + row[k]] = scale;
         }
@@ -96,7 +96,7 @@ SSD_KERNEL(256) void quantise_tile_kernel(QuantParams p)
         for (int e = 0; e < 8; ++e)
             m[e] = max_u(m[e], f2u(v[j][e]) & 0x7fffffffu);
     }
-    float inv[8];
+    float by[8], inv[8];      // the scales and their reciprocals
     if (WHOLE) {
         uint32_t t = 0;
 #pragma unroll
@@ -112,8 +112,10 @@ SSD_KERNEL(256) void quantise_tile_kernel(QuantParams p)
         if (tid == 0)
             p.scale[TURN ? ct * rtiles + rt : rt * ctiles + ct] = scale;
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
+        for (int e = 0; e < 8; ++e) {
+            by[e] = scale;
             inv[e] = 1.f / scale;
+        }
     } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e)
@@ -132,6 +134,7 @@ SSD_KERNEL(256) void quantise_tile_kernel(QuantParams p)
             const float scale = e4m3_scale(top[16 * e + cg]);
             if (rg == 0 && e < nc)
                 p.scale[rt * p.cols + c0 + e] = scale;
+            by[e] = scale;
             inv[e] = 1.f / scale;
         }
     }
@@ -139,13 +142,13 @@ SSD_KERNEL(256) void quantise_tile_kernel(QuantParams p)
 #pragma unroll
         for (int j = 0; j < 8; ++j)
             if (j < nr && nc > 0)
-                store_e4m3(p.q + (r0 + j) * p.q_stride + c0, nc, e4m3_pack8(v[j], inv[0]));
+                store_e4m3(p.q + (r0 + j) * p.q_stride + c0, nc, e4m3_pack8(v[j], by[0], inv[0]));
         return;
     }
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
         const float col[8] = {v[0][e], v[1][e], v[2][e], v[3][e], v[4][e], v[5][e], v[6][e], v[7][e]};
-        *(v2u *)&tile[(16 * e + cg) * kTileLd + 8 * rg] = e4m3_pack8(col, inv[e]);
+        *(v2u *)&tile[(16 * e + cg) * kTileLd + 8 * rg] = e4m3_pack8(col, by[e], inv[e]);
     }
     block_sync();
 #pragma unroll
