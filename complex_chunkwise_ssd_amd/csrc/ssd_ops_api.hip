@@ -283,6 +283,7 @@ struct GatedPlan {
     int ch;                   // channels per lane
     int blocks;               // channel blocks
     int segments, seg_tokens;
+    bool walk;                // a lane per channel walks over the tokens
     size_t seg_bytes;
 };
 
@@ -299,18 +300,39 @@ int check_gated(int dtype, int64_t batch, int64_t T, int64_t C, int64_t s0, int6
     return SSD_OK;
 }
 
-// Segments: as many as give about 256 workgroups (one per compute unit), of whole chunks and
-// at least 256 tokens.
-GatedPlan gated_plan(int64_t batch, int64_t T, int64_t C, int dtype)
+// Segments that give about 256 workgroups (one per compute unit), each at least 256 tokens.
+int64_t gated_segments(int64_t groups, int64_t T)
+{
+    const int64_t seg = 256 / groups < T / 256 ? 256 / groups : T / 256;
+    return seg < 1 ? 1 : seg;
+}
+
+// How the work is cut. Measured in us, bfloat16 unless said:
+//  - Channels per lane: two take 1.6 times as long as one, and a compute unit holds one workgroup
+//    at a time (32 x 2048 x 1024: 135 with two, 165 with one; cut into segments either way,
+//    8 x 4096 x 1024: 113 and 128). But one where only two would need segments, whose gates are
+//    formed twice (16 x 2048 x 1024: 81 with one, 118 with two).
+//  - Two segments are not worth their second pass in float32, whose forward is bound by memory with
+//    128 workgroups already (8 x 4096 x 1024: 143 in one, 164 in two; 1 x 8192 x 5504: 236 and
+//    239). In bfloat16, and backwards in either type, they are (8 x 4096 x 1023: 143 against
+//    147; gradients of 8 x 4096 x 1024 in float32: 229 against 255). About 128 or 512 workgroups
+//    instead of 256: 1 x 32768 x 1024 in float32 239 and 205 against 188.
+//  - The walk: a round of the scan's workgroups costs 7 to 10 however few the tokens, the walk 0.2
+//    a token (64 x 8 x 1024: 6 and 21; 64 x 32 x 1024: 11 and 20; in one round, 4 x 16 x 256, 7.5
+//    and 6.7).
+GatedPlan gated_plan(int64_t batch, int64_t T, int64_t C, int dtype, bool backward)
 {
     GatedPlan p{};
-    p.ch = dtype == SSD_BF16 && C % 2 == 0 && batch * ((C + 127) / 128) >= 256 ? 2 : 1;
+    batch = batch > 0 ? batch : 1;
+    const int64_t one = batch * ((C + 63) / 64), two = batch * ((C + 127) / 128);
+    const bool pairs = dtype == SSD_BF16 && C % 2 == 0;
+    p.ch = pairs && (gated_segments(two, T) == 1 || gated_segments(one, T) > 1) ? 2 : 1;
+    const int64_t groups = p.ch == 2 ? two : one;
     p.blocks = (int)((C + 64 * p.ch - 1) / (64 * p.ch));
-    const int64_t groups = batch * p.blocks;
-    int64_t seg = groups > 0 ? 256 / groups : 1;
-    const int64_t most = T / 256;
-    seg = seg > most ? most : seg;
-    seg = seg < 1 ? 1 : seg;
+    p.walk = !backward && (T <= 8 || (T <= ssd::kGatedWalk && groups > 256));
+    int64_t seg = gated_segments(groups, T);
+    if (!backward && dtype == SSD_F32 && seg == 2)
+        seg = 1;
     int64_t tokens = (T + seg - 1) / seg;
     tokens = (tokens + ssd::kGatedChunk - 1) / ssd::kGatedChunk * ssd::kGatedChunk;
     p.segments = T > 0 ? (int)((T + tokens - 1) / tokens) : 1;
@@ -610,7 +632,7 @@ size_t ssd_gated_scan_workspace_bytes(int64_t batch, int64_t T, int64_t C, int d
 {
     if (check_gated(dtype, batch, T, C, C, C, C) || batch == 0 || T == 0)
         return 0;
-    return gated_plan(batch, T, C, dtype).seg_bytes;
+    return gated_plan(batch, T, C, dtype, false).seg_bytes;
 }
 
 int ssd_gated_scan(const void *x, int64_t x_stride, const void *input_gate,
@@ -642,7 +664,7 @@ int ssd_gated_scan(const void *x, int64_t x_stride, const void *input_gate,
     }
     if (!x || !input_gate || !decay_gate || !lam || !h)
         return SSD_ERR_NULL;
-    const GatedPlan plan = gated_plan(batch, T, C, dtype);
+    const GatedPlan plan = gated_plan(batch, T, C, dtype, false);
     if (!gated_grid_ok(plan, batch))
         return SSD_ERR_UNSUPPORTED;
     if (plan.seg_bytes > 0 && (!workspace || workspace_bytes < plan.seg_bytes))
@@ -689,7 +711,7 @@ int ssd_gated_scan(const void *x, int64_t x_stride, const void *input_gate,
     p.seg_tokens = plan.seg_tokens;
     p.launched = plan.segments;
     p.k = decay_scale;
-    if (T <= ssd::kGatedFew) {
+    if (plan.walk) {
         p.blocks = (int)((C + 63) / 64);
         p.segments = p.launched = 1;
         p.seg_tokens = (int)T;
@@ -711,7 +733,7 @@ size_t ssd_gated_scan_backward_workspace_bytes(int64_t batch, int64_t T, int64_t
 {
     if (check_gated(dtype, batch, T, C, C, C, C) || batch == 0 || T == 0)
         return 0;
-    const GatedPlan plan = gated_plan(batch, T, C, dtype);
+    const GatedPlan plan = gated_plan(batch, T, C, dtype, true);
     return plan.seg_bytes + align256((size_t)batch * plan.segments * C * 4);
 }
 
@@ -741,7 +763,7 @@ int ssd_gated_scan_backward(const void *x, int64_t x_stride, const void *input_g
     if (tokens > 0 && (!x || !input_gate || !decay_gate || !lam || !chunk_states || !grad_h ||
                        !grad_x || !grad_input_gate || !grad_decay_gate))
         return SSD_ERR_NULL;
-    const GatedPlan plan = gated_plan(batch, T, C, dtype);
+    const GatedPlan plan = gated_plan(batch, T, C, dtype, true);
     if (tokens > 0 && !gated_grid_ok(plan, batch))
         return SSD_ERR_UNSUPPORTED;
     const size_t need = ssd_gated_scan_backward_workspace_bytes(batch, T, C, dtype);
