@@ -10,6 +10,11 @@
 // 16 lanes a row of up to 128 values, a wave one of up to 1024, and four to sixteen waves a
 // longer one, which meet once per row. The workgroups walk over the rows, so that the weights
 // are loaded once per wave, and hold the next row's values in flight.
+//
+// Bound by memory. Measured in bfloat16 with the residual (a copy runs at 5160 GB/s): 65536 x 1024 to
+// 8 bits 92 us (5.1 TB/s), its gradients 112 us (4.8 TB/s); 32768 x 4096 190 us (4.9 TB/s);
+// 65536 x 64 8.6 us. Eight rows take 2.8 us, mostly the launch. The gradients of float32 rows above
+// 8192 spill 144 bytes a lane and reach 57 % of the copy's rate.
 #pragma once
 
 #include <ssd_elem.h>

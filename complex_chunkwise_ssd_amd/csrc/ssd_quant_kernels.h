@@ -3,6 +3,8 @@
 // Three forms of block: 1 x 128 along a row, 1 x 128 along a column (the matrix turned, for
 // a product that sums over its rows) and 128 x 128 (weights), this one plain or turned.
 // All are bound by memory: each value is read once (2 or 4 bytes) and written once (1 byte).
+// Measured (a copy runs at 5160 GB/s): 65536 x 1024 bfloat16 along the rows 35 us (5.7 TB/s), turned
+// 43 us (4.7 TB/s); 5136 x 1024 float32 in 128 x 128 blocks, turned, 5.2 us (5.1 TB/s).
 #pragma once
 
 #include <ssd_elem.h>
@@ -17,7 +19,8 @@ struct QuantParams {
 };
 
 // 1 x 128 blocks along the rows. 16 lanes hold a block; a workgroup's 256 threads hold
-// kQuantUnroll x 16 neighbouring blocks of the row-major (row, block) order.
+// kQuantUnroll x 16 neighbouring blocks of the row-major (row, block) order. Four in flight per
+// thread: 65536 x 1024 bfloat16 35 us, with one 41, with eight 38 (float32: 65, 60, 67).
 constexpr int kQuantUnroll = 4;
 
 template <int T>
