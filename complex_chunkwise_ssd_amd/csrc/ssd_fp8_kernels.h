@@ -7,7 +7,8 @@
 // The inner sum of 128 products is exactly one 16x16x128 e4m3 MFMA, started from zero; its
 // four results per lane are then multiplied by the two scales and added to the float32
 // sums. That is four vector FMAs per MFMA (16 of its 32 cycles), which run beside the next
-// MFMAs: a loop of MFMAs alone ran at 4.4e15 flop/s, with four FMAs each 3 % slower, with six 24 %. b's rows are the MFMA's rows and a's rows its columns, so that a lane holds one m:
+// MFMAs: a loop of MFMAs alone ran at 4.4e15 flop/s, with four FMAs each 3 % slower, with six 24 %.
+// b's rows are the MFMA's rows and a's rows its columns, so that a lane holds one m:
 // its a-scale is one register per 16 rows of a, and b's block scale is the wave's.
 //
 // Precision. The e4m3 MFMA holds its inner sums to 2^-13 of the largest of each eight products,
@@ -245,7 +246,8 @@ SSD_KERNEL_WAVES(512, 2) void fp8_matmul_big_kernel(Fp8Params p)
         Fp8Operand<WIDE> bf[NB];
 #pragma unroll
         for (int j = 0; j < NB; ++j)
-            bf[j] = fp8_operand<WIDE>(*(const v4u *)&tile[b_lo + 512 * (j & 1) + 4096 * (j >> 1)], *(const v4u *)&tile[b_hi + 512 * (j & 1) + 4096 * (j >> 1)]);
+            bf[j] = fp8_operand<WIDE>(*(const v4u *)&tile[b_lo + 512 * (j & 1) + 4096 * (j >> 1)],
+                                      *(const v4u *)&tile[b_hi + 512 * (j & 1) + 4096 * (j >> 1)]);
         v4f sb4[BROW ? NB : 1];
         float sb = 1.f;
         if (BROW) {
@@ -329,7 +331,8 @@ SSD_KERNEL_WAVES(512, 2) void fp8_matmul_big_kernel(Fp8Params p)
 }
 
 // Few rows of a (16 MB at most): bound by reading b once, and below some 10 MB of it by the time that a
-// launch and one trip to memory take. Measured: 8 x 5136 x 1024 4.0 us, 64 x 5136 x 1024 7.7. A wave takes 16 rows of b and every
+// launch and one trip to memory take. Measured: 8 x 5136 x 1024 4.0 us, 64 x 5136 x 1024 7.7.
+// A wave takes 16 rows of b and every
 // WK-th k block, straight from memory into the MFMA's registers (four lanes cover a row's 128
 // bytes), AHEAD blocks in flight; the workgroup's WK waves add up through shared memory in
 // wave order. a comes from the caches.

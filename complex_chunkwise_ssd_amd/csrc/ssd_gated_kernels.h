@@ -461,8 +461,8 @@ SSD_KERNEL(64 * WAVES) void gated_bwd_summary_kernel(GatedParams p)
 }
 
 // The gradients, tile by tile from the last to the first. In bfloat16 116 registers with two channels
-// per lane, so that a compute unit holds one workgroup of 16 waves; 8 waves with twice the tokens
-// each spilled and were slower. A tile is one chunk (64 tokens):
+// per lane, so that a compute unit holds one workgroup of 16 waves; workgroups of 8 waves, and
+// loads issued earlier, gained nothing. A tile is one chunk (64 tokens):
 // its entering state was stored, so the states inside it come from a fold to the right and
 // the adjoints from a fold to the left, over the same products A.
 template <int T, int CH, int WAVES>
