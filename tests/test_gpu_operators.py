@@ -316,7 +316,15 @@ def test_steps_of_one_token_follow_the_scan():
     ref.close(_n(state), want[1], err[1], "f32", "final")
 
 
-@pytest.mark.parametrize("B,T,C", [(32, 130, 256), (1, 9000, 320), (300, 70, 64)])
+@pytest.mark.parametrize("B,T,C", [(2, 3000, 256), (300, 20, 64), (260, 32, 6), (260, 33, 6), (140, 600, 100)])
+def test_gated_scan_in_bfloat16_of_many_groups(B, T, C):
+    """Two channels per lane in segments, walks of more than eight tokens, a padded batch."""
+    lengths = [T - (T // 2) * (b % 3 == 1) for b in range(B)]
+    cases.gated(_Gpu, B, T, C, "bf16", True, lengths, 2)
+    cases.gated_backward(_Gpu, B, T, C, "bf16", True, lengths, 2)
+
+
+@pytest.mark.parametrize("B,T,C", [(32, 130, 256), (1, 9000, 320), (300, 70, 64), (300, 20, 64), (2, 4200, 3000), (8, 600, 1024)])
 def test_gated_scan_of_many_groups(B, T, C):
     """Grids beyond the emulator's: many sequences, and a long one cut into many segments. Against
     torch in float64, one token after the other."""
