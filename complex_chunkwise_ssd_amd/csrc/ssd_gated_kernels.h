@@ -154,14 +154,16 @@ SSD_DEVICE GatedPlace<CH> gated_place(const GatedParams &p)
     g.t1 = g.t0 + p.seg_tokens < p.T ? g.t0 + p.seg_tokens : p.T;
     g.lim = g.t1;
     if (p.lengths) {
-        const int len = uniform_i(p.lengths[g.b]);
+        int len = uniform_i(p.lengths[g.b]);
+        len = len > 0 ? len : 0;  // lim - 1 below has to be a number
         g.lim = len < g.t1 ? len : g.t1;
     }
     return g;
 }
 
 // One token's channels of this lane. A token that is padding or past the segment reads the last
-// one that is not (the segment's first, if none is): its values are replaced afterwards.
+// one that is not (the segment's first, if none is, padding itself): its values are replaced
+// afterwards.
 template <int T, int CH>
 SSD_DEVICE GatedRaw<T, CH> gated_read(const void *p, int64_t stride, const GatedParams &q,
                                       const GatedPlace<CH> &g, int t)

@@ -83,8 +83,8 @@ def gated_scan(x, input_gate, decay_gate, lam, decay_scale: float = 8.0, initial
 
     x, input_gate, decay_gate (B, T, C) float32 or bfloat16, contiguous or column ranges of
     one (B, T, S) tensor of projected rows; lam (C,) float32; initial_state (B, C) float32;
-    lengths (B,) int32: tokens from a row's length on are padding (not read, h = 0, the state
-    stays). T = 1 is one step of generation; final_state may be initial_state (in place).
+    lengths (B,) int32: tokens from a row's length on are padding (whatever they hold, h = 0 and
+    the state stays). T = 1 is one step of generation; final_state may be initial_state (in place).
     Returns GatedScan(h (B, T, C), final_state (B, C) float32 or None, chunk_states
     (B, ceil(T / 64), C) float32 or None: the states that gated_scan_backward starts from).
     """

@@ -382,8 +382,9 @@ enum {
  *   lam          (C) float32. decay_scale: >= 0, at most 1e30.
  *   initial_state nullable: (batch, C) float32, h_{-1}; NULL means zero.
  *   lengths      nullable: (batch) int32 in device memory: the tokens of each
- *                row, clamped to 0 .. T. Tokens from there on are padding: they
- *                are not read, their h is 0, and the state stays as it is.
+ *                row, clamped to 0 .. T. Tokens from there on are padding: what they
+ *                hold does not matter, their h is 0, and the state stays as it is.
+ *                (They are memory that may be read: a first token is, and then left out.)
  *   h            out: (batch, T, C) of `dtype`, dense.
  *   final_state  out, nullable: (batch, C) float32, the state after the row's last
  *                token. It may be initial_state itself (updated in place).
@@ -411,7 +412,7 @@ int ssd_gated_scan(const void *x, int64_t x_stride, const void *input_gate,
  * ssd_gated_scan_backward -- gradients of l = sum grad_h * h + sum
  * grad_final_state * final_state for ssd_gated_scan.
  *   x .. C, lengths as for the forward; chunk_states as it wrote them.
- *   grad_h       (batch, T, C) of `dtype`, dense; not read in the padding.
+ *   grad_h       (batch, T, C) of `dtype`, dense; what the padding holds does not matter.
  *   grad_final_state nullable: (batch, C) float32.
  *   grad_x, grad_input_gate, grad_decay_gate
  *                out: (batch, T, C) of `dtype`, dense; 0 in the padding.
