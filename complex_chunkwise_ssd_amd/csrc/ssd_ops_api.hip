@@ -16,8 +16,10 @@ using ssd::grid_1d;
 using ssd::launch_status;
 using ssd::overlap_bytes;
 
-constexpr int64_t kMaxGrid = (1LL << 31) - 1;
+constexpr int64_t kMaxThreads = (1LL << 32) - 1;  // of one launch: HIP refuses 2^32 and more
 constexpr int64_t kMaxElems = 1LL << 40;  // of one operand: products of sizes and strides stay in 64 bits
+
+bool grid_ok(int64_t groups, int threads) { return groups <= kMaxThreads / threads; }
 
 size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 
@@ -122,13 +124,13 @@ int launch_quantise(const ssd::QuantParams &p, bool whole, bool turn, hipStream_
     if (!whole && !turn) {
         const int64_t blocks = p.rows * ((p.cols + 127) / 128);
         const int64_t grid = (blocks + 16 * ssd::kQuantUnroll - 1) / (16 * ssd::kQuantUnroll);
-        if (grid > kMaxGrid)
+        if (!grid_ok(grid, 256))
             return SSD_ERR_UNSUPPORTED;
         hipLaunchKernelGGL((ssd::quantise_rows_kernel<T>), dim3((unsigned)grid), dim3(256), 0, s, p);
         return launch_status();
     }
     const int64_t tiles = ((p.rows + 127) / 128) * ((p.cols + 127) / 128);
-    if (tiles > kMaxGrid)
+    if (!grid_ok(tiles, 256))
         return SSD_ERR_UNSUPPORTED;
     const dim3 grid((unsigned)tiles), block(256);
     if (whole && turn)
@@ -144,6 +146,7 @@ int launch_quantise(const ssd::QuantParams &p, bool whole, bool turn, hipStream_
 struct Fp8Plan {
     bool few;
     int mb;                   // 16 mb rows of a per wave
+    int waves;                // few: waves of a workgroup
     int tiles_m, tiles_n, splits, split_blocks;
     size_t part_bytes;        // partial sums
     size_t a_bytes, b_bytes;  // operands laid out anew (rows that do not start on 16 bytes)
@@ -156,8 +159,8 @@ int check_fp8(int64_t M, int64_t N, int64_t K, int64_t b_block_rows, int out_dty
         return SSD_ERR_SHAPE;
     if (M > (1LL << 30) || N > (1LL << 30) || K > (1LL << 24) - 16)
         return SSD_ERR_UNSUPPORTED;
-    const int64_t tiles = ((M + 127) / 128) * ((N + 127) / 128);
-    return tiles > kMaxGrid / 64 ? SSD_ERR_UNSUPPORTED : SSD_OK;
+    const int64_t tiles = ((M + 127) / 128) * ((N + 127) / 128);  // a plan's numbers stay in 32 bits
+    return tiles > 1LL << 25 ? SSD_ERR_UNSUPPORTED : SSD_OK;
 }
 
 // Time of a product in us by the large form: every compute unit takes tiles * splits / 256 of
@@ -204,12 +207,14 @@ Fp8Plan fp8_plan(int64_t M, int64_t N, int64_t K, int out_dtype, bool aligned_ro
         // 16384: 38 against 18).
         const int mb = M <= 16 ? 1 : M <= 32 ? 2 : 4;
         const int64_t groups = (N + 15) / 16;
+        // with fewer workgroups than fill the chip, more waves share a workgroup's sum
         const int waves = groups < 512 && kb > 8 ? (mb == 1 ? 16 : 8) : 4;
         const double few = 3 + (double)((groups + 511) / 512) * (double)((kb + waves - 1) / waves) *
                                    (mb == 1 ? 1.2 : mb == 2 ? 1.4 : 2.2);
         if (few < best + (aligned_rows ? 6. : 10.)) {
             p.few = true;
             p.mb = mb;
+            p.waves = waves;
             p.splits = 1;
             return p;
         }
@@ -223,13 +228,11 @@ Fp8Plan fp8_plan(int64_t M, int64_t N, int64_t K, int out_dtype, bool aligned_ro
 }
 
 template <int MB, bool BROW, int OUT>
-int launch_fp8_few(const ssd::Fp8Params &p, hipStream_t s)
+int launch_fp8_few(const ssd::Fp8Params &p, int waves, hipStream_t s)
 {
     const unsigned groups = (unsigned)((p.N + 15) / 16);
-    const int kb = (p.K + 127) / 128;
-    // a workgroup per 16 rows of b: with fewer of those than fill the chip, more waves share its sum
     constexpr int MANY = MB == 1 ? 16 : 8;
-    if (groups < 512 && kb > 8)
+    if (waves == MANY)
         hipLaunchKernelGGL((ssd::fp8_matmul_few_kernel<MB, MANY, BROW, OUT>), dim3(groups), dim3(64 * MANY), 0, s, p);
     else
         hipLaunchKernelGGL((ssd::fp8_matmul_few_kernel<MB, 4, BROW, OUT>), dim3(groups), dim3(256), 0, s, p);
@@ -254,9 +257,9 @@ int launch_fp8(ssd::Fp8Params p, const Fp8Plan &plan, bool aligned_rows, char *w
         return launch_status();
     }
     if (plan.few)
-        return plan.mb == 1   ? launch_fp8_few<1, BROW, OUT>(p, s)
-               : plan.mb == 2 ? launch_fp8_few<2, BROW, OUT>(p, s)
-                              : launch_fp8_few<4, BROW, OUT>(p, s);
+        return plan.mb == 1   ? launch_fp8_few<1, BROW, OUT>(p, plan.waves, s)
+               : plan.mb == 2 ? launch_fp8_few<2, BROW, OUT>(p, plan.waves, s)
+                              : launch_fp8_few<4, BROW, OUT>(p, plan.waves, s);
     if (!aligned_rows) {
         uint8_t *a = (uint8_t *)workspace + plan.part_bytes, *b = a + plan.a_bytes;
         if (int st = launch_pack(p.a, p.a_stride, p.M, p.K, a, s))
@@ -284,7 +287,7 @@ int launch_fp8(ssd::Fp8Params p, const Fp8Plan &plan, bool aligned_rows, char *w
 
 // ------------------------------------------------------------ gated recurrence
 
-constexpr int kGatedWaves = 16, kGatedSteps = 8, kGatedBwdWaves = 16;
+constexpr int kGatedWaves = 16, kGatedSteps = 8;  // backwards a wave takes 64 / kGatedWaves tokens
 
 struct GatedPlan {
     int ch;                   // channels per lane
@@ -337,6 +340,12 @@ GatedPlan gated_plan(int64_t batch, int64_t T, int64_t C, int dtype, bool backwa
     const int64_t groups = p.ch == 2 ? two : one;
     p.blocks = (int)((C + 64 * p.ch - 1) / (64 * p.ch));
     p.walk = !backward && (T <= 8 || (T <= ssd::kGatedWalk && groups > 256));
+    if (p.walk) {
+        p.ch = p.segments = 1;
+        p.blocks = (int)((C + 63) / 64);
+        p.seg_tokens = (int)T;
+        return p;
+    }
     int64_t seg = gated_segments(groups, T);
     if (!backward && dtype == SSD_F32 && seg == 2)
         seg = 1;
@@ -350,7 +359,7 @@ GatedPlan gated_plan(int64_t batch, int64_t T, int64_t C, int dtype, bool backwa
 
 bool gated_grid_ok(const GatedPlan &p, int64_t batch)
 {
-    return batch * p.blocks <= kMaxGrid / p.segments;
+    return grid_ok(batch * p.blocks * p.segments, p.walk ? 64 : 64 * kGatedWaves);
 }
 
 template <int T, int CH>
@@ -383,8 +392,8 @@ int launch_gated_bwd(ssd::GatedParams p, float *grad_lam, hipStream_t s)
         if (int st = launch_status())
             return st;
     }
-    hipLaunchKernelGGL((ssd::gated_scan_bwd_kernel<T, CH, kGatedBwdWaves>),
-                       dim3((unsigned)((int64_t)p.B * p.blocks * p.segments)), dim3(64 * kGatedBwdWaves), 0, s, p);
+    hipLaunchKernelGGL((ssd::gated_scan_bwd_kernel<T, CH, kGatedWaves>),
+                       dim3((unsigned)((int64_t)p.B * p.blocks * p.segments)), dim3(64 * kGatedWaves), 0, s, p);
     if (int st = launch_status())
         return st;
     hipLaunchKernelGGL(ssd::gated_lam_kernel, dim3(grid_1d(p.C, 64)), dim3(1024), 0, s,
@@ -595,6 +604,8 @@ int ssd_fp8_matmul(const uint8_t *a, int64_t a_stride, const float *a_scale, con
     const bool rows16 = K % 16 == 0 && aligned(a, 16) && aligned(b, 16) && a_stride % 16 == 0 &&
                         b_stride % 16 == 0 && a_stride < (1 << 24) && b_stride < (1 << 24);
     const Fp8Plan plan = fp8_plan(M, N, K, out_dtype, rows16);
+    if (K > 0 && !plan.few && !grid_ok((int64_t)plan.tiles_m * plan.tiles_n * plan.splits, 512))
+        return SSD_ERR_UNSUPPORTED;
     const size_t need = K > 0 ? plan.bytes() : 0;
     if (need > 0 && (!workspace || workspace_bytes < need))
         return SSD_ERR_WORKSPACE;
@@ -719,11 +730,6 @@ int ssd_gated_scan(const void *x, int64_t x_stride, const void *input_gate,
     p.launched = plan.segments;
     p.k = decay_scale;
     if (plan.walk) {
-        p.blocks = (int)((C + 63) / 64);
-        p.segments = p.launched = 1;
-        p.seg_tokens = (int)T;
-        if (batch > kMaxGrid / p.blocks)
-            return SSD_ERR_UNSUPPORTED;
         const dim3 grid((unsigned)(batch * p.blocks));
         if (dtype == SSD_BF16)
             hipLaunchKernelGGL((ssd::gated_step_kernel<ssd::kBF16>), grid, dim3(64), 0, s, p);

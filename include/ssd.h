@@ -398,6 +398,9 @@ enum {
  * No output may overlap an input or another output (SSD_ERR_ALIAS), but for the
  * state in place. Alignment: the element size. batch equal to 0 is a no-op; T
  * equal to 0 copies the initial state (or zeros) into final_state.
+ * SSD_ERR_UNSUPPORTED: T above 2^30, batch or C above 2^24, or more workgroups than one
+ * launch takes, which begins at batch * ceil(C / 64) = 2^22 (for T up to 32 at 2^26). The
+ * same for the backward, at 2^22 whatever T.
  */
 size_t ssd_gated_scan_workspace_bytes(int64_t batch, int64_t T, int64_t C, int dtype);
 
@@ -498,6 +501,8 @@ int ssd_rms_norm_backward(const void *s, int64_t s_stride, const float *weight, 
  *                the rows are not written.
  * A block with an infinity or a NaN comes back as NaN (its scale is infinite or
  * NaN); other blocks are untouched by it. rows equal to 0 is a no-op.
+ * SSD_ERR_UNSUPPORTED: rows or cols above 2^31, from 2^24 tiles of 128 x 128 on (plain with
+ * block_rows 1: from 2^30 blocks on).
  * Alignment: the element size; 4 bytes for scale.
  */
 int ssd_fp8_quantise(const void *x, int64_t x_stride, int dtype, int64_t rows, int64_t cols,
@@ -529,8 +534,9 @@ int ssd_fp8_quantise(const void *x, int64_t x_stride, int dtype, int64_t rows, i
  * transpose in blocks of 1 x 128.
  * Sums are float32, rounded once to out_dtype; for a bfloat16 result the sum inside a block
  * is the 8-bit matrix instruction's, which holds each eight neighbouring products to 2^-13
- * of the largest of them. M equal to 0 is a no-op; K equal to 0 writes zeros. K below 2^24
- * (SSD_ERR_UNSUPPORTED). No output may overlap an input (SSD_ERR_ALIAS).
+ * of the largest of them. M equal to 0 is a no-op; K equal to 0 writes zeros. M and N at most
+ * 2^30 and K at most 2^24 - 16, at most 2^25 tiles of 128 x 128 results and fewer than 2^32
+ * threads in one launch (SSD_ERR_UNSUPPORTED). No output may overlap an input (SSD_ERR_ALIAS).
  * Alignment: 4 bytes for the scales, the element size for out; rows of a and b that start
  * on 16 bytes are read fastest.
  */
