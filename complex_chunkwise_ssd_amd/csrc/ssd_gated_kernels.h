@@ -101,11 +101,29 @@ SSD_DEVICE float softplus(float v)
     return fmaxf(v, 0.f) + log1pf(expf(-fabsf(v)));
 }
 
-// The gates of one value. nk = -k softplus(lam). Near a = 1 the recurrence remembers 1 / (1 - a)
-// steps, and an error of the exponential would add up over them: with w = -l below 1/16,
-// 1 - exp(-w) comes from its series (the first term left out is w^5 / 720 of it, 1e-9) and a is one
-// minus that, right to half a unit; above, 1 - a loses at most four bits. 1 - a^2 is (1 - a)
-// (1 + a) in either case.
+// a = exp(l), l <= 0, and 1 - a. Near a = 1 the recurrence remembers 1 / (1 - a) steps, and an error
+// of the exponential would add up over them: with w = -l below 1/16, 1 - exp(-w) comes from its
+// series (the first term left out is w^5 / 720 of it, 1e-9) and a is one minus that, right to half a
+// unit; above, 1 - a loses at most four bits. Every kernel takes its decays from here, so that an
+// adjoint passes over the same ones as the state.
+struct Decay {
+    float a, rest;
+};
+SSD_DEVICE Decay decay_of(float l)
+{
+    const float w = -l;
+    float s = 1.f / 120.f;
+    s = s * w - 1.f / 24.f;
+    s = s * w + 1.f / 6.f;
+    s = s * w - 0.5f;
+    s = s * w + 1.f;
+    s = s * w;
+    const float e = hw_exp2(kLog2e * l);
+    const bool near = w < 0.0625f;
+    return {near ? 1.f - s : e, near ? s : 1.f - e};
+}
+
+// The gates of one value. nk = -k softplus(lam); 1 - a^2 is (1 - a) (1 + a).
 struct Gates {
     float i, r, l, a, m;
 };
@@ -115,18 +133,9 @@ SSD_DEVICE Gates gates(float gi, float gr, float nk)
     g.i = sigmoid(gi);
     g.r = sigmoid(gr);
     g.l = nk * g.r;
-    const float w = -g.l;
-    float s = 1.f / 120.f;
-    s = s * w - 1.f / 24.f;
-    s = s * w + 1.f / 6.f;
-    s = s * w - 0.5f;
-    s = s * w + 1.f;
-    s = s * w;
-    const float e = hw_exp2(kLog2e * g.l);
-    const bool near = w < 0.0625f;
-    const float rest = near ? s : 1.f - e;
-    g.a = near ? 1.f - s : e;
-    g.m = hw_sqrt(rest * (1.f + g.a));
+    const Decay d = decay_of(g.l);
+    g.a = d.a;
+    g.m = hw_sqrt(d.rest * (1.f + d.a));
     return g;
 }
 
@@ -429,7 +438,7 @@ SSD_KERNEL(64 * WAVES) void gated_bwd_summary_kernel(GatedParams p)
             const bool in = t + k < g.lim;
 #pragma unroll
             for (int c = 0; c < CH; ++c) {
-                const float a = in ? hw_exp2(kLog2e * (nk[c] * sigmoid(gated_value<T, CH>(rr[k], c)))) : 1.f;
+                const float a = in ? decay_of(nk[c] * sigmoid(gated_value<T, CH>(rr[k], c))).a : 1.f;
                 A[c] *= a;
                 V[c] = a * (V[c] + (in ? gated_value<T, CH>(rh[k], c) : 0.f));
             }

@@ -26,4 +26,22 @@ def gated_lengths_lowest(run):
         assert np.array_equal(got[1][0], init[0]) and not got[0][0].any()
 
 
-ALL = {f.__name__: f for f in (gated_lengths_lowest,)}
+def gated_adjoint_takes_the_decays_of_the_forward(run):
+    """One state that only decays, and one gradient that comes back to it over several segments:
+    with a = 1 (a closed decay gate) at every token but one or two, their product is rounded once at most
+    and both directions give the same bits."""
+    for kind, T, C, tokens in (("f32", 1000, 130, (600,)), ("f32", 1000, 130, (450, 900)), ("bf16", 1500, 256, (700, 1400)),
+                               ("bf16", 1500, 255, (5, 1499))):
+        g = np.random.default_rng(T)
+        zero, one = np.zeros((1, T, C)), np.ones((1, C))
+        gr = np.full((1, T, C), -200.0)
+        gr[:, tokens] = ref.rounded(g.standard_normal((1, len(tokens), C)), kind)
+        full = 1 - np.exp(g.uniform(np.log(1e-6), np.log(0.7), C))
+        lam = np.float32(np.log(np.expm1(-np.log(full) / 8))).astype(np.float64)
+        _, final, states = run.gated(zero, zero, gr, lam, 8.0, kind, init=one, states=True)
+        got = run.gated_backward(zero, zero, gr, lam, 8.0, kind, states, zero, gfinal=one)
+        assert (final < 1).any()
+        assert np.array_equal(got[4], final), (kind, tokens, np.abs(got[4] - final).max())
+
+
+ALL = {f.__name__: f for f in (gated_lengths_lowest, gated_adjoint_takes_the_decays_of_the_forward)}
