@@ -101,6 +101,14 @@ SSD_DEVICE float softplus(float v)
     return fmaxf(v, 0.f) + log1pf(expf(-fabsf(v)));
 }
 
+// -k softplus(lam), l at an open gate: held to a finite number, so that l times a closed gate is 0, and
+// so is l times a decay of 0 in the gradients.
+SSD_DEVICE float decay_rate(float k, float lam)
+{
+    const float most = -3.402823466e38f, rate = -k * softplus(lam);
+    return rate < most ? most : rate;
+}
+
 // a = exp(l), l <= 0, and 1 - a. Near a = 1 the recurrence remembers 1 / (1 - a) steps, and an error
 // of the exponential would add up over them: with w = -l below 1/16, 1 - exp(-w) comes from its
 // series (the first term left out is w^5 / 720 of it, 1e-9) and a is one minus that, right to half a
@@ -123,7 +131,7 @@ SSD_DEVICE Decay decay_of(float l)
     return {near ? 1.f - s : e, near ? s : 1.f - e};
 }
 
-// The gates of one value. nk = -k softplus(lam); 1 - a^2 is (1 - a) (1 + a).
+// The gates of one value. nk: decay_rate; 1 - a^2 is (1 - a) (1 + a).
 struct Gates {
     float i, r, l, a, m;
 };
@@ -247,7 +255,7 @@ SSD_KERNEL(64 * WAVES) void gated_scan_kernel(GatedParams p)
     float nk[CH], carry[CH], decay[CH];
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-        nk[c] = g.live ? -p.k * softplus(p.lam[g.c0 + c]) : 0.f;
+        nk[c] = g.live ? decay_rate(p.k, p.lam[g.c0 + c]) : 0.f;
         carry[c] = 0.f;
         decay[c] = 1.f;
         if (g.live) {
@@ -378,7 +386,7 @@ SSD_KERNEL(64) void gated_step_kernel(GatedParams p)
     const GatedPlace<1> g = gated_place<1>(p);
     if (!g.live)
         return;
-    const float nk = -p.k * softplus(p.lam[g.c0]);
+    const float nk = decay_rate(p.k, p.lam[g.c0]);
     float h = p.init ? p.init[g.b * p.C + g.c0] : 0.f;
     if (p.states)
         p.states[g.b * p.C + g.c0] = h;
@@ -410,7 +418,7 @@ SSD_KERNEL(64 * WAVES) void gated_bwd_summary_kernel(GatedParams p)
     float nk[CH], carry[CH], decay[CH];
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-        nk[c] = g.live ? -p.k * softplus(p.lam[g.c0 + c]) : 0.f;
+        nk[c] = g.live ? decay_rate(p.k, p.lam[g.c0 + c]) : 0.f;
         carry[c] = 0.f;
         decay[c] = 1.f;
     }
@@ -488,7 +496,7 @@ SSD_KERNEL(64 * WAVES) void gated_scan_bwd_kernel(GatedParams p)
     float nk[CH], carry[CH], sum_e[CH];
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-        nk[c] = g.live ? -p.k * softplus(p.lam[g.c0 + c]) : 0.f;
+        nk[c] = g.live ? decay_rate(p.k, p.lam[g.c0 + c]) : 0.f;
         carry[c] = p.gfinal && g.live ? p.gfinal[g.b * p.C + g.c0 + c] : 0.f;
         sum_e[c] = 0.f;
     }
@@ -605,7 +613,7 @@ SSD_KERNEL(64 * WAVES) void gated_scan_bwd_kernel(GatedParams p)
                 right[c] = a * gt;
                 const float ratio = m > 0.f ? l * hw_rcp(m) : 0.f;
                 const float gi = gt * i;
-                e[c] = right[c] * (hb[k][c] * l) - gi * xv * (a * a * ratio);
+                e[c] = right[c] * l * hb[k][c] - gi * xv * (a * a * ratio);  // a l first: it is bounded
                 gx[c] = gi * m;
                 ggi[c] = gx[c] * xv * (1.f - i);
                 ggr[c] = e[c] * (1.f - r);

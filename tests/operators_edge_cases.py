@@ -44,4 +44,26 @@ def gated_adjoint_takes_the_decays_of_the_forward(run):
         assert np.array_equal(got[4], final), (kind, tokens, np.abs(got[4] - final).max())
 
 
-ALL = {f.__name__: f for f in (gated_lengths_lowest, gated_adjoint_takes_the_decays_of_the_forward)}
+def gated_decays_beyond_float32(run):
+    """decay_scale * softplus(lam) past the largest float, large states and gradients: a = 0 and the gradients
+    by the decay are 0, not infinity times zero; a closed gate (r = 0) still keeps the state."""
+    B, T, C = 2, 6, 8
+    for kind in ("f32", "bf16"):
+        for k, lam_at in ((1e30, 1e9), (1e30, 10.0), (8.0, 3e38), (8.0, np.inf)):
+            g = np.random.default_rng(3)
+            x, gi, gr, gh = (ref.rounded(g.standard_normal((B, T, C)), kind) for _ in range(4))
+            lam, init = np.full(C, lam_at), np.full((B, C), 1e10)
+            i = ref.sigmoid(gi)
+            h, final, states = run.gated(x, gi, gr, lam, k, kind, init=init, states=True)
+            bar = 30 * ref.U * np.abs(x) + ref.HALF[kind] * np.abs(i * x)
+            assert (np.abs(h - i * x) <= bar).all()     # a = 0, m = 1
+            gx, ggi, ggr, glam, ginit = run.gated_backward(x, gi, gr, lam, k, kind, states, gh, gfinal=np.ones((B, C)))
+            assert not ggr.any() and not glam.any() and not ginit.any(), (kind, k, lam_at)
+            last = gh + np.concatenate([np.zeros((B, T - 1, C)), np.ones((B, 1, C))], 1)
+            assert (np.abs(gx - i * last) <= 40 * ref.U * np.abs(last) + ref.HALF[kind] * np.abs(i * last)).all()
+            closed = np.full((B, T, C), -np.inf)
+            assert np.array_equal(run.gated(x, gi, closed, lam, k, kind, init=init)[1], np.float32(init))
+
+
+ALL = {f.__name__: f for f in (gated_lengths_lowest, gated_adjoint_takes_the_decays_of_the_forward,
+                               gated_decays_beyond_float32)}
