@@ -655,7 +655,7 @@ SSD_KERNEL(64 * WAVES) void gated_scan_bwd_kernel(GatedParams p)
 }
 
 // g_lam = sigmoid(lam) / softplus(lam) * sum of the shares, in their order (the ratio goes to
-// 1 where lam is so low that both underflow). 64 channels per workgroup, 16 waves.
+// 1, and is 1 where lam is so low that both are 0). 64 channels per workgroup, 16 waves.
 SSD_KERNEL(64 * 16) void gated_lam_kernel(const float *part, int rows, int C, const float *lam, float *out)
 {
     SSD_LDS float sums[16][64];
@@ -675,8 +675,9 @@ SSD_KERNEL(64 * 16) void gated_lam_kernel(const float *part, int rows, int C, co
         for (int i = 0; i < 16; ++i)
             t += sums[i][lane];
         const float v = lam[c];
+        const float e = expf(-fabsf(v));  // of -|v|: exp(-v) would be infinite from lam = -89 down
         const float sp = softplus(v);
-        out[c] = t * (sp > 0.f ? 1.f / (1.f + expf(-v)) / sp : 1.f);
+        out[c] = t * (sp > 0.f ? (v < 0.f ? e : 1.f) / (1.f + e) / sp : 1.f);
     }
 }
 

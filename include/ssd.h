@@ -394,6 +394,10 @@ enum {
  *                allowed when that is 0); needed when batch and C alone give too
  *                few workgroups, the tokens are then cut into segments.
  * Gates, products and the state are float32; h is rounded once to `dtype`.
+ * Where 1 - a^2 lies below 2^-126, the smallest normal float, its root and so the
+ * input's share and the gradients through it may come out as 0 (they are below 2^-63 of
+ * the input). An infinity or a NaN in a sequence makes what follows it in its channel
+ * infinite or NaN.
  * T = 1 is the form for generation: one step on the state.
  * No output may overlap an input or another output (SSD_ERR_ALIAS), but for the
  * state in place. Alignment: the element size. batch equal to 0 is a no-op; T

@@ -65,5 +65,22 @@ def gated_decays_beyond_float32(run):
             assert np.array_equal(run.gated(x, gi, closed, lam, k, kind, init=init)[1], np.float32(init))
 
 
+def gated_lowest_lam(run):
+    """grad_lam where exp(-lam) passes the largest float and softplus(lam) = exp(lam) is denormal: sigmoid /
+    softplus is 1, down to where both are 0. A large state makes the sum a number: -k sigmoid(lam) sum r g h.
+    softplus and l are off by 4 units of the denormals, 2^-149, at most; the rest as elsewhere (below 100 U)."""
+    T, k = 70, 8.0
+    lam = np.array([-60.0, -85, -88, -89, -90, -93, -95, -200])
+    C = len(lam)
+    gr = ref.rounded(np.random.default_rng(4).standard_normal((1, T, C)), "f32")
+    zero, init = np.zeros((1, T, C)), np.float32(np.full((1, C), 1e30)).astype(np.float64)
+    states = run.gated(zero, zero, gr, lam, k, "f32", init=init, states=True)[2]
+    got = run.gated_backward(zero, zero, gr, lam, k, "f32", states, zero, gfinal=np.ones((1, C)))[3]
+    want = -k * np.exp(lam) * ref.sigmoid(gr).sum((0, 1)) * init[0]     # a is 1, g is 1, sigmoid(lam) exp(lam)
+    rel = 100 * ref.U + 4 * 2.0 ** -149 / np.exp(lam)
+    ok = np.abs(got - want) <= rel * np.abs(want)
+    assert ok[:-1].all() and abs(got[-1]) <= 1e-12, got / want
+
+
 ALL = {f.__name__: f for f in (gated_lengths_lowest, gated_adjoint_takes_the_decays_of_the_forward,
-                               gated_decays_beyond_float32)}
+                               gated_decays_beyond_float32, gated_lowest_lam)}
