@@ -66,13 +66,16 @@ SSD_DEVICE float row_sum(float v, float *red)
 
 // 1 / sqrt(v) to little more than half a unit, once per row: a Newton step on the hardware's, its
 // residue 1 - v r^2 without rounding errors of the first order (left out where it is no number: v
-// is 0, infinite or NaN).
-SSD_DEVICE float exact_rsq(float v)
+// is 0, infinite or NaN). The hardware's takes a denormal for 0: small values are scaled by 2^100.
+SSD_DEVICE float exact_rsq(float value)
 {
+    const bool small = value < 0x1p-100f;
+    const float v = small ? value * 0x1p+100f : value;
     const float r = hw_rsq(v);
     const float h = v * r, low = __builtin_fmaf(v, r, -h);
     const float d = __builtin_fmaf(-h, r, 1.f) - low * r;
-    return d * d < 1.f ? __builtin_fmaf(0.5f * r, d, r) : r;
+    const float root = d * d < 1.f ? __builtin_fmaf(0.5f * r, d, r) : r;
+    return small ? root * 0x1p+50f : root;
 }
 
 template <int T, int LANES, int STEPS>

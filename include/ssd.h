@@ -460,8 +460,9 @@ int ssd_gated_scan_backward(const void *x, int64_t x_stride, const void *input_g
  *                and as ssd_fp8_matmul reads them; q is taken of the float32 y.
  *                One of y and q has to be given.
  *   rstd         out, nullable: (rows) float32, for the backward.
- * Sums are float32 and taken of the unrounded s. F at most 16384
- * (SSD_ERR_UNSUPPORTED). eps >= 0. rows equal to 0 is a no-op. No other overlap of
+ * Sums are float32 and taken of the unrounded s: a row's sum of squares has to stay below
+ * 2^128, and without an epsilon a row whose mean square is below 2^-150 counts as zeros (its
+ * rstd is infinite). F at most 16384 (SSD_ERR_UNSUPPORTED). eps >= 0. rows equal to 0 is a no-op. No other overlap of
  * outputs (SSD_ERR_ALIAS). Alignment: the element size.
  */
 int ssd_rms_norm(const void *x, int64_t x_stride, const void *residual, int64_t residual_stride,

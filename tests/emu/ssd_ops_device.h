@@ -11,9 +11,11 @@ typedef int v8i __attribute__((ext_vector_type(8)));
 SSD_DEVICE uint32_t f2u(float v) { return __builtin_bit_cast(uint32_t, v); }
 SSD_DEVICE float u2f(uint32_t v) { return __builtin_bit_cast(float, v); }
 
-SSD_DEVICE float hw_rcp(float x) { return 1.f / x; }
-SSD_DEVICE float hw_sqrt(float x) { return sqrtf(x); }
-SSD_DEVICE float hw_rsq(float x) { return 1.f / sqrtf(x); }
+// The hardware's take a denormal argument for zero, and give zero for a denormal result.
+SSD_DEVICE float emu_flushed(float x) { return fabsf(x) < 1.17549435e-38f ? copysignf(0.f, x) : x; }
+SSD_DEVICE float hw_rcp(float x) { return emu_flushed(1.f / emu_flushed(x)); }
+SSD_DEVICE float hw_sqrt(float x) { return sqrtf(emu_flushed(x)); }
+SSD_DEVICE float hw_rsq(float x) { return 1.f / sqrtf(emu_flushed(x)); }
 
 // e4m3: nearest, ties to even; NaN stays NaN; past the border to overflow NaN as well.
 SSD_DEVICE uint32_t emu_e4m3(float v)

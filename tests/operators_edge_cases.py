@@ -82,5 +82,25 @@ def gated_lowest_lam(run):
     assert ok[:-1].all() and abs(got[-1]) <= 1e-12, got / want
 
 
+def norm_of_small_rows(run):
+    """Rows whose mean square is denormal, without an epsilon: still normed. Each square and the mean
+    are off by half a unit of the denormals, 2^-150, so v by 2^-149 and rstd by 2^-150 / v. A row of zeros has
+    no norm; rows next to it do not see it."""
+    F = 200
+    g = np.random.default_rng(5)
+    x = g.standard_normal((7, F)) * np.array([1e-15, 1e-18, 2e-19, 3e-20, 1e-20, 3e-21, 0.0])[:, None]
+    w = np.float32(1 + 0.3 * g.standard_normal(F)).astype(np.float64)
+    for kind in ("f32", "bf16"):
+        v = ref.rounded(x, kind)
+        got = run.norm(v, None, w, 0.0, kind, fp8=False)
+        mean = (v[:6] ** 2).mean(1)
+        rel = 40 * ref.U + 2.0 ** -150 / mean
+        want = 1 / np.sqrt(mean)
+        assert (np.abs(got["rstd"][:6] - want) <= rel * want).all(), got["rstd"][:6] / want
+        y = v[:6] * want[:, None] * w
+        assert (np.abs(got["y"][:6] - y) <= (rel[:, None] + 4 * ref.U + ref.HALF[kind]) * np.abs(y)).all()
+        assert np.isnan(got["y"][6]).all() and np.isposinf(got["rstd"][6])
+
+
 ALL = {f.__name__: f for f in (gated_lengths_lowest, gated_adjoint_takes_the_decays_of_the_forward,
-                               gated_decays_beyond_float32, gated_lowest_lam)}
+                               gated_decays_beyond_float32, gated_lowest_lam, norm_of_small_rows)}
