@@ -23,7 +23,7 @@ def hipcc_command(out: str, extra=()):
         "hipcc", "--offload-arch=" + ARCH, "-O3", "-std=c++17", "-fPIC", "-shared",
         # keep hipcc from forming packed fp32 instructions on its own
         "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
-        "-Wl,-soname,libssd.so", "-I" + INCLUDE, "-I" + CSRC, *extra,
+        "-I" + INCLUDE, "-I" + CSRC, *extra,
         *(os.path.join(CSRC, f) for f in SOURCES), "-o", out,
     ]
 
@@ -40,8 +40,7 @@ def binding_command(out: str):
         "-I" + INCLUDE, "-I" + include, "-I" + os.path.join(include, "torch", "csrc", "api", "include"),
         "-I/opt/rocm/include", "-I" + sysconfig.get_paths()["include"],
         os.path.join(CSRC, "ssd_ops_binding.cpp"), "-o", out,
-        LIB, "-L" + os.path.join(torch_dir, "lib"), "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch",
-        "-ltorch_python", "-Wl,-rpath,$ORIGIN",
+        "-L" + os.path.join(torch_dir, "lib"), "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch", "-ltorch_python",
     ]
 
 

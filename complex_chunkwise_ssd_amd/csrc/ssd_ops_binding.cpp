@@ -4,9 +4,14 @@
 // steps in Python took longer than the kernels (12 us a call against 3 us).
 #include <torch/extension.h>
 
+#include <pybind11/functional.h>
+#include <pybind11/stl.h>
+
 #include <c10/core/DeviceGuard.h>
 #include <c10/hip/HIPStream.h>
 
+#include <functional>
+#include <map>
 #include <optional>
 #include <string>
 #include <tuple>
@@ -18,6 +23,37 @@ namespace {
 using at::Tensor;
 using std::optional;
 namespace py = pybind11;
+
+// The entry points of the library that the package loaded, by address: the loader would take the
+// first library of that name in the process, whichever file it came from.
+#define SSD_OPERATORS(F)                                                              \
+    F(ssd_gated_scan_workspace_bytes) F(ssd_gated_scan)                               \
+    F(ssd_gated_scan_backward_workspace_bytes) F(ssd_gated_scan_backward)             \
+    F(ssd_rms_norm) F(ssd_rms_norm_backward_workspace_bytes) F(ssd_rms_norm_backward) \
+    F(ssd_fp8_quantise) F(ssd_fp8_matmul_workspace_bytes) F(ssd_fp8_matmul)
+struct Library {
+#define F(name) decltype(&::name) name = nullptr;
+    SSD_OPERATORS(F)
+#undef F
+} library;
+
+void bind(const std::function<uintptr_t(const char *)> &address)
+{
+    Library found;
+#define F(name) found.name = (decltype(found.name))address(#name);
+    SSD_OPERATORS(F)
+#undef F
+    library = found;
+}
+
+std::map<std::string, uintptr_t> bound()
+{
+    std::map<std::string, uintptr_t> r;
+#define F(name) r[#name] = (uintptr_t)library.name;
+    SSD_OPERATORS(F)
+#undef F
+    return r;
+}
 
 [[noreturn]] void bad(const std::string &what) { throw py::value_error(what); }
 
@@ -31,6 +67,8 @@ std::string text(at::IntArrayRef s)
 
 void need_gpu(const Tensor &t)
 {
+    if (!library.ssd_fp8_matmul)
+        throw std::runtime_error("the binding has no library yet (complex_chunkwise_ssd_amd.ops gives it one)");
     if (!t.device().is_cuda())
         bad("tensors must be on a GPU device, got " + t.device().str());
 }
@@ -204,8 +242,8 @@ gated_scan(const Tensor &x, const Tensor &gi, const Tensor &gr, const Tensor &la
     const Tensor h = output(h_, "h", g.type, x.sizes(), g.dev);
     const auto fin = maybe_output(final_, "final_state", at::kFloat, {g.B, g.C}, g.dev, want_final);
     const auto cs = maybe_output(states_, "chunk_states", at::kFloat, {g.B, g.chunks, g.C}, g.dev, want_states);
-    const Workspace ws = workspace_of(ws_, ssd_gated_scan_workspace_bytes(g.B, g.T, g.C, g.dtype), g.dev);
-    check_status(ssd_gated_scan(at_of(x), g.sx, at_of(gi), g.si, at_of(gr), g.sr, at_of<float>(lam), (float)k,
+    const Workspace ws = workspace_of(ws_, library.ssd_gated_scan_workspace_bytes(g.B, g.T, g.C, g.dtype), g.dev);
+    check_status(library.ssd_gated_scan(at_of(x), g.sx, at_of(gi), g.si, at_of(gr), g.sr, at_of<float>(lam), (float)k,
                                 g.dtype, g.B, g.T, g.C, at_of<float>(init), at_of<int32_t>(lengths), at_of(h),
                                 at_of<float>(fin), at_of<float>(cs), ws.at, ws.bytes, stream_of(g.dev)),
                  "ssd_gated_scan");
@@ -232,8 +270,8 @@ gated_scan_backward(const Tensor &x, const Tensor &gi, const Tensor &gr, const T
     const Tensor glam = output(glam_, "grad lam", at::kFloat, {g.C}, g.dev);
     const auto ginit = maybe_output(ginit_, "grad initial_state", at::kFloat, {g.B, g.C}, g.dev, want_init);
     const Workspace ws =
-        workspace_of(ws_, ssd_gated_scan_backward_workspace_bytes(g.B, g.T, g.C, g.dtype), g.dev);
-    check_status(ssd_gated_scan_backward(at_of(x), g.sx, at_of(gi), g.si, at_of(gr), g.sr, at_of<float>(lam),
+        workspace_of(ws_, library.ssd_gated_scan_backward_workspace_bytes(g.B, g.T, g.C, g.dtype), g.dev);
+    check_status(library.ssd_gated_scan_backward(at_of(x), g.sx, at_of(gi), g.si, at_of(gr), g.sr, at_of<float>(lam),
                                          (float)k, g.dtype, g.B, g.T, g.C, at_of<float>(states),
                                          at_of<int32_t>(lengths), at_of(grad_h), at_of<float>(grad_final),
                                          at_of(gx), at_of(ggi), at_of(ggr), at_of<float>(glam),
@@ -265,7 +303,7 @@ rms_norm(const Tensor &x, const Tensor &weight, const optional<Tensor> &residual
     const auto q = maybe_output(q_, "q", at::kFloat8_e4m3fn, x.sizes(), dev, fp8);
     const auto scale = maybe_output(scale_, "scale", at::kFloat, {(F + 127) / 128, rows}, dev, q.has_value());
     const auto rstd = maybe_output(rstd_, "rstd", at::kFloat, {rows}, dev, want_rstd);
-    check_status(ssd_rms_norm(at_of(x), sx, at_of(residual), sr, at_of<float>(weight), dtype, rows, F,
+    check_status(library.ssd_rms_norm(at_of(x), sx, at_of(residual), sr, at_of<float>(weight), dtype, rows, F,
                               (float)eps, at_of(y), at_of(s), at_of<uint8_t>(q), at_of<float>(scale),
                               at_of<float>(rstd), stream_of(dev)),
                  "ssd_rms_norm");
@@ -292,8 +330,8 @@ std::tuple<Tensor, Tensor> rms_norm_backward(const Tensor &s, const Tensor &weig
     const c10::DeviceGuard guard(dev);
     const Tensor gx = output(gx_, "grad_x", type, s.sizes(), dev);
     const Tensor gw = output(gw_, "grad_weight", at::kFloat, {F}, dev);
-    const Workspace ws = workspace_of(ws_, ssd_rms_norm_backward_workspace_bytes(rows, F), dev);
-    check_status(ssd_rms_norm_backward(at_of(s), ss, at_of<float>(weight), at_of<float>(rstd), at_of(grad_y),
+    const Workspace ws = workspace_of(ws_, library.ssd_rms_norm_backward_workspace_bytes(rows, F), dev);
+    check_status(library.ssd_rms_norm_backward(at_of(s), ss, at_of<float>(weight), at_of<float>(rstd), at_of(grad_y),
                                        sg, at_of(grad_residual), sr, dtype, rows, F, at_of(gx),
                                        at_of<float>(gw), ws.at, ws.bytes, stream_of(dev)),
                  "ssd_rms_norm_backward");
@@ -327,7 +365,7 @@ std::tuple<Tensor, Tensor> fp8_quantise(const Tensor &x, int64_t block_rows, boo
     const Tensor scale = block_rows == 1
                              ? output(scale_, "scale", at::kFloat, {(K + 127) / 128, R}, dev)
                              : output(scale_, "scale", at::kFloat, {(R + 127) / 128, (K + 127) / 128}, dev);
-    check_status(ssd_fp8_quantise(at_of(x), sx, dtype, rows, cols, block_rows, transpose, at_of<uint8_t>(q), sq,
+    check_status(library.ssd_fp8_quantise(at_of(x), sx, dtype, rows, cols, block_rows, transpose, at_of<uint8_t>(q), sq,
                                   at_of<float>(scale), stream_of(dev)),
                  "ssd_fp8_quantise");
     return {q, scale};
@@ -359,8 +397,8 @@ Tensor fp8_matmul(const Tensor &a, const Tensor &a_scale, const Tensor &b, const
     const int dt = out_dtype == at::kBFloat16 ? SSD_BF16 : SSD_F32;
     const uintptr_t bits = (uintptr_t)a.data_ptr() | (uintptr_t)b.data_ptr() | (uintptr_t)sa | (uintptr_t)sb;
     const int on16 = bits % 16 == 0 && sa < (1 << 24) && sb < (1 << 24);
-    const Workspace ws = workspace_of(ws_, ssd_fp8_matmul_workspace_bytes(M, N, K, block_rows, dt, on16), dev);
-    check_status(ssd_fp8_matmul(at_of<uint8_t>(a), sa, at_of<float>(a_scale), at_of<uint8_t>(b), sb,
+    const Workspace ws = workspace_of(ws_, library.ssd_fp8_matmul_workspace_bytes(M, N, K, block_rows, dt, on16), dev);
+    check_status(library.ssd_fp8_matmul(at_of<uint8_t>(a), sa, at_of<float>(a_scale), at_of<uint8_t>(b), sb,
                                 at_of<float>(b_scale), M, N, K, block_rows, dt, at_of(out), so, ws.at, ws.bytes,
                                 stream_of(dev)),
                  "ssd_fp8_matmul");
@@ -371,6 +409,8 @@ Tensor fp8_matmul(const Tensor &a, const Tensor &a_scale, const Tensor &b, const
 
 PYBIND11_MODULE(TORCH_EXTENSION_NAME, m)
 {
+    m.def("bind", &bind);
+    m.def("bound", &bound);
     m.def("row_stride", [](const Tensor &t) { return row_stride(t, "t"); });
     m.def("gated_scan", &gated_scan);
     m.def("gated_scan_backward", &gated_scan_backward);

@@ -60,11 +60,12 @@ def _binding():
     global _loaded
     if _loaded is None:
         from . import load_library
-        load_library()
+        lib = load_library()
         try:
             from . import _binding as module
         except ImportError as e:
             raise OSError("_binding.so not loaded (%s); build it with `python -m complex_chunkwise_ssd_amd.build`" % e)
+        module.bind(lambda name: ctypes.cast(getattr(lib, name), ctypes.c_void_p).value)
         _loaded = module
     return _loaded
 
