@@ -101,12 +101,15 @@ SSD_KERNEL(NormShape<LANES>::threads) void rms_norm_kernel(NormParams p)
     const int64_t end = (p.rows + Shape::rows - 1) / Shape::rows * Shape::rows;
     const int64_t last = p.rows - 1;
     auto fetch = [&](int64_t r) {
-        r = r < last ? r : last;  // rows past the end are computed and not stored
+        // rows past the end are computed and not stored; the last row's residual is not read for
+        // them, which may be in place and so be written by the row's own lanes
+        const bool in = r <= last;
+        r = in ? r : last;
 #pragma unroll
         for (int k = 0; k < STEPS; ++k) {
             rx[k] = load8<T>(x + (r * p.x_stride + (n[k] > 0 ? at[k] : 0)) * E, n[k]);
             if (res)
-                rr[k] = load8<T>(res + (r * p.res_stride + (n[k] > 0 ? at[k] : 0)) * E, n[k]);
+                rr[k] = load8<T>(res + (r * p.res_stride + (n[k] > 0 ? at[k] : 0)) * E, in ? n[k] : 0);
         }
     };
     fetch(row);

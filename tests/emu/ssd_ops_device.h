@@ -125,19 +125,64 @@ SSD_DEVICE v4f mfma_bf16_16x16x32(v4u a, v4u b, v4f c)
     return d;
 }
 
+// Loads straight into shared memory. Each lane's bytes arrive when its wave waits for them and not
+// before, so that a read without the wait finds what was there. With shuffled threads, and under
+// ThreadSanitizer, some (all) arrive at once as well, as they may: a load into what another wave still
+// reads then shows. A workgroup that ends with loads in flight ends the process.
+struct EmuLoad {
+    void *at;
+    char data[16];
+    int n;
+};
+struct EmuLoads {
+    EmuLoad load[16];
+    int count;
+    int64_t block;
+};
+static EmuLoads emu_loads[1024];
+
+SSD_DEVICE void emu_async(void *at, const void *data, int n)
+{
+    EmuLoads &l = emu_loads[thread_id()];
+    if (l.count > 0 && l.block != block_id()) {
+        fprintf(stderr, "emu: workgroup %lld ended with loads in flight\n", (long long)l.block);
+        abort();
+    }
+    if (l.count == 16) {
+        fprintf(stderr, "emu: more loads in flight than are emulated\n");
+        abort();
+    }
+#ifdef EMU_TSAN
+    const bool now = true;
+#else
+    const bool now = emu::g_shuffle & 1;
+#endif
+    if (now)
+        memcpy(at, data, (size_t)n);
+    l.block = block_id();
+    EmuLoad &e = l.load[l.count++];
+    e.at = at;
+    e.n = n;
+    memcpy(e.data, data, (size_t)n);
+}
 SSD_DEVICE void async_load16(buf_t r, uint32_t off, void *lds)
 {
     const v4f v = buf_load4(r, off);
-    memcpy((char *)lds + 16 * (thread_id() & 63), &v, 16);
+    emu_async((char *)lds + 16 * (thread_id() & 63), &v, 16);
 }
 SSD_DEVICE void async_load4(buf_t r, uint32_t off, void *lds)
 {
     const uint32_t v = buf_load_u32(r, off);
-    memcpy((char *)lds + 4 * (thread_id() & 63), &v, 4);
+    emu_async((char *)lds + 4 * (thread_id() & 63), &v, 4);
 }
 template <int n>
 SSD_DEVICE void async_wait()
 {
+    static_assert(n == 0, "a wait for some of the loads is not emulated");
+    EmuLoads &l = emu_loads[thread_id()];
+    for (int i = 0; i < l.count; ++i)
+        memcpy(l.load[i].at, l.load[i].data, (size_t)l.load[i].n);
+    l.count = 0;
 }
 SSD_DEVICE void bare_barrier() { block_sync(); }
 
