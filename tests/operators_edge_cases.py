@@ -102,5 +102,91 @@ def norm_of_small_rows(run):
         assert np.isnan(got["y"][6]).all() and np.isposinf(got["rstd"][6])
 
 
+def _over(v, scale):
+    """v / scale in float32, rounded once more to the nearest e4m3 value (ties to even), as values."""
+    t = (np.float32(v) / np.float32(scale)).astype(np.float64)
+    _, e = np.frexp(t)
+    step = 2.0 ** (np.maximum(e - 1, -6) - 3)
+    return np.rint(t / step) * step
+
+
+def quantise_is_a_division(run):
+    """Scales and values bit for bit those of float32 divisions: bfloat16 values often lie on a border of
+    two e4m3 values, where half a unit decides."""
+    for kind in ("bf16", "f32"):
+        for block_rows, turn in ((1, False), (1, True), (128, False), (128, True)):
+            x = ref.rounded(np.random.default_rng(7).standard_normal((256, 384)), kind)
+            q, scale = run.quantise(x, kind, block_rows, turn)
+            v = x.T if turn else x
+            R, K = v.shape
+            top = np.abs(v).reshape(R // block_rows, block_rows, K // 128, 128).max((1, 3))
+            want = np.float32(top) / np.float32(448)
+            assert np.array_equal(scale, want.T if block_rows == 1 else want)
+            full = np.repeat(np.repeat(want, block_rows, 0), 128, 1)
+            assert np.array_equal(ref.E4M3[q], _over(v, full)), (kind, block_rows, turn)
+
+
+# One value's largest relative errors in U for gates of any size, as operators_ref derives them for gates
+# within 6: sigmoid(v) is off by 3 |v| + 5, l by 8 more; a by |l| (that + 3) + 2; 1 - a from the series (l below
+# 1/16) by 8 and l's error, else by a's times a / (1 - a); its root by half of that and 4.
+def _gate_errors(gi, gr, l, a):
+    e_i, e_r = 3 * np.abs(gi) + 5, 3 * np.abs(gr) + 5
+    e_l = e_r + 8
+    e_a = np.abs(l) * (e_l + 3) + 2
+    near, far = (8 + e_l) / 2, e_a * a / np.maximum(1 - a, 1e-3) / 2
+    border = np.abs(-l - 0.0625) < 1e-3
+    e_m = 4 + np.where(border, np.maximum(near, far), np.where(-l < 0.0625, near, far))
+    return e_i, e_r, e_l, e_a, e_m
+
+
+def gated_extreme_gates(run):
+    """Gates saturated at both ends, lam from where a = 1 to where it is 0, no decay at all: one token from a
+    given state, and its gradients, against float64."""
+    for kind in ("f32", "bf16"):
+        g = np.random.default_rng(8)
+        at = np.array([-80.0, -30, -12, -3, 0, 3, 12, 30, 80])
+        gi, gr = (ref.rounded(v.reshape(1, 1, -1), kind) for v in np.meshgrid(at, at))
+        for k in (0.0, 1e-3, 8.0):
+            for lam_at in (-20.0, -5, 0, 5, 50):
+                C = gi.shape[2]
+                x, gh = (ref.rounded(g.standard_normal((1, 1, C)), kind) for _ in range(2))
+                init, gf = (np.float32(g.standard_normal((1, C))).astype(np.float64) for _ in range(2))
+                lam = np.full(C, lam_at)
+                k = float(np.float32(k))
+                i, r, l, a, m = ref.gates(gi, gr, lam, k)
+                e_i, e_r, e_l, e_a, e_m = _gate_errors(gi, gr, l, a)
+                u = m * i * x
+                want = a * init[:, None] + u
+                err = ref.U * ((e_a + 3) * a * np.abs(init[:, None]) + (e_m + e_i + 4) * np.abs(u) + 2 * np.abs(want))
+                # below 2^-126 the hardware's results and roots' arguments may be flushed to zero
+                flush = 2.0 ** -63 * np.abs(x) * (1 - a * a < 2.0 ** -125) + 2.0 ** -120
+                h, final, states = run.gated(x, gi, gr, lam, k, kind, init=init, states=True)
+                ref.close(h, want, err + flush, kind, "h")
+                ref.close(final, want[:, 0], (err + flush)[:, 0], "f32", "final")
+                gx, ggi, ggr, glam, ginit = run.gated_backward(x, gi, gr, lam, k, kind, states, gh, gfinal=gf)
+                adj = gh + gf[:, None]
+                ratio = np.where(m > 0, l / np.where(m > 0, m, 1), 0)
+                w_gx = adj * m * i
+                rel = (e_m + e_i + 6) * ref.U
+                ref.close(gx, w_gx, rel * np.abs(w_gx) + np.abs(adj) * flush, kind, "grad x")
+                w_ggi = w_gx * x * (1 - i)      # 1 - i is off by i's error and half a unit of 1
+                one_i = (e_i * i + 1) * ref.U
+                ref.close(ggi, w_ggi, np.abs(w_gx * x) * (rel * (1 - i) + 2 * one_i + 4 * ref.U) + np.abs(adj * x) * flush, kind,
+                          "grad input_gate")
+                one, two = adj * a * init[:, None] * l, adj * i * x * a * a * ratio
+                e_err = ref.U * ((e_a + e_l + 8) * np.abs(one) + (e_i + 2 * e_a + e_l + e_m + 12) * np.abs(two)) + \
+                    np.abs(adj * x) * flush
+                e = one - two
+                one_r = (e_r * r + 1) * ref.U
+                ref.close(ggr, e * (1 - r), e_err * (1 - r) + (np.abs(one) + np.abs(two)) * (2 * one_r + 4 * ref.U), kind,
+                          "grad decay_gate")
+                factor = ref.sigmoid(lam) / ref.softplus(lam)
+                ref.close(glam, factor * e[0, 0], factor * (e_err + 20 * ref.U * (np.abs(one) + np.abs(two)))[0, 0], "f32", "grad lam")
+                # a gf + (a gh): each product is rounded for itself, before the sum, which may cancel
+                parts = np.abs(gh) + np.abs(gf[:, None])
+                ref.close(ginit, (a * adj)[:, 0], (ref.U * (e_a + 4) * a * parts + 2.0 ** -120)[:, 0], "f32", "grad init")
+
+
 ALL = {f.__name__: f for f in (gated_lengths_lowest, gated_adjoint_takes_the_decays_of_the_forward,
-                               gated_decays_beyond_float32, gated_lowest_lam, norm_of_small_rows)}
+                               gated_decays_beyond_float32, gated_lowest_lam, norm_of_small_rows,
+                               quantise_is_a_division, gated_extreme_gates)}
