@@ -36,9 +36,9 @@ def binding_command(out: str):
     include = os.path.join(torch_dir, "include")
     return [
         "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-D__HIP_PLATFORM_AMD__=1",
-        "-DTORCH_API_INCLUDE_EXTENSION_H", "-DTORCH_EXTENSION_NAME=_binding", "-w",
-        "-I" + INCLUDE, "-I" + include, "-I" + os.path.join(include, "torch", "csrc", "api", "include"),
-        "-I/opt/rocm/include", "-I" + sysconfig.get_paths()["include"],
+        "-DTORCH_API_INCLUDE_EXTENSION_H", "-DTORCH_EXTENSION_NAME=_binding", "-Wall", "-Wextra",
+        "-I" + INCLUDE, "-isystem", include, "-isystem", os.path.join(include, "torch", "csrc", "api", "include"),
+        "-isystem", "/opt/rocm/include", "-isystem", sysconfig.get_paths()["include"],
         os.path.join(CSRC, "ssd_ops_binding.cpp"), "-o", out,
         "-L" + os.path.join(torch_dir, "lib"), "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch", "-ltorch_python",
     ]

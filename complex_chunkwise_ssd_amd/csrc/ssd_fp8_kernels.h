@@ -128,8 +128,8 @@ SSD_KERNEL(256) void fp8_pack_kernel(const uint8_t *x, int64_t stride, int64_t r
 // The large form: a workgroup of 8 waves, 4 along b's rows and 2 along a's, each 64 rows of b by
 // 16 MB rows of a: 256 x 32 MB results. The next block's rows go straight into the other of two
 // stages of shared memory, in five parts between the MFMAs, so that a compute unit holds one
-// workgroup and two waves per SIMD. A wave reads 12 16-byte pieces per 32 MFMAs (MB = 8), three
-// quarters of the shared memory's rate, without bank conflicts.
+// workgroup and two waves per SIMD. A wave reads 24 16-byte pieces per 32 MFMAs (MB = 8; 8 of b, 16 of a),
+// three quarters of the shared memory's rate, without bank conflicts.
 //
 // Measured: 8192 x 8192 x 8192 to bfloat16 475 us (2310 Tflop/s at 1.9 GHz, the MFMAs busy 53 % of the
 // time), to float32 1020 us (1080); 65536 x 5136 x 1024 410 to 450 us (1690 to 1530), of

@@ -7,8 +7,8 @@
 //     g_decay = E (1 - r)     g_lam = sigmoid(lam) / softplus(lam) sum_t E
 // (l / m and not 1 / m: as r goes to 0 so do l and m, and their ratio with them).
 //
-// Both are bound by memory in float32 and by the arithmetic of the gates in bfloat16 (four
-// transcendentals, a root and some 25 other instructions a value, all at the vector unit's rate).
+// Both are bound by memory in float32 and by the arithmetic of the gates in bfloat16 (three
+// exponentials, two reciprocals, a root and some 25 other instructions a value, all on the vector unit).
 // Measured, with a copy at 5160 GB/s: 4 x 2048 x 4096 float32, 4.74 TB/s forward and 4.63
 // backward; 32 x 2048 x 1024 bfloat16 125 us (4.3 TB/s), gradients 218 us (4.3 TB/s); cut into
 // segments, 3 x 16411 x 1000 float32, 220 us (90 of them the pass before).

@@ -211,6 +211,10 @@ Fp8Plan fp8_plan(int64_t M, int64_t N, int64_t K, int out_dtype, bool aligned_ro
         const int waves = groups < 512 && kb > 8 ? (mb == 1 ? 16 : 8) : 4;
         const double few = 3 + (double)((groups + 511) / 512) * (double)((kb + waves - 1) / waves) *
                                    (mb == 1 ? 1.2 : mb == 2 ? 1.4 : 2.2);
+        // The large form's model leaves out some 6 us (10 where it lays rows out anew first) of what it
+        // takes at these sizes. Over 240 products (M 1 to 64, N 64 to 16384, K 512 to 16384, both results),
+        // each measured in both forms, the choice is 2.1 % slower than the better one on average
+        // (without the 6 and 10: 3.7 %), at worst 64 x 5136 x 16384 to float32, 75 against 30.
         if (few < best + (aligned_rows ? 6. : 10.)) {
             p.few = true;
             p.mb = mb;

@@ -139,7 +139,8 @@ def fp8_quantise(x, block_rows: int = 1, transpose: bool = False, q=None, scale=
     block_rows 1: 1 x 128 blocks, scale (ceil(K / 128), R); 128: 128 x 128 blocks, scale
     (ceil(R / 128), ceil(K / 128)). With transpose the same of x turned: q (K, R).
     Returns (q, scale). q's rows start on multiples of 16 bytes (K is padded in memory, not in
-    shape), as fp8_matmul reads them fastest."""
+    shape). fp8_matmul reads such rows as they lie where K is a multiple of 16; for other K its
+    form for more than a few rows lays both operands out anew in every call."""
     return (_loaded or _binding()).fp8_quantise(x, block_rows, transpose, q, scale)
 
 

@@ -531,7 +531,8 @@ int ssd_fp8_quantise(const void *x, int64_t x_stride, int dtype, int64_t rows, i
  *   workspace    ssd_fp8_matmul_workspace_bytes(...) bytes, 256-byte aligned (NULL
  *                allowed when that is 0): partial sums where few outputs and a long K
  *                have the sum over k split (they are added in a fixed order), and the
- *                operands laid out anew where their rows do not start on 16 bytes.
+ *                operands laid out anew where their rows do not start on 16 bytes or K is no
+ *                multiple of 16.
  *                rows_on_16: whether they do, that is a, b, a_stride and b_stride are
  *                multiples of 16 and the strides below 2^24.
  * With y = x W^T: forward a = x, b = W (blocks of 128 x 128); grad_x takes a = grad_y and
@@ -542,8 +543,9 @@ int ssd_fp8_quantise(const void *x, int64_t x_stride, int dtype, int64_t rows, i
  * of the largest of them. M equal to 0 is a no-op; K equal to 0 writes zeros. M and N at most
  * 2^30 and K at most 2^24 - 16, at most 2^25 tiles of 128 x 128 results and fewer than 2^32
  * threads in one launch (SSD_ERR_UNSUPPORTED). No output may overlap an input (SSD_ERR_ALIAS).
+ * The product of the two scales of a block has to be a float32 number.
  * Alignment: 4 bytes for the scales, the element size for out; rows of a and b that start
- * on 16 bytes are read fastest.
+ * on 16 bytes, with K a multiple of 16, are read fastest.
  */
 size_t ssd_fp8_matmul_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t b_block_rows,
                                       int out_dtype, int rows_on_16);
