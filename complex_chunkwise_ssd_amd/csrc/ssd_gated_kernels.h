@@ -10,8 +10,8 @@
 // Both are bound by memory in float32 and by the arithmetic of the gates in bfloat16 (three
 // exponentials, two reciprocals, a root and some 25 other instructions a value, all on the vector unit).
 // Measured, with a copy at 5160 GB/s: 4 x 2048 x 4096 float32, 4.74 TB/s forward and 4.63
-// backward; 32 x 2048 x 1024 bfloat16 125 us (4.3 TB/s), gradients 218 us (4.3 TB/s); cut into
-// segments, 3 x 16411 x 1000 float32, 220 us (90 of them the pass before).
+// backward; 32 x 2048 x 1024 bfloat16 126 us (4.3 TB/s), gradients 214 us (4.4 TB/s); cut into
+// segments, 3 x 16411 x 1000 float32, 273 us, with random lengths 228 us (91 of them the pass before).
 //
 // A composition of steps over a span is a pair (A, U):
 // h -> A h + U. A workgroup walks over the tokens of one block of channels in tiles; its

@@ -14,7 +14,7 @@
 // Bound by memory. Measured in bfloat16 with the residual (a copy runs at 5160 GB/s): 65536 x 1024 to
 // 8 bits 92 us (5.1 TB/s), its gradients 112 us (4.8 TB/s); 32768 x 4096 190 us (4.9 TB/s);
 // 65536 x 64 8.6 us. Eight rows take 2.8 us, mostly the launch. The gradients of float32 rows above
-// 8192 spill 144 bytes a lane and reach 57 % of the copy's rate.
+// 8192 spill 144 bytes a lane and reach 49 to 68 % of the copy's rate (4096 x 9000: 235 us).
 #pragma once
 
 #include <ssd_elem.h>
