@@ -5,6 +5,7 @@ import os
 import shutil
 import subprocess
 import sys
+from concurrent.futures import ThreadPoolExecutor
 
 import pytest
 
@@ -47,26 +48,62 @@ def _run(*cmd):
                           env={**os.environ, "TSAN_OPTIONS": "halt_on_error=1"})
 
 
-def test_bounds(tmp_path):
-    r = _run(_build(harness.ROOT, "ops_emu_main.cpp", tmp_path / "asan", "-fsanitize=address", "-fno-omit-frame-pointer"))
+def _bounds(root):
+    return _run(_build(harness.ROOT, "ops_emu_main.cpp", root / "asan", "-fsanitize=address", "-fno-omit-frame-pointer"))
+
+
+def _races(root):
+    return _run(_build(harness.ROOT, "ops_emu_main.cpp", root / "tsan", "-fsanitize=thread"))
+
+
+def _without_barrier(root):
+    copy = _copy(root, "ssd_gated_kernels.h", "        block_sync();\n        if (SUMMARY) {", "        if (SUMMARY) {")
+    return _run(_build(copy, "ops_emu_main.cpp", root / "planted", "-fsanitize=thread"))
+
+
+WAIT = "        async_wait<0>();\n        bare_barrier();"
+
+
+def _with_wait(root, wait=WAIT):
+    copy = _copy(root, "ssd_fp8_kernels.h", WAIT, wait)
+    return _run(sys.executable, "-c", PLANTED % harness.HERE, _build(copy, "ops_emu_lib.cpp", root / "lib.so", "-fPIC", "-shared"))
+
+
+def _without_wait(root):
+    return _with_wait(root, "        bare_barrier();")
+
+
+@pytest.fixture(scope="module")
+def results(tmp_path_factory):
+    """Every build and run, side by side: name -> its result, once it is there."""
+    root = tmp_path_factory.mktemp("sanitized")
+    with ThreadPoolExecutor(max_workers=5) as pool:
+        futures = {}
+        for job in (_bounds, _races, _without_barrier, _with_wait, _without_wait):
+            (root / job.__name__).mkdir()
+            futures[job.__name__] = pool.submit(job, root / job.__name__)
+        yield lambda name: futures[name].result()
+
+
+def test_bounds(results):
+    r = results("_bounds")
     assert r.returncode == 0 and r.stdout.endswith("OK\n"), r.stdout[-500:] + r.stderr[:3000]
 
 
-def test_no_unordered_access(tmp_path):
-    r = _run(_build(harness.ROOT, "ops_emu_main.cpp", tmp_path / "tsan", "-fsanitize=thread"))
+def test_no_unordered_access(results):
+    r = results("_races")
     assert "WARNING: ThreadSanitizer" not in r.stderr, r.stderr[:6000]
     assert r.returncode == 0 and r.stdout.endswith("OK\n"), r.stdout[-500:] + r.stderr[-2000:]
 
 
-def test_a_missing_barrier_is_reported(tmp_path):
-    root = _copy(tmp_path, "ssd_gated_kernels.h", "        block_sync();\n        if (SUMMARY) {", "        if (SUMMARY) {")
-    r = _run(_build(root, "ops_emu_main.cpp", tmp_path / "planted", "-fsanitize=thread"))
+def test_a_missing_barrier_is_reported(results):
+    r = results("_without_barrier")
     assert "WARNING: ThreadSanitizer: data race" in r.stderr and "gated_scan_kernel" in r.stderr, r.stderr[-3000:]
 
 
-@pytest.mark.parametrize("left_out", [False, True])
-def test_a_missing_wait_shows(tmp_path, left_out):
-    wait = "        async_wait<0>();\n        bare_barrier();"
-    root = _copy(tmp_path, "ssd_fp8_kernels.h", wait, wait if not left_out else "        bare_barrier();")
-    r = _run(sys.executable, "-c", PLANTED % harness.HERE, _build(root, "ops_emu_lib.cpp", tmp_path / "lib.so", "-fPIC", "-shared"))
-    assert ("right" in r.stdout) != left_out, r.stdout + r.stderr[-2000:]
+def test_a_missing_wait_shows(results):
+    r = results("_with_wait")
+    assert r.returncode == 0 and "right" in r.stdout, r.stdout + r.stderr[-2000:]
+    r = results("_without_wait")
+    assert r.returncode != 0 and "right" not in r.stdout and ("off, worst" in r.stderr or "emu:" in r.stderr), \
+        r.stdout + r.stderr[-2000:]
