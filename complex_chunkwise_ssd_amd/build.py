@@ -51,6 +51,8 @@ def _compile(cmd, out: str, tmp: str, verbose: bool):
     if res.returncode != 0:
         sys.stderr.write(res.stdout + res.stderr)
         raise RuntimeError("%s failed for %s" % (cmd[0], os.path.basename(out)))
+    if verbose:
+        sys.stderr.write(res.stderr)  # warnings
     os.replace(tmp, out)
 
 

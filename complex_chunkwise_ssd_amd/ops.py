@@ -2,7 +2,8 @@
 quantisation and the 8-bit product. As for the scan, argument marshalling only (in
 the compiled ``_binding.so``): every step runs in the HIP kernels of ``libssd.so`` on
 the current stream of the tensors' device, and a call that the library rejects raises
-``SSDError``. Tensors of a wrong type, shape, layout or device raise ValueError.
+``SSDError``. Tensors of a wrong type, shape, layout or device raise ValueError. Results carry
+no autograd history, also of inputs that require gradients: the gradients are calls of their own.
 
     h, final_state, chunk_states = gated_scan(x, input_gate, decay_gate, lam)
     grads = gated_scan_backward(x, input_gate, decay_gate, lam, chunk_states, grad_h)
