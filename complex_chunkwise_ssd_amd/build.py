@@ -1,5 +1,5 @@
-"""Compiles the gfx950 library (libssd.so, hipcc) and the compiled part of the Python
-binding (_binding.so, the C++ compiler against torch's headers) in place.
+"""Compiles the gfx950 library (libssd.so, hipcc) and the compiled parts of the Python binding
+(_binding.so, _block_binding.so, the C++ compiler against torch's headers) in place.
 
     python -m complex_chunkwise_ssd_amd.build
 """
@@ -7,20 +7,21 @@ binding (_binding.so, the C++ compiler against torch's headers) in place.
 import os
 import subprocess
 import sys
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libssd.so")
-BINDING = os.path.join(PKG, "_binding.so")
+BINDINGS = {"_binding": "ssd_ops_binding.cpp", "_block_binding": "ssd_block_binding.cpp"}
 ARCH = "gfx950"
-SOURCES = ("ssd_api.hip", "ssd_ops_api.hip")
+SOURCES = ("ssd_api.hip", "ssd_ops_api.hip", "ssd_delta_api.hip")
 
 
 def hipcc_command(out: str, extra=()):
     return [
-        "hipcc", "--offload-arch=" + ARCH, "-O3", "-std=c++17", "-fPIC", "-shared",
+        "hipcc", "--offload-arch=" + ARCH, "-O3", "-std=c++17", "-fPIC", "-shared", "-parallel-jobs=8",
         # keep hipcc from forming packed fp32 instructions on its own
         "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
         "-I" + INCLUDE, "-I" + CSRC, *extra,
@@ -28,7 +29,7 @@ def hipcc_command(out: str, extra=()):
     ]
 
 
-def binding_command(out: str):
+def binding_command(name: str, out: str):
     import sysconfig
 
     import torch
@@ -36,10 +37,10 @@ def binding_command(out: str):
     include = os.path.join(torch_dir, "include")
     return [
         "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-D__HIP_PLATFORM_AMD__=1",
-        "-DTORCH_API_INCLUDE_EXTENSION_H", "-DTORCH_EXTENSION_NAME=_binding", "-Wall", "-Wextra",
+        "-DTORCH_API_INCLUDE_EXTENSION_H", "-DTORCH_EXTENSION_NAME=" + name, "-Wall", "-Wextra",
         "-I" + INCLUDE, "-isystem", include, "-isystem", os.path.join(include, "torch", "csrc", "api", "include"),
         "-isystem", "/opt/rocm/include", "-isystem", sysconfig.get_paths()["include"],
-        os.path.join(CSRC, "ssd_ops_binding.cpp"), "-o", out,
+        os.path.join(CSRC, BINDINGS[name]), "-o", out,
         "-L" + os.path.join(torch_dir, "lib"), "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch", "-ltorch_python",
     ]
 
@@ -57,10 +58,14 @@ def _compile(cmd, out: str, tmp: str, verbose: bool):
 
 
 def build(verbose: bool = False, extra=()) -> str:
-    tmp = LIB + ".tmp%d" % os.getpid()
-    _compile(hipcc_command(tmp, extra), LIB, tmp, verbose)
-    tmp = BINDING + ".tmp%d" % os.getpid()
-    _compile(binding_command(tmp), BINDING, tmp, verbose)
+    tag = ".tmp%d" % os.getpid()
+    jobs = [(hipcc_command(LIB + tag, extra), LIB, LIB + tag)]
+    for name in BINDINGS:
+        so = os.path.join(PKG, name + ".so")
+        jobs.append((binding_command(name, so + tag), so, so + tag))
+    with ThreadPoolExecutor() as pool:
+        for job in [pool.submit(_compile, *j, verbose) for j in jobs]:
+            job.result()
     return LIB
 
 

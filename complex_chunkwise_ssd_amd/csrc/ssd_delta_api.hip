@@ -1,0 +1,273 @@
+// ssd_delta_api.hip -- C ABI of the gated delta rule (declared in include/ssd.h): argument checks,
+// work planning and kernel launches on the caller's stream; nothing is allocated.
+#include "ssd.h"
+
+#include <ssd_delta_kernels.h>
+#include <ssd_host.h>
+
+#include <math.h>
+
+namespace {
+
+using ssd::align256;
+using ssd::aligned;
+using ssd::grid_ok;
+using ssd::kMaxElems;
+using ssd::launch_status;
+
+struct DeltaSizes {
+    int64_t B, T, Hk, Hv, Dk, Dv;
+    int64_t chunks() const { return (T + ssd::kDeltaChunk - 1) / ssd::kDeltaChunk; }
+    int64_t states() const { return B * Hv * Dk * Dv * 4; }  // bytes
+    bool empty() const { return B == 0 || T == 0; }
+};
+
+int check_delta(const DeltaSizes &z, int dtype, float scale)
+{
+    if (!ssd::dtype_ok(dtype) || z.B < 0 || z.T < 0 || z.Hk < 1 || z.Hv < 1 || z.Dk < 1 || z.Dv < 1 ||
+        !(fabsf(scale) <= 1e30f))
+        return SSD_ERR_SHAPE;
+    if (z.Dk > 128 || z.Dv > 256)
+        return SSD_ERR_BLOCK_DIMS;
+    if (z.B > (1LL << 24) || z.T > (1LL << 30) || z.Hk > (1LL << 16) || z.Hv > (1LL << 16))
+        return SSD_ERR_UNSUPPORTED;
+    if (z.Hv % z.Hk != 0)
+        return SSD_ERR_SHAPE;
+    const int64_t column_blocks = (z.Dv + 63) / 64;
+    const int64_t most = column_blocks > z.chunks() ? column_blocks : z.chunks();
+    return grid_ok(z.B * z.Hv * most, 256) ? SSD_OK : SSD_ERR_UNSUPPORTED;
+}
+
+int check_delta_strides(const DeltaSizes &z, int64_t q, int64_t k, int64_t v)
+{
+    if (q < z.Hk * z.Dk || k < z.Hk * z.Dk || v < z.Hv * z.Dv)
+        return SSD_ERR_SHAPE;
+    const int64_t most = q > k ? (q > v ? q : v) : (k > v ? k : v);
+    if (!z.empty() && most > kMaxElems / (z.B * z.T))
+        return SSD_ERR_UNSUPPORTED;
+    return SSD_OK;
+}
+
+bool delta_few(const DeltaSizes &z) { return z.T <= ssd::kDeltaFew; }
+
+size_t delta_frag_bytes(const DeltaSizes &z)
+{
+    return align256((size_t)(z.B * z.Hv * z.chunks()) * ssd::kDeltaFragFloats * 4);
+}
+
+ssd::DeltaParams delta_params(const DeltaSizes &z, const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                              const void *v, int64_t v_stride, const float *g, const float *beta, float scale,
+                              const int32_t *lengths)
+{
+    ssd::DeltaParams p{};
+    p.q = q;
+    p.k = k;
+    p.v = v;
+    p.g = g;
+    p.beta = beta;
+    p.lengths = lengths;
+    p.q_stride = q_stride;
+    p.k_stride = k_stride;
+    p.v_stride = v_stride;
+    p.B = (int)z.B;
+    p.T = (int)z.T;
+    p.Hk = (int)z.Hk;
+    p.Hv = (int)z.Hv;
+    p.Dk = (int)z.Dk;
+    p.Dv = (int)z.Dv;
+    p.chunks = (int)z.chunks();
+    p.columns = (int)((z.Dv + 63) / 64);
+    p.scale = scale;
+    return p;
+}
+
+template <int T>
+int launch_delta_few(const ssd::DeltaParams &p, hipStream_t s)
+{
+    const dim3 grid((unsigned)((int64_t)p.B * p.Hv * p.columns)), block(256);
+    if (p.Dk <= 64)
+        hipLaunchKernelGGL((ssd::delta_few_kernel<T, 4>), grid, block, 0, s, p);
+    else
+        hipLaunchKernelGGL((ssd::delta_few_kernel<T, 8>), grid, block, 0, s, p);
+    return launch_status();
+}
+
+template <int T, int KP>
+int launch_delta(const ssd::DeltaParams &p, hipStream_t s)
+{
+    const dim3 block(256);
+    hipLaunchKernelGGL((ssd::delta_prepare_kernel<T, KP, false>), dim3((unsigned)((int64_t)p.B * p.Hv * p.chunks)), block,
+                       0, s, p);
+    if (int st = launch_status())
+        return st;
+    hipLaunchKernelGGL((ssd::delta_scan_kernel<T, KP>), dim3((unsigned)((int64_t)p.B * p.Hv * p.columns)), block, 0, s, p);
+    return launch_status();
+}
+
+template <int T, int KP>
+int launch_delta_bwd(const ssd::DeltaParams &p, hipStream_t s)
+{
+    const dim3 block(256);
+    hipLaunchKernelGGL((ssd::delta_prepare_kernel<T, KP, true>), dim3((unsigned)((int64_t)p.B * p.Hv * p.chunks)), block,
+                       0, s, p);
+    if (int st = launch_status())
+        return st;
+    hipLaunchKernelGGL((ssd::delta_scan_bwd_kernel<T, KP>), dim3((unsigned)((int64_t)p.B * p.Hv * p.columns)), block, 0, s,
+                       p);
+    if (int st = launch_status())
+        return st;
+    hipLaunchKernelGGL((ssd::delta_grad_kernel<T, KP>), dim3((unsigned)((int64_t)p.B * p.Hk * p.chunks)), block, 0, s, p);
+    return launch_status();
+}
+
+int launch_delta_copy(const float *from, float *to, int64_t n, hipStream_t s)
+{
+    const int64_t blocks = (n + 255) / 256 < 4096 ? (n + 255) / 256 : 4096;
+    if (!to || n == 0 || from == to)
+        return SSD_OK;
+    hipLaunchKernelGGL(ssd::delta_copy_kernel, dim3((unsigned)blocks), dim3(256), 0, s, from, to, n);
+    return launch_status();
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t ssd_gated_delta_workspace_bytes(int64_t batch, int64_t T, int64_t Hk, int64_t Hv, int64_t Dk, int64_t Dv,
+                                       int dtype)
+{
+    const DeltaSizes z{batch, T, Hk, Hv, Dk, Dv};
+    if (check_delta(z, dtype, 1.f) || z.empty() || delta_few(z))
+        return 0;
+    return delta_frag_bytes(z);
+}
+
+int ssd_gated_delta(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                    const float *g, const float *beta, float scale, int dtype, int64_t batch, int64_t T, int64_t Hk,
+                    int64_t Hv, int64_t Dk, int64_t Dv, const float *initial_state, const int32_t *lengths, void *o,
+                    float *final_state, float *chunk_states, void *workspace, size_t workspace_bytes,
+                    ssd_stream_t stream)
+{
+    const DeltaSizes z{batch, T, Hk, Hv, Dk, Dv};
+    if (int st = check_delta(z, dtype, scale))
+        return st;
+    if (int st = check_delta_strides(z, q_stride, k_stride, v_stride))
+        return st;
+    const int e = ssd::elem_size(dtype);
+    if (!aligned(initial_state, 4) || !aligned(final_state, 4))
+        return SSD_ERR_ALIGN;
+    const int64_t tokens = batch * T, heads = tokens * Hv * 4;
+    const size_t need = ssd_gated_delta_workspace_bytes(batch, T, Hk, Hv, Dk, Dv, dtype);
+    const bool in_place = final_state == initial_state;
+    const ssd::Range in[7] = {{q, ssd::span(tokens, Hk * Dk, q_stride, e)}, {k, ssd::span(tokens, Hk * Dk, k_stride, e)},
+                              {v, ssd::span(tokens, Hv * Dv, v_stride, e)}, {g, heads}, {beta, heads},
+                              {lengths, batch * 4}, {in_place ? nullptr : initial_state, z.states()}};
+    const ssd::Range out[4] = {{o, tokens * Hv * Dv * e}, {final_state, z.states()},
+                               {chunk_states, z.states() * z.chunks()}, {workspace, (int64_t)need}};
+    const hipStream_t s = (hipStream_t)stream;
+    if (z.empty()) {
+        if (ssd::overlaps(out + 1, 1, in + 6, 1))
+            return SSD_ERR_ALIAS;
+        return launch_delta_copy(initial_state, final_state, batch * Hv * Dk * Dv, s);
+    }
+    if (!q || !k || !v || !g || !beta || !o)
+        return SSD_ERR_NULL;
+    if (!aligned(q, e) || !aligned(k, e) || !aligned(v, e) || !aligned(o, e) || !aligned(g, 4) || !aligned(beta, 4) ||
+        !aligned(lengths, 4) || !aligned(chunk_states, 4))
+        return SSD_ERR_ALIGN;
+    if (need > 0 && (!workspace || workspace_bytes < need))
+        return SSD_ERR_WORKSPACE;
+    if (need > 0 && !aligned(workspace, 256))
+        return SSD_ERR_ALIGN;
+    // the state in place is its own input, and no other output may reach into it
+    if (ssd::overlaps(out, 4, in, 7))
+        return SSD_ERR_ALIAS;
+    ssd::DeltaParams p = delta_params(z, q, q_stride, k, k_stride, v, v_stride, g, beta, scale, lengths);
+    p.init = initial_state;
+    p.o = o;
+    p.final_state = final_state;
+    p.states = chunk_states;
+    p.tri = (float *)workspace;
+    if (delta_few(z))
+        return dtype == SSD_BF16 ? launch_delta_few<ssd::kBF16>(p, s) : launch_delta_few<ssd::kF32>(p, s);
+    if (dtype == SSD_BF16)
+        return Dk <= 64 ? launch_delta<ssd::kBF16, 2>(p, s) : launch_delta<ssd::kBF16, 4>(p, s);
+    return Dk <= 64 ? launch_delta<ssd::kF32, 2>(p, s) : launch_delta<ssd::kF32, 4>(p, s);
+}
+
+size_t ssd_gated_delta_backward_workspace_bytes(int64_t batch, int64_t T, int64_t Hk, int64_t Hv, int64_t Dk, int64_t Dv,
+                                                int dtype)
+{
+    const DeltaSizes z{batch, T, Hk, Hv, Dk, Dv};
+    if (check_delta(z, dtype, 1.f) || z.empty())
+        return 0;
+    const int64_t each = batch * Hv * z.chunks();
+    return 3 * delta_frag_bytes(z) + align256((size_t)(each * Dk * Dv) * 4) + align256((size_t)(each * 64 * Dv) * 4);
+}
+
+int ssd_gated_delta_backward(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                             int64_t v_stride, const float *g, const float *beta, float scale, int dtype, int64_t batch,
+                             int64_t T, int64_t Hk, int64_t Hv, int64_t Dk, int64_t Dv, const float *chunk_states,
+                             const int32_t *lengths, const void *grad_o, const float *grad_final_state, void *grad_q,
+                             void *grad_k, void *grad_v, float *grad_g, float *grad_beta, float *grad_initial_state,
+                             void *workspace, size_t workspace_bytes, ssd_stream_t stream)
+{
+    const DeltaSizes z{batch, T, Hk, Hv, Dk, Dv};
+    if (int st = check_delta(z, dtype, scale))
+        return st;
+    if (int st = check_delta_strides(z, q_stride, k_stride, v_stride))
+        return st;
+    const int e = ssd::elem_size(dtype);
+    if (!aligned(grad_final_state, 4) || !aligned(grad_initial_state, 4))
+        return SSD_ERR_ALIGN;
+    const int64_t tokens = batch * T, heads = tokens * Hv * 4;
+    const size_t need = ssd_gated_delta_backward_workspace_bytes(batch, T, Hk, Hv, Dk, Dv, dtype);
+    const ssd::Range in[9] = {{q, ssd::span(tokens, Hk * Dk, q_stride, e)}, {k, ssd::span(tokens, Hk * Dk, k_stride, e)},
+                              {v, ssd::span(tokens, Hv * Dv, v_stride, e)}, {g, heads}, {beta, heads},
+                              {lengths, batch * 4}, {chunk_states, z.states() * z.chunks()},
+                              {grad_o, tokens * Hv * Dv * e}, {grad_final_state, z.states()}};
+    const ssd::Range out[7] = {{grad_q, tokens * Hk * Dk * e}, {grad_k, tokens * Hk * Dk * e},
+                               {grad_v, tokens * Hv * Dv * e}, {grad_g, heads}, {grad_beta, heads},
+                               {grad_initial_state, z.states()}, {workspace, (int64_t)need}};
+    const hipStream_t s = (hipStream_t)stream;
+    if (z.empty()) {
+        if (ssd::overlaps(out + 5, 1, in + 8, 1))
+            return SSD_ERR_ALIAS;
+        return launch_delta_copy(grad_final_state, grad_initial_state, batch * Hv * Dk * Dv, s);
+    }
+    if (!q || !k || !v || !g || !beta || !chunk_states || !grad_o || !grad_q || !grad_k || !grad_v || !grad_g ||
+        !grad_beta)
+        return SSD_ERR_NULL;
+    if (!aligned(q, e) || !aligned(k, e) || !aligned(v, e) || !aligned(grad_o, e) || !aligned(grad_q, e) ||
+        !aligned(grad_k, e) || !aligned(grad_v, e) || !aligned(g, 4) || !aligned(beta, 4) || !aligned(lengths, 4) ||
+        !aligned(chunk_states, 4) || !aligned(grad_g, 4) || !aligned(grad_beta, 4))
+        return SSD_ERR_ALIGN;
+    if (!workspace || workspace_bytes < need)
+        return SSD_ERR_WORKSPACE;
+    if (!aligned(workspace, 256))
+        return SSD_ERR_ALIGN;
+    if (ssd::overlaps(out, 7, in, 9))
+        return SSD_ERR_ALIAS;
+    ssd::DeltaParams p = delta_params(z, q, q_stride, k, k_stride, v, v_stride, g, beta, scale, lengths);
+    p.chunk_states = chunk_states;
+    p.go = grad_o;
+    p.gfinal = grad_final_state;
+    p.gq = grad_q;
+    p.gk = grad_k;
+    p.gv = grad_v;
+    p.gg = grad_g;
+    p.gbeta = grad_beta;
+    p.ginit = grad_initial_state;
+    char *at = (char *)workspace;
+    const size_t frags = delta_frag_bytes(z);
+    p.tri = (float *)at;
+    p.tri_t = (float *)(at + frags);
+    p.pt = (float *)(at + 2 * frags);
+    p.gs = (float *)(at + 3 * frags);
+    p.gr = (float *)(at + 3 * frags + align256((size_t)(batch * Hv * z.chunks() * Dk * Dv) * 4));
+    if (dtype == SSD_BF16)
+        return Dk <= 64 ? launch_delta_bwd<ssd::kBF16, 2>(p, s) : launch_delta_bwd<ssd::kBF16, 4>(p, s);
+    return Dk <= 64 ? launch_delta_bwd<ssd::kF32, 2>(p, s) : launch_delta_bwd<ssd::kF32, 4>(p, s);
+}
+
+}  // extern "C"

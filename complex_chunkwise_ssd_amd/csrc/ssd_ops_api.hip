@@ -11,26 +11,16 @@
 
 namespace {
 
+using ssd::align256;
 using ssd::aligned;
+using ssd::dtype_ok;
+using ssd::elem_size;
 using ssd::grid_1d;
+using ssd::grid_ok;
+using ssd::kMaxElems;
 using ssd::launch_status;
 using ssd::overlap_bytes;
-
-constexpr int64_t kMaxThreads = (1LL << 32) - 1;  // of one launch: HIP refuses 2^32 and more
-constexpr int64_t kMaxElems = 1LL << 40;  // of one operand: products of sizes and strides stay in 64 bits
-
-bool grid_ok(int64_t groups, int threads) { return groups <= kMaxThreads / threads; }
-
-size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
-
-bool dtype_ok(int dtype) { return dtype == SSD_F32 || dtype == SSD_BF16; }
-int elem_size(int dtype) { return dtype == SSD_BF16 ? 2 : 4; }
-
-// Bytes from a strided matrix's first element to past its last.
-int64_t span(int64_t rows, int64_t cols, int64_t stride, int elem)
-{
-    return rows > 0 && cols > 0 ? ((rows - 1) * stride + cols) * elem : 0;
-}
+using ssd::span;
 
 // ------------------------------------------------------------------ RMS norm
 

@@ -555,6 +555,92 @@ int ssd_fp8_matmul(const uint8_t *a, int64_t a_stride, const float *a_scale, con
                    int64_t b_block_rows, int out_dtype, void *out, int64_t out_stride,
                    void *workspace, size_t workspace_bytes, ssd_stream_t stream);
 
+/* Tokens between two stored states of the gated delta rule. */
+#define SSD_DELTA_CHUNK 64
+
+/*
+ * ssd_gated_delta -- the gated delta rule: a matrix state that decays by the token and is
+ * corrected along the token's key. For every batch row b and value head h, with the key head
+ * h / (Hv / Hk) and S (Dk, Dv),
+ *
+ *   S' = exp(g_t) S_{t-1}          u_t = beta_t (v_t - S'^T k_t)
+ *   S_t = S' + k_t u_t^T           o_t = scale S_t^T q_t
+ *
+ *   q, k         (batch, T, Hk, Dk) of `dtype`; a token's heads and features lie side by side,
+ *                consecutive tokens *_stride elements apart (>= Hk Dk) and consecutive
+ *                batch rows T * *_stride, so that q, k and v may be column ranges of one
+ *                matrix of projected rows. Read only.
+ *   v            (batch, T, Hv, Dv) of `dtype`, v_stride >= Hv Dv. Hv is a multiple of Hk:
+ *                neighbouring value heads share a key head.
+ *   g, beta      (batch, T, Hv) float32, dense: the log of the decay (at most 0 for a
+ *                state that fades; below -1000, also -infinity, it counts as -1000, and the state
+ *                is forgotten) and the strength of the correction.
+ *   scale        at most 1e30 in magnitude (usually Dk^-1/2).
+ *   initial_state nullable: (batch, Hv, Dk, Dv) float32, S_{-1}; NULL means zero.
+ *   lengths      nullable: (batch) int32 in device memory: the tokens of each row, clamped
+ *                to 0 .. T. Tokens from there on are padding: what they hold does not matter, their
+ *                o is 0, and the state stays as it is.
+ *   o            out: (batch, T, Hv, Dv) of `dtype`, dense.
+ *   final_state  out, nullable: (batch, Hv, Dk, Dv) float32, the state after the row's last
+ *                token. It may be initial_state itself (updated in place).
+ *   chunk_states out, nullable: (batch, ceil(T / SSD_DELTA_CHUNK), Hv, Dk, Dv) float32, the
+ *                state before each chunk's first token, for the backward.
+ *   workspace    ssd_gated_delta_workspace_bytes(...) bytes, 256-byte aligned (NULL allowed
+ *                when that is 0).
+ * The state, sums and products are float32 (operands as sums of up to three bfloat16 parts,
+ * 24 bits); o is rounded once to `dtype`. The rule is a contraction where beta |k|^2 lies
+ * in 0 .. 2: keys are meant to be scaled to a length of at most 1. Longer ones are
+ * computed as they stand and may grow without bound, errors with them. An infinity, a NaN or a value
+ * above 3.38e38 makes what it reaches NaN (or infinite): in v its column of the head,
+ * in q the token's o of its heads, elsewhere what follows in its heads, and the tokens
+ * before it in the same chunk.
+ * T up to 8 is the form for generation: one or a few steps on the state.
+ * No output may overlap an input or another output (SSD_ERR_ALIAS), but for the state in
+ * place. Alignment: the element size. batch equal to 0 is a no-op; T equal to 0
+ * copies the initial state (or zeros) into final_state.
+ * SSD_ERR_BLOCK_DIMS: Dk above 128 or Dv above 256. SSD_ERR_UNSUPPORTED: T above 2^30,
+ * batch above 2^24, heads above 2^16, a stride that makes an operand longer than 2^40, or
+ * batch * Hv * max(ceil(T / 64), ceil(Dv / 64)) from 2^24 on.
+ */
+size_t ssd_gated_delta_workspace_bytes(int64_t batch, int64_t T, int64_t Hk, int64_t Hv,
+                                       int64_t Dk, int64_t Dv, int dtype);
+
+int ssd_gated_delta(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                    const void *v, int64_t v_stride, const float *g, const float *beta,
+                    float scale, int dtype, int64_t batch, int64_t T, int64_t Hk, int64_t Hv,
+                    int64_t Dk, int64_t Dv, const float *initial_state, const int32_t *lengths,
+                    void *o, float *final_state, float *chunk_states, void *workspace,
+                    size_t workspace_bytes, ssd_stream_t stream);
+
+/*
+ * ssd_gated_delta_backward -- gradients of l = sum grad_o * o + sum grad_final_state *
+ * final_state for ssd_gated_delta.
+ *   q .. Dv, lengths as for the forward; chunk_states as it wrote them.
+ *   grad_o       (batch, T, Hv, Dv) of `dtype`, dense; what the padding holds does not matter.
+ *   grad_final_state nullable: (batch, Hv, Dk, Dv) float32.
+ *   grad_q, grad_k out: (batch, T, Hk, Dk) of `dtype`, dense: the sums over the value heads
+ *                that share the key head, in a fixed order; 0 in the padding.
+ *   grad_v       out: (batch, T, Hv, Dv) of `dtype`, dense; 0 in the padding.
+ *   grad_g, grad_beta out: (batch, T, Hv) float32; 0 in the padding.
+ *   grad_initial_state out, nullable: (batch, Hv, Dk, Dv) float32.
+ *   workspace    ssd_gated_delta_backward_workspace_bytes(...) bytes, 256-byte aligned.
+ * What the chunks hold between the stored states is computed again in float32. No output
+ * may overlap an input, another output or the workspace (SSD_ERR_ALIAS). batch or T
+ * equal to 0 copies grad_final_state (or zeros) into grad_initial_state.
+ */
+size_t ssd_gated_delta_backward_workspace_bytes(int64_t batch, int64_t T, int64_t Hk, int64_t Hv,
+                                                int64_t Dk, int64_t Dv, int dtype);
+
+int ssd_gated_delta_backward(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                             const void *v, int64_t v_stride, const float *g, const float *beta,
+                             float scale, int dtype, int64_t batch, int64_t T, int64_t Hk,
+                             int64_t Hv, int64_t Dk, int64_t Dv, const float *chunk_states,
+                             const int32_t *lengths, const void *grad_o,
+                             const float *grad_final_state, void *grad_q, void *grad_k,
+                             void *grad_v, float *grad_g, float *grad_beta,
+                             float *grad_initial_state, void *workspace, size_t workspace_bytes,
+                             ssd_stream_t stream);
+
 /* Static text for a status code (never NULL). */
 const char *ssd_status_string(int status);
 
