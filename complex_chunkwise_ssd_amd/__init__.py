@@ -14,8 +14,8 @@ and a visible GPU, and fails loudly otherwise (there is no fallback path).
     grad_y, grad_W = head_mix_backward(y, W, grad_z)
 
 The operators around the scan (module ops): gated_scan, rms_norm, fp8_quantise,
-fp8_matmul and the gradients of the first two. The gated delta rule (module block):
-gated_delta and its gradients.
+fp8_matmul and the gradients of the first two. The gated delta rule and the
+norms around a block (module block): gated_delta, gated_norm, block_norm and their gradients.
 """
 
 from __future__ import annotations
@@ -29,7 +29,9 @@ import threading
 import torch
 
 from . import block, ops
-from .block import DELTA_CHUNK, DeltaGrads, GatedDelta, gated_delta, gated_delta_backward
+from .block import (DELTA_CHUNK, BlockNorm, BlockNormGrads, DeltaGrads, GatedDelta, GatedNorm, GatedNormGrads,
+                    block_norm, block_norm_backward, gated_delta, gated_delta_backward, gated_norm,
+                    gated_norm_backward)
 from .ops import (GATED_CHUNK, GatedGrads, GatedScan, RMSNorm, fp8_matmul, fp8_quantise, gated_scan,
                   gated_scan_backward, rms_norm, rms_norm_backward)
 
@@ -107,6 +109,7 @@ def load_library(path: str | None = None):
         lib.ssd_head_mix_backward.restype = ctypes.c_int
         ops.declare(lib)
         block.declare_delta(lib)
+        block.declare_norms(lib)
         lib.ssd_status_string.argtypes = [ctypes.c_int]
         lib.ssd_status_string.restype = ctypes.c_char_p
         lib.ssd_version.restype = ctypes.c_int

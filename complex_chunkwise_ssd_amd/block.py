@@ -6,6 +6,8 @@ history: the gradients are calls of their own.
 
     o, final_state, chunk_states = gated_delta(q, k, v, g, beta)
     grads = gated_delta_backward(q, k, v, g, beta, chunk_states, grad_o)
+    n = gated_norm(o.flatten(-2), z, weight, fp8=True)                 # n.q, n.scale
+    b = block_norm(x, residual, post_weight, pre_weight, fp8=True)     # b.q, b.scale, b.residual
 """
 
 from __future__ import annotations
@@ -20,22 +22,42 @@ _DTYPES = {torch.float32: 0, torch.bfloat16: 1}  # SSD_F32, SSD_BF16
 
 GatedDelta = collections.namedtuple("GatedDelta", "o final_state chunk_states")
 DeltaGrads = collections.namedtuple("DeltaGrads", "q k v g beta initial_state")
+GatedNorm = collections.namedtuple("GatedNorm", "y q scale rstd")
+GatedNormGrads = collections.namedtuple("GatedNormGrads", "x gate weight")
+BlockNorm = collections.namedtuple("BlockNorm", "y residual q scale post_rstd pre_rstd")
+BlockNormGrads = collections.namedtuple("BlockNormGrads", "x residual post_weight pre_weight")
+
+
+_VP, _I64, _I32, _F32, _SIZE = (ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_float,
+                                ctypes.c_size_t)
+
+
+def _entry(lib, name, res, *args):
+    fn = getattr(lib, name)
+    fn.argtypes, fn.restype = list(args), res
 
 
 def declare_delta(lib):
     """Argument types of the delta rule's entry points."""
-    vp, i64, i32, f32, size = (ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_float,
-                               ctypes.c_size_t)
-
-    def entry(name, res, *args):
-        fn = getattr(lib, name)
-        fn.argtypes, fn.restype = list(args), res
-
+    vp, i64, i32, f32, size = _VP, _I64, _I32, _F32, _SIZE
     inputs = [vp, i64, vp, i64, vp, i64, vp, vp, f32, i32] + [i64] * 6
-    entry("ssd_gated_delta_workspace_bytes", size, *[i64] * 6, i32)
-    entry("ssd_gated_delta", i32, *inputs, *[vp] * 6, size, vp)
-    entry("ssd_gated_delta_backward_workspace_bytes", size, *[i64] * 6, i32)
-    entry("ssd_gated_delta_backward", i32, *inputs, *[vp] * 11, size, vp)
+    _entry(lib, "ssd_gated_delta_workspace_bytes", size, *[i64] * 6, i32)
+    _entry(lib, "ssd_gated_delta", i32, *inputs, *[vp] * 6, size, vp)
+    _entry(lib, "ssd_gated_delta_backward_workspace_bytes", size, *[i64] * 6, i32)
+    _entry(lib, "ssd_gated_delta_backward", i32, *inputs, *[vp] * 11, size, vp)
+
+
+def declare_norms(lib):
+    """Argument types of the norms' entry points."""
+    vp, i64, i32, f32, size = _VP, _I64, _I32, _F32, _SIZE
+    _entry(lib, "ssd_gated_norm", i32, vp, i64, vp, i64, vp, i32, i64, i64, i64, f32, vp, vp, vp, vp, vp)
+    _entry(lib, "ssd_gated_norm_backward_workspace_bytes", size, i64, i64, i64)
+    _entry(lib, "ssd_gated_norm_backward", i32, vp, i64, vp, i64, vp, vp, vp, i64, i32, i64, i64, i64, vp, vp, vp,
+           vp, size, vp)
+    _entry(lib, "ssd_block_norm", i32, vp, i64, vp, i64, vp, vp, f32, i32, i64, i64, f32, *[vp] * 6, vp)
+    _entry(lib, "ssd_block_norm_backward_workspace_bytes", size, i64, i64)
+    _entry(lib, "ssd_block_norm_backward", i32, vp, i64, vp, i64, vp, vp, vp, vp, f32, vp, i64, vp, i64, i32, i64, i64,
+           vp, vp, vp, vp, vp, size, vp)
 
 
 _loaded = None
@@ -99,3 +121,57 @@ def gated_delta_backward(q, k, v, g, beta, chunk_states, grad_o, grad_final_stat
 def gated_delta_workspace_bytes(B, T, Hk, Hv, Dk, Dv, dtype, backward=False) -> int:
     name = "ssd_gated_delta_backward_workspace_bytes" if backward else "ssd_gated_delta_workspace_bytes"
     return _size(name, B, T, Hk, Hv, Dk, Dv, _DTYPES[dtype])
+
+
+def gated_norm(x, gate, weight, eps: float = 1e-6, want_y: bool = True, fp8: bool = False, want_rstd: bool = False,
+               y=None, q=None, scale=None, rstd=None):
+    """The norm of a mixer's outputs by heads, fused with their gate: y = x / sqrt(mean(x^2) + eps) * weight *
+    silu(gate), the mean over each D neighbours of the last dimension F.
+
+    x, gate (..., F) float32 or bfloat16 with evenly spaced rows; weight (D,) float32, D >= 8 a divisor of F
+    (the same weights for every head). Returns GatedNorm(y in x's type or None, q (..., F)
+    float8_e4m3fn and scale (ceil(F / 128), rows) float32 with fp8 (y in 8 bits, as fp8_matmul reads
+    it), rstd (rows, F / D) float32 if wanted)."""
+    return GatedNorm(*(_loaded or _binding()).gated_norm(x, gate, weight, eps, want_y, fp8, want_rstd, y, q, scale,
+                                                         rstd))
+
+
+def gated_norm_backward(x, gate, weight, rstd, grad_y, grad_x=None, grad_gate=None, grad_weight=None, workspace=None):
+    """Gradients of sum(grad_y * y) for gated_norm; rstd (rows, F / D) as it returned it. Returns
+    GatedNormGrads(x, gate (..., F) in x's type, weight (D,) float32, summed over rows and heads)."""
+    return GatedNormGrads(*(_loaded or _binding()).gated_norm_backward(x, gate, weight, rstd, grad_y, grad_x, grad_gate,
+                                                                       grad_weight, workspace))
+
+
+def gated_norm_backward_workspace_bytes(rows, F, D) -> int:
+    return _size("ssd_gated_norm_backward_workspace_bytes", rows, F, D)
+
+
+def block_norm(x, residual, post_weight, pre_weight, residual_scale: float = 1.0, eps: float = 1e-6,
+               want_y: bool = True, fp8: bool = False, want_rstd: bool = False, y=None, residual_out=None, q=None,
+               scale=None, post_rstd=None, pre_rstd=None):
+    """The end of a block and the start of the next: s = residual + residual_scale * x / sqrt(mean(x^2) + eps) *
+    post_weight, y = s / sqrt(mean(s^2) + eps) * pre_weight, over the last dimension F.
+
+    x, residual (..., F) float32 or bfloat16 with evenly spaced rows; both weights (F,) float32. Returns
+    BlockNorm(y in x's type or None, residual = s in x's type, q (..., F) float8_e4m3fn and scale
+    (ceil(F / 128), rows) float32 with fp8 (y in 8 bits, as fp8_matmul reads it), post_rstd and pre_rstd
+    (rows,) float32 if wanted). residual_out may be residual (in place)."""
+    return BlockNorm(*(_loaded or _binding()).block_norm(x, residual, post_weight, pre_weight, residual_scale, eps,
+                                                         want_y, fp8, want_rstd, y, residual_out, q, scale, post_rstd,
+                                                         pre_rstd))
+
+
+def block_norm_backward(x, s, post_weight, pre_weight, post_rstd, pre_rstd, grad_y, grad_residual=None,
+                        residual_scale: float = 1.0, grad_x=None, grad_residual_in=None, grad_post_weight=None,
+                        grad_pre_weight=None, workspace=None):
+    """Gradients of sum(grad_y * y) + sum(grad_residual * s) for block_norm: s is its residual output, the rstds
+    (rows,) as it returned them. Returns BlockNormGrads(x, residual (..., F) in x's type, post_weight,
+    pre_weight (F,) float32)."""
+    return BlockNormGrads(*(_loaded or _binding()).block_norm_backward(
+        x, s, post_weight, pre_weight, post_rstd, pre_rstd, grad_y, grad_residual, residual_scale, grad_x,
+        grad_residual_in, grad_post_weight, grad_pre_weight, workspace))
+
+
+def block_norm_backward_workspace_bytes(rows, F) -> int:
+    return _size("ssd_block_norm_backward_workspace_bytes", rows, F)

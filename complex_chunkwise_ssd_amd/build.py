@@ -16,7 +16,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libssd.so")
 BINDINGS = {"_binding": "ssd_ops_binding.cpp", "_block_binding": "ssd_block_binding.cpp"}
 ARCH = "gfx950"
-SOURCES = ("ssd_api.hip", "ssd_ops_api.hip", "ssd_delta_api.hip")
+SOURCES = ("ssd_api.hip", "ssd_ops_api.hip", "ssd_delta_api.hip", "ssd_block_api.hip")
 
 
 def hipcc_command(out: str, extra=()):

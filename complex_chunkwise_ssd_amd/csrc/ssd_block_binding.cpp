@@ -6,7 +6,9 @@ namespace {
 
 #define SSD_OPERATORS(F)                                     \
     F(ssd_gated_delta_workspace_bytes) F(ssd_gated_delta)    \
-    F(ssd_gated_delta_backward_workspace_bytes) F(ssd_gated_delta_backward)
+    F(ssd_gated_delta_backward_workspace_bytes) F(ssd_gated_delta_backward) \
+    F(ssd_gated_norm) F(ssd_gated_norm_backward_workspace_bytes) F(ssd_gated_norm_backward) \
+    F(ssd_block_norm) F(ssd_block_norm_backward_workspace_bytes) F(ssd_block_norm_backward)
 struct Library {
 #define F(name) decltype(&::name) name = nullptr;
     SSD_OPERATORS(F)
@@ -142,6 +144,124 @@ gated_delta_backward(const Tensor &q, const Tensor &k, const Tensor &v, const Te
     return {gq, gk, gv, gg, gbeta, ginit};
 }
 
+struct Rows {
+    at::Device dev;
+    int dtype;
+    at::ScalarType type;
+    int64_t rows, F, stride;
+};
+Rows rows_input(const Tensor &x, const char *name)
+{
+    need_gpu(x);
+    if (x.dim() < 1)
+        bad(std::string(name) + " must have a last dimension");
+    return {x.device(), dtype_of(x, name), x.scalar_type(), rows_of(x), x.size(-1), row_stride(x, name)};
+}
+
+using MaybeTensor = optional<Tensor>;
+
+std::tuple<MaybeTensor, MaybeTensor, MaybeTensor, MaybeTensor>
+gated_norm(const Tensor &x, const Tensor &gate, const Tensor &weight, double eps, bool want_y, bool fp8, bool want_rstd,
+           const MaybeTensor &y_, const MaybeTensor &q_, const MaybeTensor &scale_, const MaybeTensor &rstd_)
+{
+    const Rows r = rows_input(x, "x");
+    const int64_t sg = strided(gate, "gate", r.type, x.sizes(), r.dev);
+    if (weight.dim() != 1 || weight.size(0) < 1 || r.F % weight.size(0) != 0)
+        bad("weight must be a (D,) tensor, D a divisor of x's last dimension, got " + text(weight.sizes()));
+    const int64_t D = weight.size(0);
+    check(weight, "weight", at::kFloat, {D}, r.dev);
+    const c10::DeviceGuard guard(r.dev);
+    const auto y = maybe_output(y_, "y", r.type, x.sizes(), r.dev, want_y);
+    const auto q = maybe_output(q_, "q", at::kFloat8_e4m3fn, x.sizes(), r.dev, fp8);
+    const auto scale = maybe_output(scale_, "scale", at::kFloat, {(r.F + 127) / 128, r.rows}, r.dev, q.has_value());
+    const auto rstd = maybe_output(rstd_, "rstd", at::kFloat, {r.rows, r.F / D}, r.dev, want_rstd);
+    check_status(library.ssd_gated_norm(at_of(x), r.stride, at_of(gate), sg, at_of<float>(weight), r.dtype, r.rows, r.F,
+                                        D, (float)eps, at_of(y), at_of<uint8_t>(q), at_of<float>(scale),
+                                        at_of<float>(rstd), stream_of(r.dev)),
+                 "ssd_gated_norm");
+    return {y, q, scale, rstd};
+}
+
+std::tuple<Tensor, Tensor, Tensor> gated_norm_backward(const Tensor &x, const Tensor &gate, const Tensor &weight,
+                                                       const Tensor &rstd, const Tensor &grad_y, const MaybeTensor &gx_,
+                                                       const MaybeTensor &gz_, const MaybeTensor &gw_,
+                                                       const MaybeTensor &ws_)
+{
+    const Rows r = rows_input(x, "x");
+    const int64_t sz = strided(gate, "gate", r.type, x.sizes(), r.dev);
+    const int64_t sg = strided(grad_y, "grad_y", r.type, x.sizes(), r.dev);
+    if (weight.dim() != 1 || weight.size(0) < 1 || r.F % weight.size(0) != 0)
+        bad("weight must be a (D,) tensor, D a divisor of x's last dimension, got " + text(weight.sizes()));
+    const int64_t D = weight.size(0);
+    check(weight, "weight", at::kFloat, {D}, r.dev);
+    check(rstd, "rstd", at::kFloat, {r.rows, r.F / D}, r.dev);
+    const c10::DeviceGuard guard(r.dev);
+    const Tensor gx = output(gx_, "grad_x", r.type, x.sizes(), r.dev);
+    const Tensor gz = output(gz_, "grad_gate", r.type, x.sizes(), r.dev);
+    const Tensor gw = output(gw_, "grad_weight", at::kFloat, {D}, r.dev);
+    const Workspace ws = workspace_of(ws_, library.ssd_gated_norm_backward_workspace_bytes(r.rows, r.F, D), r.dev);
+    check_status(library.ssd_gated_norm_backward(at_of(x), r.stride, at_of(gate), sz, at_of<float>(weight),
+                                                 at_of<float>(rstd), at_of(grad_y), sg, r.dtype, r.rows, r.F, D,
+                                                 at_of(gx), at_of(gz), at_of<float>(gw), ws.at, ws.bytes,
+                                                 stream_of(r.dev)),
+                 "ssd_gated_norm_backward");
+    return {gx, gz, gw};
+}
+
+std::tuple<MaybeTensor, Tensor, MaybeTensor, MaybeTensor, MaybeTensor, MaybeTensor>
+block_norm(const Tensor &x, const Tensor &residual, const Tensor &post, const Tensor &pre, double alpha, double eps,
+           bool want_y, bool fp8, bool want_rstd, const MaybeTensor &y_, const MaybeTensor &residual_out_,
+           const MaybeTensor &q_, const MaybeTensor &scale_, const MaybeTensor &post_rstd_,
+           const MaybeTensor &pre_rstd_)
+{
+    const Rows r = rows_input(x, "x");
+    const int64_t sr = strided(residual, "residual", r.type, x.sizes(), r.dev);
+    check(post, "post_weight", at::kFloat, {r.F}, r.dev);
+    check(pre, "pre_weight", at::kFloat, {r.F}, r.dev);
+    const c10::DeviceGuard guard(r.dev);
+    const auto y = maybe_output(y_, "y", r.type, x.sizes(), r.dev, want_y);
+    const Tensor s = output(residual_out_, "residual_out", r.type, x.sizes(), r.dev);
+    const auto q = maybe_output(q_, "q", at::kFloat8_e4m3fn, x.sizes(), r.dev, fp8);
+    const auto scale = maybe_output(scale_, "scale", at::kFloat, {(r.F + 127) / 128, r.rows}, r.dev, q.has_value());
+    const auto rstd1 = maybe_output(post_rstd_, "post_rstd", at::kFloat, {r.rows}, r.dev, want_rstd);
+    const auto rstd2 = maybe_output(pre_rstd_, "pre_rstd", at::kFloat, {r.rows}, r.dev, want_rstd);
+    check_status(library.ssd_block_norm(at_of(x), r.stride, at_of(residual), sr, at_of<float>(post), at_of<float>(pre),
+                                        (float)alpha, r.dtype, r.rows, r.F, (float)eps, at_of(y), at_of(s),
+                                        at_of<uint8_t>(q), at_of<float>(scale), at_of<float>(rstd1),
+                                        at_of<float>(rstd2), stream_of(r.dev)),
+                 "ssd_block_norm");
+    return {y, s, q, scale, rstd1, rstd2};
+}
+
+std::tuple<Tensor, Tensor, Tensor, Tensor>
+block_norm_backward(const Tensor &x, const Tensor &s, const Tensor &post, const Tensor &pre, const Tensor &post_rstd,
+                    const Tensor &pre_rstd, const Tensor &grad_y, const MaybeTensor &grad_residual, double alpha,
+                    const MaybeTensor &gx_, const MaybeTensor &gr_, const MaybeTensor &gpost_, const MaybeTensor &gpre_,
+                    const MaybeTensor &ws_)
+{
+    const Rows r = rows_input(x, "x");
+    const int64_t ss = strided(s, "s", r.type, x.sizes(), r.dev);
+    const int64_t sg = strided(grad_y, "grad_y", r.type, x.sizes(), r.dev);
+    const int64_t sr = grad_residual ? strided(*grad_residual, "grad_residual", r.type, x.sizes(), r.dev) : 0;
+    check(post, "post_weight", at::kFloat, {r.F}, r.dev);
+    check(pre, "pre_weight", at::kFloat, {r.F}, r.dev);
+    check(post_rstd, "post_rstd", at::kFloat, {r.rows}, r.dev);
+    check(pre_rstd, "pre_rstd", at::kFloat, {r.rows}, r.dev);
+    const c10::DeviceGuard guard(r.dev);
+    const Tensor gx = output(gx_, "grad_x", r.type, x.sizes(), r.dev);
+    const Tensor gr = output(gr_, "grad_residual_in", r.type, x.sizes(), r.dev);
+    const Tensor gpost = output(gpost_, "grad_post_weight", at::kFloat, {r.F}, r.dev);
+    const Tensor gpre = output(gpre_, "grad_pre_weight", at::kFloat, {r.F}, r.dev);
+    const Workspace ws = workspace_of(ws_, library.ssd_block_norm_backward_workspace_bytes(r.rows, r.F), r.dev);
+    check_status(library.ssd_block_norm_backward(at_of(x), r.stride, at_of(s), ss, at_of<float>(post), at_of<float>(pre),
+                                                 at_of<float>(post_rstd), at_of<float>(pre_rstd), (float)alpha,
+                                                 at_of(grad_y), sg, at_of(grad_residual), sr, r.dtype, r.rows, r.F,
+                                                 at_of(gx), at_of(gr), at_of<float>(gpost), at_of<float>(gpre), ws.at,
+                                                 ws.bytes, stream_of(r.dev)),
+                 "ssd_block_norm_backward");
+    return {gx, gr, gpost, gpre};
+}
+
 }  // namespace
 
 PYBIND11_MODULE(TORCH_EXTENSION_NAME, m)
@@ -151,4 +271,8 @@ PYBIND11_MODULE(TORCH_EXTENSION_NAME, m)
     m.def("token_stride", [](const Tensor &t) { return token_stride(t, "t"); });
     m.def("gated_delta", &gated_delta);
     m.def("gated_delta_backward", &gated_delta_backward);
+    m.def("gated_norm", &gated_norm);
+    m.def("gated_norm_backward", &gated_norm_backward);
+    m.def("block_norm", &block_norm);
+    m.def("block_norm_backward", &block_norm_backward);
 }

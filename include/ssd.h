@@ -641,6 +641,108 @@ int ssd_gated_delta_backward(const void *q, int64_t q_stride, const void *k, int
                              float *grad_initial_state, void *workspace, size_t workspace_bytes,
                              ssd_stream_t stream);
 
+/*
+ * ssd_gated_norm -- the norm of a mixer's outputs by heads, fused with their gate, its result in
+ * `dtype`, in 8 bits, or both. Per row of F values and head of D of them:
+ *
+ *   rstd = 1 / sqrt(sum x^2 / D + eps)     y = x * rstd * weight * silu(gate)
+ *   q = e4m3(y / scale), one scale per 128 neighbours of the row
+ *
+ *   x, gate      (rows, F) of `dtype`, rows *_stride elements apart (>= F).
+ *   weight       (D) float32, the same for every head. D divides F.
+ *   y            out, nullable: (rows, F) of `dtype`, dense.
+ *   q, scale     out, nullable together: (rows, F) e4m3 bytes and (ceil(F / 128), rows)
+ *                float32, as ssd_fp8_matmul reads them; q is taken of the float32 y.
+ *                One of y and q has to be given.
+ *   rstd         out, nullable: (rows, F / D) float32, for the backward.
+ * Sums are float32: a head's sum of squares has to stay below 2^128, and without an epsilon a
+ * head whose mean square is below 2^-150 counts as zeros (its rstd is infinite). eps >= 0.
+ * rows equal to 0 is a no-op. No output may overlap an input or another output
+ * (SSD_ERR_ALIAS). Alignment: the element size. SSD_ERR_UNSUPPORTED: F above 16384, D below 8.
+ */
+int ssd_gated_norm(const void *x, int64_t x_stride, const void *gate, int64_t gate_stride,
+                   const float *weight, int dtype, int64_t rows, int64_t F, int64_t D, float eps,
+                   void *y, uint8_t *q, float *scale, float *rstd, ssd_stream_t stream);
+
+/*
+ * ssd_gated_norm_backward -- gradients of l = sum grad_y * y for ssd_gated_norm. With
+ * n = x rstd, z = gate and b = grad_y silu(z) weight:
+ *
+ *   grad_x = rstd (b - n (sum b n) / D)        sums over the head
+ *   grad_gate = grad_y n weight sigmoid(z) (1 + z (1 - sigmoid(z)))
+ *   grad_weight = sum over rows and heads grad_y silu(z) n
+ *
+ *   rstd         as the forward wrote it.
+ *   grad_y       (rows, F) of `dtype`, rows grad_y_stride elements apart.
+ *   grad_x, grad_gate out: (rows, F) of `dtype`, dense.
+ *   grad_weight  out: (D) float32, summed in a fixed order.
+ *   workspace    ssd_gated_norm_backward_workspace_bytes(rows, F, D) bytes, 256-byte aligned.
+ * rows equal to 0 sets grad_weight to zero. No output may overlap an input, another
+ * output or the workspace (SSD_ERR_ALIAS).
+ */
+size_t ssd_gated_norm_backward_workspace_bytes(int64_t rows, int64_t F, int64_t D);
+
+int ssd_gated_norm_backward(const void *x, int64_t x_stride, const void *gate,
+                            int64_t gate_stride, const float *weight, const float *rstd,
+                            const void *grad_y, int64_t grad_y_stride, int dtype, int64_t rows,
+                            int64_t F, int64_t D, void *grad_x, void *grad_gate,
+                            float *grad_weight, void *workspace, size_t workspace_bytes,
+                            ssd_stream_t stream);
+
+/*
+ * ssd_block_norm -- the end of a block and the start of the next: the norm of the block's
+ * output, its scaled addition to the residual stream, and the norm of that. Per row of F:
+ *
+ *   post_rstd = 1 / sqrt(sum x^2 / F + eps)   s = residual + residual_scale x post_rstd post_weight
+ *   pre_rstd = 1 / sqrt(sum s^2 / F + eps)    y = s pre_rstd pre_weight
+ *   q = e4m3(y / scale), one scale per 128 neighbours
+ *
+ *   x, residual  (rows, F) of `dtype`, rows *_stride elements apart (>= F).
+ *   post_weight, pre_weight (F) float32. residual_scale: at most 1e30 in magnitude.
+ *   y            out, nullable: (rows, F) of `dtype`, dense.
+ *   residual_out out: s, rounded to `dtype`, (rows, F) dense. It may be residual itself if
+ *                that is dense.
+ *   q, scale     out, nullable together: as ssd_gated_norm. One of y and q has to be given.
+ *   post_rstd, pre_rstd out, nullable: (rows) float32, for the backward.
+ * Sums are float32 and taken of the unrounded s, with the limits of ssd_rms_norm. rows equal to
+ * 0 is a no-op. No other overlap of outputs (SSD_ERR_ALIAS). Alignment: the element
+ * size. SSD_ERR_UNSUPPORTED: F above 16384.
+ */
+int ssd_block_norm(const void *x, int64_t x_stride, const void *residual, int64_t residual_stride,
+                   const float *post_weight, const float *pre_weight, float residual_scale,
+                   int dtype, int64_t rows, int64_t F, float eps, void *y, void *residual_out,
+                   uint8_t *q, float *scale, float *post_rstd, float *pre_rstd,
+                   ssd_stream_t stream);
+
+/*
+ * ssd_block_norm_backward -- gradients of l = sum grad_y * y + sum grad_residual * s for
+ * ssd_block_norm. With m = s pre_rstd and n = x post_rstd, means over the row:
+ *
+ *   grad_residual_in = grad_residual + pre_rstd (w grad_y - m mean(w grad_y m)), w = pre_weight
+ *   a = residual_scale grad_residual_in
+ *   grad_x = post_rstd (w a - n mean(w a n)), w = post_weight
+ *   grad_post_weight = sum over rows a n      grad_pre_weight = sum over rows grad_y m
+ *
+ *   s            (rows, F) of `dtype`: the forward's residual_out.
+ *   grad_y       (rows, F) of `dtype`; grad_residual nullable, the same: the gradient that
+ *                reaches s through the residual stream.
+ *   grad_x, grad_residual_in out: (rows, F) of `dtype`, dense.
+ *   grad_post_weight, grad_pre_weight out: (F) float32, summed in a fixed order.
+ *   workspace    ssd_block_norm_backward_workspace_bytes(rows, F) bytes, 256-byte aligned.
+ * rows equal to 0 sets the weights' gradients to zero. No output may overlap an input,
+ * another output or the workspace (SSD_ERR_ALIAS).
+ */
+size_t ssd_block_norm_backward_workspace_bytes(int64_t rows, int64_t F);
+
+int ssd_block_norm_backward(const void *x, int64_t x_stride, const void *s, int64_t s_stride,
+                            const float *post_weight, const float *pre_weight,
+                            const float *post_rstd, const float *pre_rstd, float residual_scale,
+                            const void *grad_y, int64_t grad_y_stride, const void *grad_residual,
+                            int64_t grad_residual_stride, int dtype, int64_t rows, int64_t F,
+                            void *grad_x, void *grad_residual_in, float *grad_post_weight,
+                            float *grad_pre_weight, void *workspace, size_t workspace_bytes,
+                            ssd_stream_t stream);
+
 /* Static text for a status code (never NULL). */
 const char *ssd_status_string(int status);
 
