@@ -92,16 +92,18 @@ int launch_delta_few(const ssd::DeltaParams &p, hipStream_t s)
     return launch_status();
 }
 
+template <int T, int KP, int WAVES>
+int launch_delta_as(ssd::DeltaParams p, hipStream_t s)
+{
+    p.columns = (p.Dv + 16 * WAVES - 1) / (16 * WAVES);
+    hipLaunchKernelGGL((ssd::delta_scan_kernel<T, KP, WAVES>), dim3((unsigned)((int64_t)p.B * p.Hv * p.columns)),
+                       dim3(64 * WAVES), 0, s, p);
+    return launch_status();
+}
 template <int T, int KP>
 int launch_delta(const ssd::DeltaParams &p, hipStream_t s)
 {
-    const dim3 block(256);
-    hipLaunchKernelGGL((ssd::delta_prepare_kernel<T, KP, false>), dim3((unsigned)((int64_t)p.B * p.Hv * p.chunks)), block,
-                       0, s, p);
-    if (int st = launch_status())
-        return st;
-    hipLaunchKernelGGL((ssd::delta_scan_kernel<T, KP>), dim3((unsigned)((int64_t)p.B * p.Hv * p.columns)), block, 0, s, p);
-    return launch_status();
+    return p.Dv > 64 && KP == 4 ? launch_delta_as<T, KP, 8>(p, s) : launch_delta_as<T, KP, 4>(p, s);
 }
 
 template <int T, int KP>
@@ -139,7 +141,7 @@ size_t ssd_gated_delta_workspace_bytes(int64_t batch, int64_t T, int64_t Hk, int
     const DeltaSizes z{batch, T, Hk, Hv, Dk, Dv};
     if (check_delta(z, dtype, 1.f) || z.empty() || delta_few(z))
         return 0;
-    return delta_frag_bytes(z);
+    return 0;
 }
 
 int ssd_gated_delta(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v, int64_t v_stride,

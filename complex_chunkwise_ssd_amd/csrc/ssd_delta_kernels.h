@@ -28,6 +28,7 @@
 // where exp is 0. Everything else is float32 (see ssd_split.h), rounded once as it is stored.
 #pragma once
 
+#include <ssd_delta_device.h>
 #include <ssd_split.h>
 
 namespace ssd {
@@ -135,48 +136,89 @@ struct DeltaGates {
 };
 
 // By one wave, lane = token; tokens from n on leave the state as it is.
-SSD_DEVICE void delta_gates(DeltaGates &s, const float *g, const float *beta, int64_t at, int step, int n)
+SSD_DEVICE void delta_gates_of(DeltaGates &s, float g, float beta, int n)
 {
     const int t = thread_id() & 63;
-    const double sum = wave_scan_d(t < n ? delta_log2(g[at + (int64_t)t * step]) : 0.);
+    const double sum = wave_scan_d(t < n ? delta_log2(g) : 0.);
     const double last = lane_read_d(sum, 63);
     s.sum[t] = sum;
     s.since[t] = delta_exp(sum);
     s.left[t] = delta_exp(last - sum);
-    s.beta[t] = t < n ? beta[at + (int64_t)t * step] : 0.f;
+    s.beta[t] = t < n ? beta : 0.f;
     if (t == 0)
         s.whole = delta_exp(last);
 }
+SSD_DEVICE void delta_gates(DeltaGates &s, const float *g, const float *beta, int64_t at, int step, int n)
+{
+    const int t = (thread_id() & 63) < n ? thread_id() & 63 : n - 1;
+    delta_gates_of(s, g[at + (int64_t)t * step], beta[at + (int64_t)t * step], n);
+}
 
-// Rows 0 .. 63 (tokens, zeros from n on) by 32 KP columns (zeros from D on) of a matrix in memory into
-// shared memory, as they are and / or turned, by 256 threads: each takes blocks of 4 x 4.
-template <int T, int KP, bool ROWS, bool TURNED>
-SSD_DEVICE void delta_stage(const void *src, int64_t stride, int D, int n, typename DeltaElem<T>::type *rows,
-                            typename DeltaElem<T>::type *turned)
+// Rows 0 .. 63 (tokens, zeros from n on; n > 0) by COLS columns (zeros from D on) of a matrix in memory, on
+// their way into shared memory by NT threads: each takes blocks of 4 x 4. Loads are made without branches, at
+// the nearest place that exists, and what lies outside is cleared afterwards: a branch around a load would make
+// each wait for its own. Offsets within a chunk are 32 bits wide.
+template <int T, int COLS, int NT>
+struct Blocks {
+    static constexpr int across = COLS / 4, units = (16 * across + NT - 1) / NT;
+    static constexpr bool even = 16 * across % NT == 0;
+    typename DeltaElem<T>::type v[units][4][4];
+};
+template <int COLS, int NT>
+SSD_DEVICE int block_col(int thread, int i) { return 4 * ((thread + NT * i) % (COLS / 4)); }
+template <int COLS, int NT>
+SSD_DEVICE int block_row(int thread, int i) { return 4 * ((thread + NT * i) / (COLS / 4)); }
+
+template <int T, int COLS, int NT>
+SSD_DEVICE void blocks_load(Blocks<T, COLS, NT> &d, const void *src, int stride, int D, int n)
 {
     typedef typename DeltaElem<T>::type E;
-    constexpr int pad = DeltaElem<T>::pad, RS = 32 * KP + pad, TS = 64 + pad;
-    const E *x = (const E *)src;
+    const char *x = (const char *)src;
+    const uint32_t step = opaque_uniform((uint32_t)stride * sizeof(E));
+    const int thread = (int)opaque((uint32_t)thread_id());
 #pragma unroll
-    for (int i = 0; i < KP / 2 + KP % 2; ++i) {
-        const int unit = thread_id() + 256 * i;
-        const int f = 4 * (unit % (8 * KP)), t = 4 * (unit / (8 * KP));
-        if (KP % 2 && t >= 64)
+    for (int i = 0; i < d.units; ++i) {
+        const int f = block_col<COLS, NT>(thread, i), t = block_row<COLS, NT>(thread, i);
+        if (D % 4 == 0 && n == 64 && d.even) {
+            const uint32_t off = (uint32_t)t * step + (uint32_t)(f < D ? f : 0) * sizeof(E);
+#pragma unroll
+            for (int a = 0; a < 4; ++a)
+                __builtin_memcpy(d.v[i][a], x + (off + a * step), sizeof(d.v[i][a]));
+        } else if (D % 4 == 0) {
+#pragma unroll
+            for (int a = 0; a < 4; ++a)
+                __builtin_memcpy(d.v[i][a], x + ((uint32_t)(t + a < n ? t + a : n - 1) * step +
+                                                 (uint32_t)(f < D ? f : 0) * sizeof(E)), sizeof(d.v[i][a]));
+        } else {
+#pragma unroll
+            for (int a = 0; a < 4; ++a)
+#pragma unroll
+                for (int b = 0; b < 4; ++b)
+                    __builtin_memcpy(&d.v[i][a][b], x + ((uint32_t)(t + a < n ? t + a : n - 1) * step +
+                                                         (uint32_t)(f + b < D ? f + b : D - 1) * sizeof(E)), sizeof(E));
+        }
+    }
+}
+// Into rows (RS apart) and / or their transpose.
+template <int T, int COLS, int NT, bool ROWS, bool TURNED>
+SSD_DEVICE void blocks_store(Blocks<T, COLS, NT> &d, int D, int n, typename DeltaElem<T>::type *rows,
+                             typename DeltaElem<T>::type *turned)
+{
+    typedef typename DeltaElem<T>::type E;
+    constexpr int pad = DeltaElem<T>::pad, RS = COLS + pad, TS = 64 + pad;
+    const int thread = (int)opaque((uint32_t)thread_id());
+#pragma unroll
+    for (int i = 0; i < d.units; ++i) {
+        const int f = block_col<COLS, NT>(thread, i), t = block_row<COLS, NT>(thread, i);
+        if (!d.even && t >= 64)
             break;
-        E v[4][4];
+        E (&v)[4][4] = d.v[i];
+        if (n < 64 || D < COLS) {
 #pragma unroll
-        for (int a = 0; a < 4; ++a) {
-            const E *p = x + (t + a) * stride + f;
-            if (t + a < n && f + 4 <= D) {
-                __builtin_memcpy(v[a], p, sizeof(v[a]));
-            } else {
+            for (int a = 0; a < 4; ++a)
 #pragma unroll
-                for (int b = 0; b < 4; ++b) {
-                    v[a][b] = 0;
-                    if (t + a < n && f + b < D)
-                        v[a][b] = p[b];
-                }
-            }
+                for (int b = 0; b < 4; ++b)
+                    v[a][b] = t + a < n && f + b < D ? v[a][b] : (E)0;
         }
         if (ROWS)
 #pragma unroll
@@ -189,6 +231,14 @@ SSD_DEVICE void delta_stage(const void *src, int64_t stride, int D, int n, typen
                 __builtin_memcpy(__builtin_assume_aligned(turned + (f + b) * TS + t, sizeof(w)), w, sizeof(w));
             }
     }
+}
+template <int T, int KP, bool ROWS, bool TURNED>
+SSD_DEVICE void delta_stage(const void *src, int64_t stride, int D, int n, typename DeltaElem<T>::type *rows,
+                            typename DeltaElem<T>::type *turned)
+{
+    Blocks<T, 32 * KP, 256> blocks;
+    blocks_load<T, 32 * KP, 256>(blocks, src, (int)stride, D, n);
+    blocks_store<T, 32 * KP, 256, ROWS, TURNED>(blocks, D, n, rows, turned);
 }
 
 SSD_DEVICE int delta_valid(const DeltaParams &p, int b)  // tokens of a sequence
@@ -411,110 +461,292 @@ SSD_DEVICE void delta_store(typename DeltaElem<T>::type *p, float v)
 
 // ------------------------------------------------------------- the walk over chunks
 
-// A workgroup of four waves takes 64 columns of a value head, a wave 16 of them: lane l the column
-// l, and of 2 KP tiles the features 32 s + 8 q + 4 h + r of the state.
-template <int T, int KP>
-SSD_KERNEL(256) void delta_scan_kernel(DeltaParams p)
+constexpr int kPairStride = 36;
+
+// Four neighbours (i, j .. j + 3) of a 64 x 64 matrix into its operand tiles, in N parts.
+template <int N>
+SSD_DEVICE void frag_store(v4u *frags, int f, int i, int j, v4f w)
+{
+    const float v[8] = {w[0], w[1], w[2], w[3], 0.f, 0.f, 0.f, 0.f};
+    const Parts<N> parts = split8<N>(v);
+    const int lane = 16 * (j >> 3 & 3) + 4 * (i >> 3 & 3) + (i & 3);
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+        const v2u half = {parts.p[e][0], parts.p[e][1]};
+        *(v2u *)((char *)&frags[(e * kDeltaFrags + f) * 64 + lane] + 2 * (j & 7)) = half;
+    }
+}
+
+// One of the ten tiles (ti, tj) of A = beta D o K K^T below the diagonal and of P = scale Q K^T o D: into the two
+// 32 x 32 blocks on the diagonal (pairs, float32, transposed) or the operand tiles of A_10, and the operand tiles of P.
+template <int T, int KP, int OUT>
+SSD_DEVICE void delta_tiles(const typename DeltaElem<T>::type *k, const typename DeltaElem<T>::type *q,
+                            const DeltaGates &gates, float scale, int ti, int tj, float *pairs, v4u *tri, v4u *pf)
+{
+    const int l = thread_id() & 15, quarter = (thread_id() & 63) >> 4;
+    const v4f kk = delta_tile<T, KP>(k, tj, k, ti), qk = delta_tile<T, KP>(k, tj, q, ti);  // rows j, column i
+    const int i = 16 * ti + l, j = 16 * tj + 4 * quarter;
+    const double sum = gates.sum[i];
+    const float beta = gates.beta[i];
+    v4f a, w;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        const float d = delta_exp(sum - gates.sum[j + r]);
+        a[r] = i > j + r ? beta * d * kk[r] : 0.f;
+        w[r] = i >= j + r ? scale * d * qk[r] : 0.f;
+    }
+    const int f = frag_of(i >> 5, i >> 2 & 1, j >> 5);
+    if (ti >> 1 == tj >> 1)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            pairs[((i >> 5) * 32 + (j & 31) + r) * kPairStride + (i & 31)] = a[r];
+    else
+        frag_store<kParts>(tri, f, i, j, a);
+    frag_store<OUT>(pf, f, i, j, w);
+}
+
+// (I + A)^-1 of a block of 32 on the diagonal, held transposed, by one wave: column c of each block of 16 by
+// substitution in lanes 16 d + c (and again in 32 + 16 d + c), each value taken from all that follow it as soon
+// as it is known; the corner between them as - T_1 A T_0. Into operand tiles.
+SSD_DEVICE void delta_invert(float *block, int pair, v4u *tri)
+{
+    const int l = thread_id() & 15, quarter = (thread_id() & 63) >> 4, d = quarter & 1;
+    float *own = block + 16 * d * kPairStride + 16 * d;
+    float x[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        x[i] = i == l ? 1.f : 0.f;
+#pragma unroll
+    for (int j = 0; j < 15; ++j) {
+#pragma unroll
+        for (int i = (j + 1) / 4 * 4; i < 16; i += 4) {
+            const v4f a = *(const v4f *)(own + j * kPairStride + i);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (i + e > j)
+                    x[i + e] = __builtin_fmaf(-a[e], x[j], x[i + e]);
+        }
+        if (j % 4 == 3)
+            sched_fence();  // no more than four columns in flight
+    }
+    // the transpose's D = - T_0^T A^T T_1^T: y = A^T T_1^T, of which the transposed T_1 has its columns in the lanes
+    wave_lds_sync();
+#pragma unroll
+    for (int i = 0; i < 16; i += 4)
+        *(v4f *)(own + l * kPairStride + i) = v4f{x[i], x[i + 1], x[i + 2], x[i + 3]};  // row l of T^T
+    wave_lds_sync();
+    float *corner = block + 16;  // A^T: rows of the first 16, columns of the second
+    const v4f a = *(const v4f *)(corner + l * kPairStride + 4 * quarter);
+    const v4f t0 = *(const v4f *)(block + l * kPairStride + 4 * quarter);
+    v4f y = {0.f, 0.f, 0.f, 0.f}, z = y;
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+        y = mfma_16x16x4(a[r], corner[(16 + 4 * quarter + r) * kPairStride + l], y);
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+        z = mfma_16x16x4(t0[r], -y[r], z);
+    wave_lds_sync();
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+        corner[(4 * quarter + r) * kPairStride + l] = z[r];
+    wave_lds_sync();
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {  // row i of the operand is column i of what is held
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            v[e] = block[8 * quarter * kPairStride + tile_row(0, l) + (e * kPairStride + 4 * h)];
+        const Parts<kParts> parts = split8<kParts>(v);
+#pragma unroll
+        for (int e = 0; e < kParts; ++e)
+            tri[(e * kDeltaFrags + frag_of(pair, h, pair)) * 64 + (thread_id() & 63)] = parts.p[e];
+    }
+}
+
+// The feature that a lane holds in component r of tile i of its state, less 8 q.
+SSD_DEVICE constexpr int state_at(int i, int r) { return 32 * (i >> 1) + 4 * (i & 1) + r; }
+
+template <int KP>
+SSD_DEVICE void state_store(const v4f (&S)[2 * KP], float *to, int Dk, int Dv)
+{
+    const uint32_t step = opaque_uniform((uint32_t)Dv * 4);
+    const int q8 = (int)opaque(8 * (((uint32_t)thread_id() & 63) >> 4));
+    const uint32_t off = (uint32_t)q8 * step;
+    char *at = (char *)to;
+    if (Dk == 32 * KP) {
+#pragma unroll
+        for (int i = 0; i < 2 * KP; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                *(float *)(at + (off + (uint32_t)state_at(i, r) * step)) = S[i][r];
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 2 * KP; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            if (q8 < Dk - state_at(i, r))
+                *(float *)(at + (off + (uint32_t)state_at(i, r) * step)) = S[i][r];
+}
+template <int KP>
+SSD_DEVICE void state_load(v4f (&S)[2 * KP], const float *from, int Dk, int Dv)
+{
+    const int q8 = 8 * ((thread_id() & 63) >> 4);
+#pragma unroll
+    for (int i = 0; i < 2 * KP; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            S[i][r] = from[(uint32_t)(q8 < Dk - state_at(i, r) ? q8 + state_at(i, r) : 0) * (uint32_t)Dv];
+#pragma unroll
+    for (int i = 0; i < 2 * KP; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            S[i][r] = q8 < Dk - state_at(i, r) ? S[i][r] : 0.f;
+}
+
+// A workgroup takes 16 WAVES columns of a value head, a wave 16 of them: lane l the column l, and of 2 KP tiles
+// the features 32 s + 8 q + 4 h + r of the state. The chunk's triangle and P are made by all of them; while two
+// waves solve the blocks of 32, the others go on with what the state gives. The next chunk's rows are in
+// flight meanwhile.
+template <int T, int KP, int WAVES>
+SSD_KERNEL_WAVES(64 * WAVES, 2) void delta_scan_kernel(DeltaParams p)
 {
     typedef typename DeltaElem<T>::type E;
+    constexpr int NT = 64 * WAVES, COLS = 16 * WAVES;
     constexpr int pad = DeltaElem<T>::pad, RS = 32 * KP + pad, TS = 64 + pad;
     constexpr int OUT = T == kBF16 ? 2 : 3;  // parts of what only reaches o
-    SSD_LDS E k[64 * RS], q[64 * RS], kt[32 * KP * TS];
+    constexpr bool STAGE_V = T == kBF16;      // float32 rows leave no room
+    SSD_LDS E k[64 * RS], q[64 * RS], kt[32 * KP * TS], vt[STAGE_V ? COLS * TS : 8];
+    SSD_LDS float pairs[64 * kPairStride];
     SSD_LDS v4u tri[kParts * kDeltaFrags * 64], pf[OUT * kDeltaFrags * 64];
-    SSD_LDS DeltaGates gates;
+    SSD_LDS DeltaGates both[2];
     const int64_t id = block_id();
     const int block = (int)(id % p.columns), hv = (int)(id / p.columns % p.Hv), b = (int)(id / p.columns / p.Hv);
-    const int hk = hv / (p.Hv / p.Hk);
-    const int l = thread_id() & 15, quarter = (thread_id() & 63) >> 4;
-    const int dv = 64 * block + 16 * wave_id() + l;
+    const int hk = hv / (p.Hv / p.Hk), wave = wave_id(), lane = thread_id() & 63;
+    const int l = thread_id() & 15, quarter = lane >> 4, q8 = 8 * quarter;
+    const int first = COLS * block, dv = first + 16 * wave + l;
     const bool live = dv < p.Dv;
     const int64_t head = ((int64_t)b * p.Hv + hv) * p.Dk * p.Dv;
     v4f S[2 * KP];
 #pragma unroll
     for (int i = 0; i < 2 * KP; ++i)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int f = 32 * (i >> 1) + 8 * quarter + 4 * (i & 1) + r;
-            S[i][r] = p.init && live && f < p.Dk ? p.init[head + (int64_t)f * p.Dv + dv] : 0.f;
-        }
+        S[i] = v4f{0.f, 0.f, 0.f, 0.f};
+    if (p.init && live)
+        state_load<KP>(S, p.init + head + dv, p.Dk, p.Dv);
     const int length = delta_valid(p, b);
-    const int row_dv = hv * p.Dv + dv;
-    const int64_t o_stride = (int64_t)p.Hv * p.Dv;
-    for (int chunk = 0; chunk < p.chunks; ++chunk) {
-        const int n = delta_chunk_tokens(length, chunk);
-        const int64_t token = (int64_t)b * p.T + chunk * kDeltaChunk;
-        const int rows = p.T - chunk * kDeltaChunk < 64 ? p.T - chunk * kDeltaChunk : 64;
-        if (p.states && live) {
-            float *to = p.states + (((int64_t)b * p.chunks + chunk) * p.Hv + hv) * p.Dk * p.Dv + dv;
-#pragma unroll
-            for (int i = 0; i < 2 * KP; ++i)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int f = 32 * (i >> 1) + 8 * quarter + 4 * (i & 1) + r;
-                    if (f < p.Dk)
-                        to[(int64_t)f * p.Dv] = S[i][r];
-                }
+    const int o_stride = p.Hv * p.Dv;
+    const int64_t row = (int64_t)b * p.T;
+    const E *qrow = (const E *)p.q + row * p.q_stride + hk * p.Dk, *krow = (const E *)p.k + row * p.k_stride + hk * p.Dk;
+    const E *vrow = (const E *)p.v + row * p.v_stride + hv * p.Dv + first;
+    const int vcols = p.Dv - first;
+
+    Blocks<T, 32 * KP, NT> nk, nq;
+    Blocks<T, COLS, NT> nv;
+    float ng = 0.f, nbeta = 0.f;
+    auto fetch = [&](int chunk, int n) {
+        const int64_t t = (int64_t)chunk * kDeltaChunk;
+        blocks_load<T, 32 * KP, NT>(nk, krow + t * p.k_stride, (int)p.k_stride, p.Dk, n);
+        blocks_load<T, 32 * KP, NT>(nq, qrow + t * p.q_stride, (int)p.q_stride, p.Dk, n);
+        if (STAGE_V)
+            blocks_load<T, COLS, NT>(nv, vrow + t * p.v_stride, (int)p.v_stride, vcols, n);
+        if (wave == WAVES - 1) {
+            const int64_t at = (row + t + (lane < n ? lane : n - 1)) * p.Hv + hv;
+            ng = p.g[at];
+            nbeta = p.beta[at];
         }
-        E *o = (E *)p.o + token * o_stride + row_dv;
+    };
+    const E *kl = k + tile_row(0, l) * RS + q8, *ql = q + tile_row(0, l) * RS + q8, *ktl = kt + tile_row(0, l) * TS + q8;
+    const E *vl = vt + (STAGE_V ? (16 * wave + l) * TS + q8 : 0);
+    int n = delta_chunk_tokens(length, 0);
+    if (n > 0) {
+        fetch(0, n);
+        if (wave == WAVES - 1)
+            delta_gates_of(both[0], ng, nbeta, n);
+    }
+    // above the diagonal the blocks (held transposed) and tiles stay zero
+    for (int i = thread_id(); i < 16 * 16; i += NT)
+        pairs[(16 + (i >> 4)) * kPairStride + (i & 15)] = pairs[(48 + (i >> 4)) * kPairStride + (i & 15)] = 0.f;
+    for (int i = thread_id(); i < OUT * kDeltaFrags * 64; i += NT)
+        pf[i] = v4u{0u, 0u, 0u, 0u};
+    for (int chunk = 0; chunk < p.chunks; ++chunk) {
+        n = delta_chunk_tokens(length, chunk);
+        const int rows = p.T - chunk * kDeltaChunk < 64 ? p.T - chunk * kDeltaChunk : 64;
+        if (p.states && live)
+            state_store<KP>(S, p.states + (((int64_t)b * p.chunks + chunk) * p.Hv + hv) * p.Dk * p.Dv + dv, p.Dk, p.Dv);
+        E *o = (E *)p.o + (row + chunk * kDeltaChunk) * o_stride + hv * p.Dv + dv;
         if (n == 0) {  // padding
             if (live)
                 for (int t = quarter; t < rows; t += 4)
-                    delta_store<T>(o + t * o_stride, 0.f);
+                    delta_store<T>(o + (int64_t)t * o_stride, 0.f);
             continue;
         }
+        const DeltaGates &gates = both[chunk & 1];
         block_sync();  // the last chunk's operands have been read
-        delta_stage<T, KP, true, true>((const E *)p.k + token * p.k_stride + hk * p.Dk, p.k_stride, p.Dk, n, k, kt);
-        delta_stage<T, KP, true, false>((const E *)p.q + token * p.q_stride + hk * p.Dk, p.q_stride, p.Dk, n, q, nullptr);
-        delta_stage_frags<kParts>(p.tri + (((int64_t)b * p.Hv + hv) * p.chunks + chunk) * kDeltaFragFloats, tri, 256);
-        if (wave_id() == 0)
-            delta_gates(gates, p.g, p.beta, token * p.Hv + hv, p.Hv, n);
+        blocks_store<T, 32 * KP, NT, true, true>(nk, p.Dk, n, k, kt);
+        blocks_store<T, 32 * KP, NT, true, false>(nq, p.Dk, n, q, (E *)nullptr);
+        if (STAGE_V)
+            blocks_store<T, COLS, NT, false, true>(nv, vcols, n, (E *)nullptr, vt);
         block_sync();
-        // P = scale Q K^T o D as operand tiles
-        for (int i = wave_id(); i < 12; i += 4) {
-            const int ti = i < 10 ? (i < 1 ? 0 : i < 3 ? 1 : i < 6 ? 2 : 3) : i == 10 ? 0 : 2;
-            const int tj = i < 10 ? i - ti * (ti + 1) / 2 : ti + 1;
-            const v4f c = delta_tile<T, KP>(k, tj, q, ti);  // rows j, column i
-            const int row = 16 * ti + l, col = 16 * tj + 4 * quarter;
-            float w[8] = {};
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-                w[r] = row >= col + r ? p.scale * delta_exp(gates.sum[row] - gates.sum[col + r]) * c[r] : 0.f;
-            const Parts<OUT> parts = split8<OUT>(w);
-            const int s = row >> 5, in = row & 31, m = 4 * (in >> 3) + (in & 3);
-            const int f = frag_of(s, in >> 2 & 1, col >> 5), lane = 16 * (col >> 3 & 3) + m;
-#pragma unroll
-            for (int e = 0; e < OUT; ++e) {
-                const v2u half = {parts.p[e][0], parts.p[e][1]};
-                *(v2u *)((char *)&pf[(e * kDeltaFrags + f) * 64 + lane] + 2 * (col & 7)) = half;
+        const int next = delta_chunk_tokens(length, chunk + 1);
+        if (next > 0)
+            fetch(chunk + 1, next);
+        // the ten tiles, the first two waves having the blocks to solve later on
+        if (WAVES == 4) {
+            const int from = wave < 2 ? 2 * wave : 3 * wave - 2, to = wave < 2 ? from + 2 : from + 3;
+            for (int i = from; i < to; ++i) {
+                const int ti = i < 1 ? 0 : i < 3 ? 1 : i < 6 ? 2 : 3;
+                delta_tiles<T, KP, OUT>(k, q, gates, p.scale, ti, i - ti * (ti + 1) / 2, pairs, tri, pf);
+            }
+        } else {
+            for (int i = wave; i < 10; i += WAVES) {
+                const int ti = i < 1 ? 0 : i < 3 ? 1 : i < 6 ? 2 : 3;
+                delta_tiles<T, KP, OUT>(k, q, gates, p.scale, ti, i - ti * (ti + 1) / 2, pairs, tri, pf);
             }
         }
+        block_sync();
+        if (wave < 2)
+            delta_invert(pairs + 32 * wave * kPairStride, wave, tri);
         // R = beta (V - e^G K S), and e^G Q S
         Parts<kParts> Sp[KP];
 #pragma unroll
         for (int s = 0; s < KP; ++s)
             Sp[s] = split_tiles<kParts>(S[2 * s], S[2 * s + 1]);
-        const E *v = (const E *)p.v + token * p.v_stride + row_dv;
         float R[2][8], O[2][8];
 #pragma unroll
-        for (int s = 0; s < 2; ++s)
+        for (int s = 0; s < 2; ++s) {
+            float v[8];
+            if (STAGE_V) {
+                Raw8<T> raw;
+                raw.w[0] = *(const v4u *)(vl + 32 * s);
+                unpack8<T>(raw, v);
+            } else {
+                const E *at = vrow + (int64_t)chunk * kDeltaChunk * p.v_stride + (live ? 16 * wave + l : 0);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    v[e] = delta_load<T>(at + (uint32_t)(q8 < n - (32 * s + e) ? q8 + (32 * s + e) : n - 1) * (uint32_t)p.v_stride);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    v[e] = live && q8 < n - (32 * s + e) ? v[e] : 0.f;
+            }
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 v4f ks = {0.f, 0.f, 0.f, 0.f}, qs = ks;
-                const int at = (32 * s + tile_row(h, l)) * RS + 8 * quarter;
 #pragma unroll
                 for (int f = 0; f < KP; ++f) {
-                    ks = mm<kParts>(lds_operand(k + at + 32 * f), Sp[f], ks);
-                    qs = mm<OUT>(lds_operand(q + at + 32 * f), Sp[f], qs);
+                    ks = mm<kParts>(lds_operand(kl + ((32 * s + 4 * h) * RS + 32 * f)), Sp[f], ks);
+                    qs = mm<OUT>(lds_operand(ql + ((32 * s + 4 * h) * RS + 32 * f)), Sp[f], qs);
                 }
+                const v4f since = *(const v4f *)(gates.since + q8 + (32 * s + 4 * h));
+                const v4f beta = *(const v4f *)(gates.beta + q8 + (32 * s + 4 * h));
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    const int t = 32 * s + 8 * quarter + 4 * h + r;
-                    const float x = live && t < n ? delta_load<T>(v + t * p.v_stride) : 0.f;
-                    R[s][4 * h + r] = gates.beta[t] * (x - gates.since[t] * ks[r]);
-                    O[s][4 * h + r] = p.scale * gates.since[t] * qs[r];
+                    R[s][4 * h + r] = beta[r] * (v[4 * h + r] - since[r] * ks[r]);
+                    O[s][4 * h + r] = p.scale * since[r] * qs[r];
                 }
+                sched_fence();
             }
-        block_sync();  // P is there
+        }
+        block_sync();  // the triangle is there
         // U, and O += P U
         const Parts<kParts> R0 = split8<kParts>(R[0]);
         v4f U[4];
@@ -538,24 +770,41 @@ SSD_KERNEL(256) void delta_scan_kernel(DeltaParams p)
         for (int s = 0; s < 2; ++s)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                v4f c = mm<OUT>(frag_operand<OUT>(pf, frag_of(s, h, 0)), U0, v4f{0.f, 0.f, 0.f, 0.f});
+                v4f c = {O[s][4 * h], O[s][4 * h + 1], O[s][4 * h + 2], O[s][4 * h + 3]};
+                c = mm<OUT>(frag_operand<OUT>(pf, frag_of(s, h, 0)), U0, c);
                 if (s == 1)
                     c = mm<OUT>(frag_operand<OUT>(pf, frag_of(1, h, 1)), U1, c);
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int t = 32 * s + 8 * quarter + 4 * h + r;
-                    if (live && t < rows)
-                        delta_store<T>(o + t * o_stride, t < n ? O[s][4 * h + r] + c[r] : 0.f);
-                }
+                for (int r = 0; r < 4; ++r)
+                    O[s][4 * h + r] = c[r];
             }
+        if (live) {
+            const uint32_t step = opaque_uniform((uint32_t)o_stride * sizeof(E)), off = opaque((uint32_t)q8 * step);
+            if (n == 64) {
+#pragma unroll
+                for (int s = 0; s < 2; ++s)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        delta_store<T>((E *)((char *)o + (off + (32 * s + e) * step)), O[s][e]);
+            } else {
+#pragma unroll
+                for (int s = 0; s < 2; ++s)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        if (q8 < rows - (32 * s + e))
+                            delta_store<T>((E *)((char *)o + (off + (32 * s + e) * step)),
+                                           q8 < n - (32 * s + e) ? O[s][e] : 0.f);
+            }
+        }
         // the state
         Parts<kParts> W[2];
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
             float w[8];
+            const float *left = gates.left + q8 + 32 * s;
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-                w[e] = gates.left[32 * s + 8 * quarter + e] * U[2 * s + (e >> 2)][e & 3];
+                w[e] = left[e] * U[2 * s + (e >> 2)][e & 3];
             W[s] = split8<kParts>(w);
         }
         const float whole = gates.whole;
@@ -565,22 +814,18 @@ SSD_KERNEL(256) void delta_scan_kernel(DeltaParams p)
 #pragma unroll
             for (int r = 0; r < 4; ++r)
                 c[r] = whole * S[i][r];
-            const E *row = kt + (32 * (i >> 1) + tile_row(i & 1, l)) * TS + 8 * quarter;
 #pragma unroll
             for (int s = 0; s < 2; ++s)
-                c = mm<kParts>(lds_operand(row + 32 * s), W[s], c);
+                c = mm<kParts>(lds_operand(ktl + (state_at(i, 0) * TS + 32 * s)), W[s], c);
             S[i] = c;
+            if (i & 1)
+                sched_fence();
         }
+        if (next > 0 && wave == WAVES - 1)
+            delta_gates_of(both[(chunk + 1) & 1], ng, nbeta, next);
     }
     if (p.final_state && live)
-#pragma unroll
-        for (int i = 0; i < 2 * KP; ++i)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int f = 32 * (i >> 1) + 8 * quarter + 4 * (i & 1) + r;
-                if (f < p.Dk)
-                    p.final_state[head + (int64_t)f * p.Dv + dv] = S[i][r];
-            }
+        state_store<KP>(S, p.final_state + head + dv, p.Dk, p.Dv);
 }
 
 // ------------------------------------------------------------ a few tokens on the state
@@ -757,7 +1002,7 @@ SSD_KERNEL(256) void delta_scan_bwd_kernel(DeltaParams p)
 #pragma unroll
         for (int s = 0; s < KP; ++s)
             Sp[s] = split_tiles<kParts>(S[2 * s], S[2 * s + 1]);
-        const E *go = (const E *)p.go + token * o_stride + row_dv;
+        const E *go = (const E *)p.go + token * o_stride + (live ? row_dv : 0);
         Parts<IN> G[2];
         float raw[2][8];
 #pragma unroll
@@ -765,7 +1010,10 @@ SSD_KERNEL(256) void delta_scan_bwd_kernel(DeltaParams p)
             const int t = 32 * s + 8 * quarter;
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-                raw[s][e] = live && t + e < n ? delta_load<T>(go + (t + e) * o_stride) : 0.f;
+                raw[s][e] = delta_load<T>(go + (t + e < n ? t + e : n - 1) * o_stride);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                raw[s][e] = live && t + e < n ? raw[s][e] : 0.f;
             G[s] = split8<IN>(raw[s]);
         }
         float dU[2][8], dR[2][8];
@@ -980,8 +1228,11 @@ SSD_KERNEL(256) void delta_grad_kernel(DeltaParams p)
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         const int f = 32 * s + 8 * quarter + e;
-                        w[e] = live && f < p.Dk ? S[(int64_t)f * p.Dv + dv] : 0.f;
+                        w[e] = S[(int64_t)(f < p.Dk ? f : 0) * p.Dv + (live ? dv : 0)];
                     }
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        w[e] = live && 32 * s + 8 * quarter + e < p.Dk ? w[e] : 0.f;
                     Sp[s] = split8<kParts>(w);
                 }
                 float R[2][8];
@@ -998,11 +1249,11 @@ SSD_KERNEL(256) void delta_grad_kernel(DeltaParams p)
 #pragma unroll
                         for (int r = 0; r < 4; ++r) {
                             const int t = 32 * s + 8 * quarter + 4 * h + r;
-                            const float x = live && t < n ? delta_load<T>(v + t * p.v_stride + dv) : 0.f;
-                            const float read = x - lds.gates.since[t] * ks[r];
+                            const float x = delta_load<T>(v + (t < n ? t : n - 1) * p.v_stride + (live ? dv : 0));
+                            const float read = (live && t < n ? x : 0.f) - lds.gates.since[t] * ks[r];
+                            const float by = gr[(int64_t)t * p.Dv + (live ? dv : 0)];
                             R[s][4 * h + r] = lds.gates.beta[t] * read;
-                            if (live)
-                                by_beta[s][4 * h + r] += read * gr[(int64_t)t * p.Dv + dv];
+                            by_beta[s][4 * h + r] += live ? read * by : 0.f;
                         }
                     }
                 const float *tri = p.tri + at * kDeltaFragFloats + 8 * lane;
