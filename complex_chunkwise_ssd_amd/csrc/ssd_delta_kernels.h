@@ -477,64 +477,83 @@ SSD_DEVICE void frag_store(v4u *frags, int f, int i, int j, v4f w)
     }
 }
 
-// One of the ten tiles (ti, tj) of A = beta D o K K^T below the diagonal and of P = scale Q K^T o D: into the two
-// 32 x 32 blocks on the diagonal (pairs, float32, transposed) or the operand tiles of A_10, and the operand tiles of P.
-template <int T, int KP, int OUT>
+// A chunk's triangle and P, by all waves, in tiles of 16: A = beta D o K K^T below the diagonal and
+// P = scale Q K^T o D. Of the two 32 x 32 blocks of I + A on the diagonal the inverses of their own blocks of 16 and
+// A between them go into `pairs` (float32, transposed); A_10 and P into operand tiles. Each of the first four
+// waves has one tile on the diagonal, the others are dealt out so that the first two, which finish the
+// inverses afterwards, have the fewest.
+template <int T, int KP, int OUT, int WAVES>
 SSD_DEVICE void delta_tiles(const typename DeltaElem<T>::type *k, const typename DeltaElem<T>::type *q,
-                            const DeltaGates &gates, float scale, int ti, int tj, float *pairs, v4u *tri, v4u *pf)
+                            const DeltaGates &gates, float scale, float *pairs, v4u *tri, v4u *pf)
 {
-    const int l = thread_id() & 15, quarter = (thread_id() & 63) >> 4;
-    const v4f kk = delta_tile<T, KP>(k, tj, k, ti), qk = delta_tile<T, KP>(k, tj, q, ti);  // rows j, column i
-    const int i = 16 * ti + l, j = 16 * tj + 4 * quarter;
-    const double sum = gates.sum[i];
-    const float beta = gates.beta[i];
-    v4f a, w;
+    const int l = thread_id() & 15, quarter = (thread_id() & 63) >> 4, wave = wave_id();
+    // off the diagonal: (1,0) (3,2) (2,0) (2,1) (3,0) (3,1); of four waves 2 and 3 take two of them
+    const int mine = WAVES == 4 ? (wave < 2 ? 4 + wave : 2 * wave - 4) : (wave < 4 ? 2 + wave : wave - 4);
+    const int many = WAVES == 4 ? (wave < 2 ? 1 : 2) : (wave < 2 ? 0 : 1);
+    constexpr int most = WAVES == 4 ? 3 : 2;
+    int ti[most], tj[most];
+    bool has[most];
+    v4f kk[most], qk[most];
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-        const float d = delta_exp(sum - gates.sum[j + r]);
-        a[r] = i > j + r ? beta * d * kk[r] : 0.f;
-        w[r] = i >= j + r ? scale * d * qk[r] : 0.f;
+    for (int c = 0; c < most; ++c) {
+        const int o = mine + c - 1;
+        has[c] = c == 0 ? wave < 4 : c <= many;
+        ti[c] = c == 0 ? wave : o == 0 ? 1 : o == 2 || o == 3 ? 2 : 3;
+        tj[c] = c == 0 ? wave : o == 1 ? 2 : o == 3 || o == 5 ? 1 : 0;
+        if (has[c]) {
+            kk[c] = delta_tile<T, KP>(k, tj[c], k, ti[c]);  // rows j, column i
+            qk[c] = delta_tile<T, KP>(k, tj[c], q, ti[c]);
+        }
     }
-    const int f = frag_of(i >> 5, i >> 2 & 1, j >> 5);
-    if (ti >> 1 == tj >> 1)
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-            pairs[((i >> 5) * 32 + (j & 31) + r) * kPairStride + (i & 31)] = a[r];
-    else
-        frag_store<kParts>(tri, f, i, j, a);
-    frag_store<OUT>(pf, f, i, j, w);
+    for (int c = 0; c < most; ++c) {
+        if (!has[c])
+            continue;
+        const int i = 16 * ti[c] + l, j = 16 * tj[c] + 4 * quarter;
+        const double sum = gates.sum[i];
+        const float beta = gates.beta[i];
+        v4f a, w;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const float d = delta_exp(sum - gates.sum[j + r]);
+            a[r] = c > 0 || i > j + r ? beta * d * kk[c][r] : 0.f;
+            w[r] = c > 0 || i >= j + r ? scale * d * qk[c][r] : 0.f;
+        }
+        const int f = frag_of(i >> 5, i >> 2 & 1, j >> 5);
+        frag_store<OUT>(pf, f, i, j, w);
+        if (c == 0) {
+            // column l of the block's inverse, in every quarter: each value is taken from all that follow it
+            // as soon as it is known; the block's entries reach all lanes as scalars
+            float x[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+                x[e] = e == l ? 1.f : 0.f;
+            const v4f minus = -a;
+#pragma unroll
+            for (int e = 0; e < 15; ++e)
+#pragma unroll
+                for (int u = e + 1; u < 16; ++u)
+                    x[u] = __builtin_fmaf(lane_read(minus[e & 3], 16 * (e >> 2) + u), x[e], x[u]);
+            if (quarter == 0)
+#pragma unroll
+                for (int e = 0; e < 16; e += 4)
+                    *(v4f *)(pairs + i * kPairStride + (16 * wave & 16) + e) = v4f{x[e], x[e + 1], x[e + 2], x[e + 3]};
+        } else if (ti[c] >> 1 == tj[c] >> 1) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                pairs[(j + r) * kPairStride + (i & 31)] = a[r];
+        } else {
+            frag_store<kParts>(tri, f, i, j, a);
+        }
+    }
 }
 
-// (I + A)^-1 of a block of 32 on the diagonal, held transposed, by one wave: column c of each block of 16 by
-// substitution in lanes 16 d + c (and again in 32 + 16 d + c), each value taken from all that follow it as soon
-// as it is known; the corner between them as - T_1 A T_0. Into operand tiles.
+// The corner of the inverse of a block of 32 (held transposed), - T_1 A T_0, and the block into operand tiles, by
+// one wave.
 SSD_DEVICE void delta_invert(float *block, int pair, v4u *tri)
 {
-    const int l = thread_id() & 15, quarter = (thread_id() & 63) >> 4, d = quarter & 1;
-    float *own = block + 16 * d * kPairStride + 16 * d;
-    float x[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-        x[i] = i == l ? 1.f : 0.f;
-#pragma unroll
-    for (int j = 0; j < 15; ++j) {
-#pragma unroll
-        for (int i = (j + 1) / 4 * 4; i < 16; i += 4) {
-            const v4f a = *(const v4f *)(own + j * kPairStride + i);
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (i + e > j)
-                    x[i + e] = __builtin_fmaf(-a[e], x[j], x[i + e]);
-        }
-        if (j % 4 == 3)
-            sched_fence();  // no more than four columns in flight
-    }
-    // the transpose's D = - T_0^T A^T T_1^T: y = A^T T_1^T, of which the transposed T_1 has its columns in the lanes
-    wave_lds_sync();
-#pragma unroll
-    for (int i = 0; i < 16; i += 4)
-        *(v4f *)(own + l * kPairStride + i) = v4f{x[i], x[i + 1], x[i + 2], x[i + 3]};  // row l of T^T
-    wave_lds_sync();
+    const int l = thread_id() & 15, quarter = (thread_id() & 63) >> 4;
+    // the transpose's is - T_0^T (A^T T_1^T)
     float *corner = block + 16;  // A^T: rows of the first 16, columns of the second
     const v4f a = *(const v4f *)(corner + l * kPairStride + 4 * quarter);
     const v4f t0 = *(const v4f *)(block + l * kPairStride + 4 * quarter);
@@ -690,19 +709,7 @@ SSD_KERNEL_WAVES(64 * WAVES, 2) void delta_scan_kernel(DeltaParams p)
         const int next = delta_chunk_tokens(length, chunk + 1);
         if (next > 0)
             fetch(chunk + 1, next);
-        // the ten tiles, the first two waves having the blocks to solve later on
-        if (WAVES == 4) {
-            const int from = wave < 2 ? 2 * wave : 3 * wave - 2, to = wave < 2 ? from + 2 : from + 3;
-            for (int i = from; i < to; ++i) {
-                const int ti = i < 1 ? 0 : i < 3 ? 1 : i < 6 ? 2 : 3;
-                delta_tiles<T, KP, OUT>(k, q, gates, p.scale, ti, i - ti * (ti + 1) / 2, pairs, tri, pf);
-            }
-        } else {
-            for (int i = wave; i < 10; i += WAVES) {
-                const int ti = i < 1 ? 0 : i < 3 ? 1 : i < 6 ? 2 : 3;
-                delta_tiles<T, KP, OUT>(k, q, gates, p.scale, ti, i - ti * (ti + 1) / 2, pairs, tri, pf);
-            }
-        }
+        delta_tiles<T, KP, OUT, WAVES>(k, q, gates, p.scale, pairs, tri, pf);
         block_sync();
         if (wave < 2)
             delta_invert(pairs + 32 * wave * kPairStride, wave, tri);
@@ -743,8 +750,8 @@ SSD_KERNEL_WAVES(64 * WAVES, 2) void delta_scan_kernel(DeltaParams p)
                     R[s][4 * h + r] = beta[r] * (v[4 * h + r] - since[r] * ks[r]);
                     O[s][4 * h + r] = p.scale * since[r] * qs[r];
                 }
-                sched_fence();
             }
+            sched_fence();
         }
         block_sync();  // the triangle is there
         // U, and O += P U
