@@ -43,16 +43,24 @@ int check_delta_strides(const DeltaSizes &z, int64_t q, int64_t k, int64_t v)
     if (q < z.Hk * z.Dk || k < z.Hk * z.Dk || v < z.Hv * z.Dv)
         return SSD_ERR_SHAPE;
     const int64_t most = q > k ? (q > v ? q : v) : (k > v ? k : v);
-    if (!z.empty() && most > kMaxElems / (z.B * z.T))
+    // offsets within a chunk of 64 tokens have 32 bits
+    if (most > (1LL << 23) || z.Hv * z.Dv > (1LL << 23) || (!z.empty() && most > kMaxElems / (z.B * z.T)))
         return SSD_ERR_UNSUPPORTED;
     return SSD_OK;
 }
 
 bool delta_few(const DeltaSizes &z) { return z.T <= ssd::kDeltaFew; }
 
-size_t delta_frag_bytes(const DeltaSizes &z)
+// Workspace of the gradients: dS' and dR of every chunk, and dQ and dK by value heads where they share keys.
+struct DeltaSpace {
+    size_t gs, gr, w;
+    size_t bytes() const { return gs + gr + 2 * w; }
+};
+DeltaSpace delta_space(const DeltaSizes &z)
 {
-    return align256((size_t)(z.B * z.Hv * z.chunks()) * ssd::kDeltaFragFloats * 4);
+    const size_t each = (size_t)(z.B * z.Hv * z.chunks());
+    return {align256(each * z.Dk * z.Dv * 4), align256(each * 64 * z.Dv * 4),
+            z.Hv > z.Hk ? align256((size_t)(z.B * z.T * z.Hv) * z.Dk * 4) : 0};
 }
 
 ssd::DeltaParams delta_params(const DeltaSizes &z, const void *q, int64_t q_stride, const void *k, int64_t k_stride,
@@ -106,20 +114,32 @@ int launch_delta(const ssd::DeltaParams &p, hipStream_t s)
     return p.Dv > 64 && KP == 4 ? launch_delta_as<T, KP, 8>(p, s) : launch_delta_as<T, KP, 4>(p, s);
 }
 
+template <int T, int KP, int WAVES>
+int launch_delta_scan_bwd(ssd::DeltaParams p, hipStream_t s)
+{
+    p.columns = (p.Dv + 16 * WAVES - 1) / (16 * WAVES);
+    hipLaunchKernelGGL((ssd::delta_scan_bwd_kernel<T, KP, WAVES>), dim3((unsigned)((int64_t)p.B * p.Hv * p.columns)),
+                       dim3(64 * WAVES), 0, s, p);
+    return launch_status();
+}
 template <int T, int KP>
 int launch_delta_bwd(const ssd::DeltaParams &p, hipStream_t s)
 {
-    const dim3 block(256);
-    hipLaunchKernelGGL((ssd::delta_prepare_kernel<T, KP, true>), dim3((unsigned)((int64_t)p.B * p.Hv * p.chunks)), block,
-                       0, s, p);
+    if (int st = p.Dv > 64 && KP == 4 ? launch_delta_scan_bwd<T, KP, 8>(p, s) : launch_delta_scan_bwd<T, KP, 4>(p, s))
+        return st;
+    const dim3 grid((unsigned)((int64_t)p.B * p.Hv * p.chunks)), block(256);
+    if (p.Dv > 64)
+        hipLaunchKernelGGL((ssd::delta_grad_kernel<T, KP, true>), grid, block, 0, s, p);
+    else
+        hipLaunchKernelGGL((ssd::delta_grad_kernel<T, KP, false>), grid, block, 0, s, p);
     if (int st = launch_status())
         return st;
-    hipLaunchKernelGGL((ssd::delta_scan_bwd_kernel<T, KP>), dim3((unsigned)((int64_t)p.B * p.Hv * p.columns)), block, 0, s,
-                       p);
-    if (int st = launch_status())
-        return st;
-    hipLaunchKernelGGL((ssd::delta_grad_kernel<T, KP>), dim3((unsigned)((int64_t)p.B * p.Hk * p.chunks)), block, 0, s, p);
-    return launch_status();
+    if (p.Hv > p.Hk) {
+        const int64_t blocks = ((int64_t)p.B * p.T * p.Hk * p.Dk + 255) / 256;
+        hipLaunchKernelGGL((ssd::delta_share_kernel<T>), dim3((unsigned)(blocks < 8192 ? blocks : 8192)), block, 0, s, p);
+        return launch_status();
+    }
+    return SSD_OK;
 }
 
 int launch_delta_copy(const float *from, float *to, int64_t n, hipStream_t s)
@@ -189,7 +209,6 @@ int ssd_gated_delta(const void *q, int64_t q_stride, const void *k, int64_t k_st
     p.o = o;
     p.final_state = final_state;
     p.states = chunk_states;
-    p.tri = (float *)workspace;
     if (delta_few(z))
         return dtype == SSD_BF16 ? launch_delta_few<ssd::kBF16>(p, s) : launch_delta_few<ssd::kF32>(p, s);
     if (dtype == SSD_BF16)
@@ -203,8 +222,7 @@ size_t ssd_gated_delta_backward_workspace_bytes(int64_t batch, int64_t T, int64_
     const DeltaSizes z{batch, T, Hk, Hv, Dk, Dv};
     if (check_delta(z, dtype, 1.f) || z.empty())
         return 0;
-    const int64_t each = batch * Hv * z.chunks();
-    return 3 * delta_frag_bytes(z) + align256((size_t)(each * Dk * Dv) * 4) + align256((size_t)(each * 64 * Dv) * 4);
+    return delta_space(z).bytes();
 }
 
 int ssd_gated_delta_backward(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
@@ -260,13 +278,12 @@ int ssd_gated_delta_backward(const void *q, int64_t q_stride, const void *k, int
     p.gg = grad_g;
     p.gbeta = grad_beta;
     p.ginit = grad_initial_state;
+    const DeltaSpace space = delta_space(z);
     char *at = (char *)workspace;
-    const size_t frags = delta_frag_bytes(z);
-    p.tri = (float *)at;
-    p.tri_t = (float *)(at + frags);
-    p.pt = (float *)(at + 2 * frags);
-    p.gs = (float *)(at + 3 * frags);
-    p.gr = (float *)(at + 3 * frags + align256((size_t)(batch * Hv * z.chunks() * Dk * Dv) * 4));
+    p.gs = (float *)at;
+    p.gr = (float *)(at + space.gs);
+    p.wq = (float *)(at + space.gs + space.gr);
+    p.wk = (float *)(at + space.gs + space.gr + space.w);
     if (dtype == SSD_BF16)
         return Dk <= 64 ? launch_delta_bwd<ssd::kBF16, 2>(p, s) : launch_delta_bwd<ssd::kBF16, 4>(p, s);
     return Dk <= 64 ? launch_delta_bwd<ssd::kF32, 2>(p, s) : launch_delta_bwd<ssd::kF32, 4>(p, s);

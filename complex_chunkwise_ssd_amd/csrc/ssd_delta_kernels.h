@@ -35,7 +35,6 @@ namespace ssd {
 
 constexpr int kDeltaChunk = 64;
 constexpr int kDeltaFrags = 6;            // operand tiles of the solve: (span, tile, span of k)
-constexpr int kDeltaFragFloats = kDeltaFrags * 64 * 8;
 
 struct DeltaParams {
     const void *q, *k, *v;                // (B, T, heads, D), tokens *_stride elements apart
@@ -45,7 +44,6 @@ struct DeltaParams {
     void *o;                              // (B, T, Hv, Dv)
     float *final_state;                   // nullable: (B, Hv, Dk, Dv)
     float *states;                        // nullable: (B, chunks, Hv, Dk, Dv), the state entering each chunk
-    float *tri;                           // (B, Hv, chunks) times kDeltaFragFloats: T_00, A_10, T_11
     // backward
     const float *chunk_states;
     const void *go;                       // (B, T, Hv, Dv)
@@ -53,7 +51,7 @@ struct DeltaParams {
     void *gq, *gk, *gv;                   // as q, k, v, dense
     float *gg, *gbeta;                    // (B, T, Hv)
     float *ginit;                         // nullable: (B, Hv, Dk, Dv)
-    float *tri_t, *pt;                    // as tri: the transposed ones, and P^T
+    float *wq, *wk;                       // (B, T, Hv, Dk): dQ and dK by value heads, where they share keys
     float *gs;                            // (B, Hv, chunks, Dk, Dv): dS' of each chunk
     float *gr;                            // (B, Hv, chunks, 64, Dv): dR
     int64_t q_stride, k_stride, v_stride;
@@ -256,9 +254,7 @@ SSD_DEVICE int delta_chunk_tokens(int length, int chunk)
 
 // --------------------------------------------------------- a chunk's triangle
 
-constexpr int kTriStride = 68;
-
-// Tile (ti, tj) of X Y^T: rows (lanes' components) of X, columns of Y, in tiles of 16 as they lie.
+// Tile (tx, ty) of X Y^T: rows (lanes' components) of X, columns of Y, in tiles of 16 as they lie.
 template <int T, int KP>
 SSD_DEVICE v4f delta_tile(const typename DeltaElem<T>::type *x, int tx, const typename DeltaElem<T>::type *y, int ty)
 {
@@ -272,160 +268,6 @@ SSD_DEVICE v4f delta_tile(const typename DeltaElem<T>::type *x, int tx, const ty
     return c;
 }
 
-// A (below the diagonal, zeros on it) of a chunk into tri[64][kTriStride], by four waves; the two tiles
-// above the diagonal that the blocks of 32 hold become zeros.
-template <int T, int KP>
-SSD_DEVICE void delta_products(const typename DeltaElem<T>::type *k, const DeltaGates &gates, float *tri)
-{
-    const int l = thread_id() & 15, q = (thread_id() & 63) >> 4;
-    for (int i = wave_id(); i < 10; i += 4) {  // (0,0) (1,0) (1,1) (2,0) ... (3,3)
-        const int ti = i < 1 ? 0 : i < 3 ? 1 : i < 6 ? 2 : 3, tj = i - ti * (ti + 1) / 2;
-        const v4f c = delta_tile<T, KP>(k, tj, k, ti);  // rows j, column i
-        const int row = 16 * ti + l, col = 16 * tj + 4 * q;
-        v4f w;
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-            w[r] = row > col + r ? gates.beta[row] * delta_exp(gates.sum[row] - gates.sum[col + r]) * c[r] : 0.f;
-        *(v4f *)(tri + row * kTriStride + col) = w;
-    }
-    if (wave_id() < 2) {
-        const v4f zero = {0.f, 0.f, 0.f, 0.f};
-        *(v4f *)(tri + (32 * wave_id() + l) * kTriStride + 32 * wave_id() + 16 + 4 * q) = zero;
-    }
-}
-
-// The blocks of 16 on the diagonal become (I + A)^-1, by one wave: lane 16 d + c finds column c of
-// block d, one value after the other.
-SSD_DEVICE void delta_diagonal(float *tri)
-{
-    const int c = thread_id() & 15, d = (thread_id() & 63) >> 4;
-    float *block = tri + 16 * d * kTriStride + 16 * d;
-    float x[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        float s = i == c ? 1.f : 0.f;
-#pragma unroll
-        for (int j = 0; j < i; j += 4) {
-            const v4f a = *(const v4f *)(block + i * kTriStride + j);
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (j + e < i)
-                    s = __builtin_fmaf(-a[e], x[j + e], s);
-        }
-        x[i] = s;
-    }
-    wave_lds_sync();
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-        block[i * kTriStride + c] = x[i];
-    wave_lds_sync();
-}
-
-// ... and the block of 32 around two of them: - T_1 A T_0 in its lower left, by one wave.
-SSD_DEVICE void delta_corner(float *tri, int pair)
-{
-    const int l = thread_id() & 15, q = (thread_id() & 63) >> 4;
-    float *t0 = tri + 32 * pair * kTriStride + 32 * pair, *a = t0 + 16 * kTriStride, *t1 = a + 16;
-    const v4f ra = *(const v4f *)(a + l * kTriStride + 4 * q), r1 = *(const v4f *)(t1 + l * kTriStride + 4 * q);
-    v4f y = {0.f, 0.f, 0.f, 0.f}, z = y;
-#pragma unroll
-    for (int r = 0; r < 4; ++r)
-        y = mfma_16x16x4(ra[r], t0[(4 * q + r) * kTriStride + l], y);
-#pragma unroll
-    for (int r = 0; r < 4; ++r)
-        z = mfma_16x16x4(r1[r], -y[r], z);
-    wave_lds_sync();
-#pragma unroll
-    for (int r = 0; r < 4; ++r)
-        a[(4 * q + r) * kTriStride + l] = z[r];
-}
-
-// The triangles of every chunk (and, for the backward pass, their transposes and P^T), in the order in
-// which the walks read them as operands: tile, lane, eight values.
-template <int T, int KP, bool BACKWARD>
-SSD_KERNEL(256) void delta_prepare_kernel(DeltaParams p)
-{
-    typedef typename DeltaElem<T>::type E;
-    constexpr int RS = 32 * KP + DeltaElem<T>::pad;
-    SSD_LDS E k[64 * RS], q[BACKWARD ? 64 * RS : 8];
-    SSD_LDS float tri[64 * kTriStride], pp[BACKWARD ? 64 * kTriStride : 4];
-    SSD_LDS DeltaGates gates;
-    const int64_t id = block_id();
-    const int chunk = (int)(id % p.chunks), hv = (int)(id / p.chunks % p.Hv), b = (int)(id / p.chunks / p.Hv);
-    const int hk = hv / (p.Hv / p.Hk);
-    const int n = delta_chunk_tokens(delta_valid(p, b), chunk);
-    if (n == 0)
-        return;
-    const int64_t token = (int64_t)b * p.T + chunk * kDeltaChunk;
-    delta_stage<T, KP, true, false>((const E *)p.k + token * p.k_stride + hk * p.Dk, p.k_stride, p.Dk, n, k, nullptr);
-    if (BACKWARD)
-        delta_stage<T, KP, true, false>((const E *)p.q + token * p.q_stride + hk * p.Dk, p.q_stride, p.Dk, n, q, nullptr);
-    if (wave_id() == 0)
-        delta_gates(gates, p.g, p.beta, token * p.Hv + hv, p.Hv, n);
-    block_sync();
-    delta_products<T, KP>(k, gates, tri);
-    const int l = thread_id() & 15, quarter = (thread_id() & 63) >> 4;
-    if (BACKWARD) {
-        for (int i = wave_id(); i < 10; i += 4) {
-            const int ti = i < 1 ? 0 : i < 3 ? 1 : i < 6 ? 2 : 3, tj = i - ti * (ti + 1) / 2;
-            const v4f c = delta_tile<T, KP>(q, ti, k, tj);  // rows i, column j
-            const int row = 16 * ti + 4 * quarter, col = 16 * tj + l;
-            v4f w;
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-                w[r] = row + r >= col ? p.scale * delta_exp(gates.sum[row + r] - gates.sum[col]) * c[r] : 0.f;
-            *(v4f *)(pp + col * kTriStride + row) = w;  // P^T: row j, column i
-        }
-        if (wave_id() < 2) {  // what lies below its diagonal in the blocks of 32
-            const v4f zero = {0.f, 0.f, 0.f, 0.f};
-            *(v4f *)(pp + (32 * wave_id() + 16 + l) * kTriStride + 32 * wave_id() + 4 * quarter) = zero;
-        }
-    }
-    block_sync();
-    if (wave_id() == 0)
-        delta_diagonal(tri);
-    block_sync();
-    if (wave_id() < 2)
-        delta_corner(tri, wave_id());
-    block_sync();
-    const int64_t out = id * kDeltaFragFloats;
-    for (int unit = thread_id(); unit < kDeltaFrags * 64; unit += 256) {
-        const int f = unit >> 6, m = unit & 15, k8 = 8 * ((unit & 63) >> 4);
-        {
-            const int s = f >= 2, h = s ? (f - 2) >> 1 : f, t = s ? (f - 2) & 1 : 0;
-            const float *row = tri + (32 * s + tile_row(h, m)) * kTriStride + 32 * t + k8;
-            *(v4f *)(p.tri + out + 8 * unit) = *(const v4f *)row;
-            *(v4f *)(p.tri + out + 8 * unit + 4) = *(const v4f *)(row + 4);
-        }
-        if (BACKWARD) {
-            const int s = f >= 4, h = s ? f - 4 : f >> 1, t = s ? 1 : f & 1;
-            const int j = 32 * s + tile_row(h, m);
-            const float *row = pp + j * kTriStride + 32 * t + k8;
-            *(v4f *)(p.pt + out + 8 * unit) = *(const v4f *)row;
-            *(v4f *)(p.pt + out + 8 * unit + 4) = *(const v4f *)(row + 4);
-            v4f a, c;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                a[e] = tri[(32 * t + k8 + e) * kTriStride + j];
-                c[e] = tri[(32 * t + k8 + 4 + e) * kTriStride + j];
-            }
-            *(v4f *)(p.tri_t + out + 8 * unit) = a;
-            *(v4f *)(p.tri_t + out + 8 * unit + 4) = c;
-        }
-    }
-}
-
-// Operand tiles from memory (as delta_prepare_kernel leaves them) into shared memory in parts.
-template <int N>
-SSD_DEVICE void delta_stage_frags(const float *src, v4u *dst, int threads)
-{
-    for (int unit = thread_id(); unit < kDeltaFrags * 64; unit += threads) {
-        const Parts<N> r = split_tiles<N>(*(const v4f *)(src + 8 * unit), *(const v4f *)(src + 8 * unit + 4));
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-            dst[(i * kDeltaFrags + (unit >> 6)) * 64 + (unit & 63)] = r.p[i];
-    }
-}
 template <int N>
 SSD_DEVICE Parts<N> frag_operand(const v4u *frags, int f)
 {
@@ -479,10 +321,10 @@ SSD_DEVICE void frag_store(v4u *frags, int f, int i, int j, v4f w)
 
 // A chunk's triangle and P, by all waves, in tiles of 16: A = beta D o K K^T below the diagonal and
 // P = scale Q K^T o D. Of the two 32 x 32 blocks of I + A on the diagonal the inverses of their own blocks of 16 and
-// A between them go into `pairs` (float32, transposed); A_10 and P into operand tiles. Each of the first four
-// waves has one tile on the diagonal, the others are dealt out so that the first two, which finish the
-// inverses afterwards, have the fewest.
-template <int T, int KP, int OUT, int WAVES>
+// A between them go into `pairs` (float32, transposed); A_10 and P into operand tiles, or, with TURNED, A_10^T and P^T.
+// Each of the first four waves has one tile on the diagonal, the others are dealt out so that the first two,
+// which finish the inverses afterwards, have the fewest.
+template <int T, int KP, int OUT, int WAVES, bool TURNED>
 SSD_DEVICE void delta_tiles(const typename DeltaElem<T>::type *k, const typename DeltaElem<T>::type *q,
                             const DeltaGates &gates, float scale, float *pairs, v4u *tri, v4u *pf)
 {
@@ -500,27 +342,29 @@ SSD_DEVICE void delta_tiles(const typename DeltaElem<T>::type *k, const typename
         has[c] = c == 0 ? wave < 4 : c <= many;
         ti[c] = c == 0 ? wave : o == 0 ? 1 : o == 2 || o == 3 ? 2 : 3;
         tj[c] = c == 0 ? wave : o == 1 ? 2 : o == 3 || o == 5 ? 1 : 0;
-        if (has[c]) {
-            kk[c] = delta_tile<T, KP>(k, tj[c], k, ti[c]);  // rows j, column i
-            qk[c] = delta_tile<T, KP>(k, tj[c], q, ti[c]);
+        if (has[c]) {  // rows j, column i; or rows i, column j
+            kk[c] = TURNED ? delta_tile<T, KP>(k, ti[c], k, tj[c]) : delta_tile<T, KP>(k, tj[c], k, ti[c]);
+            if (pf)
+                qk[c] = TURNED ? delta_tile<T, KP>(q, ti[c], k, tj[c]) : delta_tile<T, KP>(k, tj[c], q, ti[c]);
         }
     }
 #pragma unroll
     for (int c = 0; c < most; ++c) {
         if (!has[c])
             continue;
-        const int i = 16 * ti[c] + l, j = 16 * tj[c] + 4 * quarter;
-        const double sum = gates.sum[i];
-        const float beta = gates.beta[i];
+        const int row = 16 * (TURNED ? ti[c] : tj[c]) + 4 * quarter, col = 16 * (TURNED ? tj[c] : ti[c]) + l;
+        const double sum = gates.sum[col];
         v4f a, w;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            const float d = delta_exp(sum - gates.sum[j + r]);
-            a[r] = c > 0 || i > j + r ? beta * d * kk[c][r] : 0.f;
-            w[r] = c > 0 || i >= j + r ? scale * d * qk[c][r] : 0.f;
+            const float d = delta_exp(TURNED ? gates.sum[row + r] - sum : sum - gates.sum[row + r]);
+            const int below = TURNED ? row + r - col : col - row - r;  // i - j
+            a[r] = c > 0 || below > 0 ? gates.beta[TURNED ? row + r : col] * d * kk[c][r] : 0.f;
+            w[r] = pf && (c > 0 || below >= 0) ? scale * d * qk[c][r] : 0.f;
         }
-        const int f = frag_of(i >> 5, i >> 2 & 1, j >> 5);
-        frag_store<OUT>(pf, f, i, j, w);
+        const int f = TURNED ? frag_of_upper(col >> 5, col >> 2 & 1, row >> 5) : frag_of(col >> 5, col >> 2 & 1, row >> 5);
+        if (pf)
+            frag_store<OUT>(pf, f, col, row, w);
         if (c == 0) {
             // column l of the block's inverse, in every quarter: each value is taken from all that follow it
             // as soon as it is known; the block's entries reach all lanes as scalars
@@ -533,23 +377,28 @@ SSD_DEVICE void delta_tiles(const typename DeltaElem<T>::type *k, const typename
             for (int e = 0; e < 15; ++e)
 #pragma unroll
                 for (int u = e + 1; u < 16; ++u)
-                    x[u] = __builtin_fmaf(lane_read(minus[e & 3], 16 * (e >> 2) + u), x[e], x[u]);
+                    x[u] = __builtin_fmaf(TURNED ? lane_read(minus[u & 3], 16 * (u >> 2) + e)
+                                                 : lane_read(minus[e & 3], 16 * (e >> 2) + u), x[e], x[u]);
             if (quarter == 0)
 #pragma unroll
                 for (int e = 0; e < 16; e += 4)
-                    *(v4f *)(pairs + i * kPairStride + (16 * wave & 16) + e) = v4f{x[e], x[e + 1], x[e + 2], x[e + 3]};
+                    *(v4f *)(pairs + col * kPairStride + (16 * wave & 16) + e) = v4f{x[e], x[e + 1], x[e + 2], x[e + 3]};
         } else if (ti[c] >> 1 == tj[c] >> 1) {
+            if (TURNED)
+                *(v4f *)(pairs + col * kPairStride + (row & 31)) = a;
+            else
 #pragma unroll
-            for (int r = 0; r < 4; ++r)
-                pairs[(j + r) * kPairStride + (i & 31)] = a[r];
+                for (int r = 0; r < 4; ++r)
+                    pairs[(row + r) * kPairStride + (col & 31)] = a[r];
         } else {
-            frag_store<kParts>(tri, f, i, j, a);
+            frag_store<kParts>(tri, f, col, row, a);
         }
     }
 }
 
-// The corner of the inverse of a block of 32 (held transposed), - T_1 A T_0, and the block into operand tiles, by
-// one wave.
+// The corner of the inverse of a block of 32 (held transposed), - T_1 A T_0, and the block (with TURNED its transpose)
+// into operand tiles, by one wave.
+template <bool TURNED>
 SSD_DEVICE void delta_invert(float *block, int pair, v4u *tri)
 {
     const int l = thread_id() & 15, quarter = (thread_id() & 63) >> 4;
@@ -572,14 +421,30 @@ SSD_DEVICE void delta_invert(float *block, int pair, v4u *tri)
 #pragma unroll
     for (int h = 0; h < 2; ++h) {  // row i of the operand is column i of what is held
         float v[8];
+        if (TURNED) {
+            const float *row = block + (tile_row(0, l) + 4 * h) * kPairStride + 8 * quarter;
+            const v4f lo = *(const v4f *)row, hi = *(const v4f *)(row + 4);
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            v[e] = block[8 * quarter * kPairStride + tile_row(0, l) + (e * kPairStride + 4 * h)];
+            for (int e = 0; e < 8; ++e)
+                v[e] = e < 4 ? lo[e & 3] : hi[e & 3];
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                v[e] = block[8 * quarter * kPairStride + tile_row(0, l) + (e * kPairStride + 4 * h)];
+        }
         const Parts<kParts> parts = split8<kParts>(v);
+        const int f = TURNED ? frag_of_upper(pair, h, pair) : frag_of(pair, h, pair);
 #pragma unroll
         for (int e = 0; e < kParts; ++e)
-            tri[(e * kDeltaFrags + frag_of(pair, h, pair)) * 64 + (thread_id() & 63)] = parts.p[e];
+            tri[(e * kDeltaFrags + f) * 64 + (thread_id() & 63)] = parts.p[e];
     }
+}
+
+// Above the diagonal of a block of 32 (held transposed) there are zeros.
+SSD_DEVICE void delta_clear_pairs(float *pairs, int threads)
+{
+    for (int i = thread_id(); i < 16 * 16; i += threads)
+        pairs[(16 + (i >> 4)) * kPairStride + (i & 15)] = pairs[(48 + (i >> 4)) * kPairStride + (i & 15)] = 0.f;
 }
 
 // The feature that a lane holds in component r of tile i of its state, less 8 q.
@@ -682,9 +547,7 @@ SSD_KERNEL_WAVES(64 * WAVES, 2) void delta_scan_kernel(DeltaParams p)
         if (wave == WAVES - 1)
             delta_gates_of(both[0], ng, nbeta, n);
     }
-    // above the diagonal the blocks (held transposed) and tiles stay zero
-    for (int i = thread_id(); i < 16 * 16; i += NT)
-        pairs[(16 + (i >> 4)) * kPairStride + (i & 15)] = pairs[(48 + (i >> 4)) * kPairStride + (i & 15)] = 0.f;
+    delta_clear_pairs(pairs, NT);  // and they stay, as do P's tiles above its diagonal
     for (int i = thread_id(); i < OUT * kDeltaFrags * 64; i += NT)
         pf[i] = v4u{0u, 0u, 0u, 0u};
     for (int chunk = 0; chunk < p.chunks; ++chunk) {
@@ -709,10 +572,10 @@ SSD_KERNEL_WAVES(64 * WAVES, 2) void delta_scan_kernel(DeltaParams p)
         const int next = delta_chunk_tokens(length, chunk + 1);
         if (next > 0)
             fetch(chunk + 1, next);
-        delta_tiles<T, KP, OUT, WAVES>(k, q, gates, p.scale, pairs, tri, pf);
+        delta_tiles<T, KP, OUT, WAVES, false>(k, q, gates, p.scale, pairs, tri, pf);
         block_sync();
         if (wave < 2)
-            delta_invert(pairs + 32 * wave * kPairStride, wave, tri);
+            delta_invert<false>(pairs + 32 * wave * kPairStride, wave, tri);
         // R = beta (V - e^G K S), and e^G Q S
         Parts<kParts> Sp[KP];
 #pragma unroll
@@ -934,122 +797,129 @@ SSD_KERNEL(256) void delta_few_kernel(DeltaParams p)
 
 // ------------------------------------------------------------ gradients: the walk backwards
 
-// Eight tokens of one column as an operand: tokens at p and every `stride` after it, `n` of them.
-template <int T>
-SSD_DEVICE Parts<DeltaElem<T>::parts> column_operand(const typename DeltaElem<T>::type *p, int64_t stride, int n)
-{
-    float v[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-        v[e] = e < n ? delta_load<T>(p + e * stride) : 0.f;
-    return split8<DeltaElem<T>::parts>(v);
-}
-
-// As delta_scan_kernel, from the last chunk to the first, with the gradient of the state.
-template <int T, int KP>
-SSD_KERNEL(256) void delta_scan_bwd_kernel(DeltaParams p)
+// As delta_scan_kernel, from the last chunk to the first, with the gradient of the state: dS' of every chunk and
+// dR go to memory. K's rows make room for Q's columns once they have been used, Q's rows for those of dO.
+template <int T, int KP, int WAVES>
+SSD_KERNEL_WAVES(64 * WAVES, 2) void delta_scan_bwd_kernel(DeltaParams p)
 {
     typedef typename DeltaElem<T>::type E;
+    constexpr int NT = 64 * WAVES, COLS = 16 * WAVES;
     constexpr int pad = DeltaElem<T>::pad, RS = 32 * KP + pad, TS = 64 + pad;
     constexpr int IN = DeltaElem<T>::parts;
-    SSD_LDS E k[64 * RS], kt[32 * KP * TS], qt[32 * KP * TS];
+    constexpr int K_ROOM = 64 * RS > 32 * KP * TS ? 64 * RS : 32 * KP * TS;
+    constexpr int Q_ROOM = 64 * RS > COLS * TS ? 64 * RS : COLS * TS;
+    SSD_LDS E k[K_ROOM], q[Q_ROOM], kt[32 * KP * TS];
+    SSD_LDS float pairs[64 * kPairStride];
     SSD_LDS v4u tri[kParts * kDeltaFrags * 64], pt[kParts * kDeltaFrags * 64];
     SSD_LDS DeltaGates gates;
+    E *const qt = k, *const got = q;
     const int64_t id = block_id();
     const int block = (int)(id % p.columns), hv = (int)(id / p.columns % p.Hv), b = (int)(id / p.columns / p.Hv);
-    const int hk = hv / (p.Hv / p.Hk);
-    const int l = thread_id() & 15, quarter = (thread_id() & 63) >> 4;
-    const int dv = 64 * block + 16 * wave_id() + l;
+    const int hk = hv / (p.Hv / p.Hk), wave = wave_id(), lane = thread_id() & 63;
+    const int l = thread_id() & 15, quarter = lane >> 4, q8 = 8 * quarter;
+    const int first = COLS * block, dv = first + 16 * wave + l;
     const bool live = dv < p.Dv;
     const int64_t head = ((int64_t)b * p.Hv + hv) * p.Dk * p.Dv;
     v4f S[2 * KP];  // the gradient of the state after the chunk
 #pragma unroll
     for (int i = 0; i < 2 * KP; ++i)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int f = 32 * (i >> 1) + 8 * quarter + 4 * (i & 1) + r;
-            S[i][r] = p.gfinal && live && f < p.Dk ? p.gfinal[head + (int64_t)f * p.Dv + dv] : 0.f;
-        }
+        S[i] = v4f{0.f, 0.f, 0.f, 0.f};
+    if (p.gfinal && live)
+        state_load<KP>(S, p.gfinal + head + dv, p.Dk, p.Dv);
     const int length = delta_valid(p, b);
-    const int row_dv = hv * p.Dv + dv;
-    const int64_t o_stride = (int64_t)p.Hv * p.Dv;
-    for (int chunk = p.chunks - 1; chunk >= 0; --chunk) {
+    const int o_stride = p.Hv * p.Dv;
+    const int64_t row = (int64_t)b * p.T;
+    const E *qrow = (const E *)p.q + row * p.q_stride + hk * p.Dk, *krow = (const E *)p.k + row * p.k_stride + hk * p.Dk;
+    const E *orow = (const E *)p.go + row * o_stride + hv * p.Dv + first;
+    const int vcols = p.Dv - first;
+    const E *kl = k + tile_row(0, l) * RS + q8, *ktl = kt + tile_row(0, l) * TS + q8, *qtl = qt + tile_row(0, l) * TS + q8;
+    const E *gl = got + (16 * wave + l) * TS + q8;
+
+    Blocks<T, 32 * KP, NT> nk, nq;
+    Blocks<T, COLS, NT> no;
+    float ng = 0.f, nbeta = 0.f;
+    auto fetch = [&](int chunk, int n) {
+        const int64_t t = (int64_t)chunk * kDeltaChunk;
+        blocks_load<T, 32 * KP, NT>(nk, krow + t * p.k_stride, (int)p.k_stride, p.Dk, n);
+        blocks_load<T, 32 * KP, NT>(nq, qrow + t * p.q_stride, (int)p.q_stride, p.Dk, n);
+        blocks_load<T, COLS, NT>(no, orow + t * o_stride, o_stride, vcols, n);
+        if (wave == WAVES - 1) {
+            const int64_t at = (row + t + (lane < n ? lane : n - 1)) * p.Hv + hv;
+            ng = p.g[at];
+            nbeta = p.beta[at];
+        }
+    };
+    const int chunks = (length + kDeltaChunk - 1) / kDeltaChunk;  // those with tokens
+    if (chunks > 0)
+        fetch(chunks - 1, delta_chunk_tokens(length, chunks - 1));
+    delta_clear_pairs(pairs, NT);
+    for (int i = thread_id(); i < kParts * kDeltaFrags * 64; i += NT)
+        pt[i] = v4u{0u, 0u, 0u, 0u};
+    for (int chunk = chunks - 1; chunk >= 0; --chunk) {
         const int n = delta_chunk_tokens(length, chunk);
-        const int64_t token = (int64_t)b * p.T + chunk * kDeltaChunk;
-        const int rows = p.T - chunk * kDeltaChunk < 64 ? p.T - chunk * kDeltaChunk : 64;
-        E *gv = (E *)p.gv + token * o_stride + row_dv;
-        if (n == 0) {  // padding
-            if (live)
-                for (int t = quarter; t < rows; t += 4)
-                    delta_store<T>(gv + t * o_stride, 0.f);
-            continue;
-        }
         const int64_t at = ((int64_t)b * p.Hv + hv) * p.chunks + chunk;
+        if (live)
+            state_store<KP>(S, p.gs + at * p.Dk * p.Dv + dv, p.Dk, p.Dv);
         block_sync();  // the last chunk's operands have been read
-        delta_stage<T, KP, true, true>((const E *)p.k + token * p.k_stride + hk * p.Dk, p.k_stride, p.Dk, n, k, kt);
-        delta_stage<T, KP, false, true>((const E *)p.q + token * p.q_stride + hk * p.Dk, p.q_stride, p.Dk, n, nullptr, qt);
-        delta_stage_frags<kParts>(p.tri_t + at * kDeltaFragFloats, tri, 256);
-        delta_stage_frags<kParts>(p.pt + at * kDeltaFragFloats, pt, 256);
-        if (wave_id() == 0)
-            delta_gates(gates, p.g, p.beta, token * p.Hv + hv, p.Hv, n);
-        if (live) {
-            float *to = p.gs + at * p.Dk * p.Dv + dv;
-#pragma unroll
-            for (int i = 0; i < 2 * KP; ++i)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int f = 32 * (i >> 1) + 8 * quarter + 4 * (i & 1) + r;
-                    if (f < p.Dk)
-                        to[(int64_t)f * p.Dv] = S[i][r];
-                }
-        }
+        blocks_store<T, 32 * KP, NT, true, true>(nk, p.Dk, n, k, kt);
+        blocks_store<T, 32 * KP, NT, true, false>(nq, p.Dk, n, q, (E *)nullptr);
+        if (wave == WAVES - 1)
+            delta_gates_of(gates, ng, nbeta, n);
         block_sync();
-        // dU = P^T dO + e^(G_C - G) K dS'
+        delta_tiles<T, KP, kParts, WAVES, true>(k, q, gates, p.scale, pairs, tri, pt);
+        block_sync();
+        blocks_store<T, COLS, NT, false, true>(no, vcols, n, (E *)nullptr, got);
+        if (wave < 2)
+            delta_invert<true>(pairs + 32 * wave * kPairStride, wave, tri);
+        // e^(G_C - G) K dS'
         Parts<kParts> Sp[KP];
 #pragma unroll
         for (int s = 0; s < KP; ++s)
             Sp[s] = split_tiles<kParts>(S[2 * s], S[2 * s + 1]);
-        const E *go = (const E *)p.go + token * o_stride + (live ? row_dv : 0);
-        Parts<IN> G[2];
-        float raw[2][8];
+        float dU[2][8];
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-            const int t = 32 * s + 8 * quarter;
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                raw[s][e] = delta_load<T>(go + (t + e < n ? t + e : n - 1) * o_stride);
+            for (int h = 0; h < 2; ++h) {
+                v4f ks = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                raw[s][e] = live && t + e < n ? raw[s][e] : 0.f;
-            G[s] = split8<IN>(raw[s]);
+                for (int f = 0; f < KP; ++f)
+                    ks = mm<kParts>(lds_operand(kl + ((32 * s + 4 * h) * RS + 32 * f)), Sp[f], ks);
+                const v4f left = *(const v4f *)(gates.left + q8 + (32 * s + 4 * h));
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    dU[s][4 * h + r] = left[r] * ks[r];
+            }
+            sched_fence();
         }
-        float dU[2][8], dR[2][8];
+        block_sync();  // the triangle and dO are there, K's rows have been read
+        blocks_store<T, 32 * KP, NT, false, true>(nq, p.Dk, n, (E *)nullptr, qt);
+        if (chunk > 0)
+            fetch(chunk - 1, kDeltaChunk);
+        Parts<IN> G[2];
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+            G[s] = lds_operand(gl + 32 * s);
 #pragma unroll
         for (int s = 0; s < 2; ++s)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                v4f c = {0.f, 0.f, 0.f, 0.f}, ks = c;
-                const int row = (32 * s + tile_row(h, l)) * RS + 8 * quarter;
-#pragma unroll
-                for (int f = 0; f < KP; ++f)
-                    ks = mm<kParts>(lds_operand(k + row + 32 * f), Sp[f], ks);
+                v4f c = {dU[s][4 * h], dU[s][4 * h + 1], dU[s][4 * h + 2], dU[s][4 * h + 3]};
 #pragma unroll
                 for (int t = s; t < 2; ++t)
                     c = mm<kParts>(frag_operand<kParts>(pt, frag_of_upper(s, h, t)), G[t], c);
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
-                    dU[s][4 * h + r] = c[r] + gates.left[32 * s + 8 * quarter + 4 * h + r] * ks[r];
+                    dU[s][4 * h + r] = c[r];
             }
+        sched_fence();
         // dR
+        v4f dR[4];
         const Parts<kParts> u1 = split8<kParts>(dU[1]);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const v4f c = mm<kParts>(frag_operand<kParts>(tri, frag_of_upper(1, h, 1)), u1, v4f{0.f, 0.f, 0.f, 0.f});
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-                dR[1][4 * h + r] = c[r];
-        }
-        const Parts<kParts> r1 = split8<kParts>(dR[1]);
+        for (int h = 0; h < 2; ++h)
+            dR[2 + h] = mm<kParts>(frag_operand<kParts>(tri, frag_of_upper(1, h, 1)), u1, v4f{0.f, 0.f, 0.f, 0.f});
+        const Parts<kParts> r1 = split_tiles<kParts>(dR[2], dR[3]);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const v4f c = mm<kParts>(frag_operand<kParts>(tri, frag_of_upper(0, h, 1)), r1, v4f{0.f, 0.f, 0.f, 0.f});
@@ -1059,118 +929,156 @@ SSD_KERNEL(256) void delta_scan_bwd_kernel(DeltaParams p)
         }
         const Parts<kParts> u0 = split8<kParts>(dU[0]);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const v4f c = mm<kParts>(frag_operand<kParts>(tri, frag_of_upper(0, h, 0)), u0, v4f{0.f, 0.f, 0.f, 0.f});
+        for (int h = 0; h < 2; ++h)
+            dR[h] = mm<kParts>(frag_operand<kParts>(tri, frag_of_upper(0, h, 0)), u0, v4f{0.f, 0.f, 0.f, 0.f});
+        if (live) {
+            const uint32_t step = opaque_uniform((uint32_t)p.Dv * 4), off = opaque((uint32_t)q8 * step);
+            char *to = (char *)(p.gr + at * 64 * p.Dv + dv);
 #pragma unroll
-            for (int r = 0; r < 4; ++r)
-                dR[0][4 * h + r] = c[r];
+            for (int s = 0; s < 2; ++s)
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    *(float *)(to + (off + (32 * s + e) * step)) = dR[2 * s + (e >> 2)][e & 3];
         }
-        // dR and dV out, and the state's gradient before the chunk
+        // the state's gradient before the chunk
         Parts<kParts> W[2], X[2];
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
             float w[8], x[8];
+            unpack8<kF32>(load8<kF32>(gates.since + q8 + 32 * s, 8), x);
+            unpack8<kF32>(load8<kF32>(gates.beta + q8 + 32 * s, 8), w);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const int t = 32 * s + 8 * quarter + e;
-                const float by = gates.beta[t] * dR[s][e];
-                if (live) {
-                    p.gr[(at * 64 + t) * p.Dv + dv] = dR[s][e];
-                    if (t < rows)
-                        delta_store<T>(gv + t * o_stride, t < n ? by : 0.f);
-                }
-                w[e] = -gates.since[t] * by;
-                x[e] = p.scale * gates.since[t] * raw[s][e];
+                w[e] = -x[e] * w[e] * dR[2 * s + (e >> 2)][e & 3];
+                x[e] *= p.scale;
             }
             W[s] = split8<kParts>(w);
+            Raw8<T> raw;
+#pragma unroll
+            for (int i = 0; i < (T == kBF16 ? 1 : 2); ++i)
+                raw.w[i] = *(const v4u *)(gl + 32 * s + 4 * i);
+            unpack8<T>(raw, w);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                x[e] *= w[e];
             X[s] = split8<kParts>(x);
         }
         const float whole = gates.whole;
+        block_sync();  // Q's columns are there
 #pragma unroll
         for (int i = 0; i < 2 * KP; ++i) {
             v4f c;
 #pragma unroll
             for (int r = 0; r < 4; ++r)
                 c[r] = whole * S[i][r];
-            const int row = (32 * (i >> 1) + tile_row(i & 1, l)) * TS + 8 * quarter;
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
-                c = mm<kParts>(lds_operand(qt + row + 32 * s), X[s], c);
-                c = mm<kParts>(lds_operand(kt + row + 32 * s), W[s], c);
+                c = mm<kParts>(lds_operand(qtl + (state_at(i, 0) * TS + 32 * s)), X[s], c);
+                c = mm<kParts>(lds_operand(ktl + (state_at(i, 0) * TS + 32 * s)), W[s], c);
             }
             S[i] = c;
+            if (i & 1)
+                sched_fence();
         }
     }
     if (p.ginit && live)
-#pragma unroll
-        for (int i = 0; i < 2 * KP; ++i)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int f = 32 * (i >> 1) + 8 * quarter + 4 * (i & 1) + r;
-                if (f < p.Dk)
-                    p.ginit[head + (int64_t)f * p.Dv + dv] = S[i][r];
-            }
+        state_store<KP>(S, p.ginit + head + dv, p.Dk, p.Dv);
 }
 
 // -------------------------------------------------------- gradients: every chunk by itself
 
-constexpr int kGradCols = 32;            // columns (over Dv) held at a time
-constexpr int kGradStride = kGradCols + 8;
+constexpr int kGradStride = 72;   // 64 columns and room against bank conflicts
 
-// Rows by kGradCols columns of a matrix in memory into shared memory in N parts, row-major; zeros from
-// `rows_in` and from `cols` on.
-template <int T, int N>
-SSD_DEVICE void grad_stage(const typename DeltaElem<T>::type *src, int64_t stride, int rows, int rows_in, int cols,
-                           uint16_t *dst, int thread, int threads)
+// Rows by 32 TWO columns (TWO = 2: 64) of a float32 matrix in memory, on their way into shared memory in parts, row-major,
+// by 256 threads: units of eight neighbours. Zeros from `in` rows and `cols` columns on.
+template <int ROWS, int ACROSS>
+struct GradBlocks {
+    static constexpr int units = (ROWS * ACROSS + 255) / 256;
+    float v[units][8];
+};
+template <int ROWS, int ACROSS>
+SSD_DEVICE void grad_load(GradBlocks<ROWS, ACROSS> &d, const float *src, int stride, int in, int cols)
 {
-    for (int unit = thread; unit < rows * (kGradCols / 8); unit += threads) {
-        const int row = unit / (kGradCols / 8), col = 8 * (unit % (kGradCols / 8));
-        float v[8];
-        unpack8<T>(load8<T>(src + (row < rows_in ? row * stride : 0) + (cols > col ? col : 0),
-                            row < rows_in ? cols - col : 0), v);
-        const Parts<N> r = split8<N>(v);
+    const uint32_t step = opaque_uniform((uint32_t)stride * 4);
+    const int thread = (int)opaque((uint32_t)thread_id());
+    const char *x = (const char *)src;
 #pragma unroll
-        for (int i = 0; i < N; ++i)
-            *(v4u *)(dst + (i * rows + row) * kGradStride + col) = r.p[i];
+    for (int i = 0; i < d.units; ++i) {
+        const int unit = thread + 256 * i, r = unit / ACROSS, c = 8 * (unit % ACROSS);
+        const uint32_t off = (uint32_t)(r < in ? r : in - 1) * step;
+        if (cols % 4 == 0) {
+            const v4f lo = *(const v4f *)(x + (off + 4 * (uint32_t)(c < cols ? c : 0)));
+            const v4f hi = *(const v4f *)(x + (off + 4 * (uint32_t)(c + 4 < cols ? c + 4 : 0)));
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                d.v[i][e] = e < 4 ? lo[e & 3] : hi[e & 3];
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                d.v[i][e] = *(const float *)(x + (off + 4 * (uint32_t)(c + e < cols ? c + e : 0)));
+        }
     }
 }
-template <int N>
-SSD_DEVICE Parts<N> grad_operand(const uint16_t *src, int rows, int row)
+template <int ROWS, int ACROSS>
+SSD_DEVICE void grad_clear(GradBlocks<ROWS, ACROSS> &d, int in, int cols)
 {
-    Parts<N> r;
+    if (in >= ROWS && cols >= 8 * ACROSS)
+        return;
 #pragma unroll
-    for (int i = 0; i < N; ++i)
-        r.p[i] = *(const v4u *)(src + (i * rows + row) * kGradStride + 8 * ((thread_id() & 63) >> 4));
+    for (int i = 0; i < d.units; ++i) {
+        const int unit = thread_id() + 256 * i, r = unit / ACROSS, c = 8 * (unit % ACROSS);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            d.v[i][e] = r < in && c + e < cols ? d.v[i][e] : 0.f;
+    }
+}
+template <int ROWS, int ACROSS, int STRIDE>
+SSD_DEVICE void grad_store(const GradBlocks<ROWS, ACROSS> &d, uint16_t *dst)
+{
+#pragma unroll
+    for (int i = 0; i < d.units; ++i) {
+        const int unit = thread_id() + 256 * i, r = unit / ACROSS, c = 8 * (unit % ACROSS);
+        const Parts<kParts> parts = split8<kParts>(d.v[i]);
+#pragma unroll
+        for (int e = 0; e < kParts; ++e)
+            *(v4u *)(dst + (e * ROWS + r) * STRIDE + c) = parts.p[e];
+    }
+}
+template <int ROWS, int STRIDE>
+SSD_DEVICE Parts<kParts> grad_operand(const uint16_t *at)
+{
+    Parts<kParts> r;
+#pragma unroll
+    for (int i = 0; i < kParts; ++i)
+        r.p[i] = *(const v4u *)(at + i * ROWS * STRIDE);
     return r;
 }
 
-// Eight features of a token as an operand, from memory.
+// Eight features of a token as an operand, from memory: those from `at` on, zeros from D on and where the
+// token is none.
 template <int T>
-SSD_DEVICE Parts<DeltaElem<T>::parts> row_operand(const typename DeltaElem<T>::type *p, int at, int n)
+SSD_DEVICE void row_values(const typename DeltaElem<T>::type *p, int at, int D, bool in, float (&v)[8])
+{
+    if (D % 8 == 0) {
+        Raw8<T> raw;
+        __builtin_memcpy(&raw, p + (at < D ? at : 0), sizeof(raw));
+        unpack8<T>(raw, v);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            v[e] = delta_load<T>(p + (at + e < D ? at + e : 0));
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        v[e] = in && at + e < D ? v[e] : 0.f;
+}
+template <int T>
+SSD_DEVICE Parts<DeltaElem<T>::parts> row_operand(const typename DeltaElem<T>::type *p, int at, int D, bool in)
 {
     float v[8];
-    unpack8<T>(load8<T>(p + (n > at ? at : 0), n - at), v);
+    row_values<T>(p, at, D, in, v);
     return split8<DeltaElem<T>::parts>(v);
 }
-
-template <int T, int KP>
-struct GradLds {
-    typedef typename DeltaElem<T>::type E;
-    static constexpr int TS = 64 + DeltaElem<T>::pad, IN = DeltaElem<T>::parts;
-    union {
-        struct {  // while the columns are gone through
-            uint16_t u[kParts * 64 * kGradStride], r[kParts * 64 * kGradStride], o[IN * 64 * kGradStride];
-            uint16_t s[kParts * 32 * KP * kGradStride], gs[kParts * 32 * KP * kGradStride];
-        } a;
-        struct {  // after
-            E kt[32 * KP * TS], qt[32 * KP * TS];
-        } b;
-    };
-    DeltaGates gates;
-    float beta[2][64];   // shares of dbeta
-    float sums[64];      // dG
-    float dots[4];       // shares of <S, dS'>
-};
 
 // Sum over the four quarters of a wave, in every lane.
 SSD_DEVICE float quarter_sum(float v)
@@ -1180,300 +1088,408 @@ SSD_DEVICE float quarter_sum(float v)
     return v + lane_fetch(v, lane ^ 32);
 }
 
-// dQ, dK, dg and dbeta of a chunk, of one key head: its value heads one after the other. A wave takes 16
-// tokens as columns of everything: lane l token 16 w + l, and as rows the features or the other tokens.
-template <int T, int KP>
-SSD_KERNEL(256) void delta_grad_kernel(DeltaParams p)
+// Shared memory of the gradients' kernel. The columns are gone through 64 at a time: first U and dR stand in it (for the
+// products over the tokens), then the state and its gradient, 32 of their columns at a time with wide keys; at the
+// end K and Q by features. The triangle, from which U is made, lies where dR comes to stand, unless there are
+// more columns.
+template <int T, int KP, bool MANY>
+struct GradLds {
+    typedef typename DeltaElem<T>::type E;
+    static constexpr int TS = 64 + DeltaElem<T>::pad, RS = 32 * KP + DeltaElem<T>::pad;
+    static constexpr int SW = KP <= 2 ? 64 : 32, SS = SW + 8;  // columns of the state at a time
+    static constexpr int u_size = kParts * 64 * kGradStride, s_size = kParts * 32 * KP * SS;
+    static constexpr int tri_bytes = kParts * kDeltaFrags * 64 * 16 + 64 * kPairStride * 4;
+    static_assert(tri_bytes <= u_size * 2, "the triangle fits where dR comes to stand");
+    union {
+        struct {
+            uint16_t u[u_size], r[u_size];
+        } a;
+        struct {
+            uint16_t s[s_size], gs[s_size];
+        } b;
+        struct {
+            E kt[32 * KP * TS], qt[32 * KP * TS];
+        } c;
+    };
+    char own_tri[MANY ? tri_bytes : 16];
+    E k[64 * RS];
+    DeltaGates gates;
+    float beta[4][64];   // shares of dbeta
+    float sums[64];      // dG
+    float dots[4];       // shares of <S', dS'>
+};
+
+// dQ, dK, dV, dg and dbeta of a chunk and value head. A wave takes 16 tokens as columns of everything: lane l token
+// 16 w + l, and as rows the features or the other tokens. Where value heads share a key head, their dQ and dK
+// go to memory in float32 and are added afterwards.
+template <int T, int KP, bool MANY>
+SSD_KERNEL_WAVES(256, (KP <= 2 && !MANY ? 2 : 1)) void delta_grad_kernel(DeltaParams p)
 {
     typedef typename DeltaElem<T>::type E;
-    constexpr int TS = 64 + DeltaElem<T>::pad, IN = DeltaElem<T>::parts;
-    SSD_LDS GradLds<T, KP> lds;
+    typedef GradLds<T, KP, MANY> Lds;
+    constexpr int TS = Lds::TS, RS = Lds::RS, SS = Lds::SS, SW = Lds::SW, IN = DeltaElem<T>::parts;
+    SSD_LDS Lds lds;
     const int64_t id = block_id();
-    const int chunk = (int)(id % p.chunks), hk = (int)(id / p.chunks % p.Hk), b = (int)(id / p.chunks / p.Hk);
-    const int share = p.Hv / p.Hk, wave = wave_id();
-    const int l = thread_id() & 15, quarter = (thread_id() & 63) >> 4, own = 16 * wave + l, lane = thread_id() & 63;
+    const int chunk = (int)(id % p.chunks), hv = (int)(id / p.chunks % p.Hv), b = (int)(id / p.chunks / p.Hv);
+    const int share = p.Hv / p.Hk, hk = hv / share, wave = wave_id(), lane = thread_id() & 63;
+    const int l = thread_id() & 15, quarter = lane >> 4, q8 = 8 * quarter, own = 16 * wave + l;
     const int n = delta_chunk_tokens(delta_valid(p, b), chunk);
     const int rows = p.T - chunk * kDeltaChunk < 64 ? p.T - chunk * kDeltaChunk : 64;
     const int64_t token = (int64_t)b * p.T + chunk * kDeltaChunk;
-    const int64_t dense = (int64_t)p.Hk * p.Dk, o_stride = (int64_t)p.Hv * p.Dv;
-    E *gq = (E *)p.gq + (token + own) * dense + hk * p.Dk, *gk = (E *)p.gk + (token + own) * dense + hk * p.Dk;
+    const int o_stride = p.Hv * p.Dv;
+    E *gv = (E *)p.gv + token * o_stride + hv * p.Dv;
+    if (n == 0) {  // padding
+        for (int i = thread_id(); i < rows; i += 256)
+            p.gg[(token + i) * p.Hv + hv] = p.gbeta[(token + i) * p.Hv + hv] = 0.f;
+        for (int i = thread_id(); i < rows * p.Dv; i += 256)
+            delta_store<T>(gv + (int64_t)(i / p.Dv) * o_stride + i % p.Dv, 0.f);
+        for (int i = thread_id(); i < rows * p.Dk; i += 256) {
+            const int t = i / p.Dk, f = i % p.Dk;
+            if (share > 1) {
+                const int64_t to = ((token + t) * p.Hv + hv) * p.Dk + f;
+                p.wq[to] = p.wk[to] = 0.f;
+            } else {
+                const int64_t to = ((token + t) * p.Hk + hk) * p.Dk + f;
+                delta_store<T>((E *)p.gq + to, 0.f);
+                delta_store<T>((E *)p.gk + to, 0.f);
+            }
+        }
+        return;
+    }
     const E *q = (const E *)p.q + token * p.q_stride + hk * p.Dk, *k = (const E *)p.k + token * p.k_stride + hk * p.Dk;
-    v4f tq[2 * KP], tk[2 * KP];
+    const int64_t at = ((int64_t)b * p.Hv + hv) * p.chunks + chunk;
+    const float *S = p.chunk_states + (((int64_t)b * p.chunks + chunk) * p.Hv + hv) * p.Dk * p.Dv;
+    const float *gs = p.gs + at * p.Dk * p.Dv, *gr = p.gr + at * 64 * p.Dv;
+    const E *v = (const E *)p.v + token * p.v_stride + hv * p.Dv, *go = (const E *)p.go + token * o_stride + hv * p.Dv;
+    char *const tri_at = MANY ? lds.own_tri : (char *)lds.a.r;
+    v4u *const tri = (v4u *)tri_at;
+    float *const pairs = (float *)(tri_at + kParts * kDeltaFrags * 64 * 16);
+    v4f aq[2 * KP], reads[2 * KP], writes[2 * KP], m1t[4], m1[4], m2t[4], m2[4];
 #pragma unroll
     for (int i = 0; i < 2 * KP; ++i)
-        tq[i] = tk[i] = v4f{0.f, 0.f, 0.f, 0.f};
-    for (int hv = hk * share; hv < (hk + 1) * share; ++hv) {
-        if (n == 0) {  // padding
-            if (thread_id() < rows)
-                p.gg[(token + thread_id()) * p.Hv + hv] = p.gbeta[(token + thread_id()) * p.Hv + hv] = 0.f;
-            continue;
-        }
-        const int64_t at = ((int64_t)b * p.Hv + hv) * p.chunks + chunk;
-        const float *S = p.chunk_states + (((int64_t)b * p.chunks + chunk) * p.Hv + hv) * p.Dk * p.Dv;
-        const float *gs = p.gs + at * p.Dk * p.Dv, *gr = p.gr + at * 64 * p.Dv;
-        const E *v = (const E *)p.v + token * p.v_stride + hv * p.Dv, *go = (const E *)p.go + token * o_stride + hv * p.Dv;
-        v4f aq[2 * KP], reads[2 * KP], writes[2 * KP], m1t[4], m1[4], m2t[4], m2[4];
+        aq[i] = reads[i] = writes[i] = v4f{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int i = 0; i < 2 * KP; ++i)
-            aq[i] = reads[i] = writes[i] = v4f{0.f, 0.f, 0.f, 0.f};
+    for (int i = 0; i < 4; ++i)
+        m1t[i] = m1[i] = m2t[i] = m2[i] = v4f{0.f, 0.f, 0.f, 0.f};
+    float dot = 0.f;
+    delta_stage<T, KP, true, false>(k, p.k_stride, p.Dk, n, lds.k, nullptr);
+    if (wave == 3)
+        delta_gates(lds.gates, p.g, p.beta, token * p.Hv + hv, p.Hv, n);
+    delta_clear_pairs(pairs, 256);
+    block_sync();
+    const DeltaGates &gates = lds.gates;
+    delta_tiles<T, KP, 1, 4, false>(lds.k, nullptr, gates, 0.f, pairs, tri, nullptr);
+    block_sync();
+    if (wave < 2)
+        delta_invert<false>(pairs + 32 * wave * kPairStride, wave, tri);
+    const E *kl = lds.k + tile_row(0, l) * RS + q8;
+    const bool valid = own < n;
+    for (int col = 0; col < p.Dv; col += 64) {
+        const int cols = p.Dv - col;
+        // U of 16 columns, as in the walk
+        {
+            const int dv = col + 16 * wave + l;
+            const bool live = dv < p.Dv;
+            v4f s[2 * KP];
+            state_load<KP>(s, S + (live ? dv : col), p.Dk, p.Dv);
+            float R[2][8], by[2][8];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            m1t[i] = m1[i] = m2t[i] = m2[i] = v4f{0.f, 0.f, 0.f, 0.f};
-        float by_beta[2][8] = {}, dot = 0.f;
-        block_sync();  // the last head's operands have been read
-        if (wave == 0)
-            delta_gates(lds.gates, p.g, p.beta, token * p.Hv + hv, p.Hv, n);
-        block_sync();
-        for (int col = 0; col < p.Dv; col += kGradCols) {
-            if (wave < 2) {  // U of 16 columns, as in the walk
-                const int dv = col + 16 * wave + l;
-                const bool live = dv < p.Dv;
-                Parts<kParts> Sp[KP];
-#pragma unroll
-                for (int s = 0; s < KP; ++s) {
-                    float w[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const int f = 32 * s + 8 * quarter + e;
-                        w[e] = S[(int64_t)(f < p.Dk ? f : 0) * p.Dv + (live ? dv : 0)];
-                    }
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        w[e] = live && 32 * s + 8 * quarter + e < p.Dk ? w[e] : 0.f;
-                    Sp[s] = split8<kParts>(w);
-                }
-                float R[2][8];
-#pragma unroll
-                for (int s = 0; s < 2; ++s)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        v4f ks = {0.f, 0.f, 0.f, 0.f};
-                        const int row = 32 * s + tile_row(h, l);
-#pragma unroll
-                        for (int f = 0; f < KP; ++f)
-                            ks = mm<kParts>(row_operand<T>(k + (row < n ? row : 0) * p.k_stride, 32 * f + 8 * quarter,
-                                                           row < n ? p.Dk : 0), Sp[f], ks);
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) {
-                            const int t = 32 * s + 8 * quarter + 4 * h + r;
-                            const float x = delta_load<T>(v + (t < n ? t : n - 1) * p.v_stride + (live ? dv : 0));
-                            const float read = (live && t < n ? x : 0.f) - lds.gates.since[t] * ks[r];
-                            const float by = gr[(int64_t)t * p.Dv + (live ? dv : 0)];
-                            R[s][4 * h + r] = lds.gates.beta[t] * read;
-                            by_beta[s][4 * h + r] += live ? read * by : 0.f;
-                        }
-                    }
-                const float *tri = p.tri + at * kDeltaFragFloats + 8 * lane;
-                auto frag = [&](int f) {
-                    return split_tiles<kParts>(*(const v4f *)(tri + 512 * f), *(const v4f *)(tri + 512 * f + 4));
-                };
-                const Parts<kParts> R0 = split8<kParts>(R[0]);
-                v4f U[4];
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    U[h] = mm<kParts>(frag(frag_of(0, h, 0)), R0, v4f{0.f, 0.f, 0.f, 0.f});
-                const Parts<kParts> U0 = split_tiles<kParts>(U[0], U[1]);
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const v4f c = mm<kParts>(frag(frag_of(1, h, 0)), U0, v4f{0.f, 0.f, 0.f, 0.f});
-#pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        R[1][4 * h + r] -= c[r];
-                }
-                const Parts<kParts> R1 = split8<kParts>(R[1]);
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    U[2 + h] = mm<kParts>(frag(frag_of(1, h, 1)), R1, v4f{0.f, 0.f, 0.f, 0.f});
-                const Parts<kParts> up[2] = {U0, split_tiles<kParts>(U[2], U[3])};
-#pragma unroll
-                for (int s = 0; s < 2; ++s)
-#pragma unroll
-                    for (int i = 0; i < kParts; ++i)
-#pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            lds.a.u[(i * 64 + 32 * s + 8 * quarter + e) * kGradStride + 16 * wave + l] =
-                                (uint16_t)(up[s].p[i][e >> 1] >> (16 * (e & 1)));
-            } else {
-                const int thread = thread_id() - 128, cols = p.Dv - col;
-                grad_stage<kF32, kParts>(gr + col, p.Dv, 64, 64, cols, lds.a.r, thread, 128);
-                grad_stage<T, IN>(go + col, o_stride, 64, n, cols, lds.a.o, thread, 128);
-                grad_stage<kF32, kParts>(S + col, p.Dv, 32 * KP, p.Dk, cols, lds.a.s, thread, 128);
-                grad_stage<kF32, kParts>(gs + col, p.Dv, 32 * KP, p.Dk, cols, lds.a.gs, thread, 128);
-            }
-            block_sync();
-            const Parts<IN> oo = grad_operand<IN>(lds.a.o, 64, own);
-            const Parts<kParts> ro = grad_operand<kParts>(lds.a.r, 64, own), uo = grad_operand<kParts>(lds.a.u, 64, own);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int row = 32 * (i >> 1) + tile_row(i & 1, l);
-                if ((i >> 1) <= (wave >> 1)) {  // rows j up to the own token i
-                    const Parts<kParts> u = grad_operand<kParts>(lds.a.u, 64, row);
-                    m1t[i] = mm<kParts>(u, oo, m1t[i]);
-                    m2t[i] = mm<kParts>(u, ro, m2t[i]);
-                }
-                if ((i >> 1) >= (wave >> 1)) {  // rows i from the own token j on
-                    m1[i] = mm<kParts>(grad_operand<IN>(lds.a.o, 64, row), uo, m1[i]);
-                    m2[i] = mm<kParts>(grad_operand<kParts>(lds.a.r, 64, row), uo, m2[i]);
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < 2 * KP; ++i) {
-                const int row = 32 * (i >> 1) + tile_row(i & 1, l);
-                const Parts<kParts> s = grad_operand<kParts>(lds.a.s, 32 * KP, row);
-                aq[i] = mm<kParts>(s, oo, aq[i]);
-                reads[i] = mm<kParts>(s, ro, reads[i]);
-                writes[i] = mm<kParts>(grad_operand<kParts>(lds.a.gs, 32 * KP, row), uo, writes[i]);
-            }
-            block_sync();
-        }
-        // <S, dS'>
-        for (int i = thread_id(); i < p.Dk * p.Dv; i += 256)
-            dot = __builtin_fmaf(S[i], gs[i], dot);
-        dot = wave_sum(dot);
-        if (lane == 0)
-            lds.dots[wave] = dot;
-        if (wave < 2)
-#pragma unroll
-            for (int s = 0; s < 2; ++s)
+            for (int h = 0; h < 2; ++h)
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    const float sum = row16_sum(by_beta[s][e]);
-                    if (l == 0)
-                        lds.beta[wave][32 * s + 8 * quarter + e] = sum;
+                    const int t = q8 < n - (32 * h + e) ? q8 + (32 * h + e) : n - 1;
+                    R[h][e] = delta_load<T>(v + (uint32_t)t * (uint32_t)p.v_stride + (live ? dv : col));
+                    by[h][e] = gr[(uint32_t)(q8 + (32 * h + e)) * (uint32_t)p.Dv + (live ? dv : col)];
                 }
-        delta_stage<T, KP, false, true>(k, p.k_stride, p.Dk, n, nullptr, lds.b.kt);
-        delta_stage<T, KP, false, true>(q, p.q_stride, p.Dk, n, nullptr, lds.b.qt);
-        block_sync();
-        const DeltaGates &gates = lds.gates;
-        const double sum_own = gates.sum[own];
-        const float since = gates.since[own], beta = gates.beta[own], hold = gates.left[own];
+            Parts<kParts> Sp[KP];
 #pragma unroll
-        for (int i = 0; i < 2 * KP; ++i)
+            for (int i = 0; i < KP; ++i)
+                Sp[i] = split_tiles<kParts>(s[2 * i], s[2 * i + 1]);
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                aq[i][r] *= p.scale * since;
-                reads[i][r] *= -beta * since;
-                writes[i][r] *= hold;
+            for (int h = 0; h < 4; ++h) {
+                v4f ks = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int f = 0; f < KP; ++f)
+                    ks = mm<kParts>(lds_operand(kl + ((32 * (h >> 1) + 4 * (h & 1)) * RS + 32 * f)), Sp[f], ks);
+                const v4f since = *(const v4f *)(gates.since + q8 + (32 * (h >> 1) + 4 * (h & 1)));
+                const v4f beta = *(const v4f *)(gates.beta + q8 + (32 * (h >> 1) + 4 * (h & 1)));
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int e = 4 * (h & 1) + r;
+                    const float x = live && q8 < n - (32 * (h >> 1) + e) ? R[h >> 1][e] : 0.f;
+                    const float read = x - since[r] * ks[r];
+                    R[h >> 1][e] = live ? beta[r] * read : 0.f;
+                    by[h >> 1][e] = live ? by[h >> 1][e] * read : 0.f;
+                }
             }
-        // the share of <S', dS'> that U brought: sum over tokens of k . (e^(G_C - G) U dS'^T)
-        float held = 0.f, dots = 0.f;
-        const bool valid = own < n;
 #pragma unroll
-        for (int s = 0; s < KP; ++s) {
-            float w[8];
-            const int f = 32 * s + 8 * quarter;
-            unpack8<T>(load8<T>(k + (valid ? own * p.k_stride : 0) + (p.Dk > f ? f : 0), valid ? p.Dk - f : 0), w);
+            for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                held = __builtin_fmaf(w[e], writes[2 * s + (e >> 2)][e & 3], held);
-        }
-        held = wave_sum(held);
-        Parts<IN> ko[KP];
-#pragma unroll
-        for (int s = 0; s < KP; ++s)
-            ko[s] = row_operand<T>(k + (valid ? own * p.k_stride : 0), 32 * s + 8 * quarter, valid ? p.Dk : 0);
-        float by_own = 0.f;
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            if (s <= (wave >> 1)) {  // token rows j at or before the own token i
-                float d[8], e[8];
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    v4f kk = {0.f, 0.f, 0.f, 0.f};
-                    const int row = 32 * s + tile_row(h, l);
-#pragma unroll
-                    for (int f = 0; f < KP; ++f)
-                        kk = mm<kParts>(row_operand<T>(k + (row < n ? row : 0) * p.k_stride, 32 * f + 8 * quarter,
-                                                       row < n ? p.Dk : 0), ko[f], kk);
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const int j = 32 * s + 8 * quarter + 4 * h + r;
-                        const float decay = j <= own ? delta_exp(sum_own - gates.sum[j]) : 0.f;
-                        const float x = j < own ? -m2t[2 * s + h][r] * decay : 0.f;
-                        d[4 * h + r] = j <= own ? p.scale * decay * m1t[2 * s + h][r] : 0.f;
-                        e[4 * h + r] = beta * x;
-                        by_own = __builtin_fmaf(x, kk[r], by_own);
+                for (int e = 0; e < 8; ++e) {
+                    const float sum = row16_sum(by[h][e]);
+                    if (l == 0) {
+                        float *to = &lds.beta[wave][q8 + (32 * h + e)];
+                        *to = (MANY && col > 0 ? *to : 0.f) + sum;
                     }
                 }
-                const Parts<kParts> dp = split8<kParts>(d), ep = split8<kParts>(e);
+            block_sync();  // the triangle is there; with more columns the last ones have been read
+            const Parts<kParts> R0 = split8<kParts>(R[0]);
+            v4f U[2];
+            uint16_t *to = lds.a.u + tile_row(0, l) * kGradStride + 16 * wave + 4 * quarter;
+            auto put = [&](int s, int h, v4f x) {  // four columns of token 32 s + tile_row(h, l)
+                const float w[8] = {x[0], x[1], x[2], x[3], 0.f, 0.f, 0.f, 0.f};
+                const Parts<kParts> parts = split8<kParts>(w);
 #pragma unroll
-                for (int i = 0; i < 2 * KP; ++i) {
-                    const auto a = lds_operand(lds.b.kt + (32 * (i >> 1) + tile_row(i & 1, l)) * TS + 32 * s + 8 * quarter);
-                    aq[i] = mm<kParts>(a, dp, aq[i]);
-                    reads[i] = mm<kParts>(a, ep, reads[i]);
-                }
+                for (int i = 0; i < kParts; ++i)
+                    *(v2u *)(to + ((i * 64 + 32 * s + 4 * h) * kGradStride)) = v2u{parts.p[i][0], parts.p[i][1]};
+            };
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const Parts<kParts> f = frag_operand<kParts>(tri, frag_of(0, h, 0));
+                U[h] = mm<kParts>(f, R0, v4f{0.f, 0.f, 0.f, 0.f});
+                put(0, h, mm<kParts>(R0, f, v4f{0.f, 0.f, 0.f, 0.f}));
             }
-            if (s >= (wave >> 1)) {  // token rows i at or after the own token j
-                float d[8], e[8];
+            const Parts<kParts> U0 = split_tiles<kParts>(U[0], U[1]);
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
+            for (int h = 0; h < 2; ++h) {
+                const v4f c = mm<kParts>(frag_operand<kParts>(tri, frag_of(1, h, 0)), U0, v4f{0.f, 0.f, 0.f, 0.f});
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const int i = 32 * s + 8 * quarter + 4 * h + r;
-                        const float decay = i >= own ? delta_exp(gates.sum[i] - sum_own) : 0.f;
-                        d[4 * h + r] = i >= own ? p.scale * decay * m1[2 * s + h][r] : 0.f;
-                        e[4 * h + r] = i > own ? -gates.beta[i] * decay * m2[2 * s + h][r] : 0.f;
-                    }
-                const Parts<kParts> dp = split8<kParts>(d), ep = split8<kParts>(e);
-#pragma unroll
-                for (int i = 0; i < 2 * KP; ++i) {
-                    const int row = (32 * (i >> 1) + tile_row(i & 1, l)) * TS + 32 * s + 8 * quarter;
-                    writes[i] = mm<kParts>(lds_operand(lds.b.qt + row), dp, writes[i]);
-                    writes[i] = mm<kParts>(lds_operand(lds.b.kt + row), ep, writes[i]);
-                }
+                for (int r = 0; r < 4; ++r)
+                    R[1][4 * h + r] -= c[r];
             }
+            const Parts<kParts> R1 = split8<kParts>(R[1]);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                put(1, h, mm<kParts>(R1, frag_operand<kParts>(tri, frag_of(1, h, 1)), v4f{0.f, 0.f, 0.f, 0.f}));
         }
-        // q . dq + k . (reads - writes), and the sums over the value heads
+        // dR, and dV = beta dR
+        {
+            GradBlocks<64, 8> d;
+            grad_load<64, 8>(d, gr + col, p.Dv, 64, cols);
+            if (!MANY)
+                block_sync();  // the triangle has been read
+            grad_clear<64, 8>(d, 64, cols);
+            grad_store<64, 8, kGradStride>(d, lds.a.r);
 #pragma unroll
-        for (int s = 0; s < KP; ++s) {
-            float x[8], y[8];
-            const int f = 32 * s + 8 * quarter;
-            unpack8<T>(load8<T>(q + (valid ? own * p.q_stride : 0) + (p.Dk > f ? f : 0), valid ? p.Dk - f : 0), x);
-            unpack8<T>(load8<T>(k + (valid ? own * p.k_stride : 0) + (p.Dk > f ? f : 0), valid ? p.Dk - f : 0), y);
+            for (int i = 0; i < 2; ++i) {
+                const int unit = thread_id() + 256 * i, r = unit >> 3, c = 8 * (unit & 7);
+                const float beta = gates.beta[r];  // zero in the padding
+                float x[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int i = 2 * s + (e >> 2), r = e & 3;
-                dots = __builtin_fmaf(x[e], aq[i][r], dots);
-                dots = __builtin_fmaf(y[e], reads[i][r] - writes[i][r], dots);
-                tq[i][r] += aq[i][r];
-                tk[i][r] += reads[i][r] + writes[i][r];
+                for (int e = 0; e < 8; ++e)
+                    x[e] = r < n ? beta * d.v[i][e] : 0.f;
+                if (r < rows && c < cols)
+                    store8<T>(gv + (uint32_t)r * (uint32_t)o_stride + col + c, cols - c, x);
             }
-        }
-        dots = quarter_sum(dots);
-        by_own = quarter_sum(by_own);
-        if (quarter == 0) {
-            lds.sums[own] = dots;
-            lds.beta[0][own] += lds.beta[1][own] + by_own;
         }
         block_sync();
-        if (lane == 0)  // the dots of the state's gradient are read below; each wave adds its tokens' share
-            lds.dots[wave] = gates.whole * lds.dots[wave] + held;
-        block_sync();
-        if (wave == 0) {
-            // sums from the last token back: of everything less those before
-            const double all = (double)lds.sums[lane] + (lane == n - 1 ? (double)lds.dots[0] + lds.dots[1] + lds.dots[2] + lds.dots[3] : 0.);
-            const double before = wave_scan_d(all);
-            const double total = lane_read_d(before, 63);
-            if (lane < rows) {
-                const int64_t to = (token + lane) * p.Hv + hv;
-                p.gg[to] = lane < n ? (float)(total - before + all) : 0.f;
-                p.gbeta[to] = lane < n ? lds.beta[0][lane] : 0.f;
+        // over the tokens
+        Parts<IN> oo[2];
+        Parts<kParts> ro[2], uo[2];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            oo[t] = row_operand<T>(go + (uint32_t)(valid ? own : 0) * (uint32_t)o_stride + col, 32 * t + q8, cols, valid);
+            ro[t] = grad_operand<64, kGradStride>(lds.a.r + own * kGradStride + q8 + 32 * t);
+            uo[t] = grad_operand<64, kGradStride>(lds.a.u + own * kGradStride + q8 + 32 * t);
+        }
+        const uint16_t *ul = lds.a.u + tile_row(0, l) * kGradStride + q8, *rl = lds.a.r + tile_row(0, l) * kGradStride + q8;
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int at0 = (32 * (i >> 1) + 4 * (i & 1)) * kGradStride + 32 * t;
+                if ((i >> 1) <= (wave >> 1)) {  // rows j up to the own token i
+                    const Parts<kParts> u = grad_operand<64, kGradStride>(ul + at0);
+                    m1t[i] = mm<kParts>(u, oo[t], m1t[i]);
+                    m2t[i] = mm<kParts>(u, ro[t], m2t[i]);
+                }
+                if ((i >> 1) >= (wave >> 1)) {  // rows i from the own token j on
+                    const int row = 32 * (i >> 1) + tile_row(i & 1, l);
+                    m1[i] = mm<kParts>(row_operand<T>(go + (uint32_t)(row < n ? row : 0) * (uint32_t)o_stride + col, 32 * t + q8,
+                                                      cols, row < n), uo[t], m1[i]);
+                    m2[i] = mm<kParts>(grad_operand<64, kGradStride>(rl + at0), uo[t], m2[i]);
+                }
+            }
+        // over the state's columns
+#pragma unroll
+        for (int c0 = 0; c0 < 64; c0 += SW) {
+            if (c0 >= cols)
+                break;
+            GradBlocks<32 * KP, SW / 8> ds, dg;
+            grad_load<32 * KP, SW / 8>(ds, S + col + c0, p.Dv, p.Dk, cols - c0);
+            grad_load<32 * KP, SW / 8>(dg, gs + col + c0, p.Dv, p.Dk, cols - c0);
+            block_sync();  // U and dR, or the columns before, have been read
+            grad_clear<32 * KP, SW / 8>(ds, p.Dk, cols - c0);
+            grad_clear<32 * KP, SW / 8>(dg, p.Dk, cols - c0);
+#pragma unroll
+            for (int i = 0; i < ds.units; ++i)
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    dot = __builtin_fmaf(ds.v[i][e], dg.v[i][e], dot);
+            grad_store<32 * KP, SW / 8, SS>(ds, lds.b.s);
+            grad_store<32 * KP, SW / 8, SS>(dg, lds.b.gs);
+            block_sync();
+            const uint16_t *sl = lds.b.s + tile_row(0, l) * SS + q8, *gsl = lds.b.gs + tile_row(0, l) * SS + q8;
+#pragma unroll
+            for (int t = 0; t < SW / 32; ++t)
+#pragma unroll
+                for (int i = 0; i < 2 * KP; ++i) {
+                    const int t0 = c0 / 32 + t, at0 = state_at(i, 0) * SS + 32 * t;
+                    const Parts<kParts> s = grad_operand<32 * KP, SS>(sl + at0);
+                    aq[i] = mm<kParts>(s, oo[t0], aq[i]);
+                    reads[i] = mm<kParts>(s, ro[t0], reads[i]);
+                    writes[i] = mm<kParts>(grad_operand<32 * KP, SS>(gsl + at0), uo[t0], writes[i]);
+                }
+        }
+        if (MANY)
+            block_sync();  // before the next columns' U
+    }
+    dot = wave_sum(dot);
+    Blocks<T, 32 * KP, 256> kb, qb;
+    blocks_load<T, 32 * KP, 256>(kb, k, (int)p.k_stride, p.Dk, n);
+    blocks_load<T, 32 * KP, 256>(qb, q, (int)p.q_stride, p.Dk, n);
+    block_sync();
+    blocks_store<T, 32 * KP, 256, false, true>(kb, p.Dk, n, (E *)nullptr, lds.c.kt);
+    blocks_store<T, 32 * KP, 256, false, true>(qb, p.Dk, n, (E *)nullptr, lds.c.qt);
+    const double sum_own = gates.sum[own];
+    const float since = gates.since[own], beta = gates.beta[own], hold = gates.left[own];
+#pragma unroll
+    for (int i = 0; i < 2 * KP; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            aq[i][r] *= p.scale * since;
+            reads[i][r] *= -beta * since;
+            writes[i][r] *= hold;
+        }
+    // the share of <S', dS'> that U brought: sum over tokens of k . (e^(G_C - G) U dS'^T)
+    float held = 0.f, dots = 0.f;
+    Parts<IN> ko[KP];
+#pragma unroll
+    for (int s = 0; s < KP; ++s) {
+        float w[8];
+        row_values<T>(k + (uint32_t)(valid ? own : 0) * (uint32_t)p.k_stride, 32 * s + q8, p.Dk, valid, w);
+        ko[s] = split8<IN>(w);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            held = __builtin_fmaf(w[e], writes[2 * s + (e >> 2)][e & 3], held);
+    }
+    held = wave_sum(held);
+    if (lane == 0)
+        lds.dots[wave] = gates.whole * dot + held;
+    block_sync();
+    const E *ktl = lds.c.kt + tile_row(0, l) * TS + q8, *qtl = lds.c.qt + tile_row(0, l) * TS + q8;
+    float by_own = 0.f;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+        if (s <= (wave >> 1)) {  // token rows j at or before the own token i
+            float d[8], e[8];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                v4f kk = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int f = 0; f < KP; ++f)
+                    kk = mm<kParts>(lds_operand(kl + ((32 * s + 4 * h) * RS + 32 * f)), ko[f], kk);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int j = 32 * s + 4 * h + r, behind = own - q8 - j;  // i - j
+                    const float decay = behind >= 0 ? delta_exp(sum_own - gates.sum[q8 + j]) : 0.f;
+                    const float x = behind > 0 ? -m2t[2 * s + h][r] * decay : 0.f;
+                    d[4 * h + r] = behind >= 0 ? p.scale * decay * m1t[2 * s + h][r] : 0.f;
+                    e[4 * h + r] = beta * x;
+                    by_own = __builtin_fmaf(x, kk[r], by_own);
+                }
+            }
+            const Parts<kParts> dp = split8<kParts>(d), ep = split8<kParts>(e);
+#pragma unroll
+            for (int i = 0; i < 2 * KP; ++i) {
+                const auto a = lds_operand(ktl + (state_at(i, 0) * TS + 32 * s));
+                aq[i] = mm<kParts>(a, dp, aq[i]);
+                reads[i] = mm<kParts>(a, ep, reads[i]);
+            }
+        }
+        if (s >= (wave >> 1)) {  // token rows i at or after the own token j
+            float d[8], e[8];
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int i = 32 * s + 4 * h + r, ahead = q8 + i - own;  // i - j
+                    const float decay = ahead >= 0 ? delta_exp(gates.sum[q8 + i] - sum_own) : 0.f;
+                    d[4 * h + r] = ahead >= 0 ? p.scale * decay * m1[2 * s + h][r] : 0.f;
+                    e[4 * h + r] = ahead > 0 ? -gates.beta[q8 + i] * decay * m2[2 * s + h][r] : 0.f;
+                }
+            const Parts<kParts> dp = split8<kParts>(d), ep = split8<kParts>(e);
+#pragma unroll
+            for (int i = 0; i < 2 * KP; ++i) {
+                writes[i] = mm<kParts>(lds_operand(qtl + (state_at(i, 0) * TS + 32 * s)), dp, writes[i]);
+                writes[i] = mm<kParts>(lds_operand(ktl + (state_at(i, 0) * TS + 32 * s)), ep, writes[i]);
             }
         }
     }
-    if (own < rows)
+    // q . dq + k . (reads - writes), and the results
 #pragma unroll
-        for (int s = 0; s < KP; ++s) {
-            const int f = 32 * s + 8 * quarter;
-            const float x[8] = {tq[2 * s][0], tq[2 * s][1], tq[2 * s][2], tq[2 * s][3],
-                                tq[2 * s + 1][0], tq[2 * s + 1][1], tq[2 * s + 1][2], tq[2 * s + 1][3]};
-            const float y[8] = {tk[2 * s][0], tk[2 * s][1], tk[2 * s][2], tk[2 * s][3],
-                                tk[2 * s + 1][0], tk[2 * s + 1][1], tk[2 * s + 1][2], tk[2 * s + 1][3]};
-            if (f < p.Dk) {
-                store8<T>(gq + f, p.Dk - f, x);
-                store8<T>(gk + f, p.Dk - f, y);
+    for (int s = 0; s < KP; ++s) {
+        float x[8], y[8];
+        const int f = 32 * s + q8;
+        row_values<T>(q + (uint32_t)(valid ? own : 0) * (uint32_t)p.q_stride, f, p.Dk, valid, x);
+        row_values<T>(k + (uint32_t)(valid ? own : 0) * (uint32_t)p.k_stride, f, p.Dk, valid, y);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int i = 2 * s + (e >> 2), r = e & 3;
+            dots = __builtin_fmaf(x[e], aq[i][r], dots);
+            dots = __builtin_fmaf(y[e], reads[i][r] - writes[i][r], dots);
+            x[e] = aq[i][r];
+            y[e] = reads[i][r] + writes[i][r];
+        }
+        if (own < rows && f < p.Dk) {
+            if (share > 1) {
+                const int64_t to = ((token + own) * p.Hv + hv) * p.Dk + f;
+                store8<kF32>(p.wq + to, p.Dk - f, x);
+                store8<kF32>(p.wk + to, p.Dk - f, y);
+            } else {
+                const int64_t to = ((token + own) * p.Hk + hk) * p.Dk + f;
+                store8<T>((E *)p.gq + to, p.Dk - f, x);
+                store8<T>((E *)p.gk + to, p.Dk - f, y);
             }
         }
+    }
+    dots = quarter_sum(dots);
+    by_own = quarter_sum(by_own);
+    if (quarter == 0) {
+        lds.sums[own] = dots;
+        lds.beta[0][own] = lds.beta[0][own] + lds.beta[1][own] + lds.beta[2][own] + lds.beta[3][own] + by_own;
+    }
+    block_sync();
+    if (wave == 0) {
+        // sums from the last token back: of everything less those before
+        const double all = (double)lds.sums[lane] + (lane == n - 1 ? (double)lds.dots[0] + lds.dots[1] + lds.dots[2] + lds.dots[3] : 0.);
+        const double before = wave_scan_d(all);
+        const double total = lane_read_d(before, 63);
+        if (lane < rows) {
+            const int64_t to = (token + lane) * p.Hv + hv;
+            p.gg[to] = lane < n ? (float)(total - before + all) : 0.f;
+            p.gbeta[to] = lane < n ? lds.beta[0][lane] : 0.f;
+        }
+    }
+}
+
+// dQ and dK of key heads from those of the value heads that share them, in their order.
+template <int T>
+SSD_KERNEL(256) void delta_share_kernel(DeltaParams p)
+{
+    typedef typename DeltaElem<T>::type E;
+    const int share = p.Hv / p.Hk;
+    const int64_t total = (int64_t)p.B * p.T * p.Hk * p.Dk;
+    for (int64_t i = block_id() * 256 + thread_id(); i < total; i += grid_blocks() * 256) {
+        const int64_t from = i / p.Dk * share * p.Dk + i % p.Dk;
+        float x = 0.f, y = 0.f;
+        for (int s = 0; s < share; ++s) {
+            x += p.wq[from + (int64_t)s * p.Dk];
+            y += p.wk[from + (int64_t)s * p.Dk];
+        }
+        delta_store<T>((E *)p.gq + i, x);
+        delta_store<T>((E *)p.gk + i, y);
+    }
 }
 
 // out = from, or zeros.
