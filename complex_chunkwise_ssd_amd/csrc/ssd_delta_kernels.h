@@ -1184,7 +1184,7 @@ SSD_KERNEL_WAVES(256, (KP <= 2 && !MANY ? 2 : 1)) void delta_grad_kernel(DeltaPa
         delta_invert<false>(pairs + 32 * wave * kPairStride, wave, tri);
     const E *kl = lds.k + tile_row(0, l) * RS + q8;
     const bool valid = own < n;
-    for (int col = 0; col < p.Dv; col += 64) {
+    for (int col = 0; MANY ? col < p.Dv : col == 0; col += 64) {
         const int cols = p.Dv - col;
         // U of 16 columns, as in the walk
         {
