@@ -1,4 +1,4 @@
-// ssd_delta_device.h -- two further gfx950 primitives that the delta rule's kernels are written against.
+// ssd_delta_device.h -- further gfx950 primitives that the delta rule's kernels are written against.
 #pragma once
 
 #include <ssd_ops_device.h>
@@ -16,3 +16,5 @@ SSD_DEVICE uint32_t opaque_uniform(uint32_t value)
     asm volatile("" : "+s"(value));
     return value;
 }
+// Neither value is used before both are there.
+SSD_DEVICE void together(float &a, float &b) { asm volatile("" : "+v"(a), "+v"(b)); }

@@ -89,6 +89,16 @@ SSD_DEVICE Parts<3> lds_operand(const float *p)
     return split_tiles<3>(a, b);
 }
 
+template <int T>
+SSD_DEVICE void lds_values(const typename DeltaElem<T>::type *p, float (&v)[8])
+{
+    Raw8<T> raw;
+#pragma unroll
+    for (int i = 0; i < (T == kBF16 ? 1 : 2); ++i)
+        raw.w[i] = *(const v4u *)((const char *)p + 16 * i);
+    unpack8<T>(raw, v);
+}
+
 // Which six operand tiles a lower (or upper) triangle of spans has.
 SSD_DEVICE int frag_of(int s, int h, int t) { return s == 0 ? h : 2 + 2 * h + t; }          // t <= s
 SSD_DEVICE int frag_of_upper(int s, int h, int t) { return s == 1 ? 4 + h : 2 * h + t; }    // t >= s
@@ -372,13 +382,20 @@ SSD_DEVICE void delta_tiles(const typename DeltaElem<T>::type *k, const typename
 #pragma unroll
             for (int e = 0; e < 16; ++e)
                 x[e] = e == l ? 1.f : 0.f;
-            const v4f minus = -a;
+            v4f minus = -a;
 #pragma unroll
-            for (int e = 0; e < 15; ++e)
+            for (int e = 0; e < 15; ++e) {
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {  // no more scalars at a time than there are
+                    float m = minus[r];
+                    together(m, x[e]);
+                    minus[r] = m;
+                }
 #pragma unroll
                 for (int u = e + 1; u < 16; ++u)
                     x[u] = __builtin_fmaf(TURNED ? lane_read(minus[u & 3], 16 * (u >> 2) + e)
                                                  : lane_read(minus[e & 3], 16 * (e >> 2) + u), x[e], x[u]);
+            }
             if (quarter == 0)
 #pragma unroll
                 for (int e = 0; e < 16; e += 4)
@@ -493,7 +510,7 @@ SSD_DEVICE void state_load(v4f (&S)[2 * KP], const float *from, int Dk, int Dv)
 // waves solve the blocks of 32, the others go on with what the state gives. The next chunk's rows are in
 // flight meanwhile.
 template <int T, int KP, int WAVES>
-SSD_KERNEL_WAVES(64 * WAVES, 2) void delta_scan_kernel(DeltaParams p)
+SSD_KERNEL_WAVES(64 * WAVES, (WAVES == 8 || (T == kBF16 && KP <= 2) ? 2 : 1)) void delta_scan_kernel(DeltaParams p)
 {
     typedef typename DeltaElem<T>::type E;
     constexpr int NT = 64 * WAVES, COLS = 16 * WAVES;
@@ -586,9 +603,7 @@ SSD_KERNEL_WAVES(64 * WAVES, 2) void delta_scan_kernel(DeltaParams p)
         for (int s = 0; s < 2; ++s) {
             float v[8];
             if (STAGE_V) {
-                Raw8<T> raw;
-                raw.w[0] = *(const v4u *)(vl + 32 * s);
-                unpack8<T>(raw, v);
+                lds_values<T>(vl + 32 * s, v);
             } else {
                 const E *at = vrow + (int64_t)chunk * kDeltaChunk * p.v_stride + (live ? 16 * wave + l : 0);
 #pragma unroll
@@ -800,7 +815,7 @@ SSD_KERNEL(256) void delta_few_kernel(DeltaParams p)
 // As delta_scan_kernel, from the last chunk to the first, with the gradient of the state: dS' of every chunk and
 // dR go to memory. K's rows make room for Q's columns once they have been used, Q's rows for those of dO.
 template <int T, int KP, int WAVES>
-SSD_KERNEL_WAVES(64 * WAVES, 2) void delta_scan_bwd_kernel(DeltaParams p)
+SSD_KERNEL_WAVES(64 * WAVES, (WAVES == 8 || (T == kBF16 && KP <= 2) ? 2 : 1)) void delta_scan_bwd_kernel(DeltaParams p)
 {
     typedef typename DeltaElem<T>::type E;
     constexpr int NT = 64 * WAVES, COLS = 16 * WAVES;
@@ -953,11 +968,7 @@ SSD_KERNEL_WAVES(64 * WAVES, 2) void delta_scan_bwd_kernel(DeltaParams p)
                 x[e] *= p.scale;
             }
             W[s] = split8<kParts>(w);
-            Raw8<T> raw;
-#pragma unroll
-            for (int i = 0; i < (T == kBF16 ? 1 : 2); ++i)
-                raw.w[i] = *(const v4u *)(gl + 32 * s + 4 * i);
-            unpack8<T>(raw, w);
+            lds_values<T>(gl + 32 * s, w);
 #pragma unroll
             for (int e = 0; e < 8; ++e)
                 x[e] *= w[e];
@@ -1108,11 +1119,12 @@ struct GradLds {
             uint16_t s[s_size], gs[s_size];
         } b;
         struct {
-            E kt[32 * KP * TS], qt[32 * KP * TS];
+            E qt[32 * KP * TS], kt[32 * KP * TS];
         } c;
     };
+    static constexpr bool KEEP = T == kBF16;  // K by features has room of its own from the start
     char own_tri[MANY ? tri_bytes : 16];
-    E k[64 * RS];
+    E k[64 * RS], own_kt[KEEP ? 32 * KP * TS : 8];
     DeltaGates gates;
     float beta[4][64];   // shares of dbeta
     float sums[64];      // dG
@@ -1172,9 +1184,28 @@ SSD_KERNEL_WAVES(256, (KP <= 2 && !MANY ? 2 : 1)) void delta_grad_kernel(DeltaPa
     for (int i = 0; i < 4; ++i)
         m1t[i] = m1[i] = m2t[i] = m2[i] = v4f{0.f, 0.f, 0.f, 0.f};
     float dot = 0.f;
-    delta_stage<T, KP, true, false>(k, p.k_stride, p.Dk, n, lds.k, nullptr);
+    // the first columns' values are on their way while the triangle is made
+    v4f s[2 * KP];
+    float R[2][8], by[2][8];
+    auto fetch_columns = [&](int col) {
+        const int dv = col + 16 * wave + l;
+        state_load<KP>(s, S + (dv < p.Dv ? dv : col), p.Dk, p.Dv);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int t = q8 < n - (32 * h + e) ? q8 + (32 * h + e) : n - 1;
+                R[h][e] = delta_load<T>(v + (uint32_t)t * (uint32_t)p.v_stride + (dv < p.Dv ? dv : col));
+                by[h][e] = gr[(uint32_t)(q8 + (32 * h + e)) * (uint32_t)p.Dv + (dv < p.Dv ? dv : col)];
+            }
+    };
+    Blocks<T, 32 * KP, 256> kb;
+    blocks_load<T, 32 * KP, 256>(kb, k, (int)p.k_stride, p.Dk, n);
     if (wave == 3)
         delta_gates(lds.gates, p.g, p.beta, token * p.Hv + hv, p.Hv, n);
+    fetch_columns(0);
+    E *const kt = Lds::KEEP ? lds.own_kt : lds.c.kt;
+    blocks_store<T, 32 * KP, 256, true, Lds::KEEP>(kb, p.Dk, n, lds.k, kt);
     delta_clear_pairs(pairs, 256);
     block_sync();
     const DeltaGates &gates = lds.gates;
@@ -1186,21 +1217,13 @@ SSD_KERNEL_WAVES(256, (KP <= 2 && !MANY ? 2 : 1)) void delta_grad_kernel(DeltaPa
     const bool valid = own < n;
     for (int col = 0; MANY ? col < p.Dv : col == 0; col += 64) {
         const int cols = p.Dv - col;
+        GradBlocks<64, 8> d;
         // U of 16 columns, as in the walk
         {
             const int dv = col + 16 * wave + l;
             const bool live = dv < p.Dv;
-            v4f s[2 * KP];
-            state_load<KP>(s, S + (live ? dv : col), p.Dk, p.Dv);
-            float R[2][8], by[2][8];
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const int t = q8 < n - (32 * h + e) ? q8 + (32 * h + e) : n - 1;
-                    R[h][e] = delta_load<T>(v + (uint32_t)t * (uint32_t)p.v_stride + (live ? dv : col));
-                    by[h][e] = gr[(uint32_t)(q8 + (32 * h + e)) * (uint32_t)p.Dv + (live ? dv : col)];
-                }
+            if (MANY && col > 0)
+                fetch_columns(col);
             Parts<kParts> Sp[KP];
 #pragma unroll
             for (int i = 0; i < KP; ++i)
@@ -1232,6 +1255,7 @@ SSD_KERNEL_WAVES(256, (KP <= 2 && !MANY ? 2 : 1)) void delta_grad_kernel(DeltaPa
                         *to = (MANY && col > 0 ? *to : 0.f) + sum;
                     }
                 }
+            grad_load<64, 8>(d, gr + col, p.Dv, 64, cols);
             block_sync();  // the triangle is there; with more columns the last ones have been read
             const Parts<kParts> R0 = split8<kParts>(R[0]);
             v4f U[2];
@@ -1262,10 +1286,22 @@ SSD_KERNEL_WAVES(256, (KP <= 2 && !MANY ? 2 : 1)) void delta_grad_kernel(DeltaPa
             for (int h = 0; h < 2; ++h)
                 put(1, h, mm<kParts>(R1, frag_operand<kParts>(tri, frag_of(1, h, 1)), v4f{0.f, 0.f, 0.f, 0.f}));
         }
+        // dO of the own token and of those after, on its way
+        Parts<IN> oo[2], ao[2][4];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            oo[t] = row_operand<T>(go + (uint32_t)(valid ? own : 0) * (uint32_t)o_stride + col, 32 * t + q8, cols, valid);
+            if (Lds::KEEP)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if ((i >> 1) >= (wave >> 1)) {
+                        const int row = 32 * (i >> 1) + tile_row(i & 1, l);
+                        ao[t][i] = row_operand<T>(go + (uint32_t)(row < n ? row : 0) * (uint32_t)o_stride + col, 32 * t + q8,
+                                                  cols, row < n);
+                    }
+        }
         // dR, and dV = beta dR
         {
-            GradBlocks<64, 8> d;
-            grad_load<64, 8>(d, gr + col, p.Dv, 64, cols);
             if (!MANY)
                 block_sync();  // the triangle has been read
             grad_clear<64, 8>(d, 64, cols);
@@ -1284,11 +1320,9 @@ SSD_KERNEL_WAVES(256, (KP <= 2 && !MANY ? 2 : 1)) void delta_grad_kernel(DeltaPa
         }
         block_sync();
         // over the tokens
-        Parts<IN> oo[2];
         Parts<kParts> ro[2], uo[2];
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-            oo[t] = row_operand<T>(go + (uint32_t)(valid ? own : 0) * (uint32_t)o_stride + col, 32 * t + q8, cols, valid);
             ro[t] = grad_operand<64, kGradStride>(lds.a.r + own * kGradStride + q8 + 32 * t);
             uo[t] = grad_operand<64, kGradStride>(lds.a.u + own * kGradStride + q8 + 32 * t);
         }
@@ -1305,8 +1339,10 @@ SSD_KERNEL_WAVES(256, (KP <= 2 && !MANY ? 2 : 1)) void delta_grad_kernel(DeltaPa
                 }
                 if ((i >> 1) >= (wave >> 1)) {  // rows i from the own token j on
                     const int row = 32 * (i >> 1) + tile_row(i & 1, l);
-                    m1[i] = mm<kParts>(row_operand<T>(go + (uint32_t)(row < n ? row : 0) * (uint32_t)o_stride + col, 32 * t + q8,
-                                                      cols, row < n), uo[t], m1[i]);
+                    if (!Lds::KEEP)  // float32 rows would fill the registers
+                        ao[t][i] = row_operand<T>(go + (uint32_t)(row < n ? row : 0) * (uint32_t)o_stride + col, 32 * t + q8,
+                                                  cols, row < n);
+                    m1[i] = mm<kParts>(ao[t][i], uo[t], m1[i]);
                     m2[i] = mm<kParts>(grad_operand<64, kGradStride>(rl + at0), uo[t], m2[i]);
                 }
             }
@@ -1345,11 +1381,17 @@ SSD_KERNEL_WAVES(256, (KP <= 2 && !MANY ? 2 : 1)) void delta_grad_kernel(DeltaPa
             block_sync();  // before the next columns' U
     }
     dot = wave_sum(dot);
-    Blocks<T, 32 * KP, 256> kb, qb;
-    blocks_load<T, 32 * KP, 256>(kb, k, (int)p.k_stride, p.Dk, n);
+    Blocks<T, 32 * KP, 256> qb;
     blocks_load<T, 32 * KP, 256>(qb, q, (int)p.q_stride, p.Dk, n);
+    float qo[KP][8];
+#pragma unroll
+    for (int s = 0; s < KP; ++s)
+        row_values<T>(q + (uint32_t)(valid ? own : 0) * (uint32_t)p.q_stride, 32 * s + q8, p.Dk, valid, qo[s]);
+    if (!Lds::KEEP)
+        blocks_load<T, 32 * KP, 256>(kb, k, (int)p.k_stride, p.Dk, n);
     block_sync();
-    blocks_store<T, 32 * KP, 256, false, true>(kb, p.Dk, n, (E *)nullptr, lds.c.kt);
+    if (!Lds::KEEP)
+        blocks_store<T, 32 * KP, 256, false, true>(kb, p.Dk, n, (E *)nullptr, kt);
     blocks_store<T, 32 * KP, 256, false, true>(qb, p.Dk, n, (E *)nullptr, lds.c.qt);
     const double sum_own = gates.sum[own];
     const float since = gates.since[own], beta = gates.beta[own], hold = gates.left[own];
@@ -1367,7 +1409,7 @@ SSD_KERNEL_WAVES(256, (KP <= 2 && !MANY ? 2 : 1)) void delta_grad_kernel(DeltaPa
 #pragma unroll
     for (int s = 0; s < KP; ++s) {
         float w[8];
-        row_values<T>(k + (uint32_t)(valid ? own : 0) * (uint32_t)p.k_stride, 32 * s + q8, p.Dk, valid, w);
+        lds_values<T>(lds.k + own * RS + q8 + 32 * s, w);
         ko[s] = split8<IN>(w);
 #pragma unroll
         for (int e = 0; e < 8; ++e)
@@ -1377,7 +1419,7 @@ SSD_KERNEL_WAVES(256, (KP <= 2 && !MANY ? 2 : 1)) void delta_grad_kernel(DeltaPa
     if (lane == 0)
         lds.dots[wave] = gates.whole * dot + held;
     block_sync();
-    const E *ktl = lds.c.kt + tile_row(0, l) * TS + q8, *qtl = lds.c.qt + tile_row(0, l) * TS + q8;
+    const E *ktl = kt + tile_row(0, l) * TS + q8, *qtl = lds.c.qt + tile_row(0, l) * TS + q8;
     float by_own = 0.f;
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
@@ -1431,12 +1473,11 @@ SSD_KERNEL_WAVES(256, (KP <= 2 && !MANY ? 2 : 1)) void delta_grad_kernel(DeltaPa
     for (int s = 0; s < KP; ++s) {
         float x[8], y[8];
         const int f = 32 * s + q8;
-        row_values<T>(q + (uint32_t)(valid ? own : 0) * (uint32_t)p.q_stride, f, p.Dk, valid, x);
-        row_values<T>(k + (uint32_t)(valid ? own : 0) * (uint32_t)p.k_stride, f, p.Dk, valid, y);
+        lds_values<T>(lds.k + own * RS + f, y);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             const int i = 2 * s + (e >> 2), r = e & 3;
-            dots = __builtin_fmaf(x[e], aq[i][r], dots);
+            dots = __builtin_fmaf(qo[s][e], aq[i][r], dots);
             dots = __builtin_fmaf(y[e], reads[i][r] - writes[i][r], dots);
             x[e] = aq[i][r];
             y[e] = reads[i][r] + writes[i][r];

@@ -5,3 +5,4 @@
 
 SSD_DEVICE uint32_t opaque(uint32_t v) { return v; }
 SSD_DEVICE uint32_t opaque_uniform(uint32_t v) { return v; }
+SSD_DEVICE void together(float &, float &) {}
