@@ -747,36 +747,67 @@ SSD_KERNEL(256) void delta_few_kernel(DeltaParams p)
             }
     };
 #pragma unroll
-    for (int i = 0; i < ROWS; ++i) {
-        const float *at = p.init + head + (int64_t)(r + 16 * i) * p.Dv + dv;
-        const bool in = p.init && r + 16 * i < p.Dk;
-        if (in && left >= 4) {
-            __builtin_memcpy(S[i], at, 16);
-        } else {
+    for (int i = 0; i < ROWS; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            S[i][e] = 0.f;
+    if (p.init && left >= 4) {
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i)
+            __builtin_memcpy(S[i], p.init + head + (int64_t)(r + 16 * i < p.Dk ? r + 16 * i : 0) * p.Dv + dv, 16);
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                S[i][e] = in && e < left ? at[e] : 0.f;
-        }
+                S[i][e] = r + 16 * i < p.Dk ? S[i][e] : 0.f;
+    } else if (p.init && left > 0) {
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                S[i][e] = r + 16 * i < p.Dk && e < left ? p.init[head + (int64_t)(r + 16 * i) * p.Dv + dv + e] : 0.f;
     }
     if (p.states)  // one chunk
         store(p.states + head);
+    // the next token's values are on their way while one is gone through; loads go to places that exist
     const int64_t o_stride = (int64_t)p.Hv * p.Dv;
-    for (int t = 0; t < p.T; ++t) {
+    const int cols = left < 0 ? 0 : left < 4 ? left : 4;
+    float nk[ROWS], nq[ROWS], nv[4], ng, nbeta;
+    auto fetch = [&](int t) {
         const int64_t token = (int64_t)b * p.T + t;
-        E *o = (E *)p.o + token * o_stride + hv * p.Dv + dv;
+        const E *q = (const E *)p.q + token * p.q_stride + hk * p.Dk, *k = (const E *)p.k + token * p.k_stride + hk * p.Dk;
+        const E *v = (const E *)p.v + token * p.v_stride + hv * p.Dv;
+        ng = p.g[token * p.Hv + hv];
+        nbeta = p.beta[token * p.Hv + hv];
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i) {
+            const int f = r + 16 * i < p.Dk ? r + 16 * i : p.Dk - 1;
+            nk[i] = delta_load<T>(k + f);
+            nq[i] = delta_load<T>(q + f);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            nv[e] = delta_load<T>(v + (e < cols ? dv + e : 0));
+    };
+    if (length > 0)
+        fetch(0);
+    for (int t = 0; t < p.T; ++t) {
+        E *o = (E *)p.o + ((int64_t)b * p.T + t) * o_stride + hv * p.Dv + dv;
         float out[4] = {0.f, 0.f, 0.f, 0.f};
         if (t < length) {
-            const E *q = (const E *)p.q + token * p.q_stride + hk * p.Dk;
-            const E *k = (const E *)p.k + token * p.k_stride + hk * p.Dk;
-            const E *v = (const E *)p.v + token * p.v_stride + hv * p.Dv + dv;
-            const float a = delta_exp(delta_log2(p.g[token * p.Hv + hv])), beta = p.beta[token * p.Hv + hv];
             float kr[ROWS], qr[ROWS], u[4];
+            const float a = delta_exp(delta_log2(ng)), beta = nbeta;
 #pragma unroll
             for (int i = 0; i < ROWS; ++i) {
-                const bool in = r + 16 * i < p.Dk;
-                kr[i] = in ? delta_load<T>(k + r + 16 * i) : 0.f;
-                qr[i] = in ? delta_load<T>(q + r + 16 * i) : 0.f;
+                kr[i] = r + 16 * i < p.Dk ? nk[i] : 0.f;
+                qr[i] = r + 16 * i < p.Dk ? nq[i] : 0.f;
             }
+            float x[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                x[e] = e < cols ? nv[e] : 0.f;
+            if (t + 1 < length)
+                fetch(t + 1);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 u[e] = 0.f;
@@ -788,8 +819,7 @@ SSD_KERNEL(256) void delta_few_kernel(DeltaParams p)
             }
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const float x = e < left ? delta_load<T>(v + e) : 0.f;
-                u[e] = beta * (x - row16_sum(u[e]));
+                u[e] = beta * (x[e] - row16_sum(u[e]));
 #pragma unroll
                 for (int i = 0; i < ROWS; ++i) {
                     S[i][e] = __builtin_fmaf(kr[i], u[e], S[i][e]);
@@ -800,11 +830,12 @@ SSD_KERNEL(256) void delta_few_kernel(DeltaParams p)
             for (int e = 0; e < 4; ++e)
                 out[e] = p.scale * row16_sum(out[e]);
         }
-        if (r == 0)
+        if (r == 0) {
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                if (e < left)
+                if (e < cols)
                     delta_store<T>(o + e, out[e]);
+        }
     }
     if (p.final_state)
         store(p.final_state + head);
