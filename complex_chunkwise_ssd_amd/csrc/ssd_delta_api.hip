@@ -51,6 +51,33 @@ int check_delta_strides(const DeltaSizes &z, int64_t q, int64_t k, int64_t v)
 
 bool delta_few(const DeltaSizes &z) { return z.T <= ssd::kDeltaFew; }
 
+// Whether a call's heads are too few for a walk of their own to fill the chip, and what is packed for them.
+bool delta_long(const DeltaSizes &z) { return z.B * z.Hv * ((z.Dv + 63) / 64) <= 192; }
+
+template <int T, int KP>
+constexpr size_t pack_bytes(bool backward)
+{
+    return 16 * (size_t)(backward ? ssd::DeltaPack<T, KP, true>::size : ssd::DeltaPack<T, KP, false>::size);
+}
+// Bytes that a chunk of a head is packed into; chunks that are packed at a time (some 192 MB, which the caches of the
+// memory side hold until they are read).
+struct DeltaRange {
+    int64_t chunks;
+    size_t pack, carry;
+    size_t bytes() const { return pack + carry; }
+};
+DeltaRange delta_range(const DeltaSizes &z, int dtype, bool backward)
+{
+    if (!delta_long(z))
+        return {0, 0, 0};
+    const size_t one = dtype == SSD_BF16 ? (z.Dk <= 64 ? pack_bytes<ssd::kBF16, 2>(backward) : pack_bytes<ssd::kBF16, 4>(backward))
+                                         : (z.Dk <= 64 ? pack_bytes<ssd::kF32, 2>(backward) : pack_bytes<ssd::kF32, 4>(backward));
+    const size_t heads = one * (size_t)(z.B * z.Hv);
+    int64_t chunks = (int64_t)((size_t)192 * 1024 * 1024 / heads);
+    chunks = chunks < 1 ? 1 : chunks < z.chunks() ? chunks : z.chunks();
+    return {chunks, align256(heads * (size_t)chunks), align256((size_t)z.states())};
+}
+
 // Workspace of the gradients: dS' and dR of every chunk, and dQ and dK by value heads where they share keys.
 struct DeltaSpace {
     size_t gs, gr, w;
@@ -108,9 +135,38 @@ int launch_delta_as(ssd::DeltaParams p, hipStream_t s)
                        dim3(64 * WAVES), 0, s, p);
     return launch_status();
 }
-template <int T, int KP>
-int launch_delta(const ssd::DeltaParams &p, hipStream_t s)
+// Range after range of chunks, packed and walked over.
+template <int T, int KP, bool BACKWARD>
+int launch_delta_long(ssd::DeltaParams p, const DeltaRange &range, char *workspace, hipStream_t s)
 {
+    p.pack = (v4u *)workspace;
+    p.carry = (float *)(workspace + range.pack);
+    p.columns = (p.Dv + 15) / 16;
+    const int64_t heads = (int64_t)p.B * p.Hv;
+    const int ranges = (int)((p.chunks + range.chunks - 1) / range.chunks);
+    for (int i = 0; i < ranges; ++i) {
+        p.chunk_from = (int)range.chunks * (BACKWARD ? ranges - 1 - i : i);
+        p.chunk_to = p.chunk_from + (int)range.chunks < p.chunks ? p.chunk_from + (int)range.chunks : p.chunks;
+        hipLaunchKernelGGL((ssd::delta_pack_kernel<T, KP, BACKWARD>), dim3((unsigned)(heads * (p.chunk_to - p.chunk_from))),
+                           dim3(256), 0, s, p);
+        if (int st = launch_status())
+            return st;
+        const dim3 grid((unsigned)((heads + 7) / 8 * 8 * p.columns));
+        if (BACKWARD)
+            hipLaunchKernelGGL((ssd::delta_long_bwd_kernel<T, KP>), grid, dim3(64), 0, s, p);
+        else
+            hipLaunchKernelGGL((ssd::delta_long_kernel<T, KP>), grid, dim3(128), 0, s, p);
+        if (int st = launch_status())
+            return st;
+    }
+    return SSD_OK;
+}
+
+template <int T, int KP>
+int launch_delta(const ssd::DeltaParams &p, const DeltaRange &range, char *workspace, hipStream_t s)
+{
+    if (range.chunks > 0)
+        return launch_delta_long<T, KP, false>(p, range, workspace, s);
     return p.Dv > 64 && KP == 4 ? launch_delta_as<T, KP, 8>(p, s) : launch_delta_as<T, KP, 4>(p, s);
 }
 
@@ -123,9 +179,9 @@ int launch_delta_scan_bwd(ssd::DeltaParams p, hipStream_t s)
     return launch_status();
 }
 template <int T, int KP>
-int launch_delta_bwd(const ssd::DeltaParams &p, hipStream_t s)
+int launch_delta_bwd(const ssd::DeltaParams &p, const DeltaRange &range, char *workspace, hipStream_t s)
 {
-    if (int st = p.Dv > 64 && KP == 4 ? launch_delta_scan_bwd<T, KP, 8>(p, s) : launch_delta_scan_bwd<T, KP, 4>(p, s))
+    if (int st = range.chunks > 0 ? launch_delta_long<T, KP, true>(p, range, workspace, s) : p.Dv > 64 && KP == 4 ? launch_delta_scan_bwd<T, KP, 8>(p, s) : launch_delta_scan_bwd<T, KP, 4>(p, s))
         return st;
     const dim3 grid((unsigned)((int64_t)p.B * p.Hv * p.chunks)), block(256);
     if (p.Dv > 64)
@@ -161,7 +217,7 @@ size_t ssd_gated_delta_workspace_bytes(int64_t batch, int64_t T, int64_t Hk, int
     const DeltaSizes z{batch, T, Hk, Hv, Dk, Dv};
     if (check_delta(z, dtype, 1.f) || z.empty() || delta_few(z))
         return 0;
-    return 0;
+    return delta_range(z, dtype, false).bytes();
 }
 
 int ssd_gated_delta(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v, int64_t v_stride,
@@ -211,9 +267,11 @@ int ssd_gated_delta(const void *q, int64_t q_stride, const void *k, int64_t k_st
     p.states = chunk_states;
     if (delta_few(z))
         return dtype == SSD_BF16 ? launch_delta_few<ssd::kBF16>(p, s) : launch_delta_few<ssd::kF32>(p, s);
+    const DeltaRange range = delta_range(z, dtype, false);
+    char *at = (char *)workspace;
     if (dtype == SSD_BF16)
-        return Dk <= 64 ? launch_delta<ssd::kBF16, 2>(p, s) : launch_delta<ssd::kBF16, 4>(p, s);
-    return Dk <= 64 ? launch_delta<ssd::kF32, 2>(p, s) : launch_delta<ssd::kF32, 4>(p, s);
+        return Dk <= 64 ? launch_delta<ssd::kBF16, 2>(p, range, at, s) : launch_delta<ssd::kBF16, 4>(p, range, at, s);
+    return Dk <= 64 ? launch_delta<ssd::kF32, 2>(p, range, at, s) : launch_delta<ssd::kF32, 4>(p, range, at, s);
 }
 
 size_t ssd_gated_delta_backward_workspace_bytes(int64_t batch, int64_t T, int64_t Hk, int64_t Hv, int64_t Dk, int64_t Dv,
@@ -222,7 +280,7 @@ size_t ssd_gated_delta_backward_workspace_bytes(int64_t batch, int64_t T, int64_
     const DeltaSizes z{batch, T, Hk, Hv, Dk, Dv};
     if (check_delta(z, dtype, 1.f) || z.empty())
         return 0;
-    return delta_space(z).bytes();
+    return delta_space(z).bytes() + delta_range(z, dtype, true).bytes();
 }
 
 int ssd_gated_delta_backward(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
@@ -284,9 +342,11 @@ int ssd_gated_delta_backward(const void *q, int64_t q_stride, const void *k, int
     p.gr = (float *)(at + space.gs);
     p.wq = (float *)(at + space.gs + space.gr);
     p.wk = (float *)(at + space.gs + space.gr + space.w);
+    const DeltaRange range = delta_range(z, dtype, true);
+    at += space.bytes();
     if (dtype == SSD_BF16)
-        return Dk <= 64 ? launch_delta_bwd<ssd::kBF16, 2>(p, s) : launch_delta_bwd<ssd::kBF16, 4>(p, s);
-    return Dk <= 64 ? launch_delta_bwd<ssd::kF32, 2>(p, s) : launch_delta_bwd<ssd::kF32, 4>(p, s);
+        return Dk <= 64 ? launch_delta_bwd<ssd::kBF16, 2>(p, range, at, s) : launch_delta_bwd<ssd::kBF16, 4>(p, range, at, s);
+    return Dk <= 64 ? launch_delta_bwd<ssd::kF32, 2>(p, range, at, s) : launch_delta_bwd<ssd::kF32, 4>(p, range, at, s);
 }
 
 }  // extern "C"

@@ -57,6 +57,10 @@ struct DeltaParams {
     int64_t q_stride, k_stride, v_stride;
     int B, T, Hk, Hv, Dk, Dv, chunks;
     int columns;                          // column blocks of a head
+    // few heads
+    v4u *pack;                            // (B, Hv, chunk_to - chunk_from) times what a chunk is packed into
+    float *carry;                         // (B, Hv, Dk, Dv): the state between two ranges of chunks
+    int chunk_from, chunk_to;
     float scale;
 };
 
@@ -713,6 +717,332 @@ SSD_KERNEL_WAVES(64 * WAVES, (WAVES == 8 || (T == kBF16 && KP <= 2) ? 2 : 1)) vo
         state_store<KP>(S, p.final_state + head + dv, p.Dk, p.Dv);
 }
 
+// ------------------------------------------------------------- few heads, long sequences
+
+// Where sequences and heads give too few workgroups, what a chunk has beside the state is made for all chunks at once
+// (delta_pack_kernel) and laid out as the operands that the walk takes, and the walk has 16 columns a workgroup and no
+// more to do than the state asks for: one wave passes the state on, a second one makes the outputs
+// from what the first leaves in shared memory.
+
+// What a chunk is packed into, in units of 16 bytes: operand tiles of 64 lanes each, and the gates.
+template <int T, int KP, bool BACKWARD>
+struct DeltaPack {
+    static constexpr int IN = DeltaElem<T>::parts, OUT = BACKWARD || T == kF32 ? 3 : 2;
+    static constexpr int tri = 0, pf = tri + kParts * kDeltaFrags * 64, kr = pf + OUT * kDeltaFrags * 64;
+    static constexpr int kt = kr + 4 * KP * IN * 64, q = kt + 4 * KP * IN * 64;  // Q by rows, backwards by features
+    static constexpr int gates = q + 4 * KP * IN * 64, size = gates + 64;  // since, left, beta, and e^G_C in the last place
+};
+
+template <int T, int KP, bool BACKWARD>
+SSD_KERNEL(256) void delta_pack_kernel(DeltaParams p)
+{
+    typedef typename DeltaElem<T>::type E;
+    typedef DeltaPack<T, KP, BACKWARD> Pack;
+    constexpr int pad = DeltaElem<T>::pad, RS = 32 * KP + pad, TS = 64 + pad, IN = Pack::IN;
+    SSD_LDS E k[64 * RS], q[BACKWARD && 32 * KP * TS > 64 * RS ? 32 * KP * TS : 64 * RS], kt[32 * KP * TS];
+    E *const qt = q;  // by features once its rows have been used
+    SSD_LDS float pairs[64 * kPairStride];
+    SSD_LDS v4u tri[kParts * kDeltaFrags * 64], pf[Pack::OUT * kDeltaFrags * 64];
+    SSD_LDS DeltaGates gates;
+    const int64_t id = block_id();
+    const int range = p.chunk_to - p.chunk_from;
+    const int at = (int)(id % range), chunk = p.chunk_from + at, hv = (int)(id / range % p.Hv), b = (int)(id / range / p.Hv);
+    const int hk = hv / (p.Hv / p.Hk), wave = wave_id(), lane = thread_id() & 63, l = lane & 15, q8 = 8 * (lane >> 4);
+    const int n = delta_chunk_tokens(delta_valid(p, b), chunk);
+    if (n == 0)
+        return;
+    const int64_t token = (int64_t)b * p.T + chunk * kDeltaChunk;
+    Blocks<T, 32 * KP, 256> nk, nq;
+    blocks_load<T, 32 * KP, 256>(nk, (const E *)p.k + token * p.k_stride + hk * p.Dk, (int)p.k_stride, p.Dk, n);
+    blocks_load<T, 32 * KP, 256>(nq, (const E *)p.q + token * p.q_stride + hk * p.Dk, (int)p.q_stride, p.Dk, n);
+    if (wave == 3)
+        delta_gates(gates, p.g, p.beta, token * p.Hv + hv, p.Hv, n);
+    blocks_store<T, 32 * KP, 256, true, true>(nk, p.Dk, n, k, kt);
+    blocks_store<T, 32 * KP, 256, true, false>(nq, p.Dk, n, q, (E *)nullptr);
+    delta_clear_pairs(pairs, 256);
+    for (int i = thread_id(); i < Pack::OUT * kDeltaFrags * 64; i += 256)
+        pf[i] = v4u{0u, 0u, 0u, 0u};
+    block_sync();
+    delta_tiles<T, KP, Pack::OUT, 4, BACKWARD>(k, q, gates, p.scale, pairs, tri, pf);
+    block_sync();
+    if (BACKWARD)
+        blocks_store<T, 32 * KP, 256, false, true>(nq, p.Dk, n, (E *)nullptr, qt);
+    if (wave < 2)
+        delta_invert<BACKWARD>(pairs + 32 * wave * kPairStride, wave, tri);
+    block_sync();
+    v4u *out = p.pack + (((int64_t)b * p.Hv + hv) * range + at) * Pack::size;
+    const E *kl = k + tile_row(0, l) * RS + q8, *ql = q + tile_row(0, l) * RS + q8;
+    const E *ktl = kt + tile_row(0, l) * TS + q8, *qtl = qt + tile_row(0, l) * TS + q8;
+    auto put = [&](int to, int tile, const Parts<IN> &x) {
+#pragma unroll
+        for (int e = 0; e < IN; ++e)
+            out[to + (tile * IN + e) * 64 + lane] = x.p[e];
+    };
+    for (int i = wave; i < 4 * KP; i += 4) {
+        const int h = i / KP, f = i % KP, row = (32 * (h >> 1) + 4 * (h & 1)) * RS + 32 * f;   // rows: (tile, span)
+        const int col = state_at(i >> 1, 0) * TS + 32 * (i & 1);                               // features: (tile, span)
+        put(Pack::kr, i, lds_operand(kl + row));
+        put(Pack::kt, i, lds_operand(ktl + col));
+        put(Pack::q, i, BACKWARD ? lds_operand(qtl + col) : lds_operand(ql + row));
+    }
+    if (thread_id() < 64) {
+        float *to = (float *)(out + Pack::gates);
+        to[lane] = gates.since[lane];
+        to[64 + lane] = gates.left[lane];
+        to[128 + lane] = gates.beta[lane];
+        to[192 + lane] = gates.whole;
+    }
+    for (int i = thread_id(); i < kParts * kDeltaFrags * 64; i += 256)
+        out[Pack::tri + i] = tri[i];
+    for (int i = thread_id(); i < Pack::OUT * kDeltaFrags * 64; i += 256)
+        out[Pack::pf + i] = pf[i];
+}
+
+// The workgroup's head and columns: the columns of a head lie a multiple of eight workgroups apart, on the same
+// die, whose cache then holds the head's operands for all of them.
+SSD_DEVICE void long_place(const DeltaParams &p, int64_t &head, int &block)
+{
+    const int64_t id = block_id();
+    head = id / (8 * (int64_t)p.columns) * 8 + id % 8;
+    block = (int)(id / 8 % p.columns);
+}
+
+template <int N>
+SSD_DEVICE void pack_load(Parts<N> &x, const v4u *from)
+{
+#pragma unroll
+    for (int e = 0; e < N; ++e)
+        x.p[e] = from[e * 64];
+}
+// Tiles of the triangle and of P: their parts lie kDeltaFrags tiles apart.
+template <int N>
+SSD_DEVICE void pack_load_frag(Parts<N> &x, const v4u *from, int f)
+{
+#pragma unroll
+    for (int e = 0; e < N; ++e)
+        x.p[e] = from[(e * kDeltaFrags + f) * 64];
+}
+// The values of the lane's 16 tokens.
+SSD_DEVICE void pack_gate(v4f (&g)[4], const float *from, int q8)
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        g[i] = *(const v4f *)(from + q8 + (32 * (i >> 1) + 4 * (i & 1)));
+}
+
+template <int T, int KP>
+SSD_KERNEL(128) void delta_long_kernel(DeltaParams p)
+{
+    typedef typename DeltaElem<T>::type E;
+    typedef DeltaPack<T, KP, false> Pack;
+    constexpr int IN = Pack::IN, OUT = Pack::OUT;
+    constexpr bool AHEAD = T == kBF16;  // K's rows of the next chunk; in float32 there are too many
+    SSD_LDS v4u state[2][KP * OUT * 64], us[2][2 * OUT * 64];
+    int64_t bh;
+    int block;
+    long_place(p, bh, block);
+    if (bh >= (int64_t)p.B * p.Hv)
+        return;
+    const int hv = (int)(bh % p.Hv), b = (int)(bh / p.Hv);
+    const int lane = thread_id() & 63, l = lane & 15, q8 = 8 * (lane >> 4);
+    const int dv = 16 * block + l;
+    const bool live = dv < p.Dv;
+    const int length = delta_valid(p, b), range = p.chunk_to - p.chunk_from;
+    const int64_t row = (int64_t)b * p.T;
+    const v4u *pack = p.pack + bh * range * Pack::size + lane;
+    const int last = (length + kDeltaChunk - 1) / kDeltaChunk;  // chunks with tokens
+    const int to = last < p.chunk_to ? last : p.chunk_to;
+    if (wave_id() == 0) {
+        v4f S[2 * KP];
+#pragma unroll
+        for (int i = 0; i < 2 * KP; ++i)
+            S[i] = v4f{0.f, 0.f, 0.f, 0.f};
+        const float *init = p.chunk_from > 0 ? p.carry : p.init;
+        if (init && live)
+            state_load<KP>(S, init + bh * p.Dk * p.Dv + dv, p.Dk, p.Dv);
+        const E *vrow = (const E *)p.v + row * p.v_stride + hv * p.Dv + (live ? dv : 0);
+        float V[16];
+        v4f since[4], beta[4], left[4];
+        float whole = 0.f;
+        Parts<IN> kr[AHEAD ? 4 * KP : 1];
+        auto fetch = [&](int chunk) {
+            const v4u *at = pack + (int64_t)(chunk - p.chunk_from) * Pack::size;
+            const float *g = (const float *)(at - lane + Pack::gates);
+            if (AHEAD)
+#pragma unroll
+                for (int i = 0; i < 4 * KP; ++i)
+                    pack_load(kr[AHEAD ? i : 0], at + Pack::kr + i * IN * 64);
+            pack_gate(since, g, q8);
+            pack_gate(left, g + 64, q8);
+            pack_gate(beta, g + 128, q8);
+            whole = g[192];
+            const int n = delta_chunk_tokens(length, chunk);
+            const char *v = (const char *)(vrow + (int64_t)chunk * kDeltaChunk * p.v_stride);
+            const uint32_t step = opaque_uniform((uint32_t)p.v_stride * sizeof(E)), first = opaque((uint32_t)q8 * step);
+            if (n == 64) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    V[e] = delta_load<T>((const E *)(v + (first + (uint32_t)(32 * (e >> 3) + (e & 7)) * step)));
+            } else {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const int t = 32 * (e >> 3) + (e & 7);
+                    V[e] = delta_load<T>((const E *)(v + (uint32_t)(q8 < n - t ? q8 + t : n - 1) * step));
+                }
+            }
+        };
+        if (p.chunk_from < to)
+            fetch(p.chunk_from);
+        for (int chunk = p.chunk_from; chunk < p.chunk_to; ++chunk) {
+            if (p.states && live)
+                state_store<KP>(S, p.states + (((int64_t)b * p.chunks + chunk) * p.Hv + hv) * p.Dk * p.Dv + dv, p.Dk, p.Dv);
+            if (chunk >= to)
+                continue;
+            const v4u *at = pack + (int64_t)(chunk - p.chunk_from) * Pack::size;
+            const int n = delta_chunk_tokens(length, chunk);
+            Parts<kParts> tri[kDeltaFrags];
+            Parts<IN> kt[4 * KP];
+#pragma unroll
+            for (int f = 0; f < kDeltaFrags; ++f)
+                pack_load_frag(tri[f], at + Pack::tri, f);
+            Parts<kParts> Sp[KP];
+#pragma unroll
+            for (int s = 0; s < KP; ++s) {
+                Sp[s] = split_tiles<kParts>(S[2 * s], S[2 * s + 1]);
+#pragma unroll
+                for (int e = 0; e < OUT; ++e)
+                    state[chunk & 1][(s * OUT + e) * 64 + lane] = Sp[s].p[e];
+            }
+            // R = beta (V - e^G K S)
+            float R[2][8];
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+                v4f ks = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int f = 0; f < KP; ++f) {
+                    if (!AHEAD)
+                        pack_load(kr[0], at + Pack::kr + (h * KP + f) * IN * 64);
+                    ks = mm<kParts>(kr[AHEAD ? h * KP + f : 0], Sp[f], ks);
+                }
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int e = 4 * (h & 1) + r;
+                    const float x = live && q8 < n - (32 * (h >> 1) + e) ? V[8 * (h >> 1) + e] : 0.f;
+                    R[h >> 1][e] = beta[h][r] * (x - since[h][r] * ks[r]);
+                }
+            }
+            // U
+#pragma unroll
+            for (int i = 0; i < 4 * KP; ++i)
+                pack_load(kt[i], at + Pack::kt + i * IN * 64);
+            const Parts<kParts> R0 = split8<kParts>(R[0]);
+            v4f U[4];
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                U[h] = mm<kParts>(tri[frag_of(0, h, 0)], R0, v4f{0.f, 0.f, 0.f, 0.f});
+            const Parts<kParts> U0 = split_tiles<kParts>(U[0], U[1]);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const v4f c = mm<kParts>(tri[frag_of(1, h, 0)], U0, v4f{0.f, 0.f, 0.f, 0.f});
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    R[1][4 * h + r] -= c[r];
+            }
+            const Parts<kParts> R1 = split8<kParts>(R[1]);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                U[2 + h] = mm<kParts>(tri[frag_of(1, h, 1)], R1, v4f{0.f, 0.f, 0.f, 0.f});
+            const Parts<OUT> U1 = split_tiles<OUT>(U[2], U[3]);
+#pragma unroll
+            for (int e = 0; e < OUT; ++e) {
+                us[chunk & 1][e * 64 + lane] = U0.p[e];
+                us[chunk & 1][(OUT + e) * 64 + lane] = U1.p[e];
+            }
+            // the state
+            Parts<kParts> W[2];
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                float w[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    w[e] = left[2 * s + (e >> 2)][e & 3] * U[2 * s + (e >> 2)][e & 3];
+                W[s] = split8<kParts>(w);
+            }
+            const float hold = whole;
+            if (chunk + 1 < to)
+                fetch(chunk + 1);
+#pragma unroll
+            for (int i = 0; i < 2 * KP; ++i) {
+                v4f c;
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    c[r] = hold * S[i][r];
+#pragma unroll
+                for (int s = 0; s < 2; ++s)
+                    c = mm<kParts>(kt[2 * i + s], W[s], c);
+                S[i] = c;
+            }
+            block_sync();  // what the outputs need is there, those of the chunk before are made
+        }
+        float *out = p.chunk_to < p.chunks ? p.carry : p.final_state;
+        if (out && live)
+            state_store<KP>(S, out + bh * p.Dk * p.Dv + dv, p.Dk, p.Dv);
+    } else {
+        const int o_stride = p.Hv * p.Dv;
+        for (int chunk = p.chunk_from; chunk < p.chunk_to; ++chunk) {
+            const int rows = p.T - chunk * kDeltaChunk < 64 ? p.T - chunk * kDeltaChunk : 64;
+            E *o = (E *)p.o + (row + (int64_t)chunk * kDeltaChunk) * o_stride + hv * p.Dv + dv;
+            if (chunk >= to) {  // padding
+                if (live)
+                    for (int t = q8 >> 3; t < rows; t += 4)
+                        delta_store<T>(o + (int64_t)t * o_stride, 0.f);
+                continue;
+            }
+            const v4u *at = pack + (int64_t)(chunk - p.chunk_from) * Pack::size;
+            const int n = delta_chunk_tokens(length, chunk);
+            Parts<IN> qr[4 * KP];
+            Parts<OUT> pf[kDeltaFrags];
+            v4f since[4];
+#pragma unroll
+            for (int i = 0; i < 4 * KP; ++i)
+                pack_load(qr[i], at + Pack::q + i * IN * 64);
+#pragma unroll
+            for (int f = 0; f < kDeltaFrags; ++f)
+                pack_load_frag(pf[f], at + Pack::pf, f);
+            pack_gate(since, (const float *)(at - lane + Pack::gates), q8);
+            block_sync();  // the state and U are there
+            Parts<OUT> Sp[KP], U[2];
+#pragma unroll
+            for (int s = 0; s < KP; ++s)
+                pack_load(Sp[s], &state[chunk & 1][s * OUT * 64 + lane]);
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+                pack_load(U[s], &us[chunk & 1][s * OUT * 64 + lane]);
+            const uint32_t step = opaque_uniform((uint32_t)o_stride * sizeof(E)), off = opaque((uint32_t)q8 * step);
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+                v4f c = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int f = 0; f < KP; ++f)
+                    c = mm<OUT>(qr[h * KP + f], Sp[f], c);
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    c[r] *= p.scale * since[h][r];
+                c = mm<OUT>(pf[frag_of(h >> 1, h & 1, 0)], U[0], c);
+                if (h > 1)
+                    c = mm<OUT>(pf[frag_of(1, h & 1, 1)], U[1], c);
+                if (live)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const int t = 32 * (h >> 1) + 4 * (h & 1) + r;
+                        if (q8 < rows - t)
+                            delta_store<T>((E *)((char *)o + (off + (uint32_t)t * step)), q8 < n - t ? c[r] : 0.f);
+                    }
+            }
+        }
+    }
+}
+
 // ------------------------------------------------------------ a few tokens on the state
 
 constexpr int kDeltaFew = 8;  // tokens that are walked one by one
@@ -1025,6 +1355,179 @@ SSD_KERNEL_WAVES(64 * WAVES, (WAVES == 8 || (T == kBF16 && KP <= 2) ? 2 : 1)) vo
     }
     if (p.ginit && live)
         state_store<KP>(S, p.ginit + head + dv, p.Dk, p.Dv);
+}
+
+// The same with few heads: one wave a workgroup, on what delta_pack_kernel made.
+template <int T, int KP>
+SSD_KERNEL(64) void delta_long_bwd_kernel(DeltaParams p)
+{
+    typedef typename DeltaElem<T>::type E;
+    typedef DeltaPack<T, KP, true> Pack;
+    constexpr int IN = Pack::IN;
+    constexpr bool AHEAD = T == kBF16;  // K's rows of the next chunk; in float32 there are too many
+    int64_t bh;
+    int block;
+    long_place(p, bh, block);
+    if (bh >= (int64_t)p.B * p.Hv)
+        return;
+    const int hv = (int)(bh % p.Hv), b = (int)(bh / p.Hv);
+    const int lane = thread_id() & 63, l = lane & 15, q8 = 8 * (lane >> 4);
+    const int dv = 16 * block + l;
+    const bool live = dv < p.Dv;
+    const int length = delta_valid(p, b), range = p.chunk_to - p.chunk_from, o_stride = p.Hv * p.Dv;
+    const v4u *pack = p.pack + bh * range * Pack::size + lane;
+    const int last = (length + kDeltaChunk - 1) / kDeltaChunk;  // chunks with tokens
+    const int to = last < p.chunk_to ? last : p.chunk_to;
+    v4f S[2 * KP];  // the gradient of the state after the chunk
+#pragma unroll
+    for (int i = 0; i < 2 * KP; ++i)
+        S[i] = v4f{0.f, 0.f, 0.f, 0.f};
+    const float *init = p.chunk_to < p.chunks ? p.carry : p.gfinal;
+    if (init && live)
+        state_load<KP>(S, init + bh * p.Dk * p.Dv + dv, p.Dk, p.Dv);
+    const E *orow = (const E *)p.go + (int64_t)b * p.T * o_stride + hv * p.Dv + (live ? dv : 0);
+    float G[2][8];
+    v4f since[4], beta[4], left[4];
+    float whole = 0.f;
+    Parts<IN> kr[AHEAD ? 4 * KP : 1];
+    auto fetch = [&](int chunk) {
+        const v4u *at = pack + (int64_t)(chunk - p.chunk_from) * Pack::size;
+        const float *g = (const float *)(at - lane + Pack::gates);
+        if (AHEAD)
+#pragma unroll
+            for (int i = 0; i < 4 * KP; ++i)
+                pack_load(kr[AHEAD ? i : 0], at + Pack::kr + i * IN * 64);
+        pack_gate(since, g, q8);
+        pack_gate(left, g + 64, q8);
+        pack_gate(beta, g + 128, q8);
+        whole = g[192];
+        const int n = delta_chunk_tokens(length, chunk);
+        const char *o = (const char *)(orow + (int64_t)chunk * kDeltaChunk * o_stride);
+        const uint32_t step = opaque_uniform((uint32_t)o_stride * sizeof(E)), first = opaque((uint32_t)q8 * step);
+        if (n == 64) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+                G[e >> 3][e & 7] = delta_load<T>((const E *)(o + (first + (uint32_t)(32 * (e >> 3) + (e & 7)) * step)));
+        } else {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const int t = 32 * (e >> 3) + (e & 7);
+                G[e >> 3][e & 7] = delta_load<T>((const E *)(o + (uint32_t)(q8 < n - t ? q8 + t : n - 1) * step));
+            }
+        }
+    };
+    if (p.chunk_from < to)
+        fetch(to - 1);
+    for (int chunk = to - 1; chunk >= p.chunk_from; --chunk) {
+        const v4u *at = pack + (int64_t)(chunk - p.chunk_from) * Pack::size;
+        const int n = delta_chunk_tokens(length, chunk);
+        const int64_t place = bh * p.chunks + chunk;
+        Parts<kParts> tri[kDeltaFrags], pt[kDeltaFrags];
+#pragma unroll
+        for (int f = 0; f < kDeltaFrags; ++f) {
+            pack_load_frag(tri[f], at + Pack::tri, f);
+            pack_load_frag(pt[f], at + Pack::pf, f);
+        }
+        if (live)
+            state_store<KP>(S, p.gs + place * p.Dk * p.Dv + dv, p.Dk, p.Dv);
+        Parts<kParts> Sp[KP];
+#pragma unroll
+        for (int s = 0; s < KP; ++s)
+            Sp[s] = split_tiles<kParts>(S[2 * s], S[2 * s + 1]);
+        Parts<IN> go[2];
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                G[s][e] = live && q8 < n - (32 * s + e) ? G[s][e] : 0.f;
+            go[s] = split8<IN>(G[s]);
+        }
+        // dU
+        float dU[2][8];
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+            v4f ks = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int f = 0; f < KP; ++f) {
+                if (!AHEAD)
+                    pack_load(kr[0], at + Pack::kr + (h * KP + f) * IN * 64);
+                ks = mm<kParts>(kr[AHEAD ? h * KP + f : 0], Sp[f], ks);
+            }
+            v4f c;
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                c[r] = left[h][r] * ks[r];
+#pragma unroll
+            for (int t = h >> 1; t < 2; ++t)
+                c = mm<kParts>(pt[frag_of_upper(h >> 1, h & 1, t)], go[t], c);
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                dU[h >> 1][4 * (h & 1) + r] = c[r];
+        }
+        // dR
+        v4f dR[4];
+        const Parts<kParts> u1 = split8<kParts>(dU[1]);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            dR[2 + h] = mm<kParts>(tri[frag_of_upper(1, h, 1)], u1, v4f{0.f, 0.f, 0.f, 0.f});
+        const Parts<kParts> r1 = split_tiles<kParts>(dR[2], dR[3]);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const v4f c = mm<kParts>(tri[frag_of_upper(0, h, 1)], r1, v4f{0.f, 0.f, 0.f, 0.f});
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                dU[0][4 * h + r] -= c[r];
+        }
+        const Parts<kParts> u0 = split8<kParts>(dU[0]);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            dR[h] = mm<kParts>(tri[frag_of_upper(0, h, 0)], u0, v4f{0.f, 0.f, 0.f, 0.f});
+        if (live) {
+            const uint32_t step = opaque_uniform((uint32_t)p.Dv * 4), off = opaque((uint32_t)q8 * step);
+            char *out = (char *)(p.gr + place * 64 * p.Dv + dv);
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    *(float *)(out + (off + (32 * s + e) * step)) = dR[2 * s + (e >> 2)][e & 3];
+        }
+        // the state's gradient before the chunk
+        Parts<kParts> W[2], X[2];
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            float w[8], x[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int h = 2 * s + (e >> 2), r = e & 3;
+                w[e] = -since[h][r] * beta[h][r] * dR[h][r];
+                x[e] = p.scale * since[h][r] * G[s][e];
+            }
+            W[s] = split8<kParts>(w);
+            X[s] = split8<kParts>(x);
+        }
+        const float hold = whole;
+        if (chunk > p.chunk_from)
+            fetch(chunk - 1);
+#pragma unroll
+        for (int i = 0; i < 2 * KP; ++i) {
+            v4f c;
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                c[r] = hold * S[i][r];
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                Parts<IN> kt, qt;
+                pack_load(qt, at + Pack::q + (2 * i + s) * IN * 64);
+                pack_load(kt, at + Pack::kt + (2 * i + s) * IN * 64);
+                c = mm<kParts>(qt, X[s], c);
+                c = mm<kParts>(kt, W[s], c);
+            }
+            S[i] = c;
+        }
+    }
+    float *out = p.chunk_from > 0 ? p.carry : p.ginit;
+    if (out && live)
+        state_store<KP>(S, out + bh * p.Dk * p.Dv + dv, p.Dk, p.Dv);
 }
 
 // -------------------------------------------------------- gradients: every chunk by itself
