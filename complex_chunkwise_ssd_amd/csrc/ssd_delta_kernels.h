@@ -292,6 +292,23 @@ SSD_DEVICE Parts<N> frag_operand(const v4u *frags, int f)
     return r;
 }
 
+// An element as it lies in memory, and its value: what is loaded ahead is kept as it is, since a conversion
+// waits for it.
+template <int T>
+SSD_DEVICE uint32_t delta_raw(const typename DeltaElem<T>::type *p)
+{
+    if (T == kBF16) {
+        uint16_t u;
+        __builtin_memcpy(&u, p, 2);
+        return u;
+    }
+    uint32_t u;
+    __builtin_memcpy(&u, p, 4);
+    return u;
+}
+template <int T>
+SSD_DEVICE float delta_value(uint32_t raw) { return u2f(T == kBF16 ? raw << 16 : raw); }
+
 template <int T>
 SSD_DEVICE float delta_load(const typename DeltaElem<T>::type *p)
 {
@@ -861,7 +878,7 @@ SSD_KERNEL(128) void delta_long_kernel(DeltaParams p)
         if (init && live)
             state_load<KP>(S, init + bh * p.Dk * p.Dv + dv, p.Dk, p.Dv);
         const E *vrow = (const E *)p.v + row * p.v_stride + hv * p.Dv + (live ? dv : 0);
-        float V[16];
+        uint32_t V[16];
         v4f since[4], beta[4], left[4];
         float whole = 0.f;
         Parts<IN> kr[AHEAD ? 4 * KP : 1];
@@ -882,12 +899,12 @@ SSD_KERNEL(128) void delta_long_kernel(DeltaParams p)
             if (n == 64) {
 #pragma unroll
                 for (int e = 0; e < 16; ++e)
-                    V[e] = delta_load<T>((const E *)(v + (first + (uint32_t)(32 * (e >> 3) + (e & 7)) * step)));
+                    V[e] = delta_raw<T>((const E *)(v + (first + (uint32_t)(32 * (e >> 3) + (e & 7)) * step)));
             } else {
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
                     const int t = 32 * (e >> 3) + (e & 7);
-                    V[e] = delta_load<T>((const E *)(v + (uint32_t)(q8 < n - t ? q8 + t : n - 1) * step));
+                    V[e] = delta_raw<T>((const E *)(v + (uint32_t)(q8 < n - t ? q8 + t : n - 1) * step));
                 }
             }
         };
@@ -927,7 +944,7 @@ SSD_KERNEL(128) void delta_long_kernel(DeltaParams p)
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const int e = 4 * (h & 1) + r;
-                    const float x = live && q8 < n - (32 * (h >> 1) + e) ? V[8 * (h >> 1) + e] : 0.f;
+                    const float x = live && q8 < n - (32 * (h >> 1) + e) ? delta_value<T>(V[8 * (h >> 1) + e]) : 0.f;
                     R[h >> 1][e] = beta[h][r] * (x - since[h][r] * ks[r]);
                 }
             }
@@ -1102,7 +1119,8 @@ SSD_KERNEL(256) void delta_few_kernel(DeltaParams p)
     // the next token's values are on their way while one is gone through; loads go to places that exist
     const int64_t o_stride = (int64_t)p.Hv * p.Dv;
     const int cols = left < 0 ? 0 : left < 4 ? left : 4;
-    float nk[ROWS], nq[ROWS], nv[4], ng, nbeta;
+    uint32_t nk[ROWS], nq[ROWS], nv[4];
+    float ng, nbeta;
     auto fetch = [&](int t) {
         const int64_t token = (int64_t)b * p.T + t;
         const E *q = (const E *)p.q + token * p.q_stride + hk * p.Dk, *k = (const E *)p.k + token * p.k_stride + hk * p.Dk;
@@ -1112,12 +1130,12 @@ SSD_KERNEL(256) void delta_few_kernel(DeltaParams p)
 #pragma unroll
         for (int i = 0; i < ROWS; ++i) {
             const int f = r + 16 * i < p.Dk ? r + 16 * i : p.Dk - 1;
-            nk[i] = delta_load<T>(k + f);
-            nq[i] = delta_load<T>(q + f);
+            nk[i] = delta_raw<T>(k + f);
+            nq[i] = delta_raw<T>(q + f);
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-            nv[e] = delta_load<T>(v + (e < cols ? dv + e : 0));
+            nv[e] = delta_raw<T>(v + (e < cols ? dv + e : 0));
     };
     if (length > 0)
         fetch(0);
@@ -1129,13 +1147,13 @@ SSD_KERNEL(256) void delta_few_kernel(DeltaParams p)
             const float a = delta_exp(delta_log2(ng)), beta = nbeta;
 #pragma unroll
             for (int i = 0; i < ROWS; ++i) {
-                kr[i] = r + 16 * i < p.Dk ? nk[i] : 0.f;
-                qr[i] = r + 16 * i < p.Dk ? nq[i] : 0.f;
+                kr[i] = r + 16 * i < p.Dk ? delta_value<T>(nk[i]) : 0.f;
+                qr[i] = r + 16 * i < p.Dk ? delta_value<T>(nq[i]) : 0.f;
             }
             float x[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                x[e] = e < cols ? nv[e] : 0.f;
+                x[e] = e < cols ? delta_value<T>(nv[e]) : 0.f;
             if (t + 1 < length)
                 fetch(t + 1);
 #pragma unroll
@@ -1386,7 +1404,7 @@ SSD_KERNEL(64) void delta_long_bwd_kernel(DeltaParams p)
     if (init && live)
         state_load<KP>(S, init + bh * p.Dk * p.Dv + dv, p.Dk, p.Dv);
     const E *orow = (const E *)p.go + (int64_t)b * p.T * o_stride + hv * p.Dv + (live ? dv : 0);
-    float G[2][8];
+    uint32_t raw[16];
     v4f since[4], beta[4], left[4];
     float whole = 0.f;
     Parts<IN> kr[AHEAD ? 4 * KP : 1];
@@ -1407,12 +1425,12 @@ SSD_KERNEL(64) void delta_long_bwd_kernel(DeltaParams p)
         if (n == 64) {
 #pragma unroll
             for (int e = 0; e < 16; ++e)
-                G[e >> 3][e & 7] = delta_load<T>((const E *)(o + (first + (uint32_t)(32 * (e >> 3) + (e & 7)) * step)));
+                raw[e] = delta_raw<T>((const E *)(o + (first + (uint32_t)(32 * (e >> 3) + (e & 7)) * step)));
         } else {
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
                 const int t = 32 * (e >> 3) + (e & 7);
-                G[e >> 3][e & 7] = delta_load<T>((const E *)(o + (uint32_t)(q8 < n - t ? q8 + t : n - 1) * step));
+                raw[e] = delta_raw<T>((const E *)(o + (uint32_t)(q8 < n - t ? q8 + t : n - 1) * step));
             }
         }
     };
@@ -1435,11 +1453,12 @@ SSD_KERNEL(64) void delta_long_bwd_kernel(DeltaParams p)
         for (int s = 0; s < KP; ++s)
             Sp[s] = split_tiles<kParts>(S[2 * s], S[2 * s + 1]);
         Parts<IN> go[2];
+        float G[2][8];
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-                G[s][e] = live && q8 < n - (32 * s + e) ? G[s][e] : 0.f;
+                G[s][e] = live && q8 < n - (32 * s + e) ? delta_value<T>(raw[8 * s + e]) : 0.f;
             go[s] = split8<IN>(G[s]);
         }
         // dU
@@ -1720,6 +1739,7 @@ SSD_KERNEL_WAVES(256, (KP <= 2 && !MANY ? 2 : 1)) void delta_grad_kernel(DeltaPa
     float dot = 0.f;
     // the first columns' values are on their way while the triangle is made
     v4f s[2 * KP];
+    uint32_t vraw[2][8];
     float R[2][8], by[2][8];
     auto fetch_columns = [&](int col) {
         const int dv = col + 16 * wave + l;
@@ -1729,7 +1749,7 @@ SSD_KERNEL_WAVES(256, (KP <= 2 && !MANY ? 2 : 1)) void delta_grad_kernel(DeltaPa
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const int t = q8 < n - (32 * h + e) ? q8 + (32 * h + e) : n - 1;
-                R[h][e] = delta_load<T>(v + (uint32_t)t * (uint32_t)p.v_stride + (dv < p.Dv ? dv : col));
+                vraw[h][e] = delta_raw<T>(v + (uint32_t)t * (uint32_t)p.v_stride + (dv < p.Dv ? dv : col));
                 by[h][e] = gr[(uint32_t)(q8 + (32 * h + e)) * (uint32_t)p.Dv + (dv < p.Dv ? dv : col)];
             }
     };
@@ -1773,7 +1793,7 @@ SSD_KERNEL_WAVES(256, (KP <= 2 && !MANY ? 2 : 1)) void delta_grad_kernel(DeltaPa
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const int e = 4 * (h & 1) + r;
-                    const float x = live && q8 < n - (32 * (h >> 1) + e) ? R[h >> 1][e] : 0.f;
+                    const float x = live && q8 < n - (32 * (h >> 1) + e) ? delta_value<T>(vraw[h >> 1][e]) : 0.f;
                     const float read = x - since[r] * ks[r];
                     R[h >> 1][e] = live ? beta[r] * read : 0.f;
                     by[h >> 1][e] = live ? by[h >> 1][e] * read : 0.f;
