@@ -511,19 +511,41 @@ SSD_DEVICE void state_store(const v4f (&S)[2 * KP], float *to, int Dk, int Dv)
                 *(float *)(at + (off + (uint32_t)state_at(i, r) * step)) = S[i][r];
 }
 template <int KP>
-SSD_DEVICE void state_load(v4f (&S)[2 * KP], const float *from, int Dk, int Dv)
+SSD_DEVICE void state_fetch(v4f (&S)[2 * KP], const float *from, int Dk, int Dv)
 {
     const int q8 = 8 * ((thread_id() & 63) >> 4);
+    if (Dk == 32 * KP) {
+        const uint32_t step = opaque_uniform((uint32_t)Dv * 4), off = opaque((uint32_t)q8 * step);
+#pragma unroll
+        for (int i = 0; i < 2 * KP; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                S[i][r] = *(const float *)((const char *)from + (off + (uint32_t)state_at(i, r) * step));
+        return;
+    }
 #pragma unroll
     for (int i = 0; i < 2 * KP; ++i)
 #pragma unroll
         for (int r = 0; r < 4; ++r)
             S[i][r] = from[(uint32_t)(q8 < Dk - state_at(i, r) ? q8 + state_at(i, r) : 0) * (uint32_t)Dv];
+}
+template <int KP>
+SSD_DEVICE void state_mask(v4f (&S)[2 * KP], int Dk)
+{
+    if (Dk == 32 * KP)
+        return;
+    const int q8 = 8 * ((thread_id() & 63) >> 4);
 #pragma unroll
     for (int i = 0; i < 2 * KP; ++i)
 #pragma unroll
         for (int r = 0; r < 4; ++r)
             S[i][r] = q8 < Dk - state_at(i, r) ? S[i][r] : 0.f;
+}
+template <int KP>
+SSD_DEVICE void state_load(v4f (&S)[2 * KP], const float *from, int Dk, int Dv)
+{
+    state_fetch<KP>(S, from, Dk, Dv);
+    state_mask<KP>(S, Dk);
 }
 
 // A workgroup takes 16 WAVES columns of a value head, a wave 16 of them: lane l the column l, and of 2 KP tiles
@@ -1618,29 +1640,50 @@ SSD_DEVICE Parts<kParts> grad_operand(const uint16_t *at)
     return r;
 }
 
-// Eight features of a token as an operand, from memory: those from `at` on, zeros from D on and where the
-// token is none.
+// Eight features of a token from `at` on, as they lie in memory; what lies past the D features, or belongs to no
+// token, is cleared as the values are used.
 template <int T>
-SSD_DEVICE void row_values(const typename DeltaElem<T>::type *p, int at, int D, bool in, float (&v)[8])
+SSD_DEVICE void row_load(Raw8<T> &raw, const typename DeltaElem<T>::type *p, int at, int D)
 {
     if (D % 8 == 0) {
-        Raw8<T> raw;
         __builtin_memcpy(&raw, p + (at < D ? at : 0), sizeof(raw));
-        unpack8<T>(raw, v);
     } else {
+        typename DeltaElem<T>::type v[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-            v[e] = delta_load<T>(p + (at + e < D ? at + e : 0));
+            v[e] = p[at + e < D ? at + e : 0];
+        __builtin_memcpy(&raw, v, sizeof(raw));
     }
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-        v[e] = in && at + e < D ? v[e] : 0.f;
 }
+// Whole: all lanes hold eight features of a token.
 template <int T>
-SSD_DEVICE Parts<DeltaElem<T>::parts> row_operand(const typename DeltaElem<T>::type *p, int at, int D, bool in)
+SSD_DEVICE void row_values(const Raw8<T> &raw, int at, int D, bool in, bool whole, float (&v)[8])
+{
+    unpack8<T>(raw, v);
+    if (!whole)
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            v[e] = in && at + e < D ? v[e] : 0.f;
+}
+SSD_DEVICE Parts<1> row_parts(const Raw8<kBF16> &raw)
+{
+    Parts<1> r;
+    r.p[0] = raw.w[0];
+    return r;
+}
+SSD_DEVICE Parts<3> row_parts(const Raw8<kF32> &raw)
 {
     float v[8];
-    row_values<T>(p, at, D, in, v);
+    unpack8<kF32>(raw, v);
+    return split8<3>(v);
+}
+template <int T>
+SSD_DEVICE Parts<DeltaElem<T>::parts> row_operand(const Raw8<T> &raw, int at, int D, bool in, bool whole)
+{
+    if (whole)
+        return row_parts(raw);
+    float v[8];
+    row_values<T>(raw, at, D, in, false, v);
     return split8<DeltaElem<T>::parts>(v);
 }
 
@@ -1743,7 +1786,7 @@ SSD_KERNEL_WAVES(256, (KP <= 2 && !MANY ? 2 : 1)) void delta_grad_kernel(DeltaPa
     float R[2][8], by[2][8];
     auto fetch_columns = [&](int col) {
         const int dv = col + 16 * wave + l;
-        state_load<KP>(s, S + (dv < p.Dv ? dv : col), p.Dk, p.Dv);
+        state_fetch<KP>(s, S + (dv < p.Dv ? dv : col), p.Dk, p.Dv);
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -1755,9 +1798,15 @@ SSD_KERNEL_WAVES(256, (KP <= 2 && !MANY ? 2 : 1)) void delta_grad_kernel(DeltaPa
     };
     Blocks<T, 32 * KP, 256> kb;
     blocks_load<T, 32 * KP, 256>(kb, k, (int)p.k_stride, p.Dk, n);
-    if (wave == 3)
-        delta_gates(lds.gates, p.g, p.beta, token * p.Hv + hv, p.Hv, n);
+    float g0 = 0.f, beta0 = 0.f;
+    if (wave == 3) {
+        const int64_t from = (token + (lane < n ? lane : n - 1)) * p.Hv + hv;
+        g0 = p.g[from];
+        beta0 = p.beta[from];
+    }
     fetch_columns(0);
+    if (wave == 3)
+        delta_gates_of(lds.gates, g0, beta0, n);
     E *const kt = Lds::KEEP ? lds.own_kt : lds.c.kt;
     blocks_store<T, 32 * KP, 256, true, Lds::KEEP>(kb, p.Dk, n, lds.k, kt);
     delta_clear_pairs(pairs, 256);
@@ -1778,6 +1827,7 @@ SSD_KERNEL_WAVES(256, (KP <= 2 && !MANY ? 2 : 1)) void delta_grad_kernel(DeltaPa
             const bool live = dv < p.Dv;
             if (MANY && col > 0)
                 fetch_columns(col);
+            state_mask<KP>(s, p.Dk);
             Parts<kParts> Sp[KP];
 #pragma unroll
             for (int i = 0; i < KP; ++i)
@@ -1841,17 +1891,17 @@ SSD_KERNEL_WAVES(256, (KP <= 2 && !MANY ? 2 : 1)) void delta_grad_kernel(DeltaPa
                 put(1, h, mm<kParts>(R1, frag_operand<kParts>(tri, frag_of(1, h, 1)), v4f{0.f, 0.f, 0.f, 0.f}));
         }
         // dO of the own token and of those after, on its way
-        Parts<IN> oo[2], ao[2][4];
+        const bool whole = n == 64 && cols >= 64;
+        Raw8<T> oo[2], ao[2][4];
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-            oo[t] = row_operand<T>(go + (uint32_t)(valid ? own : 0) * (uint32_t)o_stride + col, 32 * t + q8, cols, valid);
+            row_load<T>(oo[t], go + (uint32_t)(valid ? own : 0) * (uint32_t)o_stride + col, 32 * t + q8, cols);
             if (Lds::KEEP)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     if ((i >> 1) >= (wave >> 1)) {
                         const int row = 32 * (i >> 1) + tile_row(i & 1, l);
-                        ao[t][i] = row_operand<T>(go + (uint32_t)(row < n ? row : 0) * (uint32_t)o_stride + col, 32 * t + q8,
-                                                  cols, row < n);
+                        row_load<T>(ao[t][i], go + (uint32_t)(row < n ? row : 0) * (uint32_t)o_stride + col, 32 * t + q8, cols);
                     }
         }
         // dR, and dV = beta dR
@@ -1873,10 +1923,14 @@ SSD_KERNEL_WAVES(256, (KP <= 2 && !MANY ? 2 : 1)) void delta_grad_kernel(DeltaPa
             }
         }
         block_sync();
-        // over the tokens
+        // over the tokens; the state's first columns on their way
+        GradBlocks<32 * KP, SW / 8> ds, dg;
+        grad_load<32 * KP, SW / 8>(ds, S + col, p.Dv, p.Dk, cols);
+        Parts<IN> op[2];
         Parts<kParts> ro[2], uo[2];
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
+            op[t] = row_operand<T>(oo[t], 32 * t + q8, cols, valid, whole);
             ro[t] = grad_operand<64, kGradStride>(lds.a.r + own * kGradStride + q8 + 32 * t);
             uo[t] = grad_operand<64, kGradStride>(lds.a.u + own * kGradStride + q8 + 32 * t);
         }
@@ -1888,15 +1942,14 @@ SSD_KERNEL_WAVES(256, (KP <= 2 && !MANY ? 2 : 1)) void delta_grad_kernel(DeltaPa
                 const int at0 = (32 * (i >> 1) + 4 * (i & 1)) * kGradStride + 32 * t;
                 if ((i >> 1) <= (wave >> 1)) {  // rows j up to the own token i
                     const Parts<kParts> u = grad_operand<64, kGradStride>(ul + at0);
-                    m1t[i] = mm<kParts>(u, oo[t], m1t[i]);
+                    m1t[i] = mm<kParts>(u, op[t], m1t[i]);
                     m2t[i] = mm<kParts>(u, ro[t], m2t[i]);
                 }
                 if ((i >> 1) >= (wave >> 1)) {  // rows i from the own token j on
                     const int row = 32 * (i >> 1) + tile_row(i & 1, l);
                     if (!Lds::KEEP)  // float32 rows would fill the registers
-                        ao[t][i] = row_operand<T>(go + (uint32_t)(row < n ? row : 0) * (uint32_t)o_stride + col, 32 * t + q8,
-                                                  cols, row < n);
-                    m1[i] = mm<kParts>(ao[t][i], uo[t], m1[i]);
+                        row_load<T>(ao[t][i], go + (uint32_t)(row < n ? row : 0) * (uint32_t)o_stride + col, 32 * t + q8, cols);
+                    m1[i] = mm<kParts>(row_operand<T>(ao[t][i], 32 * t + q8, cols, row < n, whole), uo[t], m1[i]);
                     m2[i] = mm<kParts>(grad_operand<64, kGradStride>(rl + at0), uo[t], m2[i]);
                 }
             }
@@ -1905,8 +1958,8 @@ SSD_KERNEL_WAVES(256, (KP <= 2 && !MANY ? 2 : 1)) void delta_grad_kernel(DeltaPa
         for (int c0 = 0; c0 < 64; c0 += SW) {
             if (c0 >= cols)
                 break;
-            GradBlocks<32 * KP, SW / 8> ds, dg;
-            grad_load<32 * KP, SW / 8>(ds, S + col + c0, p.Dv, p.Dk, cols - c0);
+            if (c0 > 0)
+                grad_load<32 * KP, SW / 8>(ds, S + col + c0, p.Dv, p.Dk, cols - c0);
             grad_load<32 * KP, SW / 8>(dg, gs + col + c0, p.Dv, p.Dk, cols - c0);
             block_sync();  // U and dR, or the columns before, have been read
             grad_clear<32 * KP, SW / 8>(ds, p.Dk, cols - c0);
@@ -1926,7 +1979,7 @@ SSD_KERNEL_WAVES(256, (KP <= 2 && !MANY ? 2 : 1)) void delta_grad_kernel(DeltaPa
                 for (int i = 0; i < 2 * KP; ++i) {
                     const int t0 = c0 / 32 + t, at0 = state_at(i, 0) * SS + 32 * t;
                     const Parts<kParts> s = grad_operand<32 * KP, SS>(sl + at0);
-                    aq[i] = mm<kParts>(s, oo[t0], aq[i]);
+                    aq[i] = mm<kParts>(s, op[t0], aq[i]);
                     reads[i] = mm<kParts>(s, ro[t0], reads[i]);
                     writes[i] = mm<kParts>(grad_operand<32 * KP, SS>(gsl + at0), uo[t0], writes[i]);
                 }
@@ -1937,10 +1990,10 @@ SSD_KERNEL_WAVES(256, (KP <= 2 && !MANY ? 2 : 1)) void delta_grad_kernel(DeltaPa
     dot = wave_sum(dot);
     Blocks<T, 32 * KP, 256> qb;
     blocks_load<T, 32 * KP, 256>(qb, q, (int)p.q_stride, p.Dk, n);
-    float qo[KP][8];
+    Raw8<T> qo[KP];
 #pragma unroll
     for (int s = 0; s < KP; ++s)
-        row_values<T>(q + (uint32_t)(valid ? own : 0) * (uint32_t)p.q_stride, 32 * s + q8, p.Dk, valid, qo[s]);
+        row_load<T>(qo[s], q + (uint32_t)(valid ? own : 0) * (uint32_t)p.q_stride, 32 * s + q8, p.Dk);
     if (!Lds::KEEP)
         blocks_load<T, 32 * KP, 256>(kb, k, (int)p.k_stride, p.Dk, n);
     block_sync();
@@ -2028,10 +2081,11 @@ SSD_KERNEL_WAVES(256, (KP <= 2 && !MANY ? 2 : 1)) void delta_grad_kernel(DeltaPa
         float x[8], y[8];
         const int f = 32 * s + q8;
         lds_values<T>(lds.k + own * RS + f, y);
+        row_values<T>(qo[s], f, p.Dk, valid, n == 64 && p.Dk == 32 * KP, x);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             const int i = 2 * s + (e >> 2), r = e & 3;
-            dots = __builtin_fmaf(qo[s][e], aq[i][r], dots);
+            dots = __builtin_fmaf(x[e], aq[i][r], dots);
             dots = __builtin_fmaf(y[e], reads[i][r] - writes[i][r], dots);
             x[e] = aq[i][r];
             y[e] = reads[i][r] + writes[i][r];
