@@ -903,14 +903,14 @@ SSD_KERNEL(128) void delta_long_kernel(DeltaParams p)
         uint32_t V[16];
         v4f since[4], beta[4], left[4];
         float whole = 0.f;
-        Parts<IN> kr[AHEAD ? 4 * KP : 1];
+        Parts<IN> kr[AHEAD ? 4 * KP : 2 * KP];
         auto fetch = [&](int chunk) {
             const v4u *at = pack + (int64_t)(chunk - p.chunk_from) * Pack::size;
             const float *g = (const float *)(at - lane + Pack::gates);
             if (AHEAD)
 #pragma unroll
                 for (int i = 0; i < 4 * KP; ++i)
-                    pack_load(kr[AHEAD ? i : 0], at + Pack::kr + i * IN * 64);
+                    pack_load(kr[AHEAD ? i : i % KP], at + Pack::kr + i * IN * 64);
             pack_gate(since, g, q8);
             pack_gate(left, g + 64, q8);
             pack_gate(beta, g + 128, q8);
@@ -941,6 +941,10 @@ SSD_KERNEL(128) void delta_long_kernel(DeltaParams p)
             const int n = delta_chunk_tokens(length, chunk);
             Parts<kParts> tri[kDeltaFrags];
             Parts<IN> kt[4 * KP];
+            if (!AHEAD)
+#pragma unroll
+                for (int f = 0; f < KP; ++f)
+                    pack_load(kr[f], at + Pack::kr + f * IN * 64);
 #pragma unroll
             for (int f = 0; f < kDeltaFrags; ++f)
                 pack_load_frag(tri[f], at + Pack::tri, f);
@@ -957,12 +961,13 @@ SSD_KERNEL(128) void delta_long_kernel(DeltaParams p)
 #pragma unroll
             for (int h = 0; h < 4; ++h) {
                 v4f ks = {0.f, 0.f, 0.f, 0.f};
+                if (!AHEAD && h < 3)
 #pragma unroll
-                for (int f = 0; f < KP; ++f) {
-                    if (!AHEAD)
-                        pack_load(kr[0], at + Pack::kr + (h * KP + f) * IN * 64);
-                    ks = mm<kParts>(kr[AHEAD ? h * KP + f : 0], Sp[f], ks);
-                }
+                    for (int f = 0; f < KP; ++f)
+                        pack_load(kr[(h + 1) % 2 * KP + f], at + Pack::kr + ((h + 1) * KP + f) * IN * 64);
+#pragma unroll
+                for (int f = 0; f < KP; ++f)
+                    ks = mm<kParts>(kr[AHEAD ? h * KP + f : h % 2 * KP + f], Sp[f], ks);
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const int e = 4 * (h & 1) + r;
@@ -1429,14 +1434,14 @@ SSD_KERNEL(64) void delta_long_bwd_kernel(DeltaParams p)
     uint32_t raw[16];
     v4f since[4], beta[4], left[4];
     float whole = 0.f;
-    Parts<IN> kr[AHEAD ? 4 * KP : 1];
+    Parts<IN> kr[AHEAD ? 4 * KP : 2 * KP];
     auto fetch = [&](int chunk) {
         const v4u *at = pack + (int64_t)(chunk - p.chunk_from) * Pack::size;
         const float *g = (const float *)(at - lane + Pack::gates);
         if (AHEAD)
 #pragma unroll
             for (int i = 0; i < 4 * KP; ++i)
-                pack_load(kr[AHEAD ? i : 0], at + Pack::kr + i * IN * 64);
+                pack_load(kr[AHEAD ? i : i % KP], at + Pack::kr + i * IN * 64);
         pack_gate(since, g, q8);
         pack_gate(left, g + 64, q8);
         pack_gate(beta, g + 128, q8);
@@ -1463,6 +1468,10 @@ SSD_KERNEL(64) void delta_long_bwd_kernel(DeltaParams p)
         const int n = delta_chunk_tokens(length, chunk);
         const int64_t place = bh * p.chunks + chunk;
         Parts<kParts> tri[kDeltaFrags], pt[kDeltaFrags];
+        if (!AHEAD)
+#pragma unroll
+            for (int f = 0; f < KP; ++f)
+                pack_load(kr[f], at + Pack::kr + f * IN * 64);
 #pragma unroll
         for (int f = 0; f < kDeltaFrags; ++f) {
             pack_load_frag(tri[f], at + Pack::tri, f);
@@ -1488,12 +1497,13 @@ SSD_KERNEL(64) void delta_long_bwd_kernel(DeltaParams p)
 #pragma unroll
         for (int h = 0; h < 4; ++h) {
             v4f ks = {0.f, 0.f, 0.f, 0.f};
+            if (!AHEAD && h < 3)
 #pragma unroll
-            for (int f = 0; f < KP; ++f) {
-                if (!AHEAD)
-                    pack_load(kr[0], at + Pack::kr + (h * KP + f) * IN * 64);
-                ks = mm<kParts>(kr[AHEAD ? h * KP + f : 0], Sp[f], ks);
-            }
+                for (int f = 0; f < KP; ++f)
+                    pack_load(kr[(h + 1) % 2 * KP + f], at + Pack::kr + ((h + 1) * KP + f) * IN * 64);
+#pragma unroll
+            for (int f = 0; f < KP; ++f)
+                ks = mm<kParts>(kr[AHEAD ? h * KP + f : h % 2 * KP + f], Sp[f], ks);
             v4f c;
 #pragma unroll
             for (int r = 0; r < 4; ++r)
@@ -1505,6 +1515,17 @@ SSD_KERNEL(64) void delta_long_bwd_kernel(DeltaParams p)
             for (int r = 0; r < 4; ++r)
                 dU[h >> 1][4 * (h & 1) + r] = c[r];
         }
+        // by features: two tiles at a time, the next on their way
+        Parts<IN> kt[2][2], qt[2][2];
+        auto features = [&](int i) {
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                pack_load(qt[i & 1][s], at + Pack::q + (2 * i + s) * IN * 64);
+                pack_load(kt[i & 1][s], at + Pack::kt + (2 * i + s) * IN * 64);
+            }
+        };
+        features(0);
+        features(1);
         // dR
         v4f dR[4];
         const Parts<kParts> u1 = split8<kParts>(dU[1]);
@@ -1557,13 +1578,12 @@ SSD_KERNEL(64) void delta_long_bwd_kernel(DeltaParams p)
                 c[r] = hold * S[i][r];
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
-                Parts<IN> kt, qt;
-                pack_load(qt, at + Pack::q + (2 * i + s) * IN * 64);
-                pack_load(kt, at + Pack::kt + (2 * i + s) * IN * 64);
-                c = mm<kParts>(qt, X[s], c);
-                c = mm<kParts>(kt, W[s], c);
+                c = mm<kParts>(qt[i & 1][s], X[s], c);
+                c = mm<kParts>(kt[i & 1][s], W[s], c);
             }
             S[i] = c;
+            if (i + 2 < 2 * KP)
+                features(i + 2);
         }
     }
     float *out = p.chunk_from > 0 ? p.carry : p.ginit;
