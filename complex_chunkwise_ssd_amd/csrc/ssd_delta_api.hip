@@ -33,7 +33,7 @@ int check_delta(const DeltaSizes &z, int dtype, float scale)
         return SSD_ERR_UNSUPPORTED;
     if (z.Hv % z.Hk != 0)
         return SSD_ERR_SHAPE;
-    const int64_t column_blocks = (z.Dv + 63) / 64;
+    const int64_t column_blocks = z.Dv <= 64 ? 1 : (z.Dv + 127) / 128 * 2;  // of 256 threads: the walks take up to 512
     const int64_t most = column_blocks > z.chunks() ? column_blocks : z.chunks();
     return grid_ok(z.B * z.Hv * most, 256) ? SSD_OK : SSD_ERR_UNSUPPORTED;
 }

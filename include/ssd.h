@@ -599,8 +599,9 @@ int ssd_fp8_matmul(const uint8_t *a, int64_t a_stride, const float *a_scale, con
  * place. Alignment: the element size. batch equal to 0 is a no-op; T equal to 0
  * copies the initial state (or zeros) into final_state.
  * SSD_ERR_BLOCK_DIMS: Dk above 128 or Dv above 256. SSD_ERR_UNSUPPORTED: T above 2^30,
- * batch above 2^24, heads above 2^16, a stride that makes an operand longer than 2^40, or
- * batch * Hv * max(ceil(T / 64), ceil(Dv / 64)) from 2^24 on.
+ * batch above 2^24, heads above 2^16, a stride or Hv Dv above 2^23, a stride that makes an
+ * operand longer than 2^40, or batch * Hv * max(ceil(T / 64), c) from 2^24 on, where c is 1 for
+ * Dv up to 64 and 2 ceil(Dv / 128) beyond.
  */
 size_t ssd_gated_delta_workspace_bytes(int64_t batch, int64_t T, int64_t Hk, int64_t Hv,
                                        int64_t Dk, int64_t Dv, int dtype);

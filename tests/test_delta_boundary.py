@@ -131,3 +131,12 @@ def test_token_strides():
 def test_chunk_matches_the_header():
     text = open(ssd.HEADER).read()
     assert "#define SSD_DELTA_CHUNK %d" % ssd.DELTA_CHUNK in text
+
+
+@pytest.mark.parametrize("call", [_fwd, _bwd])
+def test_launches_of_2_to_the_32_threads(lib, call):
+    # 129 to 192 columns are walked in two blocks of 512 threads: 2^22 heads are 2^32 threads, one less is not refused
+    # for its size (and stopped by the missing q)
+    wide = dict(T=9, Hk=1, Hv=1, Dk=65, Dv=129, qs=65, ks=65, vs=129, q=None)
+    assert call(lib, B=1 << 22, **wide) == ssd.SSD_ERR_UNSUPPORTED
+    assert call(lib, B=(1 << 22) - 1, **wide) == ssd.SSD_ERR_NULL
