@@ -152,10 +152,15 @@ int launch_delta_long(ssd::DeltaParams p, const DeltaRange &range, char *workspa
         if (int st = launch_status())
             return st;
         const dim3 grid((unsigned)((heads + 7) / 8 * 8 * p.columns));
-        if (BACKWARD)
-            hipLaunchKernelGGL((ssd::delta_long_bwd_kernel<T, KP>), grid, dim3(64), 0, s, p);
-        else
+        if constexpr (BACKWARD) {
+            hipLaunchKernelGGL((ssd::delta_spans_bwd_kernel<T, KP>), grid, dim3(64 * KP), 0, s, p);
+        } else if constexpr (T == ssd::kBF16) {
             hipLaunchKernelGGL((ssd::delta_long_kernel<T, KP>), grid, dim3(128), 0, s, p);
+        } else if (KP == 2 || heads * p.columns <= ssd::kSpansMost) {
+            hipLaunchKernelGGL((ssd::delta_spans_kernel<T, KP>), grid, dim3(64 * KP), 0, s, p);
+        } else {
+            hipLaunchKernelGGL((ssd::delta_long_kernel<T, 4>), grid, dim3(128), 0, s, p);
+        }
         if (int st = launch_status())
             return st;
     }

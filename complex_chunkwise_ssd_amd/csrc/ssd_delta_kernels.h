@@ -548,6 +548,39 @@ SSD_DEVICE void state_load(v4f (&S)[2 * KP], const float *from, int Dk, int Dv)
     state_mask<KP>(S, Dk);
 }
 
+// Waits for a state that is loaded before a walk. Without it the compiler, which counts loads in their order, would wait
+// in every chunk as if the state were what was loaded last, and so for all that is on its way to the next one.
+template <int N>
+SSD_DEVICE void state_arrived(v4f (&S)[N])
+{
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; r += 2) {
+            float a = S[i][r], b = S[i][r + 1];
+            together(a, b);
+            S[i][r] = a;
+            S[i][r + 1] = b;
+        }
+}
+
+// c += x, span f's share of K S. In float32 all forms of the forward walk sum it span by span, as the one that deals the
+// spans out to waves has to: a sequence's results are the same bits in a large batch and alone.
+SSD_DEVICE void span_add(v4f &c, v4f x, int f)
+{
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+        c[r] = f == 0 ? x[r] : c[r] + x[r];
+}
+template <int T, int N>
+SSD_DEVICE void span_mm(v4f &c, const Parts<N> &a, const Parts<kParts> &b, int f)
+{
+    if (T == kF32)
+        span_add(c, mm<kParts>(a, b, v4f{0.f, 0.f, 0.f, 0.f}), f);
+    else
+        c = mm<kParts>(a, b, c);
+}
+
 // A workgroup takes 16 WAVES columns of a value head, a wave 16 of them: lane l the column l, and of 2 KP tiles
 // the features 32 s + 8 q + 4 h + r of the state. The chunk's triangle and P are made by all of them; while two
 // waves solve the blocks of 32, the others go on with what the state gives. The next chunk's rows are in
@@ -661,7 +694,7 @@ SSD_KERNEL_WAVES(64 * WAVES, (WAVES == 8 || (T == kBF16 && KP <= 2) ? 2 : 1)) vo
                 v4f ks = {0.f, 0.f, 0.f, 0.f}, qs = ks;
 #pragma unroll
                 for (int f = 0; f < KP; ++f) {
-                    ks = mm<kParts>(lds_operand(kl + ((32 * s + 4 * h) * RS + 32 * f)), Sp[f], ks);
+                    span_mm<T>(ks, lds_operand(kl + ((32 * s + 4 * h) * RS + 32 * f)), Sp[f], f);
                     qs = mm<OUT>(lds_operand(ql + ((32 * s + 4 * h) * RS + 32 * f)), Sp[f], qs);
                 }
                 const v4f since = *(const v4f *)(gates.since + q8 + (32 * s + 4 * h));
@@ -899,6 +932,7 @@ SSD_KERNEL(128) void delta_long_kernel(DeltaParams p)
         const float *init = p.chunk_from > 0 ? p.carry : p.init;
         if (init && live)
             state_load<KP>(S, init + bh * p.Dk * p.Dv + dv, p.Dk, p.Dv);
+        state_arrived(S);
         const E *vrow = (const E *)p.v + row * p.v_stride + hv * p.Dv + (live ? dv : 0);
         uint32_t V[16];
         v4f since[4], beta[4], left[4];
@@ -967,7 +1001,7 @@ SSD_KERNEL(128) void delta_long_kernel(DeltaParams p)
                         pack_load(kr[(h + 1) % 2 * KP + f], at + Pack::kr + ((h + 1) * KP + f) * IN * 64);
 #pragma unroll
                 for (int f = 0; f < KP; ++f)
-                    ks = mm<kParts>(kr[AHEAD ? h * KP + f : h % 2 * KP + f], Sp[f], ks);
+                    span_mm<T>(ks, kr[AHEAD ? h * KP + f : h % 2 * KP + f], Sp[f], f);
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const int e = 4 * (h & 1) + r;
@@ -1085,6 +1119,266 @@ SSD_KERNEL(128) void delta_long_kernel(DeltaParams p)
             }
         }
     }
+}
+
+// The same in float32, whose operands have three parts and whose products six terms: a wave for each span of 32
+// features of the state, which sums its share of K S and updates its own rows; the shares meet in shared
+// memory, every wave solves for U, and each makes some of the outputs' tiles. Operands are loaded a chunk
+// ahead, into the registers that the last ones leave. A chunk is a chain of dependent products and their splitting
+// into parts, some 3 us of it whatever the width; one wave with all features takes 4 to 6 (T 2048, us, this form / the
+// other: 16 heads of 64 146 / 186, 96 heads 333 / 370, 32 heads of 128 262 / 376). With up to 64 features it is
+// always taken; with more, its four waves have a compute unit to themselves, and where there are more workgroups
+// than units the other form is as fast or faster (48 heads of 128: 473 / 421). In bfloat16, where K, and the products
+// of K, have a third of the parts, it gains 5 % with 64 features and loses 14 % with 128: not taken.
+constexpr int kSpansMost = 256;  // workgroups
+
+// Operands at a place that is the same for all lanes, so that its address is scalar work.
+template <int N>
+SSD_DEVICE void span_load(Parts<N> &x, const v4u *from, int apart = 1)
+{
+    const uint32_t off = 16 * ((uint32_t)thread_id() & 63);
+#pragma unroll
+    for (int e = 0; e < N; ++e)
+        x.p[e] = *(const v4u *)((const char *)(from + e * apart * 64) + off);
+}
+template <int N>
+SSD_DEVICE void span_load_frag(Parts<N> &x, const v4u *from, int f) { span_load(x, from + f * 64, kDeltaFrags); }
+SSD_DEVICE v4f span_gate(const float *from, int t)
+{
+    return *(const v4f *)((const char *)(from + t) + 32 * (((uint32_t)thread_id() & 63) >> 4));
+}
+SSD_DEVICE void span_gates(v4f (&g)[4], const float *from)
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        g[i] = span_gate(from, 32 * (i >> 1) + 4 * (i & 1));
+}
+
+template <int KP>
+struct Spans {
+    static constexpr int own = 4 / KP;    // tiles of 16 tokens that a wave makes outputs of
+    // a wave's first feature (or 0, if there is none), and how many it has
+    static SSD_DEVICE int first(int wave, int Dk) { return 32 * wave < Dk ? 32 * wave : 0; }
+    static SSD_DEVICE int many(int wave, int Dk) { return Dk - 32 * wave < 32 ? Dk - 32 * wave : 32; }
+};
+// The shares of tile h, added in the spans' order.
+template <int KP>
+SSD_DEVICE v4f spans_sum(const v4f (&share)[KP][4][64], int h, int lane)
+{
+    v4f c;
+#pragma unroll
+    for (int w = 0; w < KP; ++w)
+        span_add(c, share[w][h][lane], w);
+    return c;
+}
+
+template <int T, int KP>
+SSD_KERNEL(64 * KP) void delta_spans_kernel(DeltaParams p)
+{
+    typedef typename DeltaElem<T>::type E;
+    typedef DeltaPack<T, KP, false> Pack;
+    constexpr int IN = Pack::IN, OUT = Pack::OUT, OWN = Spans<KP>::own;
+    SSD_LDS v4f share[2][KP][4][64];
+    SSD_LDS v4u state[2][KP * OUT * 64];
+    int64_t bh;
+    int block;
+    long_place(p, bh, block);
+    if (bh >= (int64_t)p.B * p.Hv)
+        return;
+    const int hv = (int)(bh % p.Hv), b = (int)(bh / p.Hv);
+    const int lane = thread_id() & 63, l = lane & 15, q8 = 8 * (lane >> 4), wave = wave_id();
+    const int dv = 16 * block + l;
+    const bool live = dv < p.Dv;
+    const int length = delta_valid(p, b), range = p.chunk_to - p.chunk_from, o_stride = p.Hv * p.Dv;
+    const int64_t row = (int64_t)b * p.T;
+    const v4u *pack = p.pack + bh * range * Pack::size;
+    const int last = (length + kDeltaChunk - 1) / kDeltaChunk;  // chunks with tokens
+    const int to = last < p.chunk_to ? last : p.chunk_to;
+    const int first = Spans<KP>::first(wave, p.Dk), many = Spans<KP>::many(wave, p.Dk);
+    const int tile = OWN * wave, span = tile >> 1;  // of the outputs
+    const int64_t state_at0 = (int64_t)first * p.Dv + dv;
+    v4f S[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+    const float *init = p.chunk_from > 0 ? p.carry : p.init;
+    if (init && live)
+        state_load<1>(S, init + bh * p.Dk * p.Dv + state_at0, many, p.Dv);
+    state_arrived(S);
+    const E *vrow = (const E *)p.v + row * p.v_stride + hv * p.Dv + (live ? dv : 0);
+    uint32_t V[16];
+    v4f since[4], beta[4], left[4], mine[OWN];
+    float whole = 0.f;
+    Parts<IN> kr[4], kt[2][2], qr[OWN][KP];
+    Parts<kParts> tri[kDeltaFrags];
+    Parts<OUT> pf[OWN][2];
+    auto place = [&](int chunk) { return pack + (int64_t)(chunk - p.chunk_from) * Pack::size; };
+    auto fetch_rows = [&](const v4u *at) {
+#pragma unroll
+        for (int h = 0; h < 4; ++h)
+            span_load(kr[h], at + Pack::kr + (h * KP + wave) * IN * 64);
+    };
+    auto fetch_solve = [&](const v4u *at, int chunk) {
+        const float *g = (const float *)(at + Pack::gates);
+#pragma unroll
+        for (int f = 0; f < kDeltaFrags; ++f)
+            span_load_frag(tri[f], at + Pack::tri, f);
+        span_gates(since, g);
+        span_gates(left, g + 64);
+        span_gates(beta, g + 128);
+        whole = g[192];
+        const int n = delta_chunk_tokens(length, chunk);
+        const char *v = (const char *)(vrow + (int64_t)chunk * kDeltaChunk * p.v_stride);
+        const uint32_t step = opaque_uniform((uint32_t)p.v_stride * sizeof(E)), from = opaque((uint32_t)q8 * step);
+        if (n == 64) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+                V[e] = delta_raw<T>((const E *)(v + (from + (uint32_t)(32 * (e >> 3) + (e & 7)) * step)));
+        } else {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const int t = 32 * (e >> 3) + (e & 7);
+                V[e] = delta_raw<T>((const E *)(v + (uint32_t)(q8 < n - t ? q8 + t : n - 1) * step));
+            }
+        }
+    };
+    auto fetch_features = [&](const v4u *at) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+                span_load(kt[i][s], at + Pack::kt + (2 * (2 * wave + i) + s) * IN * 64);
+    };
+    auto fetch_outputs = [&](const v4u *at) {
+        const float *g = (const float *)(at + Pack::gates);
+#pragma unroll
+        for (int i = 0; i < OWN; ++i) {
+            const int h = (tile + i) & 1;
+#pragma unroll
+            for (int f = 0; f < KP; ++f)
+                span_load(qr[i][f], at + Pack::q + ((tile + i) * KP + f) * IN * 64);
+            span_load_frag(pf[i][0], at + Pack::pf, frag_of(span, h, 0));
+            span_load_frag(pf[i][1], at + Pack::pf, frag_of(span, h, span));
+            mine[i] = span_gate(g, 32 * span + 4 * h);
+        }
+    };
+    if (p.chunk_from < to) {
+        const v4u *at = place(p.chunk_from);
+        fetch_rows(at);  // in the order of the loop: what is waited for is what was loaded before
+        sched_fence();
+        fetch_solve(at, p.chunk_from);
+        fetch_features(at);
+        sched_fence();
+        fetch_outputs(at);
+    }
+    for (int chunk = p.chunk_from; chunk < p.chunk_to; ++chunk) {
+        if (p.states && live)
+            state_store<1>(S, p.states + (((int64_t)b * p.chunks + chunk) * p.Hv + hv) * p.Dk * p.Dv + state_at0, many, p.Dv);
+        const int rows = p.T - chunk * kDeltaChunk < 64 ? p.T - chunk * kDeltaChunk : 64;
+        E *o = (E *)p.o + (row + (int64_t)chunk * kDeltaChunk) * o_stride + hv * p.Dv + dv;
+        if (chunk >= to) {  // padding
+            if (live)
+                for (int t = 4 * wave + (q8 >> 3); t < rows; t += 4 * KP)
+                    delta_store<T>(o + (int64_t)t * o_stride, 0.f);
+            continue;
+        }
+        const int n = delta_chunk_tokens(length, chunk);
+        // after the last chunk its own operands once more: with branches around the loads the waits for
+        // them would be as long as if each were the only one taken
+        const int ahead = chunk + 1 < to ? chunk + 1 : chunk;
+        const v4u *next = place(ahead);
+        const Parts<kParts> Sp = split_tiles<kParts>(S[0], S[1]);
+#pragma unroll
+        for (int e = 0; e < OUT; ++e)
+            state[chunk & 1][(wave * OUT + e) * 64 + lane] = Sp.p[e];
+#pragma unroll
+        for (int h = 0; h < 4; ++h)
+            share[chunk & 1][wave][h][lane] = mm<kParts>(kr[h], Sp, v4f{0.f, 0.f, 0.f, 0.f});
+        fetch_rows(next);
+        sched_fence();
+        block_sync();  // one a chunk: the two halves of what is shared take turns
+        // R = beta (V - e^G K S)
+        float R[2][8];
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+            const v4f ks = spans_sum<KP>(share[chunk & 1], h, lane);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int e = 4 * (h & 1) + r;
+                const float x = live && q8 < n - (32 * (h >> 1) + e) ? delta_value<T>(V[8 * (h >> 1) + e]) : 0.f;
+                R[h >> 1][e] = beta[h][r] * (x - since[h][r] * ks[r]);
+            }
+        }
+        // U
+        const Parts<kParts> R0 = split8<kParts>(R[0]);
+        v4f U[4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            U[h] = mm<kParts>(tri[frag_of(0, h, 0)], R0, v4f{0.f, 0.f, 0.f, 0.f});
+        const Parts<kParts> U0 = split_tiles<kParts>(U[0], U[1]);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const v4f c = mm<kParts>(tri[frag_of(1, h, 0)], U0, v4f{0.f, 0.f, 0.f, 0.f});
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                R[1][4 * h + r] -= c[r];
+        }
+        const Parts<kParts> R1 = split8<kParts>(R[1]);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            U[2 + h] = mm<kParts>(tri[frag_of(1, h, 1)], R1, v4f{0.f, 0.f, 0.f, 0.f});
+        // the state
+        Parts<kParts> W[2];
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            float w[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                w[e] = left[2 * s + (e >> 2)][e & 3] * U[2 * s + (e >> 2)][e & 3];
+            W[s] = split8<kParts>(w);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            v4f c;
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                c[r] = whole * S[i][r];
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+                c = mm<kParts>(kt[i][s], W[s], c);
+            S[i] = c;
+        }
+        fetch_solve(next, ahead);
+        fetch_features(next);
+        sched_fence();
+        // the outputs
+        Parts<OUT> old[KP];
+#pragma unroll
+        for (int f = 0; f < KP; ++f)
+            pack_load(old[f], &state[chunk & 1][f * OUT * 64 + lane]);
+        const Parts<OUT> U1 = split_tiles<OUT>(U[2], U[3]);
+        const uint32_t step = opaque_uniform((uint32_t)o_stride * sizeof(E)), off = opaque((uint32_t)q8 * step);
+#pragma unroll
+        for (int i = 0; i < OWN; ++i) {
+            v4f c = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int f = 0; f < KP; ++f)
+                c = mm<OUT>(qr[i][f], old[f], c);
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                c[r] *= p.scale * mine[i][r];
+            c = mm<OUT>(pf[i][0], U0, c);
+            if (span == 1)
+                c = mm<OUT>(pf[i][1], U1, c);
+            const int t0 = 32 * span + 4 * ((tile + i) & 1);
+            if (live)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    if (q8 < rows - t0 - r)
+                        delta_store<T>((E *)((char *)o + (off + (uint32_t)(t0 + r) * step)), q8 < n - t0 - r ? c[r] : 0.f);
+        }
+        fetch_outputs(next);
+    }
+    float *out = p.chunk_to < p.chunks ? p.carry : p.final_state;
+    if (out && live)
+        state_store<1>(S, out + bh * p.Dk * p.Dv + state_at0, many, p.Dv);
 }
 
 // ------------------------------------------------------------ a few tokens on the state
@@ -1402,57 +1696,76 @@ SSD_KERNEL_WAVES(64 * WAVES, (WAVES == 8 || (T == kBF16 && KP <= 2) ? 2 : 1)) vo
         state_store<KP>(S, p.ginit + head + dv, p.Dk, p.Dv);
 }
 
-// The same with few heads: one wave a workgroup, on what delta_pack_kernel made.
+// The same with few heads: by spans of features, as delta_spans_kernel, on what delta_pack_kernel made. Here the walk
+// has twice the products, and one wave with all features was slower in both types (the gradients as a whole,
+// T 2048, us, this form / that: 16 heads of 128 in bfloat16 275 / 342, in float32 389 / 685; 96 heads, bfloat16
+// 1291 / 1210, float32 1889 / 2085).
 template <int T, int KP>
-SSD_KERNEL(64) void delta_long_bwd_kernel(DeltaParams p)
+SSD_KERNEL(64 * KP) void delta_spans_bwd_kernel(DeltaParams p)
 {
     typedef typename DeltaElem<T>::type E;
     typedef DeltaPack<T, KP, true> Pack;
-    constexpr int IN = Pack::IN;
-    constexpr bool AHEAD = T == kBF16;  // K's rows of the next chunk; in float32 there are too many
+    constexpr int IN = Pack::IN, OWN = Spans<KP>::own;
+    SSD_LDS v4f share[2][KP][4][64];
     int64_t bh;
     int block;
     long_place(p, bh, block);
     if (bh >= (int64_t)p.B * p.Hv)
         return;
     const int hv = (int)(bh % p.Hv), b = (int)(bh / p.Hv);
-    const int lane = thread_id() & 63, l = lane & 15, q8 = 8 * (lane >> 4);
+    const int lane = thread_id() & 63, l = lane & 15, q8 = 8 * (lane >> 4), wave = wave_id();
     const int dv = 16 * block + l;
     const bool live = dv < p.Dv;
     const int length = delta_valid(p, b), range = p.chunk_to - p.chunk_from, o_stride = p.Hv * p.Dv;
-    const v4u *pack = p.pack + bh * range * Pack::size + lane;
+    const v4u *pack = p.pack + bh * range * Pack::size;
     const int last = (length + kDeltaChunk - 1) / kDeltaChunk;  // chunks with tokens
     const int to = last < p.chunk_to ? last : p.chunk_to;
-    v4f S[2 * KP];  // the gradient of the state after the chunk
-#pragma unroll
-    for (int i = 0; i < 2 * KP; ++i)
-        S[i] = v4f{0.f, 0.f, 0.f, 0.f};
+    const int first = Spans<KP>::first(wave, p.Dk), many = Spans<KP>::many(wave, p.Dk);
+    const int tile = OWN * wave, span = tile >> 1;  // of P^T dO
+    const int64_t state_at0 = (int64_t)first * p.Dv + dv;
+    v4f S[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};  // the gradient of the state after the chunk
     const float *init = p.chunk_to < p.chunks ? p.carry : p.gfinal;
     if (init && live)
-        state_load<KP>(S, init + bh * p.Dk * p.Dv + dv, p.Dk, p.Dv);
+        state_load<1>(S, init + bh * p.Dk * p.Dv + state_at0, many, p.Dv);
+    state_arrived(S);
     const E *orow = (const E *)p.go + (int64_t)b * p.T * o_stride + hv * p.Dv + (live ? dv : 0);
     uint32_t raw[16];
     v4f since[4], beta[4], left[4];
     float whole = 0.f;
-    Parts<IN> kr[AHEAD ? 4 * KP : 2 * KP];
-    auto fetch = [&](int chunk) {
-        const v4u *at = pack + (int64_t)(chunk - p.chunk_from) * Pack::size;
-        const float *g = (const float *)(at - lane + Pack::gates);
-        if (AHEAD)
+    Parts<IN> kr[4], kt[2][2], qt[2][2];
+    Parts<kParts> tri[kDeltaFrags], pt[OWN][2];
+    auto place = [&](int chunk) { return pack + (int64_t)(chunk - p.chunk_from) * Pack::size; };
+    auto fetch_first = [&](const v4u *at) {
 #pragma unroll
-            for (int i = 0; i < 4 * KP; ++i)
-                pack_load(kr[AHEAD ? i : i % KP], at + Pack::kr + i * IN * 64);
-        pack_gate(since, g, q8);
-        pack_gate(left, g + 64, q8);
-        pack_gate(beta, g + 128, q8);
+        for (int h = 0; h < 4; ++h)
+            span_load(kr[h], at + Pack::kr + (h * KP + wave) * IN * 64);
+#pragma unroll
+        for (int i = 0; i < OWN; ++i) {
+            const int h = (tile + i) & 1;
+            span_load_frag(pt[i][0], at + Pack::pf, frag_of_upper(span, h, span));
+            span_load_frag(pt[i][1], at + Pack::pf, frag_of_upper(span, h, 1));
+        }
+    };
+    auto fetch_queries = [&](const v4u *at) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+                span_load(qt[i][s], at + Pack::q + (2 * (2 * wave + i) + s) * IN * 64);
+    };
+    auto fetch_rest = [&](const v4u *at, int chunk) {
+        const float *g = (const float *)(at + Pack::gates);
+        span_gates(since, g);
+        span_gates(left, g + 64);
+        span_gates(beta, g + 128);
         whole = g[192];
         const int n = delta_chunk_tokens(length, chunk);
         const char *o = (const char *)(orow + (int64_t)chunk * kDeltaChunk * o_stride);
-        const uint32_t step = opaque_uniform((uint32_t)o_stride * sizeof(E)), first = opaque((uint32_t)q8 * step);
+        const uint32_t step = opaque_uniform((uint32_t)o_stride * sizeof(E)), from = opaque((uint32_t)q8 * step);
         if (n == 64) {
 #pragma unroll
             for (int e = 0; e < 16; ++e)
-                raw[e] = delta_raw<T>((const E *)(o + (first + (uint32_t)(32 * (e >> 3) + (e & 7)) * step)));
+                raw[e] = delta_raw<T>((const E *)(o + (from + (uint32_t)(32 * (e >> 3) + (e & 7)) * step)));
         } else {
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
@@ -1460,29 +1773,31 @@ SSD_KERNEL(64) void delta_long_bwd_kernel(DeltaParams p)
                 raw[e] = delta_raw<T>((const E *)(o + (uint32_t)(q8 < n - t ? q8 + t : n - 1) * step));
             }
         }
+#pragma unroll
+        for (int f = 0; f < kDeltaFrags; ++f)
+            span_load_frag(tri[f], at + Pack::tri, f);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+                span_load(kt[i][s], at + Pack::kt + (2 * (2 * wave + i) + s) * IN * 64);
     };
-    if (p.chunk_from < to)
-        fetch(to - 1);
+    if (p.chunk_from < to) {
+        const v4u *at = place(to - 1);
+        fetch_first(at);  // in the order of the loop: what is waited for is what was loaded before
+        sched_fence();
+        fetch_queries(at);
+        sched_fence();
+        fetch_rest(at, to - 1);
+    }
     for (int chunk = to - 1; chunk >= p.chunk_from; --chunk) {
-        const v4u *at = pack + (int64_t)(chunk - p.chunk_from) * Pack::size;
         const int n = delta_chunk_tokens(length, chunk);
-        const int64_t place = bh * p.chunks + chunk;
-        Parts<kParts> tri[kDeltaFrags], pt[kDeltaFrags];
-        if (!AHEAD)
-#pragma unroll
-            for (int f = 0; f < KP; ++f)
-                pack_load(kr[f], at + Pack::kr + f * IN * 64);
-#pragma unroll
-        for (int f = 0; f < kDeltaFrags; ++f) {
-            pack_load_frag(tri[f], at + Pack::tri, f);
-            pack_load_frag(pt[f], at + Pack::pf, f);
-        }
+        const int ahead = chunk > p.chunk_from ? chunk - 1 : chunk;
+        const v4u *next = place(ahead);
+        const int64_t at = bh * p.chunks + chunk;
         if (live)
-            state_store<KP>(S, p.gs + place * p.Dk * p.Dv + dv, p.Dk, p.Dv);
-        Parts<kParts> Sp[KP];
-#pragma unroll
-        for (int s = 0; s < KP; ++s)
-            Sp[s] = split_tiles<kParts>(S[2 * s], S[2 * s + 1]);
+            state_store<1>(S, p.gs + at * p.Dk * p.Dv + state_at0, many, p.Dv);
+        const Parts<kParts> Sp = split_tiles<kParts>(S[0], S[1]);
         Parts<IN> go[2];
         float G[2][8];
 #pragma unroll
@@ -1492,40 +1807,49 @@ SSD_KERNEL(64) void delta_long_bwd_kernel(DeltaParams p)
                 G[s][e] = live && q8 < n - (32 * s + e) ? delta_value<T>(raw[8 * s + e]) : 0.f;
             go[s] = split8<IN>(G[s]);
         }
-        // dU
+        // the span's share of e^(G_C - G) K dS', and in some tiles all of P^T dO
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+            v4f c = mm<kParts>(kr[h], Sp, v4f{0.f, 0.f, 0.f, 0.f});
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                c[r] *= left[h][r];
+            if (h / OWN == wave) {
+                if (h < 2)
+                    c = mm<kParts>(pt[h % OWN][0], go[0], c);
+                c = mm<kParts>(pt[h % OWN][1], go[1], c);
+            }
+            share[chunk & 1][wave][h][lane] = c;
+        }
+        fetch_first(next);
+        sched_fence();
+        // what the state's gradient gets from the outputs
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                G[s][e] *= p.scale * since[2 * s + (e >> 2)][e & 3];
+            const Parts<kParts> X = split8<kParts>(G[s]);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                if (s == 0)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        S[i][r] *= whole;
+                S[i] = mm<kParts>(qt[i][s], X, S[i]);
+            }
+        }
+        fetch_queries(next);
+        sched_fence();
+        block_sync();  // one a chunk: the two halves of what is shared take turns
         float dU[2][8];
 #pragma unroll
         for (int h = 0; h < 4; ++h) {
-            v4f ks = {0.f, 0.f, 0.f, 0.f};
-            if (!AHEAD && h < 3)
-#pragma unroll
-                for (int f = 0; f < KP; ++f)
-                    pack_load(kr[(h + 1) % 2 * KP + f], at + Pack::kr + ((h + 1) * KP + f) * IN * 64);
-#pragma unroll
-            for (int f = 0; f < KP; ++f)
-                ks = mm<kParts>(kr[AHEAD ? h * KP + f : h % 2 * KP + f], Sp[f], ks);
-            v4f c;
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-                c[r] = left[h][r] * ks[r];
-#pragma unroll
-            for (int t = h >> 1; t < 2; ++t)
-                c = mm<kParts>(pt[frag_of_upper(h >> 1, h & 1, t)], go[t], c);
+            const v4f c = spans_sum<KP>(share[chunk & 1], h, lane);
 #pragma unroll
             for (int r = 0; r < 4; ++r)
                 dU[h >> 1][4 * (h & 1) + r] = c[r];
         }
-        // by features: two tiles at a time, the next on their way
-        Parts<IN> kt[2][2], qt[2][2];
-        auto features = [&](int i) {
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                pack_load(qt[i & 1][s], at + Pack::q + (2 * i + s) * IN * 64);
-                pack_load(kt[i & 1][s], at + Pack::kt + (2 * i + s) * IN * 64);
-            }
-        };
-        features(0);
-        features(1);
         // dR
         v4f dR[4];
         const Parts<kParts> u1 = split8<kParts>(dU[1]);
@@ -1546,49 +1870,33 @@ SSD_KERNEL(64) void delta_long_bwd_kernel(DeltaParams p)
             dR[h] = mm<kParts>(tri[frag_of_upper(0, h, 0)], u0, v4f{0.f, 0.f, 0.f, 0.f});
         if (live) {
             const uint32_t step = opaque_uniform((uint32_t)p.Dv * 4), off = opaque((uint32_t)q8 * step);
-            char *out = (char *)(p.gr + place * 64 * p.Dv + dv);
+            char *out = (char *)(p.gr + at * 64 * p.Dv + dv);
 #pragma unroll
-            for (int s = 0; s < 2; ++s)
+            for (int h = 0; h < 4; ++h)
+                if (h / OWN == wave)
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    *(float *)(out + (off + (32 * s + e) * step)) = dR[2 * s + (e >> 2)][e & 3];
+                    for (int r = 0; r < 4; ++r)
+                        *(float *)(out + (off + (32 * (h >> 1) + 4 * (h & 1) + r) * step)) = dR[h][r];
         }
         // the state's gradient before the chunk
-        Parts<kParts> W[2], X[2];
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-            float w[8], x[8];
+            float w[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const int h = 2 * s + (e >> 2), r = e & 3;
                 w[e] = -since[h][r] * beta[h][r] * dR[h][r];
-                x[e] = p.scale * since[h][r] * G[s][e];
             }
-            W[s] = split8<kParts>(w);
-            X[s] = split8<kParts>(x);
+            const Parts<kParts> W = split8<kParts>(w);
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                S[i] = mm<kParts>(kt[i][s], W, S[i]);
         }
-        const float hold = whole;
-        if (chunk > p.chunk_from)
-            fetch(chunk - 1);
-#pragma unroll
-        for (int i = 0; i < 2 * KP; ++i) {
-            v4f c;
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-                c[r] = hold * S[i][r];
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                c = mm<kParts>(qt[i & 1][s], X[s], c);
-                c = mm<kParts>(kt[i & 1][s], W[s], c);
-            }
-            S[i] = c;
-            if (i + 2 < 2 * KP)
-                features(i + 2);
-        }
+        fetch_rest(next, ahead);
     }
     float *out = p.chunk_from > 0 ? p.carry : p.ginit;
     if (out && live)
-        state_store<KP>(S, out + bh * p.Dk * p.Dv + dv, p.Dk, p.Dv);
+        state_store<1>(S, out + bh * p.Dk * p.Dv + state_at0, many, p.Dv);
 }
 
 // -------------------------------------------------------- gradients: every chunk by itself
