@@ -14,6 +14,10 @@
 // 8, 16, 32, 64 or 128 values are whole lanes of one row of 16 and are summed by lane exchange; other
 // widths go through shared memory, where a lane leaves the sums of the two heads that its eight values
 // may belong to.
+//
+// 65536 rows of 1024 in bfloat16: the gated norm to 8 bits 80 to 97 us (336 MB; bound by the gate's exponential and
+// reciprocal, 75.5 with the hardware's reciprocal alone), its gradients 139 (671 MB, 4.8 TB/s); the block norm to 8 bits 93
+// (470 MB, 5.0 TB/s), its gradients with the residual's 152 (805 MB, 5.3 TB/s): all but the first at the rate of a copy.
 #pragma once
 
 #include <ssd_row.h>
