@@ -1156,13 +1156,9 @@ SSD_DEVICE void span_gates(v4f (&g)[4], const float *from)
         g[i] = span_gate(from, 32 * (i >> 1) + 4 * (i & 1));
 }
 
-template <int KP>
-struct Spans {
-    static constexpr int own = 4 / KP;    // tiles of 16 tokens that a wave makes outputs of
-    // a wave's first feature (or 0, if there is none), and how many it has
-    static SSD_DEVICE int first(int wave, int Dk) { return 32 * wave < Dk ? 32 * wave : 0; }
-    static SSD_DEVICE int many(int wave, int Dk) { return Dk - 32 * wave < 32 ? Dk - 32 * wave : 32; }
-};
+// A wave's first feature (or 0, if there is none), and how many it has.
+SSD_DEVICE int span_first(int wave, int Dk) { return 32 * wave < Dk ? 32 * wave : 0; }
+SSD_DEVICE int span_many(int wave, int Dk) { return Dk - 32 * wave < 32 ? Dk - 32 * wave : 32; }
 // The shares of tile h, added in the spans' order.
 template <int KP>
 SSD_DEVICE v4f spans_sum(const v4f (&share)[KP][4][64], int h, int lane)
@@ -1179,7 +1175,7 @@ SSD_KERNEL(64 * KP) void delta_spans_kernel(DeltaParams p)
 {
     typedef typename DeltaElem<T>::type E;
     typedef DeltaPack<T, KP, false> Pack;
-    constexpr int IN = Pack::IN, OUT = Pack::OUT, OWN = Spans<KP>::own;
+    constexpr int IN = Pack::IN, OUT = Pack::OUT, OWN = 4 / KP;  // tiles of 16 tokens to a wave
     SSD_LDS v4f share[2][KP][4][64];
     SSD_LDS v4u state[2][KP * OUT * 64];
     int64_t bh;
@@ -1196,7 +1192,7 @@ SSD_KERNEL(64 * KP) void delta_spans_kernel(DeltaParams p)
     const v4u *pack = p.pack + bh * range * Pack::size;
     const int last = (length + kDeltaChunk - 1) / kDeltaChunk;  // chunks with tokens
     const int to = last < p.chunk_to ? last : p.chunk_to;
-    const int first = Spans<KP>::first(wave, p.Dk), many = Spans<KP>::many(wave, p.Dk);
+    const int first = span_first(wave, p.Dk), many = span_many(wave, p.Dk);
     const int tile = OWN * wave, span = tile >> 1;  // of the outputs
     const int64_t state_at0 = (int64_t)first * p.Dv + dv;
     v4f S[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
@@ -1709,7 +1705,7 @@ SSD_KERNEL(64 * KP) void delta_spans_bwd_kernel(DeltaParams p)
 {
     typedef typename DeltaElem<T>::type E;
     typedef DeltaPack<T, KP, true> Pack;
-    constexpr int IN = Pack::IN, OWN = Spans<KP>::own;
+    constexpr int IN = Pack::IN, OWN = 4 / KP;  // tiles of 16 tokens to a wave
     SSD_LDS v4f share[2][KP][4][64];
     int64_t bh;
     int block;
@@ -1724,7 +1720,7 @@ SSD_KERNEL(64 * KP) void delta_spans_bwd_kernel(DeltaParams p)
     const v4u *pack = p.pack + bh * range * Pack::size;
     const int last = (length + kDeltaChunk - 1) / kDeltaChunk;  // chunks with tokens
     const int to = last < p.chunk_to ? last : p.chunk_to;
-    const int first = Spans<KP>::first(wave, p.Dk), many = Spans<KP>::many(wave, p.Dk);
+    const int first = span_first(wave, p.Dk), many = span_many(wave, p.Dk);
     const int tile = OWN * wave, span = tile >> 1;  // of P^T dO
     const int64_t state_at0 = (int64_t)first * p.Dv + dv;
     v4f S[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};  // the gradient of the state after the chunk
