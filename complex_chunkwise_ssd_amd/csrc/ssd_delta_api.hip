@@ -55,10 +55,8 @@ bool delta_few(const DeltaSizes &z) { return z.T <= ssd::kDeltaFew; }
 bool delta_long(const DeltaSizes &z) { return z.B * z.Hv * ((z.Dv + 63) / 64) <= 192; }
 
 template <int T, int KP>
-constexpr size_t pack_bytes(bool backward)
-{
-    return 16 * (size_t)(backward ? ssd::DeltaPack<T, KP, true>::size : ssd::DeltaPack<T, KP, false>::size);
-}
+constexpr size_t pack_bytes() { return 16 * (size_t)ssd::DeltaPack<T, KP>::size; }
+
 // Bytes that a chunk of a head is packed into; chunks that are packed at a time (some 192 MB, which the caches of the
 // memory side hold until they are read).
 struct DeltaRange {
@@ -66,12 +64,12 @@ struct DeltaRange {
     size_t pack, carry;
     size_t bytes() const { return pack + carry; }
 };
-DeltaRange delta_range(const DeltaSizes &z, int dtype, bool backward)
+DeltaRange delta_range(const DeltaSizes &z, int dtype)
 {
     if (!delta_long(z))
         return {0, 0, 0};
-    const size_t one = dtype == SSD_BF16 ? (z.Dk <= 64 ? pack_bytes<ssd::kBF16, 2>(backward) : pack_bytes<ssd::kBF16, 4>(backward))
-                                         : (z.Dk <= 64 ? pack_bytes<ssd::kF32, 2>(backward) : pack_bytes<ssd::kF32, 4>(backward));
+    const size_t one = dtype == SSD_BF16 ? (z.Dk <= 64 ? pack_bytes<ssd::kBF16, 2>() : pack_bytes<ssd::kBF16, 4>())
+                                         : (z.Dk <= 64 ? pack_bytes<ssd::kF32, 2>() : pack_bytes<ssd::kF32, 4>());
     const size_t heads = one * (size_t)(z.B * z.Hv);
     int64_t chunks = (int64_t)((size_t)192 * 1024 * 1024 / heads);
     chunks = chunks < 1 ? 1 : chunks < z.chunks() ? chunks : z.chunks();
@@ -222,7 +220,7 @@ size_t ssd_gated_delta_workspace_bytes(int64_t batch, int64_t T, int64_t Hk, int
     const DeltaSizes z{batch, T, Hk, Hv, Dk, Dv};
     if (check_delta(z, dtype, 1.f) || z.empty() || delta_few(z))
         return 0;
-    return delta_range(z, dtype, false).bytes();
+    return delta_range(z, dtype).bytes();
 }
 
 int ssd_gated_delta(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v, int64_t v_stride,
@@ -272,7 +270,7 @@ int ssd_gated_delta(const void *q, int64_t q_stride, const void *k, int64_t k_st
     p.states = chunk_states;
     if (delta_few(z))
         return dtype == SSD_BF16 ? launch_delta_few<ssd::kBF16>(p, s) : launch_delta_few<ssd::kF32>(p, s);
-    const DeltaRange range = delta_range(z, dtype, false);
+    const DeltaRange range = delta_range(z, dtype);
     char *at = (char *)workspace;
     if (dtype == SSD_BF16)
         return Dk <= 64 ? launch_delta<ssd::kBF16, 2>(p, range, at, s) : launch_delta<ssd::kBF16, 4>(p, range, at, s);
@@ -285,7 +283,7 @@ size_t ssd_gated_delta_backward_workspace_bytes(int64_t batch, int64_t T, int64_
     const DeltaSizes z{batch, T, Hk, Hv, Dk, Dv};
     if (check_delta(z, dtype, 1.f) || z.empty())
         return 0;
-    return delta_space(z).bytes() + delta_range(z, dtype, true).bytes();
+    return delta_space(z).bytes() + delta_range(z, dtype).bytes();
 }
 
 int ssd_gated_delta_backward(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
@@ -347,7 +345,7 @@ int ssd_gated_delta_backward(const void *q, int64_t q_stride, const void *k, int
     p.gr = (float *)(at + space.gs);
     p.wq = (float *)(at + space.gs + space.gr);
     p.wk = (float *)(at + space.gs + space.gr + space.w);
-    const DeltaRange range = delta_range(z, dtype, true);
+    const DeltaRange range = delta_range(z, dtype);
     at += space.bytes();
     if (dtype == SSD_BF16)
         return Dk <= 64 ? launch_delta_bwd<ssd::kBF16, 2>(p, range, at, s) : launch_delta_bwd<ssd::kBF16, 4>(p, range, at, s);

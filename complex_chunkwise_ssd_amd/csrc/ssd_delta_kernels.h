@@ -103,9 +103,10 @@ SSD_DEVICE void lds_values(const typename DeltaElem<T>::type *p, float (&v)[8])
     unpack8<T>(raw, v);
 }
 
-// Which six operand tiles a lower (or upper) triangle of spans has.
-SSD_DEVICE int frag_of(int s, int h, int t) { return s == 0 ? h : 2 + 2 * h + t; }          // t <= s
-SSD_DEVICE int frag_of_upper(int s, int h, int t) { return s == 1 ? 4 + h : 2 * h + t; }    // t >= s
+// Which six operand tiles a lower (or upper) triangle of spans has: the first two and the last two are those of the
+// blocks on the diagonal. The parts of a tile lie one after the other.
+SSD_DEVICE int frag_of(int s, int h, int t) { return s == 0 ? h : 2 + 2 * t + h; }          // t <= s
+SSD_DEVICE int frag_of_upper(int s, int h, int t) { return s == 1 ? 4 + h : 2 * t + h; }    // t >= s
 
 // Running sums over a wave's lanes in float64.
 template <int n>
@@ -288,7 +289,7 @@ SSD_DEVICE Parts<N> frag_operand(const v4u *frags, int f)
     Parts<N> r;
 #pragma unroll
     for (int i = 0; i < N; ++i)
-        r.p[i] = frags[(i * kDeltaFrags + f) * 64 + (thread_id() & 63)];
+        r.p[i] = frags[(f * N + i) * 64 + (thread_id() & 63)];
     return r;
 }
 
@@ -336,6 +337,10 @@ SSD_DEVICE void delta_store(typename DeltaElem<T>::type *p, float v)
 
 constexpr int kPairStride = 36;
 
+// The block of 32 on the diagonal that becomes T_00 or T_11 (float32, transposed) stands where their operand tiles will.
+SSD_DEVICE float *pair_block(v4u *tri, int pair) { return (float *)(tri + 4 * pair * kParts * 64); }
+static_assert(32 * kPairStride * 4 <= 2 * kParts * 64 * 16, "a block fits where its tiles come to stand");
+
 // Four neighbours (i, j .. j + 3) of a 64 x 64 matrix into its operand tiles, in N parts.
 template <int N>
 SSD_DEVICE void frag_store(v4u *frags, int f, int i, int j, v4f w)
@@ -346,20 +351,22 @@ SSD_DEVICE void frag_store(v4u *frags, int f, int i, int j, v4f w)
 #pragma unroll
     for (int e = 0; e < N; ++e) {
         const v2u half = {parts.p[e][0], parts.p[e][1]};
-        *(v2u *)((char *)&frags[(e * kDeltaFrags + f) * 64 + lane] + 2 * (j & 7)) = half;
+        *(v2u *)((char *)&frags[(f * N + e) * 64 + lane] + 2 * (j & 7)) = half;
     }
 }
 
 // A chunk's triangle and P, by all waves, in tiles of 16: A = beta D o K K^T below the diagonal and
 // P = scale Q K^T o D. Of the two 32 x 32 blocks of I + A on the diagonal the inverses of their own blocks of 16 and
-// A between them go into `pairs` (float32, transposed); A_10 and P into operand tiles, or, with TURNED, A_10^T and P^T.
+// A between them go where pair_block says; A_10 and P into operand tiles, or, with TURNED, A_10^T and P^T.
 // Each of the first four waves has one tile on the diagonal, the others are dealt out so that the first two,
 // which finish the inverses afterwards, have the fewest.
-template <int T, int KP, int OUT, int WAVES, bool TURNED>
+template <int T, int KP, int WAVES, bool TURNED>
 SSD_DEVICE void delta_tiles(const typename DeltaElem<T>::type *k, const typename DeltaElem<T>::type *q,
-                            const DeltaGates &gates, float scale, float *pairs, v4u *tri, v4u *pf)
+                            const DeltaGates &gates, float scale, v4u *tri, v4u *pf)
 {
     const int l = thread_id() & 15, quarter = (thread_id() & 63) >> 4, wave = wave_id();
+    if (thread_id() < 128)  // above the diagonal of a block of 32 there are zeros
+        *(v4f *)(pair_block(tri, wave) + (16 + (4 * quarter + (l >> 2))) * kPairStride + 4 * (l & 3)) = v4f{0.f, 0.f, 0.f, 0.f};
     // off the diagonal: (1,0) (3,2) (2,0) (2,1) (3,0) (3,1); of four waves 2 and 3 take two of them
     const int mine = WAVES == 4 ? (wave < 2 ? 4 + wave : 2 * wave - 4) : (wave < 4 ? 2 + wave : wave - 4);
     const int many = WAVES == 4 ? (wave < 2 ? 1 : 2) : (wave < 2 ? 0 : 1);
@@ -384,6 +391,7 @@ SSD_DEVICE void delta_tiles(const typename DeltaElem<T>::type *k, const typename
         if (!has[c])
             continue;
         const int row = 16 * (TURNED ? ti[c] : tj[c]) + 4 * quarter, col = 16 * (TURNED ? tj[c] : ti[c]) + l;
+        float *const pair = pair_block(tri, col >> 5);
         const double sum = gates.sum[col];
         v4f a, w;
 #pragma unroll
@@ -395,7 +403,7 @@ SSD_DEVICE void delta_tiles(const typename DeltaElem<T>::type *k, const typename
         }
         const int f = TURNED ? frag_of_upper(col >> 5, col >> 2 & 1, row >> 5) : frag_of(col >> 5, col >> 2 & 1, row >> 5);
         if (pf)
-            frag_store<OUT>(pf, f, col, row, w);
+            frag_store<kParts>(pf, f, col, row, w);
         if (c == 0) {
             // column l of the block's inverse, in every quarter: each value is taken from all that follow it
             // as soon as it is known; the block's entries reach all lanes as scalars
@@ -420,14 +428,14 @@ SSD_DEVICE void delta_tiles(const typename DeltaElem<T>::type *k, const typename
             if (quarter == 0)
 #pragma unroll
                 for (int e = 0; e < 16; e += 4)
-                    *(v4f *)(pairs + col * kPairStride + (16 * wave & 16) + e) = v4f{x[e], x[e + 1], x[e + 2], x[e + 3]};
+                    *(v4f *)(pair + (col & 31) * kPairStride + (16 * wave & 16) + e) = v4f{x[e], x[e + 1], x[e + 2], x[e + 3]};
         } else if (ti[c] >> 1 == tj[c] >> 1) {
             if (TURNED)
-                *(v4f *)(pairs + col * kPairStride + (row & 31)) = a;
+                *(v4f *)(pair + (col & 31) * kPairStride + (row & 31)) = a;
             else
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
-                    pairs[(row + r) * kPairStride + (col & 31)] = a[r];
+                    pair[((row & 31) + r) * kPairStride + (col & 31)] = a[r];
         } else {
             frag_store<kParts>(tri, f, col, row, a);
         }
@@ -437,8 +445,9 @@ SSD_DEVICE void delta_tiles(const typename DeltaElem<T>::type *k, const typename
 // The corner of the inverse of a block of 32 (held transposed), - T_1 A T_0, and the block (with TURNED its transpose)
 // into operand tiles, by one wave.
 template <bool TURNED>
-SSD_DEVICE void delta_invert(float *block, int pair, v4u *tri)
+SSD_DEVICE void delta_invert(int pair, v4u *tri)
 {
+    float *const block = pair_block(tri, pair);
     const int l = thread_id() & 15, quarter = (thread_id() & 63) >> 4;
     // the transpose's is - T_0^T (A^T T_1^T)
     float *corner = block + 16;  // A^T: rows of the first 16, columns of the second
@@ -456,9 +465,10 @@ SSD_DEVICE void delta_invert(float *block, int pair, v4u *tri)
     for (int r = 0; r < 4; ++r)
         corner[(4 * quarter + r) * kPairStride + l] = z[r];
     wave_lds_sync();
+    float x[2][8];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {  // row i of the operand is column i of what is held
-        float v[8];
+        float (&v)[8] = x[h];
         if (TURNED) {
             const float *row = block + (tile_row(0, l) + 4 * h) * kPairStride + 8 * quarter;
             const v4f lo = *(const v4f *)row, hi = *(const v4f *)(row + 4);
@@ -470,19 +480,16 @@ SSD_DEVICE void delta_invert(float *block, int pair, v4u *tri)
             for (int e = 0; e < 8; ++e)
                 v[e] = block[8 * quarter * kPairStride + tile_row(0, l) + (e * kPairStride + 4 * h)];
         }
-        const Parts<kParts> parts = split8<kParts>(v);
+    }
+    wave_lds_sync();  // all of the block has been read
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const Parts<kParts> parts = split8<kParts>(x[h]);
         const int f = TURNED ? frag_of_upper(pair, h, pair) : frag_of(pair, h, pair);
 #pragma unroll
         for (int e = 0; e < kParts; ++e)
-            tri[(e * kDeltaFrags + f) * 64 + (thread_id() & 63)] = parts.p[e];
+            tri[(f * kParts + e) * 64 + (thread_id() & 63)] = parts.p[e];
     }
-}
-
-// Above the diagonal of a block of 32 (held transposed) there are zeros.
-SSD_DEVICE void delta_clear_pairs(float *pairs, int threads)
-{
-    for (int i = thread_id(); i < 16 * 16; i += threads)
-        pairs[(16 + (i >> 4)) * kPairStride + (i & 15)] = pairs[(48 + (i >> 4)) * kPairStride + (i & 15)] = 0.f;
 }
 
 // The feature that a lane holds in component r of tile i of its state, less 8 q.
@@ -584,7 +591,9 @@ SSD_DEVICE void span_mm(v4f &c, const Parts<N> &a, const Parts<kParts> &b, int f
 // A workgroup takes 16 WAVES columns of a value head, a wave 16 of them: lane l the column l, and of 2 KP tiles
 // the features 32 s + 8 q + 4 h + r of the state. The chunk's triangle and P are made by all of them; while two
 // waves solve the blocks of 32, the others go on with what the state gives. The next chunk's rows are in
-// flight meanwhile. 32 x 2048 tokens on 16 heads of 64 in bfloat16, with states: 329 to 360 us (822 MB, 2.4 TB/s), of all
+// flight meanwhile. Outputs have all three parts too, whatever type they are stored in: with two, 16 bits, values within 2^-16
+// of the middle of two bfloat16 numbers went to the wrong one, for 6 % less time.
+// 32 x 2048 tokens on 16 heads of 64 in bfloat16, with states: 350 us (822 MB, 2.3 TB/s; 330 with two parts), of all
 // cycles VALU 47 % and MFMA 17 %: splitting into parts and the triangle's substitution bound it, not memory. As
 // two kernels, triangles first, it was 1199 us; with the blocks on the diagonal inverted through shared memory 379.
 template <int T, int KP, int WAVES>
@@ -593,11 +602,9 @@ SSD_KERNEL_WAVES(64 * WAVES, (WAVES == 8 || (T == kBF16 && KP <= 2) ? 2 : 1)) vo
     typedef typename DeltaElem<T>::type E;
     constexpr int NT = 64 * WAVES, COLS = 16 * WAVES;
     constexpr int pad = DeltaElem<T>::pad, RS = 32 * KP + pad, TS = 64 + pad;
-    constexpr int OUT = T == kBF16 ? 2 : 3;  // parts of what only reaches o
     constexpr bool STAGE_V = T == kBF16;      // float32 rows leave no room
     SSD_LDS E k[64 * RS], q[64 * RS], kt[32 * KP * TS], vt[STAGE_V ? COLS * TS : 8];
-    SSD_LDS float pairs[64 * kPairStride];
-    SSD_LDS v4u tri[kParts * kDeltaFrags * 64], pf[OUT * kDeltaFrags * 64];
+    SSD_LDS v4u tri[kParts * kDeltaFrags * 64], pf[kParts * kDeltaFrags * 64];
     SSD_LDS DeltaGates both[2];
     const int64_t id = block_id();
     const int block = (int)(id % p.columns), hv = (int)(id / p.columns % p.Hv), b = (int)(id / p.columns / p.Hv);
@@ -642,9 +649,8 @@ SSD_KERNEL_WAVES(64 * WAVES, (WAVES == 8 || (T == kBF16 && KP <= 2) ? 2 : 1)) vo
         if (wave == WAVES - 1)
             delta_gates_of(both[0], ng, nbeta, n);
     }
-    delta_clear_pairs(pairs, NT);  // and they stay, as do P's tiles above its diagonal
-    for (int i = thread_id(); i < OUT * kDeltaFrags * 64; i += NT)
-        pf[i] = v4u{0u, 0u, 0u, 0u};
+    for (int i = thread_id(); i < kParts * kDeltaFrags * 64; i += NT)
+        pf[i] = v4u{0u, 0u, 0u, 0u};  // above its diagonal P's tiles stay so
     for (int chunk = 0; chunk < p.chunks; ++chunk) {
         n = delta_chunk_tokens(length, chunk);
         const int rows = p.T - chunk * kDeltaChunk < 64 ? p.T - chunk * kDeltaChunk : 64;
@@ -667,10 +673,10 @@ SSD_KERNEL_WAVES(64 * WAVES, (WAVES == 8 || (T == kBF16 && KP <= 2) ? 2 : 1)) vo
         const int next = delta_chunk_tokens(length, chunk + 1);
         if (next > 0)
             fetch(chunk + 1, next);
-        delta_tiles<T, KP, OUT, WAVES, false>(k, q, gates, p.scale, pairs, tri, pf);
+        delta_tiles<T, KP, WAVES, false>(k, q, gates, p.scale, tri, pf);
         block_sync();
         if (wave < 2)
-            delta_invert<false>(pairs + 32 * wave * kPairStride, wave, tri);
+            delta_invert<false>(wave, tri);
         // R = beta (V - e^G K S), and e^G Q S
         Parts<kParts> Sp[KP];
 #pragma unroll
@@ -697,7 +703,7 @@ SSD_KERNEL_WAVES(64 * WAVES, (WAVES == 8 || (T == kBF16 && KP <= 2) ? 2 : 1)) vo
 #pragma unroll
                 for (int f = 0; f < KP; ++f) {
                     span_mm<T>(ks, lds_operand(kl + ((32 * s + 4 * h) * RS + 32 * f)), Sp[f], f);
-                    qs = mm<OUT>(lds_operand(ql + ((32 * s + 4 * h) * RS + 32 * f)), Sp[f], qs);
+                    qs = mm<kParts>(lds_operand(ql + ((32 * s + 4 * h) * RS + 32 * f)), Sp[f], qs);
                 }
                 const v4f since = *(const v4f *)(gates.since + q8 + (32 * s + 4 * h));
                 const v4f beta = *(const v4f *)(gates.beta + q8 + (32 * s + 4 * h));
@@ -734,9 +740,9 @@ SSD_KERNEL_WAVES(64 * WAVES, (WAVES == 8 || (T == kBF16 && KP <= 2) ? 2 : 1)) vo
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 v4f c = {O[s][4 * h], O[s][4 * h + 1], O[s][4 * h + 2], O[s][4 * h + 3]};
-                c = mm<OUT>(frag_operand<OUT>(pf, frag_of(s, h, 0)), U0, c);
+                c = mm<kParts>(frag_operand<kParts>(pf, frag_of(s, h, 0)), U0, c);
                 if (s == 1)
-                    c = mm<OUT>(frag_operand<OUT>(pf, frag_of(1, h, 1)), U1, c);
+                    c = mm<kParts>(frag_operand<kParts>(pf, frag_of(1, h, 1)), U1, c);
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
                     O[s][4 * h + r] = c[r];
@@ -799,10 +805,10 @@ SSD_KERNEL_WAVES(64 * WAVES, (WAVES == 8 || (T == kBF16 && KP <= 2) ? 2 : 1)) vo
 // from what the first leaves in shared memory.
 
 // What a chunk is packed into, in units of 16 bytes: operand tiles of 64 lanes each, and the gates.
-template <int T, int KP, bool BACKWARD>
+template <int T, int KP>
 struct DeltaPack {
-    static constexpr int IN = DeltaElem<T>::parts, OUT = BACKWARD || T == kF32 ? 3 : 2;
-    static constexpr int tri = 0, pf = tri + kParts * kDeltaFrags * 64, kr = pf + OUT * kDeltaFrags * 64;
+    static constexpr int IN = DeltaElem<T>::parts;
+    static constexpr int tri = 0, pf = tri + kParts * kDeltaFrags * 64, kr = pf + kParts * kDeltaFrags * 64;
     static constexpr int kt = kr + 4 * KP * IN * 64, q = kt + 4 * KP * IN * 64;  // Q by rows, backwards by features
     static constexpr int gates = q + 4 * KP * IN * 64, size = gates + 64;  // since, left, beta, and e^G_C in the last place
 };
@@ -811,12 +817,11 @@ template <int T, int KP, bool BACKWARD>
 SSD_KERNEL(256) void delta_pack_kernel(DeltaParams p)
 {
     typedef typename DeltaElem<T>::type E;
-    typedef DeltaPack<T, KP, BACKWARD> Pack;
+    typedef DeltaPack<T, KP> Pack;
     constexpr int pad = DeltaElem<T>::pad, RS = 32 * KP + pad, TS = 64 + pad, IN = Pack::IN;
     SSD_LDS E k[64 * RS], q[BACKWARD && 32 * KP * TS > 64 * RS ? 32 * KP * TS : 64 * RS], kt[32 * KP * TS];
     E *const qt = q;  // by features once its rows have been used
-    SSD_LDS float pairs[64 * kPairStride];
-    SSD_LDS v4u tri[kParts * kDeltaFrags * 64], pf[Pack::OUT * kDeltaFrags * 64];
+    SSD_LDS v4u tri[kParts * kDeltaFrags * 64], pf[kParts * kDeltaFrags * 64];
     SSD_LDS DeltaGates gates;
     const int64_t id = block_id();
     const int range = p.chunk_to - p.chunk_from;
@@ -833,16 +838,15 @@ SSD_KERNEL(256) void delta_pack_kernel(DeltaParams p)
         delta_gates(gates, p.g, p.beta, token * p.Hv + hv, p.Hv, n);
     blocks_store<T, 32 * KP, 256, true, true>(nk, p.Dk, n, k, kt);
     blocks_store<T, 32 * KP, 256, true, false>(nq, p.Dk, n, q, (E *)nullptr);
-    delta_clear_pairs(pairs, 256);
-    for (int i = thread_id(); i < Pack::OUT * kDeltaFrags * 64; i += 256)
+    for (int i = thread_id(); i < kParts * kDeltaFrags * 64; i += 256)
         pf[i] = v4u{0u, 0u, 0u, 0u};
     block_sync();
-    delta_tiles<T, KP, Pack::OUT, 4, BACKWARD>(k, q, gates, p.scale, pairs, tri, pf);
+    delta_tiles<T, KP, 4, BACKWARD>(k, q, gates, p.scale, tri, pf);
     block_sync();
     if (BACKWARD)
         blocks_store<T, 32 * KP, 256, false, true>(nq, p.Dk, n, (E *)nullptr, qt);
     if (wave < 2)
-        delta_invert<BACKWARD>(pairs + 32 * wave * kPairStride, wave, tri);
+        delta_invert<BACKWARD>(wave, tri);
     block_sync();
     v4u *out = p.pack + (((int64_t)b * p.Hv + hv) * range + at) * Pack::size;
     const E *kl = k + tile_row(0, l) * RS + q8, *ql = q + tile_row(0, l) * RS + q8;
@@ -866,10 +870,10 @@ SSD_KERNEL(256) void delta_pack_kernel(DeltaParams p)
         to[128 + lane] = gates.beta[lane];
         to[192 + lane] = gates.whole;
     }
-    for (int i = thread_id(); i < kParts * kDeltaFrags * 64; i += 256)
+    for (int i = thread_id(); i < kParts * kDeltaFrags * 64; i += 256) {
         out[Pack::tri + i] = tri[i];
-    for (int i = thread_id(); i < Pack::OUT * kDeltaFrags * 64; i += 256)
         out[Pack::pf + i] = pf[i];
+    }
 }
 
 // The workgroup's head and columns: the columns of a head lie a multiple of eight workgroups apart, on the same
@@ -888,14 +892,8 @@ SSD_DEVICE void pack_load(Parts<N> &x, const v4u *from)
     for (int e = 0; e < N; ++e)
         x.p[e] = from[e * 64];
 }
-// Tiles of the triangle and of P: their parts lie kDeltaFrags tiles apart.
-template <int N>
-SSD_DEVICE void pack_load_frag(Parts<N> &x, const v4u *from, int f)
-{
-#pragma unroll
-    for (int e = 0; e < N; ++e)
-        x.p[e] = from[(e * kDeltaFrags + f) * 64];
-}
+// Tiles of the triangle and of P.
+SSD_DEVICE void pack_load_frag(Parts<kParts> &x, const v4u *from, int f) { pack_load(x, from + f * kParts * 64); }
 // The values of the lane's 16 tokens.
 SSD_DEVICE void pack_gate(v4f (&g)[4], const float *from, int q8)
 {
@@ -908,10 +906,10 @@ template <int T, int KP>
 SSD_KERNEL(128) void delta_long_kernel(DeltaParams p)
 {
     typedef typename DeltaElem<T>::type E;
-    typedef DeltaPack<T, KP, false> Pack;
-    constexpr int IN = Pack::IN, OUT = Pack::OUT;
+    typedef DeltaPack<T, KP> Pack;
+    constexpr int IN = Pack::IN;
     constexpr bool AHEAD = T == kBF16;  // K's rows of the next chunk; in float32 there are too many
-    SSD_LDS v4u state[2][KP * OUT * 64], us[2][2 * OUT * 64];
+    SSD_LDS v4u state[2][KP * kParts * 64], us[2][2 * kParts * 64];
     int64_t bh;
     int block;
     long_place(p, bh, block);
@@ -989,8 +987,8 @@ SSD_KERNEL(128) void delta_long_kernel(DeltaParams p)
             for (int s = 0; s < KP; ++s) {
                 Sp[s] = split_tiles<kParts>(S[2 * s], S[2 * s + 1]);
 #pragma unroll
-                for (int e = 0; e < OUT; ++e)
-                    state[chunk & 1][(s * OUT + e) * 64 + lane] = Sp[s].p[e];
+                for (int e = 0; e < kParts; ++e)
+                    state[chunk & 1][(s * kParts + e) * 64 + lane] = Sp[s].p[e];
             }
             // R = beta (V - e^G K S)
             float R[2][8];
@@ -1032,11 +1030,11 @@ SSD_KERNEL(128) void delta_long_kernel(DeltaParams p)
 #pragma unroll
             for (int h = 0; h < 2; ++h)
                 U[2 + h] = mm<kParts>(tri[frag_of(1, h, 1)], R1, v4f{0.f, 0.f, 0.f, 0.f});
-            const Parts<OUT> U1 = split_tiles<OUT>(U[2], U[3]);
+            const Parts<kParts> U1 = split_tiles<kParts>(U[2], U[3]);
 #pragma unroll
-            for (int e = 0; e < OUT; ++e) {
+            for (int e = 0; e < kParts; ++e) {
                 us[chunk & 1][e * 64 + lane] = U0.p[e];
-                us[chunk & 1][(OUT + e) * 64 + lane] = U1.p[e];
+                us[chunk & 1][(kParts + e) * 64 + lane] = U1.p[e];
             }
             // the state
             Parts<kParts> W[2];
@@ -1081,7 +1079,7 @@ SSD_KERNEL(128) void delta_long_kernel(DeltaParams p)
             const v4u *at = pack + (int64_t)(chunk - p.chunk_from) * Pack::size;
             const int n = delta_chunk_tokens(length, chunk);
             Parts<IN> qr[4 * KP];
-            Parts<OUT> pf[kDeltaFrags];
+            Parts<kParts> pf[kDeltaFrags];
             v4f since[4];
 #pragma unroll
             for (int i = 0; i < 4 * KP; ++i)
@@ -1091,26 +1089,26 @@ SSD_KERNEL(128) void delta_long_kernel(DeltaParams p)
                 pack_load_frag(pf[f], at + Pack::pf, f);
             pack_gate(since, (const float *)(at - lane + Pack::gates), q8);
             block_sync();  // the state and U are there
-            Parts<OUT> Sp[KP], U[2];
+            Parts<kParts> Sp[KP], U[2];
 #pragma unroll
             for (int s = 0; s < KP; ++s)
-                pack_load(Sp[s], &state[chunk & 1][s * OUT * 64 + lane]);
+                pack_load(Sp[s], &state[chunk & 1][s * kParts * 64 + lane]);
 #pragma unroll
             for (int s = 0; s < 2; ++s)
-                pack_load(U[s], &us[chunk & 1][s * OUT * 64 + lane]);
+                pack_load(U[s], &us[chunk & 1][s * kParts * 64 + lane]);
             const uint32_t step = opaque_uniform((uint32_t)o_stride * sizeof(E)), off = opaque((uint32_t)q8 * step);
 #pragma unroll
             for (int h = 0; h < 4; ++h) {
                 v4f c = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int f = 0; f < KP; ++f)
-                    c = mm<OUT>(qr[h * KP + f], Sp[f], c);
+                    c = mm<kParts>(qr[h * KP + f], Sp[f], c);
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
                     c[r] *= p.scale * since[h][r];
-                c = mm<OUT>(pf[frag_of(h >> 1, h & 1, 0)], U[0], c);
+                c = mm<kParts>(pf[frag_of(h >> 1, h & 1, 0)], U[0], c);
                 if (h > 1)
-                    c = mm<OUT>(pf[frag_of(1, h & 1, 1)], U[1], c);
+                    c = mm<kParts>(pf[frag_of(1, h & 1, 1)], U[1], c);
                 if (live)
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
@@ -1136,15 +1134,14 @@ constexpr int kSpansMost = 256;  // workgroups
 
 // Operands at a place that is the same for all lanes, so that its address is scalar work.
 template <int N>
-SSD_DEVICE void span_load(Parts<N> &x, const v4u *from, int apart = 1)
+SSD_DEVICE void span_load(Parts<N> &x, const v4u *from)
 {
     const uint32_t off = 16 * ((uint32_t)thread_id() & 63);
 #pragma unroll
     for (int e = 0; e < N; ++e)
-        x.p[e] = *(const v4u *)((const char *)(from + e * apart * 64) + off);
+        x.p[e] = *(const v4u *)((const char *)(from + e * 64) + off);
 }
-template <int N>
-SSD_DEVICE void span_load_frag(Parts<N> &x, const v4u *from, int f) { span_load(x, from + f * 64, kDeltaFrags); }
+SSD_DEVICE void span_load_frag(Parts<kParts> &x, const v4u *from, int f) { span_load(x, from + f * kParts * 64); }
 SSD_DEVICE v4f span_gate(const float *from, int t)
 {
     return *(const v4f *)((const char *)(from + t) + 32 * (((uint32_t)thread_id() & 63) >> 4));
@@ -1174,10 +1171,10 @@ template <int T, int KP>
 SSD_KERNEL(64 * KP) void delta_spans_kernel(DeltaParams p)
 {
     typedef typename DeltaElem<T>::type E;
-    typedef DeltaPack<T, KP, false> Pack;
-    constexpr int IN = Pack::IN, OUT = Pack::OUT, OWN = 4 / KP;  // tiles of 16 tokens to a wave
+    typedef DeltaPack<T, KP> Pack;
+    constexpr int IN = Pack::IN, OWN = 4 / KP;  // tiles of 16 tokens to a wave
     SSD_LDS v4f share[2][KP][4][64];
-    SSD_LDS v4u state[2][KP * OUT * 64];
+    SSD_LDS v4u state[2][KP * kParts * 64];
     int64_t bh;
     int block;
     long_place(p, bh, block);
@@ -1206,7 +1203,7 @@ SSD_KERNEL(64 * KP) void delta_spans_kernel(DeltaParams p)
     float whole = 0.f;
     Parts<IN> kr[4], kt[2][2], qr[OWN][KP];
     Parts<kParts> tri[kDeltaFrags];
-    Parts<OUT> pf[OWN][2];
+    Parts<kParts> pf[OWN][2];
     auto place = [&](int chunk) { return pack + (int64_t)(chunk - p.chunk_from) * Pack::size; };
     auto fetch_rows = [&](const v4u *at) {
 #pragma unroll
@@ -1284,8 +1281,8 @@ SSD_KERNEL(64 * KP) void delta_spans_kernel(DeltaParams p)
         const v4u *next = place(ahead);
         const Parts<kParts> Sp = split_tiles<kParts>(S[0], S[1]);
 #pragma unroll
-        for (int e = 0; e < OUT; ++e)
-            state[chunk & 1][(wave * OUT + e) * 64 + lane] = Sp.p[e];
+        for (int e = 0; e < kParts; ++e)
+            state[chunk & 1][(wave * kParts + e) * 64 + lane] = Sp.p[e];
 #pragma unroll
         for (int h = 0; h < 4; ++h)
             share[chunk & 1][wave][h][lane] = mm<kParts>(kr[h], Sp, v4f{0.f, 0.f, 0.f, 0.f});
@@ -1347,24 +1344,24 @@ SSD_KERNEL(64 * KP) void delta_spans_kernel(DeltaParams p)
         fetch_features(next);
         sched_fence();
         // the outputs
-        Parts<OUT> old[KP];
+        Parts<kParts> old[KP];
 #pragma unroll
         for (int f = 0; f < KP; ++f)
-            pack_load(old[f], &state[chunk & 1][f * OUT * 64 + lane]);
-        const Parts<OUT> U1 = split_tiles<OUT>(U[2], U[3]);
+            pack_load(old[f], &state[chunk & 1][f * kParts * 64 + lane]);
+        const Parts<kParts> U1 = split_tiles<kParts>(U[2], U[3]);
         const uint32_t step = opaque_uniform((uint32_t)o_stride * sizeof(E)), off = opaque((uint32_t)q8 * step);
 #pragma unroll
         for (int i = 0; i < OWN; ++i) {
             v4f c = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int f = 0; f < KP; ++f)
-                c = mm<OUT>(qr[i][f], old[f], c);
+                c = mm<kParts>(qr[i][f], old[f], c);
 #pragma unroll
             for (int r = 0; r < 4; ++r)
                 c[r] *= p.scale * mine[i][r];
-            c = mm<OUT>(pf[i][0], U0, c);
+            c = mm<kParts>(pf[i][0], U0, c);
             if (span == 1)
-                c = mm<OUT>(pf[i][1], U1, c);
+                c = mm<kParts>(pf[i][1], U1, c);
             const int t0 = 32 * span + 4 * ((tile + i) & 1);
             if (live)
 #pragma unroll
@@ -1524,7 +1521,6 @@ SSD_KERNEL_WAVES(64 * WAVES, (WAVES == 8 || (T == kBF16 && KP <= 2) ? 2 : 1)) vo
     constexpr int K_ROOM = 64 * RS > 32 * KP * TS ? 64 * RS : 32 * KP * TS;
     constexpr int Q_ROOM = 64 * RS > COLS * TS ? 64 * RS : COLS * TS;
     SSD_LDS E k[K_ROOM], q[Q_ROOM], kt[32 * KP * TS];
-    SSD_LDS float pairs[64 * kPairStride];
     SSD_LDS v4u tri[kParts * kDeltaFrags * 64], pt[kParts * kDeltaFrags * 64];
     SSD_LDS DeltaGates gates;
     E *const qt = k, *const got = q;
@@ -1567,7 +1563,6 @@ SSD_KERNEL_WAVES(64 * WAVES, (WAVES == 8 || (T == kBF16 && KP <= 2) ? 2 : 1)) vo
     const int chunks = (length + kDeltaChunk - 1) / kDeltaChunk;  // those with tokens
     if (chunks > 0)
         fetch(chunks - 1, delta_chunk_tokens(length, chunks - 1));
-    delta_clear_pairs(pairs, NT);
     for (int i = thread_id(); i < kParts * kDeltaFrags * 64; i += NT)
         pt[i] = v4u{0u, 0u, 0u, 0u};
     for (int chunk = chunks - 1; chunk >= 0; --chunk) {
@@ -1581,11 +1576,11 @@ SSD_KERNEL_WAVES(64 * WAVES, (WAVES == 8 || (T == kBF16 && KP <= 2) ? 2 : 1)) vo
         if (wave == WAVES - 1)
             delta_gates_of(gates, ng, nbeta, n);
         block_sync();
-        delta_tiles<T, KP, kParts, WAVES, true>(k, q, gates, p.scale, pairs, tri, pt);
+        delta_tiles<T, KP, WAVES, true>(k, q, gates, p.scale, tri, pt);
         block_sync();
         blocks_store<T, COLS, NT, false, true>(no, vcols, n, (E *)nullptr, got);
         if (wave < 2)
-            delta_invert<true>(pairs + 32 * wave * kPairStride, wave, tri);
+            delta_invert<true>(wave, tri);
         // e^(G_C - G) K dS'
         Parts<kParts> Sp[KP];
 #pragma unroll
@@ -1704,7 +1699,7 @@ template <int T, int KP>
 SSD_KERNEL(64 * KP) void delta_spans_bwd_kernel(DeltaParams p)
 {
     typedef typename DeltaElem<T>::type E;
-    typedef DeltaPack<T, KP, true> Pack;
+    typedef DeltaPack<T, KP> Pack;
     constexpr int IN = Pack::IN, OWN = 4 / KP;  // tiles of 16 tokens to a wave
     SSD_LDS v4f share[2][KP][4][64];
     int64_t bh;
@@ -2033,7 +2028,7 @@ struct GradLds {
     static constexpr int TS = 64 + DeltaElem<T>::pad, RS = 32 * KP + DeltaElem<T>::pad;
     static constexpr int SW = KP <= 2 ? 64 : 32, SS = SW + 8;  // columns of the state at a time
     static constexpr int u_size = kParts * 64 * kGradStride, s_size = kParts * 32 * KP * SS;
-    static constexpr int tri_bytes = kParts * kDeltaFrags * 64 * 16 + 64 * kPairStride * 4;
+    static constexpr int tri_bytes = kParts * kDeltaFrags * 64 * 16;
     static_assert(tri_bytes <= u_size * 2, "the triangle fits where dR comes to stand");
     union {
         struct {
@@ -2098,9 +2093,7 @@ SSD_KERNEL_WAVES(256, (KP <= 2 && !MANY ? 2 : 1)) void delta_grad_kernel(DeltaPa
     const float *S = p.chunk_states + (((int64_t)b * p.chunks + chunk) * p.Hv + hv) * p.Dk * p.Dv;
     const float *gs = p.gs + at * p.Dk * p.Dv, *gr = p.gr + at * 64 * p.Dv;
     const E *v = (const E *)p.v + token * p.v_stride + hv * p.Dv, *go = (const E *)p.go + token * o_stride + hv * p.Dv;
-    char *const tri_at = MANY ? lds.own_tri : (char *)lds.a.r;
-    v4u *const tri = (v4u *)tri_at;
-    float *const pairs = (float *)(tri_at + kParts * kDeltaFrags * 64 * 16);
+    v4u *const tri = (v4u *)(MANY ? lds.own_tri : (char *)lds.a.r);
     v4f aq[2 * KP], reads[2 * KP], writes[2 * KP], m1t[4], m1[4], m2t[4], m2[4];
 #pragma unroll
     for (int i = 0; i < 2 * KP; ++i)
@@ -2138,13 +2131,12 @@ SSD_KERNEL_WAVES(256, (KP <= 2 && !MANY ? 2 : 1)) void delta_grad_kernel(DeltaPa
         delta_gates_of(lds.gates, g0, beta0, n);
     E *const kt = Lds::KEEP ? lds.own_kt : lds.c.kt;
     blocks_store<T, 32 * KP, 256, true, Lds::KEEP>(kb, p.Dk, n, lds.k, kt);
-    delta_clear_pairs(pairs, 256);
     block_sync();
     const DeltaGates &gates = lds.gates;
-    delta_tiles<T, KP, 1, 4, false>(lds.k, nullptr, gates, 0.f, pairs, tri, nullptr);
+    delta_tiles<T, KP, 4, false>(lds.k, nullptr, gates, 0.f, tri, nullptr);
     block_sync();
     if (wave < 2)
-        delta_invert<false>(pairs + 32 * wave * kPairStride, wave, tri);
+        delta_invert<false>(wave, tri);
     const E *kl = lds.k + tile_row(0, l) * RS + q8;
     const bool valid = own < n;
     for (int col = 0; MANY ? col < p.Dv : col == 0; col += 64) {

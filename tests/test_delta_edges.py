@@ -1,0 +1,38 @@
+"""The gated delta rule's further cases (delta_edge_cases) on the CPU, in the host emulator, in one process of its own (this file
+run as a program), as test_delta_emulated."""
+
+import os
+import subprocess
+import sys
+
+import pytest
+
+sys.path.insert(0, os.path.dirname(os.path.abspath(__file__)))
+
+import delta_edge_cases as edges
+import delta_emu_harness as harness
+from test_delta_emulated import _Run
+
+
+def everything(lib):
+    """(name, function) of every case."""
+    run = _Run(lib)
+    return [("halfway %s" % (c,), lambda c=c: edges.halfway(run, *c)) for c in edges.HALFWAY]
+
+
+@pytest.fixture(scope="module")
+def report(tmp_path_factory):
+    lib = harness.build(str(tmp_path_factory.mktemp("delta_edges")))
+    return subprocess.run([sys.executable, os.path.abspath(__file__), lib], capture_output=True, text=True)
+
+
+def test_every_case(report):
+    assert report.returncode == 0 and report.stdout.rstrip().endswith("all done"), \
+        report.stdout[-2000:] + report.stderr[-2000:]
+
+
+if __name__ == "__main__":
+    for name, fn in everything(harness.load(sys.argv[1])):
+        print(name, flush=True)
+        fn()
+    print("all done", flush=True)
