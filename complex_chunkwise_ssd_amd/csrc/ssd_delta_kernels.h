@@ -139,8 +139,8 @@ SSD_DEVICE double wave_scan_d(double v)
 SSD_DEVICE double delta_log2(float g) { return (g < -1000.f ? -1000. : (double)g) * 1.44269504088896340736; }
 SSD_DEVICE float delta_exp(double log2) { return hw_exp2((float)log2); }
 
-// What a chunk's decays are, for each of its tokens.
-struct DeltaGates {
+// What a chunk's decays are, for each of its tokens; read by fours, also from the second of two side by side.
+struct alignas(16) DeltaGates {
     double sum[64];      // G, in powers of two
     float since[64];     // e^G
     float left[64];      // e^(G_C - G)
