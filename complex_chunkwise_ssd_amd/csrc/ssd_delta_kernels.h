@@ -1916,8 +1916,9 @@ SSD_DEVICE void grad_load(GradBlocks<ROWS, ACROSS> &d, const float *src, int str
         const int unit = thread + 256 * i, r = unit / ACROSS, c = 8 * (unit % ACROSS);
         const uint32_t off = (uint32_t)(r < in ? r : in - 1) * step;
         if (cols % 4 == 0) {
-            const v4f lo = *(const v4f *)(x + (off + 4 * (uint32_t)(c < cols ? c : 0)));
-            const v4f hi = *(const v4f *)(x + (off + 4 * (uint32_t)(c + 4 < cols ? c + 4 : 0)));
+            v4f lo, hi;  // at the alignment of an element: the stored states are the caller's
+            __builtin_memcpy(&lo, x + (off + 4 * (uint32_t)(c < cols ? c : 0)), sizeof(lo));
+            __builtin_memcpy(&hi, x + (off + 4 * (uint32_t)(c + 4 < cols ? c + 4 : 0)), sizeof(hi));
 #pragma unroll
             for (int e = 0; e < 8; ++e)
                 d.v[i][e] = e < 4 ? lo[e & 3] : hi[e & 3];

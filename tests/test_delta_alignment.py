@@ -21,3 +21,10 @@ def program(tmp_path_factory):
 def test_tensors_on_a_boundary(program):
     r = _run(program, "0")
     assert r.returncode == 0 and "\nOK " in r.stdout, r.stdout[-500:] + r.stderr[:3000]
+
+
+def test_tensors_one_element_off(program):
+    """Alignment to the element is all that the header asks for: the same results, bit for bit."""
+    r = _run(program, "1")
+    assert r.returncode == 0 and "\nOK " in r.stdout, r.stdout[-500:] + r.stderr[:3000]
+    assert r.stdout == _run(program, "0").stdout

@@ -4,11 +4,13 @@ import os
 import sys
 
 import pytest
+import torch
 
 sys.path.insert(0, os.path.dirname(os.path.abspath(__file__)))
 
+import complex_chunkwise_ssd_amd as ssd
 import delta_edge_cases as edges
-from test_gpu_delta import _Gpu
+from test_gpu_delta import _both, _Gpu, _inputs
 
 pytestmark = pytest.mark.gpu
 
@@ -16,3 +18,23 @@ pytestmark = pytest.mark.gpu
 @pytest.mark.parametrize("case", edges.HALFWAY, ids=str)
 def test_halfway(case):
     edges.halfway(_Gpu, *case)
+
+
+def _off(t):
+    """The same values one element past a boundary."""
+    wide = torch.empty(t.numel() + 1, dtype=t.dtype, device=t.device)
+    wide[1:] = t.reshape(-1)
+    return wide[1:].view(t.shape)
+
+
+@pytest.mark.parametrize("sizes", [(2, 140, 1, 2, 32, 40, "f32"), (2, 140, 1, 1, 72, 68, "bf16"), (97, 140, 1, 2, 64, 64, "bf16"),
+                                   (97, 70, 2, 2, 72, 36, "f32"), (97, 70, 1, 1, 128, 128, "bf16"), (3, 4, 1, 2, 24, 20, "bf16")])
+def test_tensors_one_element_off(sizes):
+    """Alignment to the element is all that is asked for: the same bits."""
+    *args, init = _inputs(*sizes)
+    want = _both(args, init, args[2])
+    got = _both([_off(w) for w in args], _off(init), _off(args[2]))
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    states = want[2]
+    grads = ssd.gated_delta_backward(*args, _off(states), args[2], grad_final_state=init)
+    assert all(torch.equal(a, b) for a, b in zip(grads, want[3:]))
