@@ -35,7 +35,8 @@ int check_delta(const DeltaSizes &z, int dtype, float scale)
         return SSD_ERR_SHAPE;
     const int64_t column_blocks = z.Dv <= 64 ? 1 : (z.Dv + 127) / 128 * 2;  // of 256 threads: the walks take up to 512
     const int64_t most = column_blocks > z.chunks() ? column_blocks : z.chunks();
-    return grid_ok(z.B * z.Hv * most, 256) ? SSD_OK : SSD_ERR_UNSUPPORTED;
+    // a batch has 2^40 heads at most, whose chunks pass 2^63
+    return z.B * z.Hv <= ssd::kMaxThreads && grid_ok(z.B * z.Hv * most, 256) ? SSD_OK : SSD_ERR_UNSUPPORTED;
 }
 
 int check_delta_strides(const DeltaSizes &z, int64_t q, int64_t k, int64_t v)

@@ -1,6 +1,7 @@
 // Alignment of what the gated delta rule reads and writes (TEST INFRASTRUCTURE), for -fsanitize=alignment on the host: in shared
 // memory, and in tensors that lie `argv[1]` elements past a boundary of 256 bytes (the workspace is always on one). Ends
-// with a number made of all results, the same for every such place.
+// with a number made of all results, the same for every such place. With "limits", for -fsanitize=signed-integer-overflow,
+// the arithmetic on sizes.
 #include "delta_emu_lib.cpp"
 
 #include <stddef.h>
@@ -102,8 +103,23 @@ bool grads_placed()
 
 }  // namespace
 
+// Sizes past the limits whose product passes 2^63: no workspace, whatever it wraps to.
+bool limits()
+{
+    const int64_t M = 1 << 24, T = 1 << 30, H = 1 << 16;
+    bool ok = true;
+    for (int64_t B : {M, M - 1, M / 2 + 5})
+        for (int64_t t : {T, T - 64, T / 2})
+            ok = ok && ssd_gated_delta_workspace_bytes(B, t, 1, H, 16, 32, SSD_BF16) == 0 &&
+                 ssd_gated_delta_backward_workspace_bytes(B, t, 1, H, 16, 32, SSD_BF16) == 0;
+    printf(ok ? "OK \n" : "a workspace\n");
+    return ok;
+}
+
 int main(int, char **argv)
 {
+    if (strcmp(argv[1], "limits") == 0)
+        return !limits();
     off = (size_t)atoi(argv[1]);
     bool ok = gates_placed() && grads_placed<ssd::kF32>() && grads_placed<ssd::kBF16>();
     if (!ok)

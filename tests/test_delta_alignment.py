@@ -1,5 +1,5 @@
-"""The gated delta rule on the host with every access held to the alignment that its type promises: a load by vectors of four
-floats may be compiled into one that needs 16 bytes."""
+"""The gated delta rule on the host with every access held to the alignment that its type promises (a load by vectors of four
+floats may be compiled into one that needs 16 bytes), and with signed sums and products held to their range."""
 
 import os
 import sys
@@ -15,7 +15,7 @@ from test_operators_sanitized import _build, _run
 @pytest.fixture(scope="module")
 def program(tmp_path_factory):
     return _build(harness.ROOT, "delta_align_main.cpp", tmp_path_factory.mktemp("delta_alignment") / "align",
-                  "-fsanitize=alignment", "-fno-sanitize-recover=alignment")
+                  "-fsanitize=alignment,signed-integer-overflow", "-fno-sanitize-recover=all")
 
 
 def test_tensors_on_a_boundary(program):
@@ -28,3 +28,8 @@ def test_tensors_one_element_off(program):
     r = _run(program, "1")
     assert r.returncode == 0 and "\nOK " in r.stdout, r.stdout[-500:] + r.stderr[:3000]
     assert r.stdout == _run(program, "0").stdout
+
+
+def test_sizes_past_the_limits(program):
+    r = _run(program, "limits")
+    assert r.returncode == 0 and r.stdout == "OK \n", r.stdout + r.stderr[:3000]
