@@ -137,7 +137,12 @@ SSD_DEVICE double wave_scan_d(double v)
 
 // A token's log decay in powers of two.
 SSD_DEVICE double delta_log2(float g) { return (g < -1000.f ? -1000. : (double)g) * 1.44269504088896340736; }
-SSD_DEVICE float delta_exp(double log2) { return hw_exp2((float)log2); }
+// To a unit or two: what the exponent's rounding to float32 takes off (22 units at 2^-125) is made up for.
+SSD_DEVICE float delta_exp(double log2)
+{
+    const float t = (float)log2, low = (float)(log2 - (double)t), e = hw_exp2(t);
+    return __builtin_fmaf(e, 0.693147182f * low, e);
+}
 
 // What a chunk's decays are, for each of its tokens; read by fours, also from the second of two side by side.
 struct alignas(16) DeltaGates {

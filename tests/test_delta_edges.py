@@ -17,7 +17,8 @@ from test_delta_emulated import _Run
 def everything(lib):
     """(name, function) of every case."""
     run = _Run(lib)
-    return [("halfway %s" % (c,), lambda c=c: edges.halfway(run, *c)) for c in edges.HALFWAY]
+    todo = [("halfway %s" % (c,), lambda c=c: edges.halfway(run, *c)) for c in edges.HALFWAY]
+    return todo + [("decays %s" % (c,), lambda c=c: edges.decays(run, *c)) for c in edges.DECAYS]
 
 
 @pytest.fixture(scope="module")

@@ -20,6 +20,11 @@ def test_halfway(case):
     edges.halfway(_Gpu, *case)
 
 
+@pytest.mark.parametrize("case", edges.DECAYS, ids=str)
+def test_decays(case):
+    edges.decays(_Gpu, *case)
+
+
 def _off(t):
     """The same values one element past a boundary."""
     wide = torch.empty(t.numel() + 1, dtype=t.dtype, device=t.device)
