@@ -41,9 +41,15 @@ int64_t row_groups(int64_t rows, int held, int64_t most)
     const int64_t need = (rows + held - 1) / held;
     return need < most ? need : most;
 }
+// Backwards a lane adds its rows' shares of the weights' gradients in float32: kChain of them at most, however many
+// rows there are, and the workgroups' shares are added in float64.
+constexpr int64_t kChain = 256;
 int64_t bwd_groups(int64_t rows, int64_t F)
 {
-    return row_groups(rows, F <= 128 ? 16 : F <= 1024 ? 4 : 1, F <= 4096 ? 1024 : 512);
+    const int held = F <= 128 ? 16 : F <= 1024 ? 4 : 1;
+    const int64_t few = F <= 4096 ? 1024 : 512, chains = (rows + held * kChain - 1) / (held * kChain);
+    const int64_t most = ssd::kMaxThreads / 1024;  // of one launch
+    return row_groups(rows, held, chains < few ? few : chains < most ? chains : most);
 }
 
 // Lanes of a head, as a power of two, or -1 (see the kernels).

@@ -314,10 +314,10 @@ SSD_KERNEL(NormShape<LANES>::threads) void gated_norm_bwd_kernel(GatedNormParams
         block_sync();
     }
     for (int d = thread_id(); d < p.D; d += Shape::threads) {
-        float s = 0.f;
+        double s = 0.;
         for (int h = 0; h < p.H; ++h)
             s += total[h * p.D + d];
-        p.part[block_id() * p.D + d] = s;
+        p.part[block_id() * p.D + d] = (float)s;
     }
 }
 
@@ -567,16 +567,16 @@ SSD_KERNEL(NormShape<LANES>::threads) void block_norm_bwd_kernel(BlockNormParams
 
 // Sums over the workgroups' shares part (rows, n), in a fixed order, the first `split` columns to out0
 // and the others to out1: 64 columns per workgroup, its 16 waves take every 16th row and their sums are
-// added in wave order.
+// added in wave order, all in float64.
 constexpr int kShareSumWaves = 16;
 
 SSD_KERNEL(64 * kShareSumWaves) void share_sum_kernel(const float *part, int rows, int n, int split, float *out0,
                                                       float *out1)
 {
-    SSD_LDS float sums[kShareSumWaves][64];
+    SSD_LDS double sums[kShareSumWaves][64];
     const int lane = thread_id() & 63, wave = wave_id();
     const int64_t c = block_id() * 64 + lane;
-    float acc = 0.f;
+    double acc = 0.;
     if (c < n) {
 #pragma unroll 8
         for (int r = wave; r < rows; r += kShareSumWaves)
@@ -585,14 +585,14 @@ SSD_KERNEL(64 * kShareSumWaves) void share_sum_kernel(const float *part, int row
     sums[wave][lane] = acc;
     block_sync();
     if (wave == 0 && c < n) {
-        float t = 0.f;
+        double t = 0.;
 #pragma unroll
         for (int i = 0; i < kShareSumWaves; ++i)
             t += sums[i][lane];
         if (c < split)
-            out0[c] = t;
+            out0[c] = (float)t;
         else
-            out1[c - split] = t;
+            out1[c - split] = (float)t;
     }
 }
 
