@@ -9,6 +9,7 @@ import pytest
 
 sys.path.insert(0, os.path.dirname(os.path.abspath(__file__)))
 
+import delta_cases as cases
 import delta_edge_cases as edges
 import delta_emu_harness as harness
 from test_delta_emulated import _Run
@@ -18,7 +19,13 @@ def everything(lib):
     """(name, function) of every case."""
     run = _Run(lib)
     todo = [("halfway %s" % (c,), lambda c=c: edges.halfway(run, *c)) for c in edges.HALFWAY]
-    return todo + [("decays %s" % (c,), lambda c=c: edges.decays(run, *c)) for c in edges.DECAYS]
+    todo += [("decays %s" % (c,), lambda c=c: edges.decays(run, *c)) for c in edges.DECAYS]
+    for c in edges.MANY:
+        todo.append(("forward %s" % (c[:7],), lambda c=c: cases.forward(run, *c)))
+        todo.append(("backward %s" % (c[:7],), lambda c=c: cases.backward(run, *c)))
+    todo += [("outputs %s" % (c[:7],), lambda c=c: edges.outputs(run, *c)) for c in edges.OUTPUTS]
+    todo += [("many heads: " + name, fn) for name, fn in edges.many(run)]
+    return todo + [("shuffled", lambda: edges.shuffled(run, lib.emu_set_shuffle_seed))]
 
 
 @pytest.fixture(scope="module")

@@ -9,6 +9,7 @@ import torch
 sys.path.insert(0, os.path.dirname(os.path.abspath(__file__)))
 
 import complex_chunkwise_ssd_amd as ssd
+import delta_cases as cases
 import delta_edge_cases as edges
 from test_gpu_delta import _both, _Gpu, _inputs
 
@@ -23,6 +24,26 @@ def test_halfway(case):
 @pytest.mark.parametrize("case", edges.DECAYS, ids=str)
 def test_decays(case):
     edges.decays(_Gpu, *case)
+
+
+@pytest.mark.parametrize("case", edges.MANY, ids=lambda c: str(c[:7]))
+def test_many_heads(case):
+    cases.forward(_Gpu, *case)
+
+
+@pytest.mark.parametrize("case", edges.MANY, ids=lambda c: str(c[:7]))
+def test_many_heads_backward(case):
+    cases.backward(_Gpu, *case)
+
+
+@pytest.mark.parametrize("case", edges.OUTPUTS, ids=lambda c: str(c[:7]))
+def test_outputs(case):
+    edges.outputs(_Gpu, *case)
+
+
+@pytest.mark.parametrize("name,fn", edges.many(_Gpu), ids=lambda x: x if isinstance(x, str) else "")
+def test_many_heads_as_few(name, fn):
+    fn()
 
 
 def _off(t):
