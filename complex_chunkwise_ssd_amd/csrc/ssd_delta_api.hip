@@ -52,8 +52,27 @@ int check_delta_strides(const DeltaSizes &z, int64_t q, int64_t k, int64_t v)
 
 bool delta_few(const DeltaSizes &z) { return z.T <= ssd::kDeltaFew; }
 
-// Whether a call's heads are too few for a walk of their own to fill the chip, and what is packed for them.
-bool delta_long(const DeltaSizes &z) { return z.B * z.Hv * ((z.Dv + 63) / 64) <= 192; }
+// Whether a call's heads are too few for a walk of their own to fill the chip, in blocks of 64 columns. A packed walk's time
+// grows with the blocks, the other's hardly does up to a workgroup (or two) for each compute unit. Both
+// measured from 32 to 768 blocks with heads of 64 and of 128; at one side and the other of each bound (2048 tokens, us, packed /
+// not; at 200 and at 8192 tokens they cross at the same place):
+//   bfloat16          64 x 64     96 blocks 223 / 252   128 blocks 274 / 253     64 x 128   128: 188 / 254   192: 274 / 257
+//                     128 x 64    96        288 / 327   128        338 / 336    128 x 128   128: 257 / 349   192: 428 / 355
+//   its gradients     64 x 64     96        361 / 393   160        609 / 499     64 x 128   128: 456 / 516   192: 725 / 655
+//   with 128 features 128 x 64    64        484 / 556    96        784 / 688    128 x 128    96: 702 / 712   128: 859 / 835
+//   float32           64 x 64    128        412 / 463   160        585 / 466     64 x 128   128: 290 / 446   192: 479 / 467
+//                     128 x 64   128        676 / 745   160        948 / 750    128 x 128   128: 524 / 872   192: 940 / 896
+//   its gradients     64 x 64    128        767 / 793   160       1032 / 879     64 x 128   128: 691 / 842   192: 1076 / 1038
+//                     128 x 64    96       1248 / 1326  160       2015 / 1731   128 x 128   128: 1241 / 1571 256: 2484 / 2268
+//   float32           128 x 256  192        756 / 877   256        912 / 919   (gradients 1530 / 1729, 2045 / 2016)
+bool delta_long(const DeltaSizes &z, int dtype, bool backward)
+{
+    const bool wide = z.Dv > 64;
+    const int64_t most = dtype == SSD_F32         ? (z.Dk > 64 && z.Dv > 128 ? 240 : wide ? 176 : 128)
+                         : backward && z.Dk > 64 ? (wide ? 112 : 80)
+                                                 : (wide ? 160 : 112);
+    return z.B * z.Hv * ((z.Dv + 63) / 64) <= most;
+}
 
 template <int T, int KP>
 constexpr size_t pack_bytes() { return 16 * (size_t)ssd::DeltaPack<T, KP>::size; }
@@ -65,9 +84,9 @@ struct DeltaRange {
     size_t pack, carry;
     size_t bytes() const { return pack + carry; }
 };
-DeltaRange delta_range(const DeltaSizes &z, int dtype)
+DeltaRange delta_range(const DeltaSizes &z, int dtype, bool backward)
 {
-    if (!delta_long(z))
+    if (!delta_long(z, dtype, backward))
         return {0, 0, 0};
     const size_t one = dtype == SSD_BF16 ? (z.Dk <= 64 ? pack_bytes<ssd::kBF16, 2>() : pack_bytes<ssd::kBF16, 4>())
                                          : (z.Dk <= 64 ? pack_bytes<ssd::kF32, 2>() : pack_bytes<ssd::kF32, 4>());
@@ -221,7 +240,7 @@ size_t ssd_gated_delta_workspace_bytes(int64_t batch, int64_t T, int64_t Hk, int
     const DeltaSizes z{batch, T, Hk, Hv, Dk, Dv};
     if (check_delta(z, dtype, 1.f) || z.empty() || delta_few(z))
         return 0;
-    return delta_range(z, dtype).bytes();
+    return delta_range(z, dtype, false).bytes();
 }
 
 int ssd_gated_delta(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v, int64_t v_stride,
@@ -271,7 +290,7 @@ int ssd_gated_delta(const void *q, int64_t q_stride, const void *k, int64_t k_st
     p.states = chunk_states;
     if (delta_few(z))
         return dtype == SSD_BF16 ? launch_delta_few<ssd::kBF16>(p, s) : launch_delta_few<ssd::kF32>(p, s);
-    const DeltaRange range = delta_range(z, dtype);
+    const DeltaRange range = delta_range(z, dtype, false);
     char *at = (char *)workspace;
     if (dtype == SSD_BF16)
         return Dk <= 64 ? launch_delta<ssd::kBF16, 2>(p, range, at, s) : launch_delta<ssd::kBF16, 4>(p, range, at, s);
@@ -284,7 +303,7 @@ size_t ssd_gated_delta_backward_workspace_bytes(int64_t batch, int64_t T, int64_
     const DeltaSizes z{batch, T, Hk, Hv, Dk, Dv};
     if (check_delta(z, dtype, 1.f) || z.empty())
         return 0;
-    return delta_space(z).bytes() + delta_range(z, dtype).bytes();
+    return delta_space(z).bytes() + delta_range(z, dtype, true).bytes();
 }
 
 int ssd_gated_delta_backward(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
@@ -346,7 +365,7 @@ int ssd_gated_delta_backward(const void *q, int64_t q_stride, const void *k, int
     p.gr = (float *)(at + space.gs);
     p.wq = (float *)(at + space.gs + space.gr);
     p.wk = (float *)(at + space.gs + space.gr + space.w);
-    const DeltaRange range = delta_range(z, dtype);
+    const DeltaRange range = delta_range(z, dtype, true);
     at += space.bytes();
     if (dtype == SSD_BF16)
         return Dk <= 64 ? launch_delta_bwd<ssd::kBF16, 2>(p, range, at, s) : launch_delta_bwd<ssd::kBF16, 4>(p, range, at, s);

@@ -1698,8 +1698,8 @@ SSD_KERNEL_WAVES(64 * WAVES, (WAVES == 8 || (T == kBF16 && KP <= 2) ? 2 : 1)) vo
 
 // The same with few heads: by spans of features, as delta_spans_kernel, on what delta_pack_kernel made. Here the walk
 // has twice the products, and one wave with all features was slower in both types (the gradients as a whole,
-// T 2048, us, this form / that: 16 heads of 128 in bfloat16 275 / 342, in float32 389 / 685; 96 heads, bfloat16
-// 1291 / 1210, float32 1889 / 2085).
+// T 2048, us, this form / that: 16 heads of 128 in bfloat16 275 / 342, in float32 389 / 685; 32 heads 438 / 526 and
+// 639 / 1119).
 template <int T, int KP>
 SSD_KERNEL(64 * KP) void delta_spans_bwd_kernel(DeltaParams p)
 {
