@@ -190,7 +190,10 @@ int launch_delta(const ssd::DeltaParams &p, const DeltaRange &range, char *works
 {
     if (range.chunks > 0)
         return launch_delta_long<T, KP, false>(p, range, workspace, s);
-    return p.Dv > 64 && KP == 4 ? launch_delta_as<T, KP, 8>(p, s) : launch_delta_as<T, KP, 4>(p, s);
+    if constexpr (KP == 4)
+        if (p.Dv > 64)
+            return launch_delta_as<T, KP, 8>(p, s);
+    return launch_delta_as<T, KP, 4>(p, s);
 }
 
 template <int T, int KP, int WAVES>
@@ -202,9 +205,19 @@ int launch_delta_scan_bwd(ssd::DeltaParams p, hipStream_t s)
     return launch_status();
 }
 template <int T, int KP>
+int launch_delta_walk_bwd(const ssd::DeltaParams &p, const DeltaRange &range, char *workspace, hipStream_t s)
+{
+    if (range.chunks > 0)
+        return launch_delta_long<T, KP, true>(p, range, workspace, s);
+    if constexpr (KP == 4)
+        if (p.Dv > 64)
+            return launch_delta_scan_bwd<T, KP, 8>(p, s);
+    return launch_delta_scan_bwd<T, KP, 4>(p, s);
+}
+template <int T, int KP>
 int launch_delta_bwd(const ssd::DeltaParams &p, const DeltaRange &range, char *workspace, hipStream_t s)
 {
-    if (int st = range.chunks > 0 ? launch_delta_long<T, KP, true>(p, range, workspace, s) : p.Dv > 64 && KP == 4 ? launch_delta_scan_bwd<T, KP, 8>(p, s) : launch_delta_scan_bwd<T, KP, 4>(p, s))
+    if (int st = launch_delta_walk_bwd<T, KP>(p, range, workspace, s))
         return st;
     const dim3 grid((unsigned)((int64_t)p.B * p.Hv * p.chunks)), block(256);
     if (p.Dv > 64)

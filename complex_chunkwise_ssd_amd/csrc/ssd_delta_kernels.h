@@ -178,8 +178,8 @@ SSD_DEVICE void delta_gates(DeltaGates &s, const float *g, const float *beta, in
 // each wait for its own. Offsets within a chunk are 32 bits wide.
 template <int T, int COLS, int NT>
 struct Blocks {
-    static constexpr int across = COLS / 4, units = (16 * across + NT - 1) / NT;
-    static constexpr bool even = 16 * across % NT == 0;
+    static constexpr int units = 4 * COLS / NT;
+    static_assert(4 * COLS % NT == 0, "every thread has as many blocks");
     typename DeltaElem<T>::type v[units][4][4];
 };
 template <int COLS, int NT>
@@ -197,7 +197,7 @@ SSD_DEVICE void blocks_load(Blocks<T, COLS, NT> &d, const void *src, int stride,
 #pragma unroll
     for (int i = 0; i < d.units; ++i) {
         const int f = block_col<COLS, NT>(thread, i), t = block_row<COLS, NT>(thread, i);
-        if (D % 4 == 0 && n == 64 && d.even) {
+        if (D % 4 == 0 && n == 64) {
             const uint32_t off = (uint32_t)t * step + (uint32_t)(f < D ? f : 0) * sizeof(E);
 #pragma unroll
             for (int a = 0; a < 4; ++a)
@@ -228,8 +228,6 @@ SSD_DEVICE void blocks_store(Blocks<T, COLS, NT> &d, int D, int n, typename Delt
 #pragma unroll
     for (int i = 0; i < d.units; ++i) {
         const int f = block_col<COLS, NT>(thread, i), t = block_row<COLS, NT>(thread, i);
-        if (!d.even && t >= 64)
-            break;
         E (&v)[4][4] = d.v[i];
         if (n < 64 || D < COLS) {
 #pragma unroll
@@ -249,14 +247,6 @@ SSD_DEVICE void blocks_store(Blocks<T, COLS, NT> &d, int D, int n, typename Delt
                 __builtin_memcpy(__builtin_assume_aligned(turned + (f + b) * TS + t, sizeof(w)), w, sizeof(w));
             }
     }
-}
-template <int T, int KP, bool ROWS, bool TURNED>
-SSD_DEVICE void delta_stage(const void *src, int64_t stride, int D, int n, typename DeltaElem<T>::type *rows,
-                            typename DeltaElem<T>::type *turned)
-{
-    Blocks<T, 32 * KP, 256> blocks;
-    blocks_load<T, 32 * KP, 256>(blocks, src, (int)stride, D, n);
-    blocks_store<T, 32 * KP, 256, ROWS, TURNED>(blocks, D, n, rows, turned);
 }
 
 SSD_DEVICE int delta_valid(const DeltaParams &p, int b)  // tokens of a sequence
@@ -1903,7 +1893,7 @@ SSD_KERNEL(64 * KP) void delta_spans_bwd_kernel(DeltaParams p)
 
 constexpr int kGradStride = 72;   // 64 columns and room against bank conflicts
 
-// Rows by 32 TWO columns (TWO = 2: 64) of a float32 matrix in memory, on their way into shared memory in parts, row-major,
+// ROWS rows by 8 ACROSS columns of a float32 matrix in memory, on their way into shared memory in parts, row-major,
 // by 256 threads: units of eight neighbours. Zeros from `in` rows and `cols` columns on.
 template <int ROWS, int ACROSS>
 struct GradBlocks {
