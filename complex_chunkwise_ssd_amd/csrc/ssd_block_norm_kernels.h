@@ -16,8 +16,12 @@
 // may belong to.
 //
 // 65536 rows of 1024 in bfloat16: the gated norm to 8 bits 80 to 97 us (336 MB; bound by the gate's exponential and
-// reciprocal, 75.5 with the hardware's reciprocal alone), its gradients 139 (671 MB, 4.8 TB/s); the block norm to 8 bits 93
-// (470 MB, 5.0 TB/s), its gradients with the residual's 152 (805 MB, 5.3 TB/s): all but the first at the rate of a copy.
+// reciprocal, VALU 93 %; 75.5 with the hardware's reciprocal alone), its gradients 140 (671 MB, 4.8 TB/s); the block norm to
+// 8 bits 94 (470 MB, 5.0 TB/s), its gradients with the residual's 159 (805 MB, 5.1 TB/s): all but the first near the
+// rate of a copy, also in float32 (128, 253, 164 and 300 us) and for rows up to 8192. Above, 16 waves share a row and a lane has
+// 128 registers: gradients spill (gated 148 to 220 bytes a lane, block 180 and 228; block_norm_kernel in float32 36), read
+// their weights again and load no row ahead. 4096 rows of 12288, TB/s in bfloat16 / float32: gated 2.7 / 3.4,
+// its gradients 2.2 / 3.6, block 4.1 / 4.1, its gradients 2.0 / 2.5.
 #pragma once
 
 #include <ssd_row.h>

@@ -6,9 +6,10 @@
 //     (I + A) U = R = beta (V - e^G K S)         O = scale (e^G Q S + (Q K^T o D) U)
 //     S' = e^{G_C} S + (e^{G_C - G} K)^T U
 // The columns of S, V, U and O (over Dv) do not meet, so a wave walks over the chunks with 16 columns
-// of the state in its registers. The 64 x 64 system is solved in two blocks of 32, whose own
-// inverses T_00 and T_11 are formed beforehand for all chunks at once (rows of 16 by substitution,
-// which is stable whatever the keys, the rest by products):
+// of the state in its registers. The 64 x 64 system is solved in two blocks of 32 with their own
+// inverses T_00 and T_11 (blocks of 16 by substitution, which is stable whatever the keys, the rest by
+// products), which the walks and the gradients' kernel form chunk by chunk; only with few heads does a kernel
+// before the walk make those of a whole range of chunks:
 //     U_0 = T_00 R_0       U_1 = T_11 (R_1 - A_10 U_0)
 //
 // Backwards, for the gradients of O and of S':
@@ -588,9 +589,12 @@ SSD_DEVICE void span_mm(v4f &c, const Parts<N> &a, const Parts<kParts> &b, int f
 // waves solve the blocks of 32, the others go on with what the state gives. The next chunk's rows are in
 // flight meanwhile. Outputs have all three parts too, whatever type they are stored in: with two, 16 bits, values within 2^-16
 // of the middle of two bfloat16 numbers went to the wrong one, for 6 % less time.
-// 32 x 2048 tokens on 16 heads of 64 in bfloat16, with states: 350 us (822 MB, 2.3 TB/s; 330 with two parts), of all
-// cycles VALU 47 % and MFMA 17 %: splitting into parts and the triangle's substitution bound it, not memory. As
-// two kernels, triangles first, it was 1199 us; with the blocks on the diagonal inverted through shared memory 379.
+// 32 x 2048 tokens on 16 heads of 64 in bfloat16, with states: 350 us (822 MB, 2.3 TB/s; 330 with two parts). No unit
+// is full: VALU 49 % of all cycles, MFMA 20 %. With 237 registers and 76 KB of shared memory two waves run on a SIMD, and
+// each waits 38 % of its time, for the four barriers of a chunk, shared memory and its own products. In float32 and
+// with 128 features it is one wave, or two that spill (eight waves: 37 registers, 152 bytes a lane); 512 heads of 64
+// 947 us, 256 heads of 128 997 (bfloat16 401). As two kernels, triangles first, it was 1199 us; with the blocks on the
+// diagonal inverted through shared memory 379.
 template <int T, int KP, int WAVES>
 SSD_KERNEL_WAVES(64 * WAVES, (WAVES == 8 || (T == kBF16 && KP <= 2) ? 2 : 1)) void delta_scan_kernel(DeltaParams p)
 {
@@ -794,7 +798,7 @@ SSD_KERNEL_WAVES(64 * WAVES, (WAVES == 8 || (T == kBF16 && KP <= 2) ? 2 : 1)) vo
 
 // ------------------------------------------------------------- few heads, long sequences
 
-// Where sequences and heads give too few workgroups, what a chunk has beside the state is made for all chunks at once
+// Where sequences and heads give too few workgroups, what a chunk has beside the state is made for a range of chunks at once
 // (delta_pack_kernel) and laid out as the operands that the walk takes, and the walk has 16 columns a workgroup and no
 // more to do than the state asks for: one wave passes the state on, a second one makes the outputs
 // from what the first leaves in shared memory.
@@ -1121,10 +1125,11 @@ SSD_KERNEL(128) void delta_long_kernel(DeltaParams p)
 // memory, every wave solves for U, and each makes some of the outputs' tiles. Operands are loaded a chunk
 // ahead, into the registers that the last ones leave. A chunk is a chain of dependent products and their splitting
 // into parts, some 3 us of it whatever the width; one wave with all features takes 4 to 6 (T 2048, us, this form / the
-// other: 16 heads of 64 146 / 186, 96 heads 333 / 370, 32 heads of 128 262 / 376). With up to 64 features it is
+// other: 16 heads of 64 139 / 184, 96 heads 331 / 374, 32 heads of 128 249 / 364). With up to 64 features it is
 // always taken; with more, its four waves have a compute unit to themselves, and where there are more workgroups
-// than units the other form is as fast or faster (48 heads of 128: 473 / 421). In bfloat16, where K, and the products
-// of K, have a third of the parts, it gains 5 % with 64 features and loses 14 % with 128: not taken.
+// than units the other form is as fast or faster (48 heads of 128: 459 / 449). In bfloat16, where K, and the products
+// of K, have a third of the parts, it gains 7 % with 64 features and loses 18 % with 128: not taken (with 64 alone it would
+// have the walk over many heads sum span by span as well, for the same bits, which costs that 3 %).
 constexpr int kSpansMost = 256;  // workgroups
 
 // Operands at a place that is the same for all lanes, so that its address is scalar work.
@@ -1505,7 +1510,8 @@ SSD_KERNEL(256) void delta_few_kernel(DeltaParams p)
 
 // As delta_scan_kernel, from the last chunk to the first, with the gradient of the state: dS' of every chunk and
 // dR go to memory. K's rows make room for Q's columns once they have been used, Q's rows for those of dO, so that
-// two workgroups fit a compute unit. 32 x 2048 tokens on 16 heads of 64 in bfloat16: 346 us, VALU 47 %, MFMA 18 %.
+// two workgroups fit a compute unit. 32 x 2048 tokens on 16 heads of 64 in bfloat16: 360 us; VALU 49 %, MFMA 17 %, and
+// a wave, of two on a SIMD, waits 36 % of its time, as forwards.
 template <int T, int KP, int WAVES>
 SSD_KERNEL_WAVES(64 * WAVES, (WAVES == 8 || (T == kBF16 && KP <= 2) ? 2 : 1)) void delta_scan_bwd_kernel(DeltaParams p)
 {
@@ -2048,8 +2054,11 @@ struct GradLds {
 
 // dQ, dK, dV, dg and dbeta of a chunk and value head. A wave takes 16 tokens as columns of everything: lane l token
 // 16 w + l, and as rows the features or the other tokens. Where value heads share a key head, their dQ and dK
-// go to memory in float32 and are added afterwards. 32 x 2048 tokens on 16 heads of 64 in bfloat16: 769 us, VALU 52 %,
-// MFMA 21 %; where it spilled registers the gradients as a whole took 1709 us, without 1308 (now 1120).
+// go to memory in float32 and are added afterwards. 32 x 2048 tokens on 16 heads of 64 in bfloat16: 800 us; VALU 54 %,
+// MFMA 21 %, and a wave waits 41 % of its time: 230 registers let two run on a SIMD. Where it spilled there, the
+// gradients as a whole took 1709 us, without 1308 (now 1160). With more features or columns one wave runs on a SIMD, and with both
+// it spills: 121 registers (488 bytes a lane) in bfloat16, 128 (516) in float32; 256 heads of 128, the gradients as a
+// whole, 2335 us (1.5 GB) and 3654.
 template <int T, int KP, bool MANY>
 SSD_KERNEL_WAVES(256, (KP <= 2 && !MANY ? 2 : 1)) void delta_grad_kernel(DeltaParams p)
 {

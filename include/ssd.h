@@ -676,7 +676,8 @@ int ssd_gated_norm(const void *x, int64_t x_stride, const void *gate, int64_t ga
  *   rstd         as the forward wrote it.
  *   grad_y       (rows, F) of `dtype`, rows grad_y_stride elements apart.
  *   grad_x, grad_gate out: (rows, F) of `dtype`, dense.
- *   grad_weight  out: (D) float32, summed in a fixed order.
+ *   grad_weight  out: (D) float32, summed in a fixed order (in float32 over at most 256 rows, then in
+ *                float64).
  *   workspace    ssd_gated_norm_backward_workspace_bytes(rows, F, D) bytes, 256-byte aligned.
  * rows equal to 0 sets grad_weight to zero. No output may overlap an input, another
  * output or the workspace (SSD_ERR_ALIAS).
@@ -728,7 +729,7 @@ int ssd_block_norm(const void *x, int64_t x_stride, const void *residual, int64_
  *   grad_y       (rows, F) of `dtype`; grad_residual nullable, the same: the gradient that
  *                reaches s through the residual stream.
  *   grad_x, grad_residual_in out: (rows, F) of `dtype`, dense.
- *   grad_post_weight, grad_pre_weight out: (F) float32, summed in a fixed order.
+ *   grad_post_weight, grad_pre_weight out: (F) float32, summed as grad_weight above.
  *   workspace    ssd_block_norm_backward_workspace_bytes(rows, F) bytes, 256-byte aligned.
  * rows equal to 0 sets the weights' gradients to zero. No output may overlap an input,
  * another output or the workspace (SSD_ERR_ALIAS).
