@@ -90,7 +90,7 @@ def gated_delta(q, k, v, g, beta, scale: float | None = None, initial_state=None
     and u_t = beta_t (v_t - S'^T k_t), S_t = S' + k_t u_t^T and o_t = scale S_t^T q_t.
 
     q, k (B, T, Hk, Dk) and v (B, T, Hv, Dv) float32 or bfloat16, contiguous or column ranges of one
-    (B, T, S) tensor of projected rows; Hv is a multiple of Hk (neighbouring value heads share a key
+    (B, T, S) tensor of projected rows (a range of tokens of several rows has to be copied first); Hv is a multiple of Hk (neighbouring value heads share a key
     head); Dk <= 128, Dv <= 256. g (log decays, <= 0) and beta (B, T, Hv) float32; scale: Dk^-1/2
     if None. initial_state (B, Hv, Dk, Dv) float32; lengths (B,) int32: tokens from a row's length
     on are padding (whatever they hold, o = 0 and the state stays). Keys are meant to have a

@@ -45,7 +45,8 @@ struct GatedNormParams {
 };
 
 // 1 / (1 + e^-z) to about a unit: the exponent's rounding is made up for (it would move a gated value across
-// the border of two e4m3 values 16 times as often), and the reciprocal gets a Newton step where it is a number.
+// the border of two e4m3 values 16 times as often), and the reciprocal gets a Newton step where it is a number. Below
+// 2^-126 (z < -87.3) it is 0.
 SSD_DEVICE float exact_sigmoid(float z)
 {
     const float log2e = 1.44269502f, rest = 1.92596303e-8f;  // their sum is log2 e to 2^-50

@@ -1,6 +1,8 @@
 """The weights' gradients of the norms around a block over very many rows: a lane adds at most 256 of them in float32, what is
 added further is float64, so that errors do not grow with the rows."""
 
+import os
+
 import pytest
 import torch
 
@@ -8,6 +10,13 @@ import complex_chunkwise_ssd_amd as ssd
 
 U = 2.0 ** -24
 CHAIN = 256
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    if not os.path.exists(ssd.LIBPATH):
+        from complex_chunkwise_ssd_amd import build
+        build.build()
 
 
 def _held(F):

@@ -12,9 +12,8 @@ sys.path.insert(0, os.path.dirname(os.path.abspath(__file__)))
 import delta_cases as cases
 import delta_edge_cases as edges
 import delta_emu_harness as harness
+from test_delta_boundary import lib  # noqa: F401
 from test_delta_emulated import _Run
-
-import complex_chunkwise_ssd_amd as ssd  # found by the harness
 
 
 def everything(lib):
@@ -41,10 +40,10 @@ def test_every_case(report):
         report.stdout[-2000:] + report.stderr[-2000:]
 
 
-def test_forms_by_blocks_of_columns():
+def test_forms_by_blocks_of_columns(lib):
     """A forward call takes a workspace only where its chunks are packed: the sizes on either side of the bounds where both forms
     were measured."""
-    size = ssd.load_library().ssd_gated_delta_workspace_bytes
+    size = lib.ssd_gated_delta_workspace_bytes
     for dtype, Dk, Dv, packed, walked in ((1, 64, 64, 96, 128), (1, 128, 64, 96, 128), (1, 64, 128, 64, 96), (1, 128, 128, 64, 96),
                                           (0, 64, 64, 128, 160), (0, 128, 64, 128, 160), (0, 64, 128, 64, 96), (0, 128, 128, 64, 96)):
         assert size(1, 2048, packed, packed, Dk, Dv, dtype) > 0 and size(1, 2048, walked, walked, Dk, Dv, dtype) == 0
